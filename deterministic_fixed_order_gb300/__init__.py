@@ -496,3 +496,14 @@ def mean_scale(W: int) -> float:
 
 def shard_plan(length: int, W: int):
     return detfold_shard_plan(length, W)
+
+
+# ------------------------------------------------------------------ the decode step's attention
+
+from . import attention as attention  # noqa: E402  (it builds on the helpers above)
+from .attention import (  # noqa: E402
+    PagedCache, Rope, detfold_attn_decode, detfold_attn_decode_workspace_bytes, detfold_attn_join,
+    detfold_kv_append)
+
+__all__ += ["attention", "PagedCache", "Rope", "detfold_attn_decode", "detfold_attn_decode_workspace_bytes",
+            "detfold_attn_join", "detfold_kv_append"]

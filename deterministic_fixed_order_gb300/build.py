@@ -8,7 +8,9 @@ any multiply-add contraction.
 
 The measurement probes (``csrc/probes/*.cu``, the latency floors that graphs
 of small folds are compared against) link into a library of their own,
-``libdetfold_probes.so``, which the fold library's binding never loads.
+``libdetfold_probes.so``, which the fold library's binding never loads. The
+decode-step attention operators (``csrc/attn/*.cu``) link into
+``libdetfold_attn.so``.
 """
 from __future__ import annotations
 
@@ -26,6 +28,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdetfold.so")
 PROBES_CSRC = os.path.join(CSRC, "probes")
 PROBES_LIB = os.path.join(PKG, "libdetfold_probes.so")
+ATTN_CSRC = os.path.join(CSRC, "attn")
+ATTN_LIB = os.path.join(PKG, "libdetfold_attn.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -51,6 +55,12 @@ def _probe_inputs() -> list[str]:
                      os.path.abspath(__file__)])
 
 
+def _attn_inputs() -> list[str]:
+    return sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu")) + glob.glob(os.path.join(ATTN_CSRC, "*.cuh"))
+                  + [os.path.join(INCLUDE, "detfold.h"), os.path.join(INCLUDE, "detfold_attn.h"),
+                     os.path.abspath(__file__)])
+
+
 def stale(lib: str = LIB, inputs=None) -> bool:
     if not os.path.exists(lib):
         return True
@@ -61,13 +71,16 @@ def stale(lib: str = LIB, inputs=None) -> bool:
 def build(force: bool = False, defines: dict | None = None, lib: str = LIB,
           build_dir: str = BUILD_DIR, verbose: bool = False) -> str:
     """Compile and link libdetfold.so (and, for the default library path, the
-    probes library); returns the fold library's path.
+    probes and attention libraries); returns the fold library's path.
 
     ``defines`` adds -D macros (launch-shape knobs of csrc/detfold_launch.cuh).
     """
     if lib == LIB and (force or stale(PROBES_LIB, _probe_inputs())):
         _link(sorted(glob.glob(os.path.join(PROBES_CSRC, "*.cu"))), PROBES_LIB,
               os.path.join(build_dir, "probes"), [], verbose)
+    if lib == LIB and (force or stale(ATTN_LIB, _attn_inputs())):
+        _link(sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu"))), ATTN_LIB,
+              os.path.join(build_dir, "attn"), [], verbose)
     if not force and not defines and not stale(lib):
         return lib
     dflags = [f"-D{k}={v}" for k, v in (defines or {}).items()]
