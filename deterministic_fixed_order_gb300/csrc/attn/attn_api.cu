@@ -143,7 +143,8 @@ int64_t detfold_attn_decode_workspace_bytes(const detfold_kv_cache *cache, int b
                                             int64_t max_len)
 {
     if (int rc = check_decode_sizes(cache, batch, q_heads, max_len)) return rc;
-    return 0;
+    return decode_workspace(cache->dtype, batch, cache->kv_heads, q_heads / cache->kv_heads, cache->head_dim,
+                            max_len);
 }
 
 int detfold_attn_decode(void *out, int64_t out_batch_stride, int64_t out_head_stride, float *lse,
@@ -194,7 +195,7 @@ int detfold_attn_decode(void *out, int64_t out_batch_stride, int64_t out_head_st
     p.group = q_heads / cache->kv_heads;
     p.batch = batch, p.q_heads = q_heads, p.max_len = (int)max_len;
     p.scale = scale, p.status = d_status;
-    return cuda_status(launch_decode(p, cache->dtype, (cudaStream_t)stream));
+    return cuda_status(launch_decode(p, cache->dtype, workspace, (cudaStream_t)stream));
 }
 
 int detfold_attn_join(void *out, float *lse, const void *const *parts, const float *const *lses, int W,

@@ -74,7 +74,9 @@ struct JoinParams {
 };
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
-cudaError_t launch_decode(const DecodeParams &p, int dtype, cudaStream_t stream);
+// `max_seen`: the most tokens that a sequence attends to (p.window of a call).
+int64_t decode_workspace(int dtype, int batch, int kv_heads, int group, int head_dim, int64_t max_seen);
+cudaError_t launch_decode(const DecodeParams &p, int dtype, void *workspace, cudaStream_t stream);
 cudaError_t launch_join(const JoinParams &p, int dtype, cudaStream_t stream);
 
 }  // namespace detfold_attn

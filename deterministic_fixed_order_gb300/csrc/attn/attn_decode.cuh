@@ -1,0 +1,484 @@
+// Attention of one new token a sequence over a paged cache: the pieces that
+// every element type shares -- the chunk rule, the spread of the work over
+// CTAs, the copy pipeline, the fold of chunk triples and the join.
+//
+// Mathematics. Per query head: s_t = scale (q . k_t), m = max s_t, p_t =
+// exp(s_t - m), l = sum p_t, o = sum p_t v_t / l. A set of tokens is summed up by
+// its triple (m, l, a = sum p_t v_t); two triples join to
+//     m' = max(m, m_i), l' = l e^(m - m') + l_i e^(m_i - m'), a' likewise.
+//
+// Fixed order. A sequence's tokens are cut into chunks; the cut follows from
+// its length and the head counts alone (chunk_rounds). Within a chunk warp w
+// takes tiles w, w + 4, ... and the four warps' triples join in warp order; the
+// chunks' triples are folded in ascending order. Which CTA takes which chunks is
+// free: a CTA that begins a sequence folds in registers, any other leaves its
+// chunks' triples in the workspace for the join kernel, which goes on with the
+// same operations on the same values. So the bits do not depend on the batch.
+//
+// Bound. Each cached key and value is read once for all the query heads that
+// share it: 4 x group flops an element pair, so memory bound while the
+// arithmetic keeps up. One pass; nothing but the triples of split sequences
+// goes back to memory.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace detfold_attn {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+// Two CTAs on each of the 152 SMs of a GB300.
+constexpr int kMaxCtas = 304;
+constexpr int kMinChunk = 128;  // tokens
+// Chunks a sequence: enough for one sequence to fill every CTA, within limits
+// that keep the join short.
+constexpr int kMinChunks = 32, kMaxChunks = 128;
+
+// A (key-value head, block of at most `heads` query heads) of a sequence is a
+// "pair": the unit that has a triple a query head.
+__host__ __device__ inline int max_chunks(int pairs)
+{
+    const int c = kMaxCtas / pairs;
+    return c < kMinChunks ? kMinChunks : c > kMaxChunks ? kMaxChunks : c;
+}
+
+// Rounds (of `round` tokens) a chunk, for a sequence of `rounds` rounds.
+__host__ __device__ inline int chunk_rounds(int rounds, int pairs, int round)
+{
+    const int most = max_chunks(pairs), least = kMinChunk / round;
+    const int r = (rounds + most - 1) / most;
+    return r < least ? least : r;
+}
+
+struct DecodeGrid {
+    int ctas;    // CTAs of the main kernel
+    int slots;   // workspace slots (one a CTA), 0: no sequence can be split
+    int chunks;  // most chunks of a sequence
+    int pairs;   // pairs a sequence
+    int heads;   // query heads a pair, at most
+    int64_t slot_floats;
+};
+
+// Workspace: `ctas` headers of four ints, then a slot a CTA: for each chunk and
+// head (m, l), then for each chunk and head the accumulator.
+inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, int64_t max_seen, int heads,
+                              int round)
+{
+    DecodeGrid g;
+    g.heads = heads < group ? heads : group;
+    const int blocks = (group + heads - 1) / heads;
+    g.pairs = kv_heads * blocks;
+    const int rounds = (int)((max_seen + round - 1) / round);
+    const int per = chunk_rounds(rounds, g.pairs, round);
+    g.chunks = (rounds + per - 1) / per;
+    const int64_t units = (int64_t)batch * g.pairs * (g.chunks > 0 ? g.chunks : 1);
+    g.ctas = units < kMaxCtas ? (int)units : kMaxCtas;
+    // shorter sequences may have more chunks than the longest
+    const int most = max_chunks(g.pairs), least = kMinChunk / round;
+    const int up_to = (rounds + least - 1) / least;
+    g.chunks = up_to < most ? up_to : most;
+    g.slots = g.chunks > 1 ? g.ctas : 0;
+    g.slot_floats = (int64_t)g.chunks * g.heads * (head_dim + 2);
+    return g;
+}
+
+inline int64_t workspace_need(const DecodeGrid &g)
+{
+    return g.slots == 0 ? 0 : (int64_t)g.slots * (16 + g.slot_floats * 4);
+}
+
+struct DecodeWork {
+    DecodeParams p;
+    int pairs, blocks, heads, chunks, slots;
+    int64_t slot_floats;
+    int4 *headers;
+    float *slot;
+};
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16 bytes from global to shared memory; `bytes` == 0 fills with zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// e^x for x <= 0: one product and the hardware's 2^x (2 units in the last place
+// of binary32 or so; results below 2^-126 become 0).
+__device__ __forceinline__ float exp_neg(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, kLog2e)));
+    return y;
+}
+// The point that exponents are taken from: the maximum, or 0 where no score is above -inf.
+__device__ __forceinline__ float base_of(float m) { return m == neg_inf() ? 0.0f : m; }
+
+// A sequence as the kernel sees it.
+struct Seq {
+    int n, first;  // attended tokens, the first one's index
+    int rounds, per;
+    bool bad;      // its length is out of range
+};
+
+template <int ROUND>
+__device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
+{
+    Seq s;
+    const int len = w.p.lens[b];
+    s.bad = len < 0 || len > w.p.max_len;
+    const int n = s.bad ? 0 : len;
+    s.n = n < w.p.window ? n : (int)w.p.window;
+    s.first = n - s.n;
+    s.rounds = (s.n + ROUND - 1) / ROUND;
+    s.per = chunk_rounds(s.rounds, w.pairs, ROUND);
+    return s;
+}
+
+// A pair's share of the work: its rounds, and one for what each pair costs anyway.
+__device__ __forceinline__ int64_t cost(const Seq &s) { return s.rounds + 1; }
+
+// Walks the pairs of a CTA's share [lo, hi) of the line on which all pairs of
+// all sequences lie, each as long as it costs. A chunk belongs to the share
+// that its first round lies in, a pair's output to the share that its start lies in.
+template <int ROUND>
+struct Walk {
+    int64_t at, lo, hi;  // start of the current pair on the line; the share
+    Seq s;
+    int b, pair;
+    int round, end;  // the share's rounds of this pair: [round, end)
+
+    __device__ __forceinline__ bool done(const DecodeWork &w) const { return at >= hi || b >= w.p.batch; }
+    __device__ __forceinline__ int chunks() const { return (s.rounds + s.per - 1) / s.per; }
+    __device__ __forceinline__ void enter()
+    {
+        // chunks whose start at + c * per lies in [lo, hi)
+        const int64_t c0 = at >= lo ? 0 : (lo - at + s.per - 1) / s.per;
+        const int64_t c1 = (hi - at + s.per - 1) / s.per;
+        const int64_t r0 = c0 * s.per, r1 = c1 * s.per;
+        round = (int)(r0 < s.rounds ? r0 : s.rounds);
+        end = (int)(r1 < s.rounds ? r1 : s.rounds);
+    }
+    __device__ __forceinline__ void next_pair(const DecodeWork &w)
+    {
+        at += cost(s);
+        if (++pair == w.pairs) {
+            pair = 0;
+            if (++b < w.p.batch) s = sequence<ROUND>(w, b);
+        }
+        if (!done(w)) enter();
+    }
+};
+
+// The start of CTA `cta`'s share: sums all costs, then finds the sequence at lo.
+template <int ROUND>
+__device__ __forceinline__ Walk<ROUND> begin_walk(const DecodeWork &w, int64_t &line)
+{
+    const int lane = threadIdx.x & 31;
+    // every warp does the same: no barrier
+    int64_t sum = 0;
+    for (int b = lane; b < w.p.batch; b += 32) sum += cost(sequence<ROUND>(w, b)) * w.pairs;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
+    line = sum;
+    Walk<ROUND> k;
+    k.lo = (int64_t)blockIdx.x * line / gridDim.x;
+    k.hi = (int64_t)(blockIdx.x + 1) * line / gridDim.x;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < w.p.batch; b0 += 32) {
+        int64_t c = b0 + lane < w.p.batch ? cost(sequence<ROUND>(w, b0 + lane)) * w.pairs : 0;
+        int64_t up = c;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, up, x);
+            if (lane >= x) up += y;
+        }
+        const unsigned past = __ballot_sync(~0u, before + up > k.lo);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            k.b = b0 + at;
+            k.at = before + __shfl_sync(~0u, up - c, at);
+            break;
+        }
+        before += __shfl_sync(~0u, up, 31);
+    }
+    k.s = sequence<ROUND>(w, k.b);
+    k.pair = (int)((k.lo - k.at) / cost(k.s));
+    k.at += k.pair * cost(k.s);
+    k.enter();
+    return k;
+}
+
+// The share that a point of the line lies in: the largest j with floor(j line / ctas) <= x.
+__device__ __forceinline__ int share_of(int64_t x, int64_t line)
+{
+    return (int)(((x + 1) * gridDim.x + line - 1) / line) - 1;
+}
+
+// A running triple of one element and its fold with the next chunk's.
+__device__ __forceinline__ void fold_weights(float m, float mi, float &top, float &fa, float &fb)
+{
+    top = fmaxf(m, mi);
+    const float base = base_of(top);
+    fa = exp_neg(m - base);
+    fb = exp_neg(mi - base);
+}
+__device__ __forceinline__ float fold_value(float a, float ai, float fa, float fb)
+{
+    return __fmaf_rn(a, fa, __fmul_rn(ai, fb));
+}
+
+template <typename T>
+__device__ __forceinline__ void write_out(const DecodeWork &w, int b, int head, int d, float m, float l, float a)
+{
+    if (d < w.p.head_dim)
+        ((T *)w.p.out)[b * w.p.out_bs + head * w.p.out_hs + d] =
+            from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a, l));
+    if (d == 0 && w.p.lse) w.p.lse[(int64_t)b * w.p.q_heads + head] = __fadd_rn(base_of(m), logf(l));
+}
+
+// One warp's ring of tiles: TOK tokens of keys, then of values, rows padded by
+// 16 bytes so that eight rows' 16-byte pieces lie in different banks.
+template <typename T, int DP, int TOK, int STAGES>
+struct Ring {
+    static constexpr int kRow = DP * (int)sizeof(T) + 16;
+    static constexpr int kTile = TOK * kRow;
+    static constexpr int kStage = 2 * kTile;
+    static constexpr int kBytes = STAGES * kStage;
+    static constexpr int kVecs = DP * (int)sizeof(T) / 16;  // 16-byte pieces a row
+    static constexpr int kRound = kWarps * TOK;
+};
+
+// Copies tiles ahead of their use, across chunks and pairs of the CTA's share.
+template <typename T, int DP, int TOK, int STAGES>
+struct Loader {
+    using R = Ring<T, DP, TOK, STAGES>;
+    Walk<R::kRound> walk;
+    uint32_t ring;       // shared address of this warp's ring
+    int stage;
+    unsigned bad;        // bit i: the tile in stage i needs a page outside the cache
+    int entry, row;      // the next tile's page and row of this lane's token, loaded one tile ahead
+    bool live;           // the lane's token exists
+
+    __device__ __forceinline__ void look(const DecodeWork &w, int warp, int lane)
+    {
+        live = false;
+        entry = row = 0;
+        if (walk.done(w)) return;
+        const int i = walk.round * R::kRound + warp * TOK + lane % TOK;
+        live = i < walk.s.n;
+        if (!live) return;
+        const unsigned t = (unsigned)(walk.s.first + i), page = t / (unsigned)w.p.page_size;
+        entry = w.p.table[walk.b * w.p.table_stride + page];
+        row = (int)(t - page * (unsigned)w.p.page_size);
+    }
+    // Skips pairs of the share that have no rounds in it.
+    __device__ __forceinline__ void settle(const DecodeWork &w)
+    {
+        while (!walk.done(w) && walk.round >= walk.end) walk.next_pair(w);
+    }
+    __device__ __forceinline__ void start(const DecodeWork &w, const Walk<R::kRound> &k, uint32_t at, int warp,
+                                          int lane)
+    {
+        walk = k;
+        ring = at;
+        stage = 0;
+        bad = 0;
+        settle(w);
+        look(w, warp, lane);
+    }
+    // Starts the copies of the next tile; a commit group a call, empty past the end.
+    __device__ __forceinline__ void issue(const DecodeWork &w, int warp, int lane)
+    {
+        if (!walk.done(w)) {
+            const bool known = entry >= 0 && entry < w.p.num_pages;
+            const bool out = live && !known;
+            if (out) flag_bad_index(w.p.status);
+            bad = (bad & ~(1u << stage)) | ((__any_sync(~0u, out) ? 1u : 0u) << stage);
+            const int hk = walk.pair / w.blocks;
+            const int64_t off = live && known ? entry * w.p.page_stride + row * w.p.token_stride +
+                                                    (int64_t)hk * w.p.head_stride
+                                              : -1;
+            const uint32_t to = ring + stage * R::kStage;
+            const int valid = w.p.head_dim * (int)sizeof(T) / 16;
+#pragma unroll
+            for (int i = 0; i < (TOK * R::kVecs + 31) / 32; ++i) {
+                const int vec = i * 32 + lane, r = vec / R::kVecs, c = vec % R::kVecs;
+                const int64_t o = __shfl_sync(~0u, off, r);
+                const int bytes = o >= 0 && c < valid ? 16 : 0;
+                const int64_t from = bytes ? o * (int64_t)sizeof(T) + c * 16 : 0;
+                const uint32_t dst = to + r * R::kRow + c * 16;
+                copy16(dst, (const char *)w.p.k + from, bytes);
+                copy16(dst + R::kTile, (const char *)w.p.v + from, bytes);
+            }
+            ++walk.round;
+            settle(w);
+            look(w, warp, lane);
+        }
+        copy_commit();
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+};
+
+// The main kernel's skeleton. Tile computes one warp's triple:
+//   Tile::kHeads, kTok, kDP, T; load_q / reset / step / leave (see the users).
+template <typename Tile, int STAGES>
+struct DecodeKernel {
+    using T = typename Tile::T;
+    static constexpr int DP = Tile::kDP, TOK = Tile::kTok, HB = Tile::kHeads;
+    using R = Ring<T, DP, TOK, STAGES>;
+    static constexpr int kPitch = DP + 4;  // floats a head: the lanes that store together hit different banks
+    static constexpr int kElems = HB * DP / kThreads;
+    struct Shared {
+        alignas(128) unsigned char ring[kWarps][R::kBytes];
+        float acc[kWarps][HB][kPitch];
+        float m[kWarps][HB], l[kWarps][HB];
+        typename Tile::Shared tile;
+    };
+    static_assert(HB * DP % kThreads == 0, "every thread folds the same number of elements");
+
+    __device__ static void run(const DecodeWork &w)
+    {
+        extern __shared__ unsigned char raw[];
+        Shared &sh = *reinterpret_cast<Shared *>(raw);
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        int64_t line;
+        Walk<R::kRound> walk = begin_walk<R::kRound>(w, line);
+        Loader<T, DP, TOK, STAGES> load;
+        load.start(w, walk, smem_addr(sh.ring[warp]), warp, lane);
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) load.issue(w, warp, lane);
+        int stage = 0;
+        int4 header = make_int4(0, 0, 0, 0);
+        Tile tile;
+        for (; !walk.done(w); walk.next_pair(w)) {
+            const bool begins = walk.at >= walk.lo;
+            if (!begins && walk.round >= walk.end) continue;
+            const int hk = walk.pair / w.blocks, block = walk.pair % w.blocks;
+            const int head0 = hk * w.p.group + block * w.heads;
+            const int heads = min(w.heads, w.p.group - block * w.heads);
+            const int chunks = walk.chunks();
+            float *slot = nullptr;
+            if (w.slots) slot = w.slot + share_of(walk.at, line) * w.slot_floats;
+            tile.load_q(w, sh.tile, walk.b, head0, heads, warp, lane);
+            tile.reset();
+            // this thread's elements of the fold: head e / DP, dimension e % DP
+            float rm[kElems], rl[kElems], ra[kElems];
+#pragma unroll
+            for (int i = 0; i < kElems; ++i) rm[i] = neg_inf(), rl[i] = 0.0f, ra[i] = 0.0f;
+            bool bad = false;
+            int chunk = walk.round / walk.s.per, left = walk.s.per;
+            for (int g = walk.round; g < walk.end; ++g) {
+                copy_wait<STAGES - 2>();
+                __syncwarp();
+                bad |= load.bad >> stage & 1;
+                load.issue(w, warp, lane);
+                const int count = walk.s.n - (g * R::kRound + warp * TOK);  // tokens of this tile
+                const unsigned char *at = sh.ring[warp] + stage * R::kStage;
+                if (count > 0) tile.step(sh.tile, at, at + R::kTile, count, w.p.scale, warp, lane);
+                stage = stage + 1 == STAGES ? 0 : stage + 1;
+                if (--left && g + 1 < walk.end) continue;
+                // the chunk's end: the warps' triples, joined in warp order
+                tile.leave(&sh.acc[warp][0][0], kPitch, sh.m[warp], sh.l[warp], bad, lane);
+                tile.reset();
+                bad = false;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kElems; ++i) {
+                    const int e = threadIdx.x + i * kThreads, h = e / DP, d = e % DP;
+                    float top = sh.m[0][h];
+#pragma unroll
+                    for (int k = 1; k < kWarps; ++k) top = fmaxf(top, sh.m[k][h]);
+                    const float base = base_of(top);
+                    float l = 0.0f, a = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) {
+                        const float f = exp_neg(sh.m[k][h] - base);
+                        l = __fmaf_rn(sh.l[k][h], f, l);
+                        a = __fmaf_rn(sh.acc[k][h][d], f, a);
+                    }
+                    if (begins) {
+                        float m, fa, fb;
+                        fold_weights(rm[i], top, m, fa, fb);
+                        rl[i] = fold_value(rl[i], l, fa, fb);
+                        ra[i] = fold_value(ra[i], a, fa, fb);
+                        rm[i] = m;
+                    } else if (h < heads) {
+                        if (d < w.p.head_dim)
+                            slot[(int64_t)w.chunks * w.heads * 2 +
+                                 ((int64_t)chunk * w.heads + h) * w.p.head_dim + d] = a;
+                        if (d == 0) {
+                            slot[((int64_t)chunk * w.heads + h) * 2] = top;
+                            slot[((int64_t)chunk * w.heads + h) * 2 + 1] = l;
+                        }
+                    }
+                }
+                __syncthreads();
+                ++chunk;
+                left = walk.s.per;
+            }
+            if (!begins) continue;
+            const bool whole = walk.end >= walk.s.rounds;
+            if (walk.s.bad && threadIdx.x == 0) flag_bad_index(w.p.status);
+#pragma unroll
+            for (int i = 0; i < kElems; ++i) {
+                const int e = threadIdx.x + i * kThreads, h = e / DP, d = e % DP;
+                if (h >= heads) continue;
+                if (whole) {
+                    write_out<T>(w, walk.b, head0 + h, d, rm[i], walk.s.bad ? quiet_nan() : rl[i], ra[i]);
+                } else {
+                    const int64_t c = chunk - 1;
+                    if (d < w.p.head_dim)
+                        slot[(int64_t)w.chunks * w.heads * 2 + (c * w.heads + h) * w.p.head_dim + d] = ra[i];
+                    if (d == 0) {
+                        slot[(c * w.heads + h) * 2] = rm[i];
+                        slot[(c * w.heads + h) * 2 + 1] = rl[i];
+                    }
+                }
+            }
+            if (!whole) header = make_int4(walk.b, walk.pair, chunk - 1, chunks);
+        }
+        copy_wait<0>();
+        if (w.slots && threadIdx.x == 0) w.headers[blockIdx.x] = header;
+    }
+};
+
+// Joins the split pairs: one CTA a (slot, query head). The triples from the
+// first stored one on are folded in ascending order, as in the main kernel.
+template <typename T>
+__device__ __forceinline__ void join_chunks(const DecodeWork &w)
+{
+    const int slot_index = blockIdx.x, h = blockIdx.y;
+    const int4 header = w.headers[slot_index];
+    if (header.w == 0) return;
+    const int hk = header.y / w.blocks, block = header.y % w.blocks;
+    const int heads = min(w.heads, w.p.group - block * w.heads);
+    if (h >= heads) return;
+    const float *slot = w.slot + slot_index * w.slot_floats;
+    const float *acc = slot + (int64_t)w.chunks * w.heads * 2;
+    for (int d = threadIdx.x; d < w.p.head_dim; d += blockDim.x) {
+        float m = neg_inf(), l = 0.0f, a = 0.0f;
+#pragma unroll 8
+        for (int c = header.z; c < header.w; ++c) {
+            const int64_t at = (int64_t)c * w.heads + h;
+            float top, fa, fb;
+            fold_weights(m, slot[at * 2], top, fa, fb);
+            l = fold_value(l, slot[at * 2 + 1], fa, fb);
+            a = fold_value(a, acc[at * w.p.head_dim + d], fa, fb);
+            m = top;
+        }
+        write_out<T>(w, header.x, hk * w.p.group + block * w.heads + h, d, m, l, a);
+    }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace detfold_attn

@@ -1,0 +1,50 @@
+// Kernels and launches of the one-token attention, for one element type a unit.
+#pragma once
+
+#include <atomic>
+
+#include "attn_decode.cuh"
+
+namespace detfold_attn {
+
+template <typename Tile, int STAGES>
+__global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant__ DecodeWork w)
+{
+    DecodeKernel<Tile, STAGES>::run(w);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeWork w)
+{
+    join_chunks<T>(w);
+}
+
+// Shared memory above 48 KB is allowed once a device.
+inline cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) return e;
+    done.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <typename Tile, int STAGES>
+cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t stream)
+{
+    using K = DecodeKernel<Tile, STAGES>;
+    static std::atomic<uint64_t> done{0};
+    const size_t bytes = sizeof(typename K::Shared);
+    if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, STAGES>, bytes, done)) return e;
+    decode_kernel<Tile, STAGES><<<g.ctas, kThreads, bytes, stream>>>(w);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    if (g.slots) {
+        decode_join_kernel<typename Tile::T><<<dim3(g.slots, g.heads), 256, 0, stream>>>(w);
+        if (cudaError_t e = cudaGetLastError()) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace detfold_attn

@@ -1,0 +1,214 @@
+// One warp's share of the attention in 16-bit types, on the matrix units.
+//
+// Scores: S^T = K Q^T, 16 tokens by 8 query heads a product, so that a group of
+// up to eight heads costs what one does. P stays in registers: S^T's layout,
+// packed to 16 bits and transposed 8x8 by movmatrix, is the second product's
+// right operand, O^T = V^T P^T (V^T by transposing loads). P is split in two
+// 16-bit parts, p = hi + lo, both multiplied: one part alone would round each
+// weight to the type's 8 or 11 bits and add as much error as rounding the output
+// does. Scores, maxima, sums and O^T are binary32.
+#pragma once
+
+#include "attn_decode.cuh"
+
+namespace detfold_attn {
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// c += a b, 16x8x16.
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(T x, T y)
+{
+    uint16_t a, b;
+    memcpy(&a, &x, 2);
+    memcpy(&b, &y, 2);
+    return (uint32_t)b << 16 | a;
+}
+
+// x and y as 16-bit pairs: hi rounded, lo what hi leaves, rounded.
+template <typename T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    const T hx = from_f32<T>(x), hy = from_f32<T>(y);
+    hi = pack2<T>(hx, hy);
+    lo = pack2<T>(from_f32<T>(__fsub_rn(x, to_f32(hx))), from_f32<T>(__fsub_rn(y, to_f32(hy))));
+}
+
+template <typename T_, int DP, int NT>
+struct MmaTile {
+    using T = T_;
+    static constexpr int kDP = DP, kTok = 16, kHeads = 8 * NT, kRow = DP * 2 + 16;
+    struct Shared {
+        int unused;
+    };
+
+    uint32_t q[DP / 16][NT][2];  // Q^T: dims 16 ks + 2t (+1) and + 8, head 8 nt + g
+    float o[DP / 16][NT][4];     // O^T: dims 16 mt + g, + 8; heads 8 nt + 2t, + 1
+    float m[NT][2], l[NT][2];    // of heads 2t, 2t + 1; l of this lane's tokens only
+
+    __device__ __forceinline__ void load_q(const DecodeWork &w, Shared &, int b, int head0, int heads, int, int lane)
+    {
+        const int g = lane / 4, t = lane % 4;
+        const T zero = from_f32<T>(0.0f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * 8 + g;
+            const T *from = (const T *)w.p.q + b * w.p.q_bs + (int64_t)(head0 + h) * w.p.q_hs;
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int d = ks * 16 + half * 8 + 2 * t;
+                    const bool in = h < heads && d < w.p.head_dim;  // head_dim is a multiple of 8
+                    q[ks][nt][half] = pack2<T>(in ? from[d] : zero, in ? from[d + 1] : zero);
+                }
+        }
+    }
+
+    __device__ __forceinline__ void reset()
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) m[nt][j] = neg_inf(), l[nt][j] = 0.0f;
+#pragma unroll
+            for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[mt][nt][j] = 0.0f;
+        }
+    }
+
+    // One tile of `count` tokens (16 or fewer; the rest of the tile is zeros).
+    __device__ __forceinline__ void step(Shared &, const unsigned char *kt, const unsigned char *vt, int count,
+                                         float scale, int, int lane)
+    {
+        const int g = lane / 4;
+        // two sums a score, joined at the end: half the length of the chain of products
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[nt][j] = s2[nt][j] = 0.0f;
+        const uint32_t ka = smem_addr(kt) + (lane % 16) * kRow + (lane / 16) * 16;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+            uint32_t a[4];
+            ldmatrix4(a, ka + ks * 32);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(ks % 2 ? s2[nt] : s[nt], a, q[ks][nt][0], q[ks][nt][1], T());
+        }
+        uint32_t hi[NT][2], lo[NT][2];
+        bool moved = false;
+        float fade[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[nt][j] = __fmul_rn(__fadd_rn(s[nt][j], s2[nt][j]), scale);
+                if (g + (j / 2) * 8 >= count) s[nt][j] = neg_inf();
+            }
+            float p[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float top = fmaxf(s[nt][j], s[nt][j + 2]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+                top = fmaxf(top, m[nt][j]);
+                const float base = base_of(top);
+                fade[nt][j] = exp_neg(m[nt][j] - base);
+                moved |= top != m[nt][j];
+                m[nt][j] = top;
+                p[j] = exp_neg(s[nt][j] - base);
+                p[j + 2] = exp_neg(s[nt][j + 2] - base);
+                l[nt][j] = __fmaf_rn(l[nt][j], fade[nt][j], __fadd_rn(p[j], p[j + 2]));
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t a, b;
+                split2<T>(p[half * 2], p[half * 2 + 1], a, b);
+                hi[nt][half] = transpose8(a);
+                lo[nt][half] = transpose8(b);
+            }
+        }
+        // where no maximum moved every factor is 1
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[mt][nt][j] = __fmul_rn(o[mt][nt][j], fade[nt][j % 2]);
+        }
+        const uint32_t va = smem_addr(vt) + ((lane / 16) * 8 + lane % 8) * kRow + ((lane / 8) % 2) * 16;
+#pragma unroll
+        for (int mt = 0; mt < DP / 16; ++mt) {
+            uint32_t a[4];
+            ldmatrix4_trans(a, va + mt * 32);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mma(o[mt][nt], a, hi[nt][0], hi[nt][1], T());
+                mma(o[mt][nt], a, lo[nt][0], lo[nt][1], T());
+            }
+        }
+    }
+
+    // Leaves the triple in shared memory; a `bad` chunk's sums are NaN.
+    __device__ __forceinline__ void leave(float *acc, int pitch, float *sm, float *sl, bool bad, int lane)
+    {
+        const int g = lane / 4, t = lane % 4;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float sum = l[nt][j];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(~0u, sum, x));
+                if (g == 0) {
+                    sm[nt * 8 + 2 * t + j] = m[nt][j];
+                    sl[nt * 8 + 2 * t + j] = bad ? quiet_nan() : sum;
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[(nt * 8 + 2 * t + j % 2) * pitch + mt * 16 + g + (j / 2) * 8] = o[mt][nt][j];
+        }
+    }
+};
+
+}  // namespace detfold_attn
