@@ -42,10 +42,10 @@ __host__ __device__ inline int max_chunks(int pairs)
     return c < kMinChunks ? kMinChunks : c > kMaxChunks ? kMaxChunks : c;
 }
 
-// Rounds (of `round` tokens) a chunk, for a sequence of `rounds` rounds.
-__host__ __device__ inline int chunk_rounds(int rounds, int pairs, int round)
+// Rounds (of `round` tokens) a chunk, for a sequence of `rounds` rounds and at most `most` chunks.
+__host__ __device__ inline int chunk_rounds(int rounds, int most, int round)
 {
-    const int most = max_chunks(pairs), least = kMinChunk / round;
+    const int least = kMinChunk / round;
     const int r = (rounds + most - 1) / most;
     return r < least ? least : r;
 }
@@ -56,7 +56,7 @@ struct DecodeGrid {
     int chunks;  // most chunks of a sequence
     int pairs;   // pairs a sequence
     int heads;   // query heads a pair, at most
-    int64_t slot_floats;
+    int64_t pair_floats, slot_floats;  // floats of a slot's (m, l) pairs; of a slot
 };
 
 // Workspace: `ctas` headers of four ints, then a slot a CTA: for each chunk and
@@ -69,7 +69,7 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     const int blocks = (group + heads - 1) / heads;
     g.pairs = kv_heads * blocks;
     const int rounds = (int)((max_seen + round - 1) / round);
-    const int per = chunk_rounds(rounds, g.pairs, round);
+    const int per = chunk_rounds(rounds, max_chunks(g.pairs), round);
     g.chunks = (rounds + per - 1) / per;
     const int64_t units = (int64_t)batch * g.pairs * (g.chunks > 0 ? g.chunks : 1);
     g.ctas = units < kMaxCtas ? (int)units : kMaxCtas;
@@ -78,7 +78,8 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     const int up_to = (rounds + least - 1) / least;
     g.chunks = up_to < most ? up_to : most;
     g.slots = g.chunks > 1 ? g.ctas : 0;
-    g.slot_floats = (int64_t)g.chunks * g.heads * (head_dim + 2);
+    g.pair_floats = ((int64_t)g.chunks * g.heads * 2 + 3) / 4 * 4;
+    g.slot_floats = g.pair_floats + ((int64_t)g.chunks * g.heads * head_dim + 3) / 4 * 4;
     return g;
 }
 
@@ -89,8 +90,11 @@ inline int64_t workspace_need(const DecodeGrid &g)
 
 struct DecodeWork {
     DecodeParams p;
-    int pairs, blocks, heads, chunks, slots;
-    int64_t slot_floats;
+    int pairs, blocks, heads, slots;
+    int most_chunks;                // max_chunks(pairs)
+    unsigned page_mul, page_shift;  // t / page_size = t * page_mul >> page_shift for t < 2^30
+    int out_vec;                    // four elements of out start at a multiple of their size
+    int64_t pair_floats, slot_floats;
     int4 *headers;
     float *slot;
 };
@@ -139,7 +143,7 @@ __device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
     s.n = n < w.p.window ? n : (int)w.p.window;
     s.first = n - s.n;
     s.rounds = (s.n + ROUND - 1) / ROUND;
-    s.per = chunk_rounds(s.rounds, w.pairs, ROUND);
+    s.per = chunk_rounds(s.rounds, w.most_chunks, ROUND);
     return s;
 }
 
@@ -160,12 +164,14 @@ struct Walk {
     __device__ __forceinline__ int chunks() const { return (s.rounds + s.per - 1) / s.per; }
     __device__ __forceinline__ void enter()
     {
-        // chunks whose start at + c * per lies in [lo, hi)
-        const int64_t c0 = at >= lo ? 0 : (lo - at + s.per - 1) / s.per;
-        const int64_t c1 = (hi - at + s.per - 1) / s.per;
-        const int64_t r0 = c0 * s.per, r1 = c1 * s.per;
-        round = (int)(r0 < s.rounds ? r0 : s.rounds);
-        end = (int)(r1 < s.rounds ? r1 : s.rounds);
+        // chunks whose start at + c * per lies in [lo, hi); both bounds as far as the pair reaches
+        const int64_t far = cost(s);
+        const int from = at >= lo ? 0 : (int)(lo - at < far ? lo - at : far);
+        const int to = (int)(hi - at < far ? hi - at : far);
+        const int r0 = (from + s.per - 1) / s.per * s.per;
+        const int r1 = (to + s.per - 1) / s.per * s.per;
+        round = r0 < s.rounds ? r0 : s.rounds;
+        end = r1 < s.rounds ? r1 : s.rounds;
     }
     __device__ __forceinline__ void next_pair(const DecodeWork &w)
     {
@@ -236,12 +242,31 @@ __device__ __forceinline__ float fold_value(float a, float ai, float fa, float f
     return __fmaf_rn(a, fa, __fmul_rn(ai, fb));
 }
 
-template <typename T>
-__device__ __forceinline__ void write_out(const DecodeWork &w, int b, int head, int d, float m, float l, float a)
+__device__ __forceinline__ float4 fold_four(float4 a, float4 ai, float fa, float fb)
 {
-    if (d < w.p.head_dim)
-        ((T *)w.p.out)[b * w.p.out_bs + head * w.p.out_hs + d] =
-            from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a, l));
+    return make_float4(fold_value(a.x, ai.x, fa, fb), fold_value(a.y, ai.y, fa, fb), fold_value(a.z, ai.z, fa, fb),
+                       fold_value(a.w, ai.w, fa, fb));
+}
+
+// Four elements of a head's output, from d on (head_dim is a multiple of 4).
+template <typename T>
+__device__ __forceinline__ void write_out(const DecodeWork &w, int b, int head, int d, float m, float l, float4 a)
+{
+    T *to = (T *)w.p.out + b * w.p.out_bs + head * w.p.out_hs + d;
+    T v[4];
+    v[0] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.x, l));
+    v[1] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.y, l));
+    v[2] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.z, l));
+    v[3] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.w, l));
+    if (w.out_vec) {
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<uint4 *>(v);
+        else
+            *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<uint2 *>(v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = v[j];
+    }
     if (d == 0 && w.p.lse) w.p.lse[(int64_t)b * w.p.q_heads + head] = __fadd_rn(base_of(m), logf(l));
 }
 
@@ -276,7 +301,8 @@ struct Loader {
         const int i = walk.round * R::kRound + warp * TOK + lane % TOK;
         live = i < walk.s.n;
         if (!live) return;
-        const unsigned t = (unsigned)(walk.s.first + i), page = t / (unsigned)w.p.page_size;
+        const unsigned t = (unsigned)(walk.s.first + i);
+        const unsigned page = (unsigned)((uint64_t)t * w.page_mul >> w.page_shift);
         entry = w.p.table[walk.b * w.p.table_stride + page];
         row = (int)(t - page * (unsigned)w.p.page_size);
     }
@@ -328,6 +354,13 @@ struct Loader {
     }
 };
 
+// Waits for the work before this launch, then lets the next launch start its prologue.
+__device__ __forceinline__ void enter_grid()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // The main kernel's skeleton. Tile computes one warp's triple:
 //   Tile::kHeads, kTok, kDP, T; load_q / reset / step / leave (see the users).
 template <typename Tile, int STAGES>
@@ -336,20 +369,26 @@ struct DecodeKernel {
     static constexpr int DP = Tile::kDP, TOK = Tile::kTok, HB = Tile::kHeads;
     using R = Ring<T, DP, TOK, STAGES>;
     static constexpr int kPitch = DP + 4;  // floats a head: the lanes that store together hit different banks
-    static constexpr int kElems = HB * DP / kThreads;
+    // The fold: kTeam threads a head, each kFours groups of four dimensions.
+    static constexpr int kTeam = kThreads / HB, kFours = DP / 4 / kTeam;
     struct Shared {
         alignas(128) unsigned char ring[kWarps][R::kBytes];
-        float acc[kWarps][HB][kPitch];
         float m[kWarps][HB], l[kWarps][HB];
         typename Tile::Shared tile;
     };
-    static_assert(HB * DP % kThreads == 0, "every thread folds the same number of elements");
+    static constexpr int kResident = sizeof(Shared) <= 113 * 1024 ? 2 : 1;  // CTAs an SM
+    static_assert(kThreads % HB == 0 && DP % (4 * kTeam) == 0, "every thread folds the same number of elements");
+    // A warp leaves its accumulator in the stage that it has just used up: the next
+    // copy into it starts after the fold.
+    static_assert(HB * kPitch * 4 <= R::kStage, "the accumulator fits a stage");
 
     __device__ static void run(const DecodeWork &w)
     {
         extern __shared__ unsigned char raw[];
         Shared &sh = *reinterpret_cast<Shared *>(raw);
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const int h = threadIdx.x / kTeam, d0 = threadIdx.x % kTeam * 4;  // the fold's head, first dimension
+        enter_grid();
         int64_t line;
         Walk<R::kRound> walk = begin_walk<R::kRound>(w, line);
         Loader<T, DP, TOK, STAGES> load;
@@ -365,15 +404,14 @@ struct DecodeKernel {
             const int hk = walk.pair / w.blocks, block = walk.pair % w.blocks;
             const int head0 = hk * w.p.group + block * w.heads;
             const int heads = min(w.heads, w.p.group - block * w.heads);
-            const int chunks = walk.chunks();
             float *slot = nullptr;
-            if (w.slots) slot = w.slot + share_of(walk.at, line) * w.slot_floats;
+            if (w.slots) slot = w.slot + (begins ? blockIdx.x : share_of(walk.at, line)) * w.slot_floats;
             tile.load_q(w, sh.tile, walk.b, head0, heads, warp, lane);
             tile.reset();
-            // this thread's elements of the fold: head e / DP, dimension e % DP
-            float rm[kElems], rl[kElems], ra[kElems];
+            float rm = neg_inf(), rl = 0.0f;
+            float4 ra[kFours];
 #pragma unroll
-            for (int i = 0; i < kElems; ++i) rm[i] = neg_inf(), rl[i] = 0.0f, ra[i] = 0.0f;
+            for (int i = 0; i < kFours; ++i) ra[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             bool bad = false;
             int chunk = walk.round / walk.s.per, left = walk.s.per;
             for (int g = walk.round; g < walk.end; ++g) {
@@ -382,44 +420,52 @@ struct DecodeKernel {
                 bad |= load.bad >> stage & 1;
                 load.issue(w, warp, lane);
                 const int count = walk.s.n - (g * R::kRound + warp * TOK);  // tokens of this tile
-                const unsigned char *at = sh.ring[warp] + stage * R::kStage;
+                unsigned char *at = sh.ring[warp] + stage * R::kStage;
                 if (count > 0) tile.step(sh.tile, at, at + R::kTile, count, w.p.scale, warp, lane);
+                const int used = stage;
                 stage = stage + 1 == STAGES ? 0 : stage + 1;
                 if (--left && g + 1 < walk.end) continue;
                 // the chunk's end: the warps' triples, joined in warp order
-                tile.leave(&sh.acc[warp][0][0], kPitch, sh.m[warp], sh.l[warp], bad, lane);
+                __syncwarp();
+                tile.leave(reinterpret_cast<float *>(at), kPitch, sh.m[warp], sh.l[warp], bad, lane);
                 tile.reset();
                 bad = false;
                 __syncthreads();
+                float top = sh.m[0][h];
 #pragma unroll
-                for (int i = 0; i < kElems; ++i) {
-                    const int e = threadIdx.x + i * kThreads, h = e / DP, d = e % DP;
-                    float top = sh.m[0][h];
+                for (int k = 1; k < kWarps; ++k) top = fmaxf(top, sh.m[k][h]);
+                const float base = base_of(top);
+                float f[kWarps], l = 0.0f;
 #pragma unroll
-                    for (int k = 1; k < kWarps; ++k) top = fmaxf(top, sh.m[k][h]);
-                    const float base = base_of(top);
-                    float l = 0.0f, a = 0.0f;
+                for (int k = 0; k < kWarps; ++k) {
+                    f[k] = exp_neg(sh.m[k][h] - base);
+                    l = __fmaf_rn(sh.l[k][h], f[k], l);
+                }
+                float m, fa, fb;
+                fold_weights(rm, top, m, fa, fb);
+#pragma unroll
+                for (int i = 0; i < kFours; ++i) {
+                    const int d = d0 + i * kTeam * 4;
+                    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int k = 0; k < kWarps; ++k) {
-                        const float f = exp_neg(sh.m[k][h] - base);
-                        l = __fmaf_rn(sh.l[k][h], f, l);
-                        a = __fmaf_rn(sh.acc[k][h][d], f, a);
+                        const float4 x = *reinterpret_cast<const float4 *>(
+                            reinterpret_cast<const float *>(sh.ring[k] + used * R::kStage) + h * kPitch + d);
+                        a.x = __fmaf_rn(x.x, f[k], a.x);
+                        a.y = __fmaf_rn(x.y, f[k], a.y);
+                        a.z = __fmaf_rn(x.z, f[k], a.z);
+                        a.w = __fmaf_rn(x.w, f[k], a.w);
                     }
-                    if (begins) {
-                        float m, fa, fb;
-                        fold_weights(rm[i], top, m, fa, fb);
-                        rl[i] = fold_value(rl[i], l, fa, fb);
-                        ra[i] = fold_value(ra[i], a, fa, fb);
-                        rm[i] = m;
-                    } else if (h < heads) {
-                        if (d < w.p.head_dim)
-                            slot[(int64_t)w.chunks * w.heads * 2 +
-                                 ((int64_t)chunk * w.heads + h) * w.p.head_dim + d] = a;
-                        if (d == 0) {
-                            slot[((int64_t)chunk * w.heads + h) * 2] = top;
-                            slot[((int64_t)chunk * w.heads + h) * 2 + 1] = l;
-                        }
-                    }
+                    if (begins)
+                        ra[i] = fold_four(ra[i], a, fa, fb);
+                    else if (h < heads && d < w.p.head_dim)
+                        put_four(w, slot, chunk, h, d, a);
+                }
+                if (begins) {
+                    rl = fold_value(rl, l, fa, fb);
+                    rm = m;
+                } else if (h < heads && d0 == 0) {
+                    put_pair(w, slot, chunk, h, top, l);
                 }
                 __syncthreads();
                 ++chunk;
@@ -427,56 +473,118 @@ struct DecodeKernel {
             }
             if (!begins) continue;
             const bool whole = walk.end >= walk.s.rounds;
-            if (walk.s.bad && threadIdx.x == 0) flag_bad_index(w.p.status);
-#pragma unroll
-            for (int i = 0; i < kElems; ++i) {
-                const int e = threadIdx.x + i * kThreads, h = e / DP, d = e % DP;
-                if (h >= heads) continue;
-                if (whole) {
-                    write_out<T>(w, walk.b, head0 + h, d, rm[i], walk.s.bad ? quiet_nan() : rl[i], ra[i]);
-                } else {
-                    const int64_t c = chunk - 1;
-                    if (d < w.p.head_dim)
-                        slot[(int64_t)w.chunks * w.heads * 2 + (c * w.heads + h) * w.p.head_dim + d] = ra[i];
-                    if (d == 0) {
-                        slot[(c * w.heads + h) * 2] = rm[i];
-                        slot[(c * w.heads + h) * 2 + 1] = rl[i];
-                    }
-                }
+            if (walk.s.bad) {
+                rl = quiet_nan();
+                if (threadIdx.x == 0) flag_bad_index(w.p.status);
             }
-            if (!whole) header = make_int4(walk.b, walk.pair, chunk - 1, chunks);
+            if (h < heads) {
+#pragma unroll
+                for (int i = 0; i < kFours; ++i) {
+                    const int d = d0 + i * kTeam * 4;
+                    if (d >= w.p.head_dim) continue;
+                    if (whole)
+                        write_out<T>(w, walk.b, head0 + h, d, rm, rl, ra[i]);
+                    else
+                        put_four(w, slot, chunk - 1, h, d, ra[i]);
+                }
+                if (!whole && d0 == 0) put_pair(w, slot, chunk - 1, h, rm, rl);
+            }
+            if (!whole) header = make_int4(walk.b, walk.pair, chunk - 1, walk.chunks());
         }
         copy_wait<0>();
         if (w.slots && threadIdx.x == 0) w.headers[blockIdx.x] = header;
     }
+
+    // A chunk's triple in a slot: (m, l) of each head, then the accumulators.
+    static __device__ __forceinline__ void put_pair(const DecodeWork &w, float *slot, int chunk, int h, float m, float l)
+    {
+        *reinterpret_cast<float2 *>(slot + ((int64_t)chunk * w.heads + h) * 2) = make_float2(m, l);
+    }
+    static __device__ __forceinline__ void put_four(const DecodeWork &w, float *slot, int chunk, int h, int d, float4 a)
+    {
+        *reinterpret_cast<float4 *>(slot + w.pair_floats + ((int64_t)chunk * w.heads + h) * w.p.head_dim + d) = a;
+    }
 };
 
-// Joins the split pairs: one CTA a (slot, query head). The triples from the
-// first stored one on are folded in ascending order, as in the main kernel.
+// Joins the split pairs: a CTA a (slot, query head) of kThreads threads. The triples
+// from the first stored one on are folded in ascending order, with the main
+// kernel's operations. The folds' factors follow from the running maxima alone
+// and are made first; the accumulators pass through shared memory so that a whole
+// batch of them is in flight at once. Bound by latency: a few tens of KB a CTA.
 template <typename T>
 __device__ __forceinline__ void join_chunks(const DecodeWork &w)
 {
-    const int slot_index = blockIdx.x, h = blockIdx.y;
+    constexpr int kBatch = 32, kPer = kBatch * DETFOLD_ATTN_MAX_HEAD_DIM / 4 / kThreads;
+    __shared__ float2 s_fold[kMaxChunks];  // fa, fb
+    __shared__ float s_top[kWarps];
+    __shared__ float4 s_acc[kBatch * DETFOLD_ATTN_MAX_HEAD_DIM / 4];
+    const int slot_index = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    enter_grid();
     const int4 header = w.headers[slot_index];
     if (header.w == 0) return;
     const int hk = header.y / w.blocks, block = header.y % w.blocks;
-    const int heads = min(w.heads, w.p.group - block * w.heads);
-    if (h >= heads) return;
+    if (h >= min(w.heads, w.p.group - block * w.heads)) return;
+    const int first = header.z, count = header.w - first, fours = w.p.head_dim / 4;
     const float *slot = w.slot + slot_index * w.slot_floats;
-    const float *acc = slot + (int64_t)w.chunks * w.heads * 2;
-    for (int d = threadIdx.x; d < w.p.head_dim; d += blockDim.x) {
-        float m = neg_inf(), l = 0.0f, a = 0.0f;
-#pragma unroll 8
-        for (int c = header.z; c < header.w; ++c) {
-            const int64_t at = (int64_t)c * w.heads + h;
-            float top, fa, fb;
-            fold_weights(m, slot[at * 2], top, fa, fb);
-            l = fold_value(l, slot[at * 2 + 1], fa, fb);
-            a = fold_value(a, acc[at * w.p.head_dim + d], fa, fb);
-            m = top;
+    const float4 *acc = reinterpret_cast<const float4 *>(slot + w.pair_floats);
+    float4 x[kPer];
+    // float4 i of a batch: chunk i / fours, group i % fours
+    auto fetch = [&](int c0) {
+        const int have = min(kBatch, count - c0) * fours;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = tid + k * kThreads;
+            if (i < have)
+                x[k] = acc[((int64_t)(first + c0 + i / fours) * w.heads + h) * fours + i % fours];
         }
-        write_out<T>(w, header.x, hk * w.p.group + block * w.heads + h, d, m, l, a);
+    };
+    fetch(0);
+    // factors: thread c takes chunk c
+    static_assert(kMaxChunks <= kThreads, "a thread a chunk");
+    float2 ml = make_float2(neg_inf(), 0.0f);
+    if (tid < count) ml = *reinterpret_cast<const float2 *>(slot + ((int64_t)(first + tid) * w.heads + h) * 2);
+    float top = ml.x;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const float y = __shfl_up_sync(~0u, top, k);
+        if (lane >= k) top = fmaxf(top, y);
     }
+    float before = __shfl_up_sync(~0u, top, 1);
+    if (lane == 0) before = neg_inf();
+    if (lane == 31) s_top[warp] = top;
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) before = fmaxf(before, s_top[k]);
+    float m, fa, fb;
+    fold_weights(before, ml.x, m, fa, fb);
+    if (tid < count) s_fold[tid] = make_float2(fa, fb);
+    // the sums l, in order, by every thread (the same values): through shared memory
+    __shared__ float s_l[kMaxChunks];
+    __shared__ float s_m;
+    if (tid < count) s_l[tid] = ml.y;
+    if (tid == count - 1) s_m = m;
+    float l = 0.0f;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c0 = 0; c0 < count; c0 += kBatch) {
+        const int have = min(kBatch, count - c0);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = tid + k * kThreads;
+            if (i < have * fours) s_acc[i] = x[k];
+        }
+        __syncthreads();
+        if (c0 + kBatch < count) fetch(c0 + kBatch);
+        if (tid < fours) {
+#pragma unroll 4
+            for (int c = 0; c < have; ++c) {
+                const float2 f = s_fold[c0 + c];
+                l = fold_value(l, s_l[c0 + c], f.x, f.y);
+                a = fold_four(a, s_acc[c * fours + tid], f.x, f.y);
+            }
+        }
+        __syncthreads();
+    }
+    if (tid < fours)
+        write_out<T>(w, header.x, hk * w.p.group + block * w.heads + h, tid * 4, s_m, l, a);
 }
 
 #endif  // __CUDACC__

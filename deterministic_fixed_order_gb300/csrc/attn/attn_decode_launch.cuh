@@ -8,13 +8,13 @@
 namespace detfold_attn {
 
 template <typename Tile, int STAGES>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant__ DecodeWork w)
+__global__ void __launch_bounds__(kThreads, DecodeKernel<Tile, STAGES>::kResident) decode_kernel(const __grid_constant__ DecodeWork w)
 {
     DecodeKernel<Tile, STAGES>::run(w);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeWork w)
+__global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeWork w)
 {
     join_chunks<T>(w);
 }
@@ -31,19 +31,33 @@ inline cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<ui
     return cudaSuccess;
 }
 
+// A launch whose prologue may overlap the end of the launch before it.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, size_t shared, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename Tile, int STAGES>
 cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t stream)
 {
     using K = DecodeKernel<Tile, STAGES>;
     static std::atomic<uint64_t> done{0};
     const size_t bytes = sizeof(typename K::Shared);
+    static_assert(sizeof(typename K::Shared) <= 227 * 1024, "an SM's shared memory");
     if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, STAGES>, bytes, done)) return e;
-    decode_kernel<Tile, STAGES><<<g.ctas, kThreads, bytes, stream>>>(w);
-    if (cudaError_t e = cudaGetLastError()) return e;
-    if (g.slots) {
-        decode_join_kernel<typename Tile::T><<<dim3(g.slots, g.heads), 256, 0, stream>>>(w);
-        if (cudaError_t e = cudaGetLastError()) return e;
-    }
+    if (cudaError_t e = launch_early(decode_kernel<Tile, STAGES>, dim3(g.ctas), bytes, stream, w)) return e;
+    if (g.slots) return launch_early(decode_join_kernel<typename Tile::T>, dim3(g.slots, g.heads), 0, stream, w);
     return cudaSuccess;
 }
 
