@@ -68,11 +68,15 @@ lib.detfold_attn_last_cuda_error.argtypes = []
 lib.detfold_attn_last_cuda_error.restype = _INT
 
 _TYPES = {}  # torch types, filled on first use
+_F32 = _I32 = _I64T = None
+_POINTERS = {}  # ctypes pointer-array types by length
 
 
 def _type_code(dtype, what: str) -> int:
+    global _F32, _I32, _I64T
     if not _TYPES:
         torch = _t()
+        _F32, _I32, _I64T = torch.float32, torch.int32, torch.int64
         _TYPES.update({torch.float32: DETFOLD_F32, torch.bfloat16: DETFOLD_BF16, torch.float16: DETFOLD_F16})
     code = _TYPES.get(dtype)
     if code is None:
@@ -96,31 +100,42 @@ class AttnError(DetfoldError):
         self.status = status
 
 
-def _want(x, dtype, device: int, dims: int, what: str):
-    """x as a CUDA tensor of this type, device and rank, its last dimension contiguous."""
+# The checks below run on every call and are written for that: the accepted case
+# asks each tensor for as little as it can, the messages are made on refusal.
+
+def _refuse(x, dtype, device: int, shape, what: str):
+    """Raises for a tensor that is not of this type, device and shape (None: any
+    length), or whose last dimension is not contiguous."""
+    if not hasattr(x, "get_device"):
+        raise TypeError(f"{what}: expected a tensor, got {type(x).__name__}")
     if x.dtype is not dtype or x.get_device() != device:
         raise TypeError(f"{what}: expected a {dtype} tensor on cuda:{device}, got {x.dtype} on {x.device}")
-    if x.dim() != dims:
-        raise ValueError(f"{what}: expected {dims} dimensions, got shape {tuple(x.shape)}")
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return x
+    text = "[" + ", ".join("any" if n is None else str(n) for n in shape) + "]"
+    if x.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, x.shape)):
+        raise ValueError(f"{what}: expected shape {text}, got {tuple(x.shape)}")
+    raise ValueError(f"{what}: strides {x.stride()} of shape {text}: the last dimension must be contiguous")
+
+
+def _rows(x, dtype, device: int, shape, what: str):
+    """(address, first stride, second stride) of [shape[0], shape[1], shape[2]] with a contiguous last dimension."""
+    s = x.stride()
+    if x.dtype is not dtype or x.get_device() != device or x.shape != shape or (s[2] != 1 and shape[2] > 1):
+        _refuse(x, dtype, device, shape, what)
+    return x.data_ptr(), s[0], s[1]
 
 
 def _flat(x, dtype, device: int, count: int, what: str) -> int:
     """Address of a contiguous CUDA tensor of this type with `count` elements."""
     if x.dtype is not dtype or x.get_device() != device:
-        raise TypeError(f"{what}: expected a {dtype} tensor on cuda:{device}, got {x.dtype} on {x.device}")
+        _refuse(x, dtype, device, (count,), what)
     if not x.is_contiguous() or x.numel() != count:
-        raise ValueError(f"{what}: expected {count} contiguous elements, got shape {tuple(x.shape)}")
+        raise ValueError(f"{what}: expected {count} contiguous elements, got shape {tuple(x.shape)}, strides "
+                         f"{x.stride()}")
     return x.data_ptr()
 
 
 def _status_word(status, device: int) -> int:
-    if status is None:
-        return 0
-    torch = _t()
-    if status.dtype is not torch.int32 or status.get_device() != device or status.numel() < 1:
+    if status.dtype is not _I32 or status.get_device() != device or status.numel() < 1:
         raise TypeError("status: expected a CUDA int32 tensor")
     return status.data_ptr()
 
@@ -135,8 +150,10 @@ class PagedCache:
         if not k.is_cuda:
             raise TypeError(f"k: expected a CUDA tensor, got {k.device}")
         self.device, self.dtype = k.get_device(), k.dtype
-        _want(k, k.dtype, self.device, 4, "k")
-        _want(v, k.dtype, self.device, 4, "v")
+        for x, what in ((k, "k"), (v, "v")):
+            if x.dtype is not k.dtype or x.get_device() != self.device or x.dim() != 4 or (
+                    x.stride(3) != 1 and x.shape[3] > 1):
+                _refuse(x, k.dtype, self.device, (None,) * 4, what)
         if k.shape != v.shape or k.stride() != v.stride():
             raise ValueError(f"k and v differ: shapes {tuple(k.shape)} and {tuple(v.shape)}, strides "
                              f"{k.stride()} and {v.stride()}")
@@ -153,8 +170,7 @@ class Rope:
     sines. Pairs are elements (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved."""
 
     def __init__(self, cos_sin, interleaved: bool = False):
-        torch = _t()
-        if cos_sin.dtype is not torch.float32 or not cos_sin.is_cuda:
+        if cos_sin.dtype is not _t().float32 or not cos_sin.is_cuda:
             raise TypeError(f"cos_sin: expected a CUDA float32 tensor, got {cos_sin.device} {cos_sin.dtype}")
         if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin: expected a contiguous [positions, rot_dim] tensor")
@@ -167,96 +183,79 @@ class Rope:
 
 def status_kv_append(cache, k, v, slots, rope=None, positions=None, q=None, q_out=None, status=None,
                      stream=None) -> int:
-    torch = _t()
     device, dtype = cache.device, cache.dtype
-    _want(k, dtype, device, 3, "k")
-    _want(v, dtype, device, 3, "v")
-    tokens, heads, width = k.shape
-    if heads != cache.kv_heads or width != cache.head_dim or v.shape != k.shape:
-        raise ValueError(f"k and v: expected [tokens, {cache.kv_heads}, {cache.head_dim}], got "
-                         f"{tuple(k.shape)} and {tuple(v.shape)}")
-    slot_ptr = _flat(slots, torch.int64, device, tokens, "slots")
+    shape = k.shape
+    tokens = shape[0] if len(shape) == 3 else 0
+    if len(shape) != 3 or shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
+        _refuse(k, dtype, device, (None, cache.kv_heads, cache.head_dim), "k")
+    k_ptr, k_ts, k_hs = _rows(k, dtype, device, shape, "k")
+    v_ptr, v_ts, v_hs = _rows(v, dtype, device, shape, "v")
+    slot_ptr = _flat(slots, _I64T, device, tokens, "slots")
     rope_ptr = pos_ptr = 0
     if rope is not None:
         if rope.device != device:
             raise TypeError("rope: on another device than the cache")
         if positions is None:
             raise ValueError("positions: needed with rope")
-        rope_ptr, pos_ptr = rope._ptr, _flat(positions, torch.int64, device, tokens, "positions")
-    ks, vs = k.stride(), v.stride()
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        return lib.detfold_kv_append(cache._ptr, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                                     slot_ptr, tokens, rope_ptr, pos_ptr, 0, 0, 0, 0, 0, 0, 0,
-                                     _status_word(status, device), _stream(stream))
-    _want(q, dtype, device, 3, "q")
-    if q_out is None:
-        raise ValueError("q_out: needed with q")
-    _want(q_out, dtype, device, 3, "q_out")
-    if q.shape[0] != tokens or q.shape[2] != width or q_out.shape != q.shape:
-        raise ValueError(f"q and q_out: expected [{tokens}, heads, {width}], got {tuple(q.shape)} and "
-                         f"{tuple(q_out.shape)}")
-    qs, os_ = q.stride(), q_out.stride()
-    return lib.detfold_kv_append(cache._ptr, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slot_ptr,
-                                 tokens, rope_ptr, pos_ptr, q_out.data_ptr(), os_[0], os_[1], q.data_ptr(),
-                                 qs[0], qs[1], q.shape[1], _status_word(status, device), _stream(stream))
+        rope_ptr, pos_ptr = rope._ptr, _flat(positions, _I64T, device, tokens, "positions")
+    q_ptr = q_ts = q_hs = o_ptr = o_ts = o_hs = heads = 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q_out: needed with q")
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != cache.head_dim:
+            _refuse(q, dtype, device, (tokens, None, cache.head_dim), "q")
+        heads = shape[1]
+        q_ptr, q_ts, q_hs = _rows(q, dtype, device, shape, "q")
+        o_ptr, o_ts, o_hs = _rows(q_out, dtype, device, shape, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    return lib.detfold_kv_append(cache._ptr, k_ptr, k_ts, k_hs, v_ptr, v_ts, v_hs, slot_ptr, tokens, rope_ptr, pos_ptr,
+                                 o_ptr, o_ts, o_hs, q_ptr, q_ts, q_hs, heads,
+                                 0 if status is None else _status_word(status, device), _stream(stream))
 
 
 def status_attn_decode(out, q, cache, block_table, seq_lens, max_len: int, scale: float, window: int = 0,
                        lse=None, workspace=None, status=None, stream=None) -> int:
-    torch = _t()
     device, dtype = cache.device, cache.dtype
-    _want(q, dtype, device, 3, "q")
-    _want(out, dtype, device, 3, "out")
-    batch, heads, width = q.shape
-    if width != cache.head_dim or out.shape != q.shape:
-        raise ValueError(f"q and out: expected [batch, heads, {cache.head_dim}], got {tuple(q.shape)} and "
-                         f"{tuple(out.shape)}")
-    _want(block_table, torch.int32, device, 2, "block_table")
-    rows, cols = block_table.shape
-    if rows != batch:
-        raise ValueError(f"block_table: expected {batch} rows, got {rows}")
-    lens_ptr = _flat(seq_lens, torch.int32, device, batch, "seq_lens")
-    lse_ptr = 0 if lse is None else _flat(lse, torch.float32, device, batch * heads, "lse")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        _refuse(q, dtype, device, (None, None, cache.head_dim), "q")
+    batch, heads, _ = shape
+    q_ptr, q_bs, q_hs = _rows(q, dtype, device, shape, "q")
+    o_ptr, o_bs, o_hs = _rows(out, dtype, device, shape, "out")
+    table, ts = block_table.shape, block_table.stride()
+    if block_table.dtype is not _I32 or block_table.get_device() != device or len(table) != 2 or (
+            table[0] != batch or (ts[1] != 1 and table[1] > 1)):
+        _refuse(block_table, _I32, device, (batch, None), "block_table")
+    lens_ptr = _flat(seq_lens, _I32, device, batch, "seq_lens")
     ws_ptr = ws_bytes = 0
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError(f"workspace: expected a contiguous tensor on cuda:{device}")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    os_, qs = out.stride(), q.stride()
-    return lib.detfold_attn_decode(out.data_ptr(), os_[0], os_[1], lse_ptr, q.data_ptr(), qs[0], qs[1],
-                                   cache._ptr, block_table.data_ptr(), block_table.stride(0), cols, lens_ptr,
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    return lib.detfold_attn_decode(o_ptr, o_bs, o_hs, 0 if lse is None else _flat(lse, _F32, device, batch * heads, "lse"),
+                                   q_ptr, q_bs, q_hs, cache._ptr, block_table.data_ptr(), ts[0], table[1], lens_ptr,
                                    batch, heads, max_len, scale, window, ws_ptr, ws_bytes,
-                                   _status_word(status, device), _stream(stream))
+                                   0 if status is None else _status_word(status, device), _stream(stream))
 
 
 def status_attn_join(out, parts, lses, lse=None, stream=None) -> int:
-    torch = _t()
-    world, device = len(parts), out.get_device()
+    world, device, dtype = len(parts), out.get_device(), out.dtype
     if len(lses) != world:
         raise ValueError(f"{world} parts, {len(lses)} lses")
-    code = _type_code(out.dtype, "out")
-    count, width = out.numel(), out.shape[-1] if out.dim() else 0
-    rows = count // width if width else 0
-    if not out.is_cuda:
+    code = _type_code(dtype, "out")
+    if device < 0:
         raise TypeError(f"out: expected a CUDA tensor, got {out.device}")
-    table = _pointers(world)
-    part_ptrs = table(*[_flat(x, out.dtype, device, count, "parts") for x in parts])
-    lse_ptrs = table(*[_flat(x, torch.float32, device, rows, "lses") for x in lses])
-    return lib.detfold_attn_join(_flat(out, out.dtype, device, count, "out"),
-                                 0 if lse is None else _flat(lse, torch.float32, device, rows, "lse"),
+    count, shape = out.numel(), out.shape
+    width = shape[-1] if shape else 0
+    rows = count // width if width else 0
+    table = _POINTERS.get(world) or _POINTERS.setdefault(world, ctypes.c_void_p * world)
+    part_ptrs = table(*[_flat(x, dtype, device, count, "parts") for x in parts])
+    lse_ptrs = table(*[_flat(x, _F32, device, rows, "lses") for x in lses])
+    return lib.detfold_attn_join(_flat(out, dtype, device, count, "out"),
+                                 0 if lse is None else _flat(lse, _F32, device, rows, "lse"),
                                  part_ptrs, lse_ptrs, world, rows, width, code, _stream(stream))
-
-
-_POINTERS = {}  # ctypes pointer-array types by length
-
-
-def _pointers(n: int):
-    got = _POINTERS.get(n)
-    if got is None:
-        got = _POINTERS.setdefault(n, ctypes.c_void_p * n)
-    return got
 
 
 # ------------------------------------------------------------------ raising calls (C names)

@@ -132,6 +132,7 @@ int detfold_kv_append(const detfold_kv_cache *cache, const void *k, int64_t k_to
     p.k_ts = k_token_stride, p.k_hs = k_head_stride, p.v_ts = v_token_stride, p.v_hs = v_head_stride;
     p.q_ts = q_token_stride, p.q_hs = q_head_stride, p.qo_ts = q_out_token_stride, p.qo_hs = q_out_head_stride;
     p.tokens = tokens, p.q_heads = q_heads, p.status = d_status;
+    p.page = divide_by(cache->page_size);
     if (rope) {
         p.cos_sin = rope->cos_sin, p.rope_rows = rope->positions;
         p.rot_dim = rope->rot_dim, p.interleaved = rope->interleaved;

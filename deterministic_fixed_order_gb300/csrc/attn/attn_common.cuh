@@ -37,6 +37,63 @@ __device__ __forceinline__ void flag_bad_index(int *status)
     if (status) *(volatile int *)status = DETFOLD_ERR_ARG;
 }
 
+// e^x for x <= 0: one product and the hardware's 2^x (2 units in the last place
+// of binary32 or so; results below 2^-126 become 0).
+__device__ __forceinline__ float exp_neg(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, kLog2e)));
+    return y;
+}
+// The point that exponents are taken from: the maximum, or 0 where no score is above -inf.
+__device__ __forceinline__ float base_of(float m) { return m == neg_inf() ? 0.0f : m; }
+
+// Waits for the work before this launch, then lets the next launch start its prologue.
+__device__ __forceinline__ void enter_grid()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// N elements that are read or written at once.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Pack {
+    T v[N];
+};
+
+// t / size = t * mul >> shift for t < 2^30: with s = ceil(log2 size) and mul =
+// ceil(2^(30 + s) / size), mul * size - 2^(30 + s) < 2^s, so the quotient is exact.
+struct Divide {
+    unsigned mul, shift;
+};
+inline Divide divide_by(int size)
+{
+    int s = 0;
+    while ((1 << s) < size) ++s;
+    return {(unsigned)((((uint64_t)1 << (30 + s)) + size - 1) / size), (unsigned)(30 + s)};
+}
+__device__ __forceinline__ unsigned quotient(unsigned t, Divide d)
+{
+    return (unsigned)((uint64_t)t * d.mul >> d.shift);
+}
+
+// A launch whose prologue may overlap the end of the launch before it.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t shared, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct AppendParams {
     detfold_kv_cache cache;
     const void *k, *v, *q;
@@ -46,6 +103,7 @@ struct AppendParams {
     int64_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs, qo_ts, qo_hs;
     int64_t tokens, rope_rows;
     int rot_dim, interleaved, q_heads;
+    Divide page;  // by the page size
     int *status;
 };
 

@@ -32,11 +32,7 @@ cudaError_t launch_decode(const DecodeParams &p, int dtype, void *workspace, cud
     w.pairs = g.pairs, w.blocks = g.pairs / p.kv_heads, w.heads = g.heads;
     w.slots = g.slots, w.most_chunks = max_chunks(g.pairs);
     w.pair_floats = g.pair_floats, w.slot_floats = g.slot_floats;
-    // s = ceil(log2 size), mul = ceil(2^(30 + s) / size): mul * size - 2^(30 + s) < 2^s, so the quotient is exact below 2^30
-    int s = 0;
-    while ((1 << s) < p.page_size) ++s;
-    w.page_shift = 30 + s;
-    w.page_mul = (unsigned)((((uint64_t)1 << w.page_shift) + p.page_size - 1) / p.page_size);
+    w.page = divide_by(p.page_size);
     const int four = dtype == DETFOLD_F32 ? 16 : 8;
     w.out_vec = (uintptr_t)p.out % four == 0 && p.out_bs % 4 == 0 && p.out_hs % 4 == 0;
     w.headers = (int4 *)workspace;

@@ -92,7 +92,7 @@ struct DecodeWork {
     DecodeParams p;
     int pairs, blocks, heads, slots;
     int most_chunks;                // max_chunks(pairs)
-    unsigned page_mul, page_shift;  // t / page_size = t * page_mul >> page_shift for t < 2^30
+    Divide page;                    // by the page size
     int out_vec;                    // four elements of out start at a multiple of their size
     int64_t pair_floats, slot_floats;
     int4 *headers;
@@ -114,17 +114,6 @@ __device__ __forceinline__ void copy_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// e^x for x <= 0: one product and the hardware's 2^x (2 units in the last place
-// of binary32 or so; results below 2^-126 become 0).
-__device__ __forceinline__ float exp_neg(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, kLog2e)));
-    return y;
-}
-// The point that exponents are taken from: the maximum, or 0 where no score is above -inf.
-__device__ __forceinline__ float base_of(float m) { return m == neg_inf() ? 0.0f : m; }
 
 // A sequence as the kernel sees it.
 struct Seq {
@@ -302,7 +291,7 @@ struct Loader {
         live = i < walk.s.n;
         if (!live) return;
         const unsigned t = (unsigned)(walk.s.first + i);
-        const unsigned page = (unsigned)((uint64_t)t * w.page_mul >> w.page_shift);
+        const unsigned page = quotient(t, w.page);
         entry = w.p.table[walk.b * w.p.table_stride + page];
         row = (int)(t - page * (unsigned)w.p.page_size);
     }
@@ -353,13 +342,6 @@ struct Loader {
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 };
-
-// Waits for the work before this launch, then lets the next launch start its prologue.
-__device__ __forceinline__ void enter_grid()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // The main kernel's skeleton. Tile computes one warp's triple:
 //   Tile::kHeads, kTok, kDP, T; load_q / reset / step / leave (see the users).

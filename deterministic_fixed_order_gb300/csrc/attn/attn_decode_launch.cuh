@@ -31,23 +31,6 @@ inline cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<ui
     return cudaSuccess;
 }
 
-// A launch whose prologue may overlap the end of the launch before it.
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, size_t shared, cudaStream_t stream, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = shared;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename Tile, int STAGES>
 cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t stream)
 {
@@ -56,8 +39,9 @@ cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t s
     const size_t bytes = sizeof(typename K::Shared);
     static_assert(sizeof(typename K::Shared) <= 227 * 1024, "an SM's shared memory");
     if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, STAGES>, bytes, done)) return e;
-    if (cudaError_t e = launch_early(decode_kernel<Tile, STAGES>, dim3(g.ctas), bytes, stream, w)) return e;
-    if (g.slots) return launch_early(decode_join_kernel<typename Tile::T>, dim3(g.slots, g.heads), 0, stream, w);
+    if (cudaError_t e = launch_early(decode_kernel<Tile, STAGES>, dim3(g.ctas), kThreads, bytes, stream, w)) return e;
+    if (g.slots)
+        return launch_early(decode_join_kernel<typename Tile::T>, dim3(g.slots, g.heads), kThreads, 0, stream, w);
     return cudaSuccess;
 }
 

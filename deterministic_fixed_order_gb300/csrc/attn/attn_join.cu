@@ -1,47 +1,110 @@
 // Rank-order join of W partial attentions.
 //
 // Per row: M = max lse_r, w_r = exp(lse_r - M), then two serial ascending
-// chains, sum w_r and sum w_r part_r, in binary32. Bound by memory: every part
-// is read once.
+// chains, sum w_r and sum w_r part_r, in binary32.
+//
+// Bound by memory: each part is read once. A thread takes N neighbouring
+// elements of a row -- the widest access that every operand's address and the row
+// allow -- and has up to eight ranks' elements in flight; the row's weights are
+// worked out by each of its threads again (one exponential a rank and access).
 #include "attn_common.cuh"
 
 namespace detfold_attn {
 namespace {
 
-// One warp a row.
-template <typename T>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinParams p)
+constexpr int kMost = 256;  // threads a CTA, at most
+constexpr int kRanks = 8;   // ranks whose elements a thread has in flight
+
+// W == 0: any number of ranks, kRanks at a time; else exactly W <= kRanks.
+// `places` accesses a row, `abreast` of them at a time.
+template <typename T, int N, int W>
+__global__ void __launch_bounds__(kMost) join_kernel(const __grid_constant__ JoinParams p, int places, int abreast)
 {
-    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    using V = Pack<T, N>;
+    constexpr int R = W ? W : kRanks;
+    const int world = W ? W : p.W;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / abreast) + threadIdx.x / abreast;
+    enter_grid();
     if (row >= p.rows) return;
-    const int lane = threadIdx.x % 32;
+    float lse[R];
     float top = neg_inf();
-    for (int r = 0; r < p.W; ++r) top = fmaxf(top, p.lses[r][row]);
-    const float base = top == neg_inf() ? 0.0f : top;
-    float total = 0.0f;
-    for (int r = 0; r < p.W; ++r) total = __fadd_rn(total, expf(p.lses[r][row] - base));
-    for (int d = lane; d < p.head_dim; d += 32) {
-        float acc = 0.0f;
-        for (int r = 0; r < p.W; ++r) {
-            const float w = expf(p.lses[r][row] - base);
-            if (!(w == 0.0f)) acc = __fmaf_rn(w, to_f32(((const T *)p.parts[r])[row * p.head_dim + d]), acc);
-        }
-        ((T *)p.out)[row * p.head_dim + d] = from_f32<T>(total == 0.0f ? 0.0f : __fdiv_rn(acc, total));
+    for (int r0 = 0; r0 < world; r0 += R) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) lse[r] = r0 + r < world ? p.lses[r0 + r][row] : neg_inf();
+#pragma unroll
+        for (int r = 0; r < R; ++r) top = fmaxf(top, lse[r]);
     }
-    if (p.lse && lane == 0) p.lse[row] = base + logf(total);
+    const float base = base_of(top);
+    for (int u = threadIdx.x % abreast; u < places; u += abreast) {
+        const int64_t at = row * p.head_dim + (int64_t)u * N;
+        float total = 0.0f, acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+        for (int r0 = 0; r0 < world; r0 += R) {
+            V x[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r0 + r < world) x[r] = *reinterpret_cast<const V *>((const T *)p.parts[r0 + r] + at);
+            if (W == 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) lse[r] = r0 + r < world ? p.lses[r0 + r][row] : neg_inf();
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float w = exp_neg(__fsub_rn(lse[r], base));
+                total = __fadd_rn(total, w);
+                // no weight: whatever the part holds stays out
+                if (!(w == 0.0f)) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] = __fmaf_rn(w, to_f32(x[r].v[i]), acc[i]);
+                }
+            }
+        }
+        V y;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y.v[i] = from_f32<T>(total == 0.0f ? 0.0f : __fdiv_rn(acc[i], total));
+        *reinterpret_cast<V *>((T *)p.out + at) = y;
+        if (u == 0 && p.lse) p.lse[row] = __fadd_rn(base, logf(total));
+    }
+}
+
+// Whether every operand can be accessed N elements at a time.
+bool fits(const JoinParams &p, int es, int n)
+{
+    if (p.head_dim % n || (uintptr_t)p.out % (uintptr_t)(es * n)) return false;
+    for (int r = 0; r < p.W; ++r)
+        if ((uintptr_t)p.parts[r] % (uintptr_t)(es * n)) return false;
+    return true;
+}
+
+template <typename T, int N>
+cudaError_t launch_packs(const JoinParams &p, cudaStream_t stream)
+{
+    const int places = p.head_dim / N, abreast = places < kMost ? places : kMost, rows = kMost / abreast;
+    const dim3 grid((unsigned)((p.rows + rows - 1) / rows));
+    const auto kernel = p.W == 2   ? join_kernel<T, N, 2>
+                        : p.W == 4 ? join_kernel<T, N, 4>
+                        : p.W == 8 ? join_kernel<T, N, 8>
+                                   : join_kernel<T, N, 0>;
+    return launch_early(kernel, grid, rows * abreast, 0, stream, p, places, abreast);
+}
+
+template <typename T>
+cudaError_t launch_type(const JoinParams &p, cudaStream_t stream)
+{
+    constexpr int wide = 16 / sizeof(T);
+    return fits(p, sizeof(T), wide) ? launch_packs<T, wide>(p, stream) : launch_packs<T, 1>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_join(const JoinParams &p, int dtype, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((p.rows + 3) / 4)), block(128);
     switch (dtype) {
-    case DETFOLD_F32: join_kernel<float><<<grid, block, 0, stream>>>(p); break;
-    case DETFOLD_BF16: join_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(p); break;
-    default: join_kernel<__half><<<grid, block, 0, stream>>>(p); break;
+    case DETFOLD_F32: return launch_type<float>(p, stream);
+    case DETFOLD_BF16: return launch_type<__nv_bfloat16>(p, stream);
+    default: return launch_type<__half>(p, stream);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace detfold_attn
