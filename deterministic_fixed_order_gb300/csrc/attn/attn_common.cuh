@@ -25,6 +25,46 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
+// Two neighbours at once.
+__device__ __forceinline__ float2 to_f32x2(const float *x) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ float2 to_f32x2(const __nv_bfloat16 *x)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(x));
+}
+__device__ __forceinline__ float2 to_f32x2(const __half *x)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(x));
+}
+__device__ __forceinline__ void from_f32x2(float *x, float2 y) { x[0] = y.x, x[1] = y.y; }
+__device__ __forceinline__ void from_f32x2(__nv_bfloat16 *x, float2 y)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(x) = __float22bfloat162_rn(y);
+}
+__device__ __forceinline__ void from_f32x2(__half *x, float2 y)
+{
+    *reinterpret_cast<__half2 *>(x) = __float22half2_rn(y);
+}
+
+// Two binary32 products, or fused multiply-adds, an instruction; each rounded as alone.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{ .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+        " mov.b64 {%0, %1}, z; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{ .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

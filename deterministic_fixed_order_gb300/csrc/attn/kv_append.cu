@@ -5,103 +5,157 @@
 // rounding to the element type. Everything else is a copy.
 //
 // Bound by memory: a token's queries, keys and values are read and written
-// once. A token is one column of the grid; a thread keeps one place in the head
-// -- N elements and the N that they turn with -- and takes head after head there,
-// so it reads the cosines and sines of its place once for all heads. N is the
-// widest access that every operand's address and stride allow.
+// once. A team of threads takes token after token; a thread keeps one place in the head --
+// N elements and the N that they turn with -- and takes head after head there, so
+// it reads the cosines and sines of its place once for all heads. N is the widest
+// access that every operand's address and stride allow. The next token's slot and
+// position are read one token ahead, so that its elements and its cosines are
+// asked for together: one load's latency a token, not three in a row.
 #include "attn_common.cuh"
 
 namespace detfold_attn {
 namespace {
 
-constexpr int kMost = 256;  // threads a CTA, at most
-constexpr int kAhead = 4;   // heads whose elements a thread has in flight
+constexpr int kMost = 128;  // threads a CTA, at most
+constexpr int kAhead = 3;   // heads whose elements a thread has in flight
+constexpr int kTurns = 2;   // times that a thread of a long prompt's CTA asks for them
 
-// `units` places a head: first those of pairs, then those of single copies.
+// Where a token's heads are read and written: queries, then keys, then values.
+template <typename T>
+struct Heads {
+    const T *q, *k, *v;
+    T *qo, *ck, *cv;
+
+    __device__ __forceinline__ const T *from(const AppendParams &p, int r) const
+    {
+        const int hk = p.cache.kv_heads;
+        return r < p.q_heads ? q + r * p.q_hs : r < p.q_heads + hk ? k + (r - p.q_heads) * p.k_hs
+                                                                   : v + (r - p.q_heads - hk) * p.v_hs;
+    }
+    __device__ __forceinline__ T *to(const AppendParams &p, int r) const
+    {
+        const int hk = p.cache.kv_heads;
+        return r < p.q_heads ? qo + r * p.qo_hs : r < p.q_heads + hk ? ck + (r - p.q_heads) * p.cache.head_stride
+                                                                     : cv + (r - p.q_heads - hk) * p.cache.head_stride;
+    }
+};
+
+// Turns the pairs of a place: element i of `a` with element i of `b`, or
+// neighbours with each other, `a` followed by `b`.
 template <typename T, int N, bool PAIRS>
-__global__ void __launch_bounds__(kMost) append_kernel(const __grid_constant__ AppendParams p, int units)
+__device__ __forceinline__ void rotate(T *a, T *b, const float *co, const float *si)
+{
+    if constexpr (N == 1) {
+        const float x = to_f32(a[0]), y = to_f32(b[0]);
+        a[0] = from_f32<T>(__fmaf_rn(x, co[0], -__fmul_rn(y, si[0])));
+        b[0] = from_f32<T>(__fmaf_rn(y, co[0], __fmul_rn(x, si[0])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            // pairs i and i + 1
+            T *p0 = PAIRS ? (2 * i < N ? a + 2 * i : b + 2 * i - N) : a + i;
+            T *p1 = PAIRS ? (2 * i + 2 < N ? a + 2 * i + 2 : b + 2 * i + 2 - N) : b + i;
+            const float2 u = to_f32x2(p0), v = to_f32x2(p1);
+            const float2 x = PAIRS ? make_float2(u.x, v.x) : u, y = PAIRS ? make_float2(u.y, v.y) : v;
+            const float2 c = make_float2(co[i], co[i + 1]), s = make_float2(si[i], si[i + 1]);
+            const float2 ys = mul2(y, s), xs = mul2(x, s);
+            const float2 d = fma2(x, c, make_float2(-ys.x, -ys.y)), e = fma2(y, c, xs);
+            from_f32x2(p0, PAIRS ? make_float2(d.x, e.x) : d);
+            from_f32x2(p1, PAIRS ? make_float2(d.y, e.y) : e);
+        }
+    }
+}
+
+// `units` places a head: first those of pairs, then those of single copies. `team`
+// threads take a token together.
+template <typename T, int N, bool PAIRS>
+__global__ void __launch_bounds__(kMost, 6) append_kernel(const __grid_constant__ AppendParams p, int units,
+                                                           int team)
 {
     using V = Pack<T, N>;
     const detfold_kv_cache &c = p.cache;
     const int half = p.rot_dim / 2, turning = half / N;
     const int abreast = min(units, kMost), rows = p.q_heads + 2 * c.kv_heads;
-    const int step = blockDim.x / abreast * gridDim.y;
-    const int64_t t = blockIdx.x;
+    const int member = threadIdx.x % team, teams = blockDim.x / team;
+    const int step = team / abreast * gridDim.y;
+    const int first = (blockIdx.y * team + member) / abreast;
     enter_grid();
-    // one place a thread, several only in heads of more than kMost places
-    for (int u = threadIdx.x % abreast; u < units; u += abreast) {
-        // this place's elements: [ia, ia + N) and, where they turn, [ib, ib + N)
-        const bool turns = u < turning;
-        const int ia = !turns ? half + u * N : PAIRS ? 2 * u * N : u * N;
-        const int ib = PAIRS ? ia + N : ia + half;
-        const int64_t slot = p.slots[t];
-        float co[N], si[N];
-        bool known = true;
-        if (turns) {
-            const int64_t pos = p.positions[t];
-            known = pos >= 0 && pos < p.rope_rows;
-            const float *row = p.cos_sin + (known ? pos : 0) * p.rot_dim + u * N;
-            constexpr int F = N < 4 ? N : 4;
-#pragma unroll
-            for (int j = 0; j < N; j += F) {
-                const Pack<float, F> x = *reinterpret_cast<const Pack<float, F> *>(row + j);
-                const Pack<float, F> y = *reinterpret_cast<const Pack<float, F> *>(row + half + j);
-#pragma unroll
-                for (int i = 0; i < F; ++i) {
-                    co[j + i] = known ? x.v[i] : quiet_nan();
-                    si[j + i] = known ? y.v[i] : quiet_nan();
-                }
-            }
-        }
-        int64_t page, at;
-        if (slot >= 0 && slot < ((int64_t)1 << 30)) {
-            page = quotient((unsigned)slot, p.page);
-            at = (unsigned)slot - (unsigned)page * (unsigned)c.page_size;
-        } else {
-            page = slot / c.page_size;
-            at = slot % c.page_size;
-        }
-        const bool keep = slot >= 0 && page < c.num_pages;
-        if (((slot >= 0 && !keep) || !known) && u == (int)threadIdx.x && blockIdx.y == 0) flag_bad_index(p.status);
-        const int64_t dst = keep ? page * c.page_stride + at * c.token_stride : 0;
-
-        const T *q = (const T *)p.q + t * p.q_ts, *k = (const T *)p.k + t * p.k_ts, *v = (const T *)p.v + t * p.v_ts;
-        T *qo = (T *)p.q_out + t * p.qo_ts, *ck = (T *)c.k + dst, *cv = (T *)c.v + dst;
-        const int last = keep ? rows : p.q_heads;
-        for (int r0 = (blockIdx.y * blockDim.x + threadIdx.x) / abreast; r0 < last; r0 += kAhead * step) {
+    const int64_t t0 = (int64_t)blockIdx.x * teams + threadIdx.x / team, apart = (int64_t)gridDim.x * teams;
+    int64_t slot = t0 < p.tokens ? p.slots[t0] : -1, pos = t0 < p.tokens && p.cos_sin ? p.positions[t0] : 0;
+    for (int64_t t = t0; t < p.tokens; t += apart) {
+        const int64_t next = t + apart;
+        const int64_t next_slot = next < p.tokens ? p.slots[next] : -1;
+        const int64_t next_pos = next < p.tokens && p.cos_sin ? p.positions[next] : 0;
+        Heads<T> heads;
+        heads.q = (const T *)p.q + t * p.q_ts;
+        heads.k = (const T *)p.k + t * p.k_ts;
+        heads.v = (const T *)p.v + t * p.v_ts;
+        heads.qo = (T *)p.q_out + t * p.qo_ts;
+        // one place a thread, several only in heads of more than kMost places
+        for (int u = member % abreast; u < units; u += abreast) {
+            // this place's elements: [ia, ia + N) and, where they turn, [ib, ib + N)
+            const bool turns = u < turning;
+            const int ia = !turns ? half + u * N : PAIRS ? 2 * u * N : u * N;
+            const int ib = PAIRS ? ia + N : ia + half;
             V a[kAhead], b[kAhead];
+            auto load = [&](int r0) {
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int r = r0 + j * step;
-                if (r >= last) break;
-                const T *from = r < p.q_heads               ? q + r * p.q_hs
-                                : r < p.q_heads + c.kv_heads ? k + (r - p.q_heads) * p.k_hs
-                                                             : v + (r - p.q_heads - c.kv_heads) * p.v_hs;
-                a[j] = *reinterpret_cast<const V *>(from + ia);
-                if (turns) b[j] = *reinterpret_cast<const V *>(from + ib);
-            }
+                for (int j = 0; j < kAhead; ++j)
+                    if (r0 + j * step < rows) {
+                        const T *from = heads.from(p, r0 + j * step);
+                        a[j] = *reinterpret_cast<const V *>(from + ia);
+                        if (turns) b[j] = *reinterpret_cast<const V *>(from + ib);
+                    }
+            };
+            load(first);
+            float co[N], si[N];
+            bool known = true;
+            if (turns) {
+                known = pos >= 0 && pos < p.rope_rows;
+                const float *row = p.cos_sin + (known ? pos : 0) * p.rot_dim + u * N;
+                constexpr int F = N < 4 ? N : 4;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int r = r0 + j * step;
-                if (r >= last) break;
-                T *to = r < p.q_heads               ? qo + r * p.qo_hs
-                        : r < p.q_heads + c.kv_heads ? ck + (r - p.q_heads) * c.head_stride
-                                                     : cv + (r - p.q_heads - c.kv_heads) * c.head_stride;
-                if (turns && r < p.q_heads + c.kv_heads) {
+                for (int j = 0; j < N; j += F) {
+                    const Pack<float, F> x = *reinterpret_cast<const Pack<float, F> *>(row + j);
+                    const Pack<float, F> y = *reinterpret_cast<const Pack<float, F> *>(row + half + j);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        // a pair: the same element of both packs, or two neighbours of one after the other
-                        T &first = PAIRS ? (2 * i < N ? a[j].v[2 * i] : b[j].v[2 * i - N]) : a[j].v[i];
-                        T &second = PAIRS ? (2 * i + 1 < N ? a[j].v[2 * i + 1] : b[j].v[2 * i + 1 - N]) : b[j].v[i];
-                        const float x = to_f32(first), y = to_f32(second);
-                        first = from_f32<T>(__fmaf_rn(x, co[i], -__fmul_rn(y, si[i])));
-                        second = from_f32<T>(__fmaf_rn(y, co[i], __fmul_rn(x, si[i])));
+                    for (int i = 0; i < F; ++i) {
+                        co[j + i] = known ? x.v[i] : quiet_nan();
+                        si[j + i] = known ? y.v[i] : quiet_nan();
                     }
                 }
-                *reinterpret_cast<V *>(to + ia) = a[j];
-                if (turns) *reinterpret_cast<V *>(to + ib) = b[j];
+            }
+            int64_t page, at;
+            if (slot >= 0 && slot < ((int64_t)1 << 30)) {
+                page = quotient((unsigned)slot, p.page);
+                at = (unsigned)slot - (unsigned)page * (unsigned)c.page_size;
+            } else {
+                page = slot / c.page_size;
+                at = slot % c.page_size;
+            }
+            const bool keep = slot >= 0 && page < c.num_pages;
+            if (((slot >= 0 && !keep) || !known) && u == member && blockIdx.y == 0) flag_bad_index(p.status);
+            const int64_t dst = keep ? page * c.page_stride + at * c.token_stride : 0;
+            heads.ck = (T *)c.k + dst;
+            heads.cv = (T *)c.v + dst;
+            const int last = keep ? rows : p.q_heads;  // a token without a place: its queries only
+            for (int r0 = first; r0 < last; r0 += kAhead * step) {
+                if (r0 != first) load(r0);
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int r = r0 + j * step;
+                    if (r >= last) break;
+                    if (turns && r < p.q_heads + c.kv_heads) {
+                        rotate<T, N, PAIRS>(a[j].v, b[j].v, co, si);
+                    }
+                    T *to = heads.to(p, r);
+                    *reinterpret_cast<V *>(to + ia) = a[j];
+                    if (turns) *reinterpret_cast<V *>(to + ib) = b[j];
+                }
             }
         }
+        slot = next_slot;
+        pos = next_pos;
     }
 }
 
@@ -126,15 +180,22 @@ cudaError_t launch_packs(const AppendParams &p, cudaStream_t stream)
     const int units = p.rot_dim / 2 / N + (c.head_dim - p.rot_dim) / N;
     const int rows = p.q_heads + 2 * c.kv_heads;
     const int abreast = units < kMost ? units : kMost;
-    // whole heads a CTA: a thread stays at its place
-    int heads = kMost / abreast;
-    heads = heads > rows ? rows : heads;
-    // a few tokens: their heads spread over more CTAs, one head a thread
-    int across = (double)p.tokens * rows * units < 152 * 1024 ? (rows + heads - 1) / heads : 1;
+    // whole heads a CTA: a thread stays at its place. A few tokens spread a head a
+    // thread over as many CTAs as that takes; many give each thread several heads,
+    // which share what a token costs anyway.
+    const int widest = kMost / abreast;
+    const bool few = (double)p.tokens * rows * units < 152 * 1024;
+    const int per = few ? 1 : kAhead * kTurns;
+    int heads = (rows + per - 1) / per;
+    heads = heads > widest ? widest : heads;
+    int across = few ? (rows + heads - 1) / heads : 1;
     across = across > 1024 ? 1024 : across;
-    const dim3 grid((unsigned)p.tokens, (unsigned)across);
-    return p.interleaved ? launch_early(append_kernel<T, N, true>, grid, heads * abreast, 0, stream, p, units)
-                         : launch_early(append_kernel<T, N, false>, grid, heads * abreast, 0, stream, p, units);
+    const int team = heads * abreast, teams = few ? 1 : kMost / team, threads = team * teams;
+    // as many CTAs as are resident at 80 registers a thread
+    const int64_t ctas = (p.tokens + teams - 1) / teams, resident = 152 * (65536 / 80 / ((threads + 31) / 32 * 32));
+    const dim3 grid((unsigned)(ctas < resident ? ctas : resident), (unsigned)across);
+    return p.interleaved ? launch_early(append_kernel<T, N, true>, grid, threads, 0, stream, p, units, team)
+                         : launch_early(append_kernel<T, N, false>, grid, threads, 0, stream, p, units, team);
 }
 
 template <typename T>
