@@ -9,12 +9,14 @@ cudaError_t launch_decode_f16(const DecodeWork &w, const DecodeGrid &g, cudaStre
 
 namespace {
 
-// Query heads a pair and tokens a round of the tile that a call takes.
+// The tile that a call takes: query heads a pair, tokens a round, CTAs an SM.
 DecodeGrid grid_of(int dtype, int batch, int kv_heads, int group, int head_dim, int64_t max_seen)
 {
-    const int heads = dtype != DETFOLD_F32 && group > 8 && head_dim <= 128 ? 16 : 8;
-    const int round = dtype == DETFOLD_F32 && head_dim > 128 ? 32 : 64;
-    return decode_grid(batch, kv_heads, group, head_dim, max_seen, heads, round);
+    const bool f32 = dtype == DETFOLD_F32;
+    const int heads = f32 ? (group == 1 ? 1 : group <= 4 ? 4 : 8) : group > 8 && head_dim <= 128 ? 16 : 8;
+    const int round = f32 && head_dim > 128 ? 32 : 64;
+    const int resident = head_dim * (f32 ? 4 : 2) <= 256 ? 2 : 1;
+    return decode_grid(batch, kv_heads, group, head_dim, max_seen, heads, round, resident);
 }
 
 }  // namespace

@@ -27,8 +27,8 @@ namespace detfold_attn {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// Two CTAs on each of the 152 SMs of a GB300.
-constexpr int kMaxCtas = 304;
+// CTAs: two on each of the 152 SMs of a GB300, or one where a CTA fills an SM.
+constexpr int kSms = 152, kMaxCtas = 2 * kSms;
 constexpr int kMinChunk = 128;  // tokens
 // Chunks a sequence: enough for one sequence to fill every CTA, within limits
 // that keep the join short.
@@ -62,7 +62,7 @@ struct DecodeGrid {
 // Workspace: `ctas` headers of four ints, then a slot a CTA: for each chunk and
 // head (m, l), then for each chunk and head the accumulator.
 inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, int64_t max_seen, int heads,
-                              int round)
+                              int round, int resident)
 {
     DecodeGrid g;
     g.heads = heads < group ? heads : group;
@@ -72,7 +72,7 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     const int per = chunk_rounds(rounds, max_chunks(g.pairs), round);
     g.chunks = (rounds + per - 1) / per;
     const int64_t units = (int64_t)batch * g.pairs * (g.chunks > 0 ? g.chunks : 1);
-    g.ctas = units < kMaxCtas ? (int)units : kMaxCtas;
+    g.ctas = units < resident * kSms ? (int)units : resident * kSms;
     // shorter sequences may have more chunks than the longest
     const int most = max_chunks(g.pairs), least = kMinChunk / round;
     const int up_to = (rounds + least - 1) / least;
@@ -271,16 +271,20 @@ struct Ring {
     static constexpr int kRound = kWarps * TOK;
 };
 
-// Copies tiles ahead of their use, across chunks and pairs of the CTA's share.
+// Copies tiles ahead of their use, across chunks and pairs of the CTA's share, by
+// 16-byte pieces (cp.async); what is not copied is filled with zeros, so nothing that
+// lies in unwritten cache rows reaches the arithmetic. Whole rows by bulk copies (a lane a
+// row) take a tenth of the instructions, but a warp starts its 32 one after the other
+// and its arithmetic waits: 64 mixed sequences took 72 us that way, 54 us this way.
 template <typename T, int DP, int TOK, int STAGES>
 struct Loader {
     using R = Ring<T, DP, TOK, STAGES>;
     Walk<R::kRound> walk;
-    uint32_t ring;       // shared address of this warp's ring
+    uint32_t ring;  // shared address of this warp's ring
     int stage;
-    unsigned bad;        // bit i: the tile in stage i needs a page outside the cache
-    int entry, row;      // the next tile's page and row of this lane's token, loaded one tile ahead
-    bool live;           // the lane's token exists
+    unsigned bad;   // bit i: the tile in stage i needs a page outside the cache
+    int entry, row; // the next tile's page and row of this lane's token, looked up one tile before they are needed
+    bool live;      // the lane's token exists
 
     __device__ __forceinline__ void look(const DecodeWork &w, int warp, int lane)
     {
@@ -300,11 +304,11 @@ struct Loader {
     {
         while (!walk.done(w) && walk.round >= walk.end) walk.next_pair(w);
     }
-    __device__ __forceinline__ void start(const DecodeWork &w, const Walk<R::kRound> &k, uint32_t at, int warp,
+    __device__ __forceinline__ void start(const DecodeWork &w, const Walk<R::kRound> &k, unsigned char *at, int warp,
                                           int lane)
     {
         walk = k;
-        ring = at;
+        ring = smem_addr(at);
         stage = 0;
         bad = 0;
         settle(w);
@@ -318,7 +322,7 @@ struct Loader {
             const bool out = live && !known;
             if (out) flag_bad_index(w.p.status);
             bad = (bad & ~(1u << stage)) | ((__any_sync(~0u, out) ? 1u : 0u) << stage);
-            const int hk = walk.pair / w.blocks;
+            const int hk = w.blocks == 1 ? walk.pair : walk.pair / w.blocks;
             const int64_t off = live && known ? entry * w.p.page_stride + row * w.p.token_stride +
                                                     (int64_t)hk * w.p.head_stride
                                               : -1;
@@ -350,16 +354,17 @@ struct DecodeKernel {
     using T = typename Tile::T;
     static constexpr int DP = Tile::kDP, TOK = Tile::kTok, HB = Tile::kHeads;
     using R = Ring<T, DP, TOK, STAGES>;
+    using Loader = detfold_attn::Loader<T, DP, TOK, STAGES>;
     static constexpr int kPitch = DP + 4;  // floats a head: the lanes that store together hit different banks
     // The fold: kTeam threads a head, each kFours groups of four dimensions.
-    static constexpr int kTeam = kThreads / HB, kFours = DP / 4 / kTeam;
+    static constexpr int kTeam = kThreads / HB < DP / 4 ? kThreads / HB : DP / 4, kFours = DP / 4 / kTeam;
     struct Shared {
         alignas(128) unsigned char ring[kWarps][R::kBytes];
         float m[kWarps][HB], l[kWarps][HB];
         typename Tile::Shared tile;
     };
     static constexpr int kResident = sizeof(Shared) <= 113 * 1024 ? 2 : 1;  // CTAs an SM
-    static_assert(kThreads % HB == 0 && DP % (4 * kTeam) == 0, "every thread folds the same number of elements");
+    static_assert(HB * kTeam <= kThreads && DP % (4 * kTeam) == 0, "every thread folds the same number of elements");
     // A warp leaves its accumulator in the stage that it has just used up: the next
     // copy into it starts after the fold.
     static_assert(HB * kPitch * 4 <= R::kStage, "the accumulator fits a stage");
@@ -369,12 +374,14 @@ struct DecodeKernel {
         extern __shared__ unsigned char raw[];
         Shared &sh = *reinterpret_cast<Shared *>(raw);
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        const int h = threadIdx.x / kTeam, d0 = threadIdx.x % kTeam * 4;  // the fold's head, first dimension
+        // this thread's head in the fold (the last one again where there are threads to spare) and first dimension
+        const bool folds = threadIdx.x < HB * kTeam;
+        const int h = folds ? threadIdx.x / kTeam : HB - 1, d0 = threadIdx.x % kTeam * 4;
         enter_grid();
         int64_t line;
         Walk<R::kRound> walk = begin_walk<R::kRound>(w, line);
-        Loader<T, DP, TOK, STAGES> load;
-        load.start(w, walk, smem_addr(sh.ring[warp]), warp, lane);
+        Loader load;
+        load.start(w, walk, sh.ring[warp], warp, lane);
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) load.issue(w, warp, lane);
         int stage = 0;
@@ -397,13 +404,13 @@ struct DecodeKernel {
             bool bad = false;
             int chunk = walk.round / walk.s.per, left = walk.s.per;
             for (int g = walk.round; g < walk.end; ++g) {
+                const int count = walk.s.n - (g * R::kRound + warp * TOK);  // tokens of this tile
+                unsigned char *at = sh.ring[warp] + stage * R::kStage;
                 copy_wait<STAGES - 2>();
                 __syncwarp();
                 bad |= load.bad >> stage & 1;
                 load.issue(w, warp, lane);
-                const int count = walk.s.n - (g * R::kRound + warp * TOK);  // tokens of this tile
-                unsigned char *at = sh.ring[warp] + stage * R::kStage;
-                if (count > 0) tile.step(sh.tile, at, at + R::kTile, count, w.p.scale, warp, lane);
+                if (count > 0) tile.step(w, sh.tile, at, at + R::kTile, count, warp, lane);
                 const int used = stage;
                 stage = stage + 1 == STAGES ? 0 : stage + 1;
                 if (--left && g + 1 < walk.end) continue;
@@ -440,13 +447,13 @@ struct DecodeKernel {
                     }
                     if (begins)
                         ra[i] = fold_four(ra[i], a, fa, fb);
-                    else if (h < heads && d < w.p.head_dim)
+                    else if (folds && h < heads && d < w.p.head_dim)
                         put_four(w, slot, chunk, h, d, a);
                 }
                 if (begins) {
                     rl = fold_value(rl, l, fa, fb);
                     rm = m;
-                } else if (h < heads && d0 == 0) {
+                } else if (folds && h < heads && d0 == 0) {
                     put_pair(w, slot, chunk, h, top, l);
                 }
                 __syncthreads();
@@ -459,7 +466,7 @@ struct DecodeKernel {
                 rl = quiet_nan();
                 if (threadIdx.x == 0) flag_bad_index(w.p.status);
             }
-            if (h < heads) {
+            if (folds && h < heads) {
 #pragma unroll
                 for (int i = 0; i < kFours; ++i) {
                     const int d = d0 + i * kTeam * 4;

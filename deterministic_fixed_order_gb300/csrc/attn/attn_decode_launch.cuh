@@ -38,6 +38,7 @@ cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t s
     static std::atomic<uint64_t> done{0};
     const size_t bytes = sizeof(typename K::Shared);
     static_assert(sizeof(typename K::Shared) <= 227 * 1024, "an SM's shared memory");
+    static_assert(K::kResident == (K::DP * sizeof(typename K::T) <= 256 ? 2 : 1), "as the grid is sized");
     if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, STAGES>, bytes, done)) return e;
     if (cudaError_t e = launch_early(decode_kernel<Tile, STAGES>, dim3(g.ctas), kThreads, bytes, stream, w)) return e;
     if (g.slots)

@@ -113,9 +113,10 @@ struct MmaTile {
     }
 
     // One tile of `count` tokens (16 or fewer; the rest of the tile is zeros).
-    __device__ __forceinline__ void step(Shared &, const unsigned char *kt, const unsigned char *vt, int count,
-                                         float scale, int, int lane)
+    __device__ __forceinline__ void step(const DecodeWork &w, Shared &, const unsigned char *kt,
+                                         const unsigned char *vt, int count, int, int lane)
     {
+        const float scale = w.p.scale;
         const int g = lane / 4;
         // two sums a score, joined at the end: half the length of the chain of products
         float s[NT][4], s2[NT][4];
