@@ -190,7 +190,7 @@ int detfold_attn_decode(void *out, int64_t out_batch_stride, int64_t out_head_st
     p.out_bs = out_batch_stride, p.out_hs = out_head_stride, p.q_bs = q_batch_stride, p.q_hs = q_head_stride;
     p.k = cache->k, p.v = cache->v, p.num_pages = cache->num_pages;
     p.page_stride = cache->page_stride, p.token_stride = cache->token_stride, p.head_stride = cache->head_stride;
-    p.table = block_table, p.lens = seq_lens, p.table_stride = table_stride;
+    p.table = block_table, p.lens = seq_lens, p.table_stride = table_stride, p.table_cols = table_cols;
     p.window = window == 0 || window > max_len ? max_len : window;
     p.page_size = cache->page_size, p.kv_heads = cache->kv_heads, p.head_dim = cache->head_dim;
     p.group = q_heads / cache->kv_heads;

@@ -155,7 +155,7 @@ struct DecodeParams {
     const void *k, *v;
     int64_t num_pages, page_stride, token_stride, head_stride;
     const int32_t *table, *lens;
-    int64_t table_stride, window;
+    int64_t table_stride, table_cols, window;
     int page_size, kv_heads, head_dim, group;
     int batch, q_heads, max_len;
     float scale;

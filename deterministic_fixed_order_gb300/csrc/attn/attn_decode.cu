@@ -33,9 +33,12 @@ cudaError_t launch_decode(const DecodeParams &p, int dtype, void *workspace, cud
     w.p = p;
     w.pairs = g.pairs, w.blocks = g.pairs / p.kv_heads, w.heads = g.heads;
     w.slots = g.slots, w.most_chunks = max_chunks(g.pairs);
+    w.most = divide_by(w.most_chunks), w.grid = divide_by(g.ctas);
+    w.short_line = (double)p.batch * g.pairs * (p.window / 32 + 2) < (1 << 30);
     w.pair_floats = g.pair_floats, w.slot_floats = g.slot_floats;
     w.page = divide_by(p.page_size);
     const int four = dtype == DETFOLD_F32 ? 16 : 8;
+    w.q_vec = (uintptr_t)p.q % (four / 2) == 0 && p.q_bs % 2 == 0 && p.q_hs % 2 == 0;
     w.out_vec = (uintptr_t)p.out % four == 0 && p.out_bs % 4 == 0 && p.out_hs % 4 == 0;
     w.headers = (int4 *)workspace;
     w.slot = (float *)((char *)workspace + (int64_t)g.slots * 16);

@@ -43,7 +43,7 @@ __host__ __device__ inline int max_chunks(int pairs)
 }
 
 // Rounds (of `round` tokens) a chunk, for a sequence of `rounds` rounds and at most `most` chunks.
-__host__ __device__ inline int chunk_rounds(int rounds, int most, int round)
+inline int chunk_rounds(int rounds, int most, int round)
 {
     const int least = kMinChunk / round;
     const int r = (rounds + most - 1) / most;
@@ -92,8 +92,11 @@ struct DecodeWork {
     DecodeParams p;
     int pairs, blocks, heads, slots;
     int most_chunks;                // max_chunks(pairs)
+    Divide most, grid;              // by most_chunks, by the number of CTAs
+    int short_line;                 // the shares' line is shorter than 2^30
     Divide page;                    // by the page size
     int out_vec;                    // four elements of out start at a multiple of their size
+    int q_vec;                      // two elements of q do
     int64_t pair_floats, slot_floats;
     int4 *headers;
     float *slot;
@@ -132,7 +135,7 @@ __device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
     s.n = n < w.p.window ? n : (int)w.p.window;
     s.first = n - s.n;
     s.rounds = (s.n + ROUND - 1) / ROUND;
-    s.per = chunk_rounds(s.rounds, w.most_chunks, ROUND);
+    s.per = max(kMinChunk / ROUND, (int)quotient(s.rounds + w.most_chunks - 1, w.most));  // chunk_rounds
     return s;
 }
 
@@ -155,12 +158,16 @@ struct Walk {
     {
         // chunks whose start at + c * per lies in [lo, hi); both bounds as far as the pair reaches
         const int64_t far = cost(s);
-        const int from = at >= lo ? 0 : (int)(lo - at < far ? lo - at : far);
-        const int to = (int)(hi - at < far ? hi - at : far);
-        const int r0 = (from + s.per - 1) / s.per * s.per;
-        const int r1 = (to + s.per - 1) / s.per * s.per;
-        round = r0 < s.rounds ? r0 : s.rounds;
-        end = r1 < s.rounds ? r1 : s.rounds;
+        round = 0;
+        end = s.rounds;
+        if (at < lo) {
+            const unsigned from = (unsigned)(lo - at < far ? lo - at : far);
+            round = min((int)((from + s.per - 1) / (unsigned)s.per * s.per), s.rounds);
+        }
+        if (hi - at < far) {
+            const unsigned to = (unsigned)(hi - at);
+            end = min((int)((to + s.per - 1) / (unsigned)s.per * s.per), s.rounds);
+        }
     }
     __device__ __forceinline__ void next_pair(const DecodeWork &w)
     {
@@ -173,49 +180,93 @@ struct Walk {
     }
 };
 
-// The start of CTA `cta`'s share: sums all costs, then finds the sequence at lo.
-template <int ROUND>
-__device__ __forceinline__ Walk<ROUND> begin_walk(const DecodeWork &w, int64_t &line)
+// The line cut into one share a CTA: share j begins at floor(j line / CTAs), so that
+// equal chunks meet equal shares.
+struct Shares {
+    int64_t line, each;
+    int over;
+
+    __device__ __forceinline__ void cut(const DecodeWork &w, int64_t length)
+    {
+        line = length;
+        each = w.short_line ? quotient((unsigned)line, w.grid) : line / gridDim.x;
+        over = (int)(line - each * gridDim.x);
+    }
+    __device__ __forceinline__ int64_t begin(const DecodeWork &w, unsigned j) const
+    {
+        return j * each + quotient(j * over, w.grid);
+    }
+    // The share that a point of the line lies in.
+    __device__ __forceinline__ int of(const DecodeWork &w, int64_t x) const
+    {
+        const int64_t up = (x + 1) * gridDim.x + line - 1;
+        return (int)(up >> 32 ? up / line : (unsigned)up / (unsigned)line) - 1;
+    }
+};
+
+// The sequence that `at` lies in and its start, by a scan of all sequences' costs, 32 at
+// a time, and the cut of the line into shares. I holds the line's length.
+template <int ROUND, typename I>
+__device__ __forceinline__ void find_sequence(const DecodeWork &w, Shares &shares, int64_t &lo, int &b, int64_t &at)
 {
     const int lane = threadIdx.x & 31;
-    // every warp does the same: no barrier
-    int64_t sum = 0;
-    for (int b = lane; b < w.p.batch; b += 32) sum += cost(sequence<ROUND>(w, b)) * w.pairs;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
-    line = sum;
-    Walk<ROUND> k;
-    k.lo = (int64_t)blockIdx.x * line / gridDim.x;
-    k.hi = (int64_t)(blockIdx.x + 1) * line / gridDim.x;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < w.p.batch; b0 += 32) {
-        int64_t c = b0 + lane < w.p.batch ? cost(sequence<ROUND>(w, b0 + lane)) * w.pairs : 0;
-        int64_t up = c;
+    const auto cost_of = [&](int i) { return i < w.p.batch ? (I)(cost(sequence<ROUND>(w, i)) * w.pairs) : (I)0; };
+    const auto scan = [&](I up) {
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
-            const int64_t y = __shfl_up_sync(~0u, up, x);
+            const I y = __shfl_up_sync(~0u, up, x);
             if (lane >= x) up += y;
         }
-        const unsigned past = __ballot_sync(~0u, before + up > k.lo);
+        return up;
+    };
+    const I mine = cost_of(lane);
+    I rest = 0;
+    for (int i = lane + 32; i < w.p.batch; i += 32) rest += cost_of(i);
+    I up = scan(mine);
+    I total = __shfl_sync(~0u, up, 31);
+    if (w.p.batch > 32) total += __shfl_sync(~0u, scan(rest), 31);
+    shares.cut(w, total);
+    lo = shares.begin(w, blockIdx.x);
+    I before = 0, c = mine;
+    for (int b0 = 0;;) {
+        const unsigned past = __ballot_sync(~0u, before + up > (I)lo);
         if (past) {
-            const int at = __ffs(past) - 1;
-            k.b = b0 + at;
-            k.at = before + __shfl_sync(~0u, up - c, at);
-            break;
+            const int i = __ffs(past) - 1;
+            b = b0 + i;
+            at = before + __shfl_sync(~0u, up - c, i);
+            return;
         }
         before += __shfl_sync(~0u, up, 31);
+        b0 += 32;
+        c = cost_of(b0 + lane);
+        up = scan(c);
     }
-    k.s = sequence<ROUND>(w, k.b);
-    k.pair = (int)((k.lo - k.at) / cost(k.s));
+}
+
+// This CTA's share. Every warp does the same: no barrier.
+template <int ROUND>
+__device__ __forceinline__ Walk<ROUND> begin_walk(const DecodeWork &w, Shares &shares)
+{
+    Walk<ROUND> k;
+    if (w.p.batch == 1) {
+        k.b = 0;
+        k.at = 0;
+        k.s = sequence<ROUND>(w, 0);
+        shares.cut(w, cost(k.s) * w.pairs);
+        k.lo = shares.begin(w, blockIdx.x);
+    } else {
+        if (w.short_line)
+            find_sequence<ROUND, int>(w, shares, k.lo, k.b, k.at);
+        else
+            find_sequence<ROUND, int64_t>(w, shares, k.lo, k.b, k.at);
+        k.s = sequence<ROUND>(w, k.b);
+    }
+    k.hi = shares.begin(w, blockIdx.x + 1);
+    const int64_t in = k.lo - k.at;
+    k.pair = w.pairs == 1 ? 0 : (int)(in >> 32 ? in / cost(k.s) : (unsigned)in / (unsigned)cost(k.s));
     k.at += k.pair * cost(k.s);
     k.enter();
     return k;
-}
-
-// The share that a point of the line lies in: the largest j with floor(j line / ctas) <= x.
-__device__ __forceinline__ int share_of(int64_t x, int64_t line)
-{
-    return (int)(((x + 1) * gridDim.x + line - 1) / line) - 1;
 }
 
 // A running triple of one element and its fold with the next chunk's.
@@ -273,74 +324,128 @@ struct Ring {
 
 // Copies tiles ahead of their use, across chunks and pairs of the CTA's share, by
 // 16-byte pieces (cp.async); what is not copied is filled with zeros, so nothing that
-// lies in unwritten cache rows reaches the arithmetic. Whole rows by bulk copies (a lane a
-// row) take a tenth of the instructions, but a warp starts its 32 one after the other
-// and its arithmetic waits: 64 mixed sequences took 72 us that way, 54 us this way.
+// lies in unwritten cache rows reaches the arithmetic.
+//
+// Pages of at least a tile's tokens: a tile lies in one page or two. The lanes hold 64
+// entries of the sequence's table row, 32 of them in use and the next 32, so a tile's
+// pages cost an exchange, not a load, and a row's address is its page's plus its place.
+// Smaller pages: each lane looks its own token's page up and the lanes exchange rows.
+//
+// Whole rows by bulk copies (a lane a row) take a tenth of the instructions, but a warp
+// starts its 32 one after the other and its arithmetic waits: 64 mixed sequences took
+// 72 us that way and 54 us by pieces.
 template <typename T, int DP, int TOK, int STAGES>
 struct Loader {
     using R = Ring<T, DP, TOK, STAGES>;
-    Walk<R::kRound> walk;
-    uint32_t ring;  // shared address of this warp's ring
-    int stage;
-    unsigned bad;   // bit i: the tile in stage i needs a page outside the cache
-    int entry, row; // the next tile's page and row of this lane's token, looked up one tile before they are needed
-    bool live;      // the lane's token exists
+    static constexpr int kTimes = TOK * R::kVecs / 32;       // pieces a lane copies of keys, and of values
+    static constexpr bool kWide = R::kVecs > 32;             // a row takes more than one of them
+    static constexpr int kRows = kWide ? 1 : 32 / R::kVecs;  // rows that the lanes copy at once
+    static_assert(TOK * R::kVecs % 32 == 0, "every lane copies the same number of pieces");
 
-    __device__ __forceinline__ void look(const DecodeWork &w, int warp, int lane)
-    {
-        live = false;
-        entry = row = 0;
-        if (walk.done(w)) return;
-        const int i = walk.round * R::kRound + warp * TOK + lane % TOK;
-        live = i < walk.s.n;
-        if (!live) return;
-        const unsigned t = (unsigned)(walk.s.first + i);
-        const unsigned page = quotient(t, w.page);
-        entry = w.p.table[walk.b * w.p.table_stride + page];
-        row = (int)(t - page * (unsigned)w.p.page_size);
-    }
-    // Skips pairs of the share that have no rounds in it.
-    __device__ __forceinline__ void settle(const DecodeWork &w)
-    {
-        while (!walk.done(w) && walk.round >= walk.end) walk.next_pair(w);
-    }
-    __device__ __forceinline__ void start(const DecodeWork &w, const Walk<R::kRound> &k, unsigned char *at, int warp,
-                                          int lane)
+    Walk<R::kRound> walk;
+    uint32_t ring;     // shared address of this warp's ring
+    int stage;
+    unsigned bad;      // bit i: the tile in stage i needs a page outside the cache
+    int known, first;  // the sequence whose table row the lanes hold; the page that lane 0 holds
+    int now, later;    // entries of pages first + lane, first + 32 + lane
+
+    __device__ __forceinline__ void start(const Walk<R::kRound> &k, unsigned char *at)
     {
         walk = k;
         ring = smem_addr(at);
         stage = 0;
         bad = 0;
-        settle(w);
-        look(w, warp, lane);
+        known = -1;
+    }
+    __device__ __forceinline__ int entry(const DecodeWork &w, int64_t page) const
+    {
+        return page < w.p.table_cols ? w.p.table[walk.b * w.p.table_stride + page] : -1;
+    }
+    // Makes `page` and the one after it part of what the lanes hold.
+    __device__ __forceinline__ void hold(const DecodeWork &w, int page, int lane)
+    {
+        if (known != walk.b || page < first || page >= first + 63) {
+            known = walk.b;
+            first = page;
+            now = entry(w, (int64_t)first + lane);
+            later = entry(w, (int64_t)first + 32 + lane);
+        } else if (page >= first + 32) {
+            first += 32;
+            now = later;
+            later = entry(w, (int64_t)first + 32 + lane);
+        }
+    }
+    __device__ __forceinline__ int held(int page) const
+    {
+        const int i = page - first;
+        const int x = __shfl_sync(~0u, now, i & 31), y = __shfl_sync(~0u, later, i & 31);
+        return i < 32 ? x : y;
+    }
+    __device__ __forceinline__ int64_t page_offset(const DecodeWork &w, int e) const
+    {
+        const int hk = w.blocks == 1 ? walk.pair : walk.pair / w.blocks;
+        return e * w.p.page_stride + hk * w.p.head_stride;
+    }
+    __device__ __forceinline__ void note(const DecodeWork &w, bool out)
+    {
+        if (out) flag_bad_index(w.p.status);
+        bad = (bad & ~(1u << stage)) | ((__any_sync(~0u, out) ? 1u : 0u) << stage);
+    }
+    // One piece of a row of keys and of values, or zeros.
+    __device__ __forceinline__ void piece(const DecodeWork &w, uint32_t to, int64_t off, int row, int col, bool live)
+    {
+        live &= col * 16 < w.p.head_dim * (int)sizeof(T);
+        const int bytes = live ? 16 : 0;
+        const int64_t from = live ? off * (int64_t)sizeof(T) + col * 16 : 0;
+        const uint32_t dst = to + row * R::kRow + col * 16;
+        copy16(dst, (const char *)w.p.k + from, bytes);
+        copy16(dst + R::kTile, (const char *)w.p.v + from, bytes);
     }
     // Starts the copies of the next tile; a commit group a call, empty past the end.
     __device__ __forceinline__ void issue(const DecodeWork &w, int warp, int lane)
     {
+        while (!walk.done(w) && walk.round >= walk.end) walk.next_pair(w);  // pairs without rounds in this share
         if (!walk.done(w)) {
-            const bool known = entry >= 0 && entry < w.p.num_pages;
-            const bool out = live && !known;
-            if (out) flag_bad_index(w.p.status);
-            bad = (bad & ~(1u << stage)) | ((__any_sync(~0u, out) ? 1u : 0u) << stage);
-            const int hk = w.blocks == 1 ? walk.pair : walk.pair / w.blocks;
-            const int64_t off = live && known ? entry * w.p.page_stride + row * w.p.token_stride +
-                                                    (int64_t)hk * w.p.head_stride
-                                              : -1;
+            const int i0 = walk.round * R::kRound + warp * TOK;
+            const int count = min(walk.s.n - i0, TOK);
+            const unsigned t0 = (unsigned)(walk.s.first + i0);
             const uint32_t to = ring + stage * R::kStage;
-            const int valid = w.p.head_dim * (int)sizeof(T) / 16;
-#pragma unroll
-            for (int i = 0; i < (TOK * R::kVecs + 31) / 32; ++i) {
-                const int vec = i * 32 + lane, r = vec / R::kVecs, c = vec % R::kVecs;
-                const int64_t o = __shfl_sync(~0u, off, r);
-                const int bytes = o >= 0 && c < valid ? 16 : 0;
-                const int64_t from = bytes ? o * (int64_t)sizeof(T) + c * 16 : 0;
-                const uint32_t dst = to + r * R::kRow + c * 16;
-                copy16(dst, (const char *)w.p.k + from, bytes);
-                copy16(dst + R::kTile, (const char *)w.p.v + from, bytes);
-            }
             ++walk.round;
-            settle(w);
-            look(w, warp, lane);
+            if (count > 0 && w.p.page_size >= TOK) {
+                const int page = (int)quotient(t0, w.page);
+                const int row0 = (int)(t0 - (unsigned)page * (unsigned)w.p.page_size);
+                const int split = w.p.page_size - row0;  // rows of the tile that lie in `page`
+                hold(w, page, lane);
+                const int e0 = held(page), e1 = held(page + 1);
+                const bool ok0 = e0 >= 0 && e0 < w.p.num_pages, ok1 = e1 >= 0 && e1 < w.p.num_pages;
+                note(w, !ok0 || (split < count && !ok1));
+                const int have = !ok0 ? 0 : split < count && !ok1 ? split : count;
+                // element offsets of tile rows 0 .. split - 1, and of those from split on
+                const int64_t off0 = page_offset(w, e0) + row0 * w.p.token_stride;
+                const int64_t off1 = page_offset(w, e1) - split * w.p.token_stride;
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) {
+                    const int row = kWide ? i * 32 / R::kVecs : i * kRows + lane / R::kVecs;
+                    const int col = kWide ? i * 32 % R::kVecs + lane : lane % R::kVecs;
+                    piece(w, to, (row < split ? off0 : off1) + row * w.p.token_stride, row, col, row < have);
+                }
+            } else if (count > 0) {
+                const unsigned t = t0 + lane % TOK, page = quotient(t, w.page);
+                const bool live = lane % TOK < count;
+                const int e = live ? w.p.table[walk.b * w.p.table_stride + page] : 0;
+                const bool ok = e >= 0 && e < w.p.num_pages;
+                note(w, live && !ok);
+                const int64_t off =
+                    live && ok ? page_offset(w, e) + (int)(t - page * (unsigned)w.p.page_size) * w.p.token_stride : -1;
+                int64_t o[kTimes];
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) o[i] = __shfl_sync(~0u, off, (i * 32 + lane) / R::kVecs);
+#pragma unroll
+                for (int i = 0; i < kTimes; ++i) {
+                    const int vec = i * 32 + lane;
+                    piece(w, to, o[i], vec / R::kVecs, vec % R::kVecs, o[i] >= 0);
+                }
+            }
         }
         copy_commit();
         stage = stage + 1 == STAGES ? 0 : stage + 1;
@@ -378,14 +483,13 @@ struct DecodeKernel {
         const bool folds = threadIdx.x < HB * kTeam;
         const int h = folds ? threadIdx.x / kTeam : HB - 1, d0 = threadIdx.x % kTeam * 4;
         enter_grid();
-        int64_t line;
-        Walk<R::kRound> walk = begin_walk<R::kRound>(w, line);
+        Shares shares;
+        Walk<R::kRound> walk = begin_walk<R::kRound>(w, shares);
         Loader load;
-        load.start(w, walk, sh.ring[warp], warp, lane);
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) load.issue(w, warp, lane);
+        load.start(walk, sh.ring[warp]);
         int stage = 0;
         int4 header = make_int4(0, 0, 0, 0);
+        bool started = false;
         Tile tile;
         for (; !walk.done(w); walk.next_pair(w)) {
             const bool begins = walk.at >= walk.lo;
@@ -394,8 +498,14 @@ struct DecodeKernel {
             const int head0 = hk * w.p.group + block * w.heads;
             const int heads = min(w.heads, w.p.group - block * w.heads);
             float *slot = nullptr;
-            if (w.slots) slot = w.slot + (begins ? blockIdx.x : share_of(walk.at, line)) * w.slot_floats;
+            if (w.slots) slot = w.slot + (begins ? (int)blockIdx.x : shares.of(w, walk.at)) * w.slot_floats;
             tile.load_q(w, sh.tile, walk.b, head0, heads, warp, lane);
+            if (!started) {
+                // the first copies, after the first queries are asked for
+                started = true;
+#pragma unroll 1
+                for (int i = 0; i < STAGES - 1; ++i) load.issue(w, warp, lane);
+            }
             tile.reset();
             float rm = neg_inf(), rl = 0.0f;
             float4 ra[kFours];

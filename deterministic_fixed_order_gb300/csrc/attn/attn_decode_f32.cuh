@@ -11,16 +11,6 @@
 
 namespace detfold_attn {
 
-__device__ __forceinline__ float4 lds4(uint32_t at)
-{
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(at)
-                 : "memory");
-    return v;
-}
-
 template <int DP, int TOK, int HB>
 struct F32Tile {
     using T = float;
@@ -72,14 +62,14 @@ struct F32Tile {
         float2 sum[HB];
 #pragma unroll
         for (int h = 0; h < HB; ++h) sum[h] = make_float2(0.0f, 0.0f);
-        const uint32_t ka = smem_addr(kt) + token * kRow, qa = smem_addr(&sh.q[0][0]);
+        const float4 *kr = reinterpret_cast<const float4 *>(kt + token * kRow);
         const int fours = w.p.head_dim / 4;
 #pragma unroll 4
         for (int i = part; i < fours; i += kParts) {
-            const float4 k = lds4(ka + i * 16);
+            const float4 k = kr[i];
 #pragma unroll
             for (int h = 0; h < HB; ++h) {
-                const float4 q = lds4(qa + h * DP * 4 + i * 16);
+                const float4 q = reinterpret_cast<const float4 *>(sh.q[h])[i];
                 sum[h] = fma2(make_float2(q.x, q.y), make_float2(k.x, k.y), sum[h]);
                 sum[h] = fma2(make_float2(q.z, q.w), make_float2(k.z, k.w), sum[h]);
             }

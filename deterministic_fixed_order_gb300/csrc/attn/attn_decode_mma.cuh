@@ -37,14 +37,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 // c += a b, 16x8x16.
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -83,19 +83,33 @@ struct MmaTile {
     __device__ __forceinline__ void load_q(const DecodeWork &w, Shared &, int b, int head0, int heads, int, int lane)
     {
         const int g = lane / 4, t = lane % 4;
-        const T zero = from_f32<T>(0.0f);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + g;
+            // lanes past the last head repeat it: their columns are never written out
+            const int h = min(nt * 8 + g, heads - 1);
             const T *from = (const T *)w.p.q + b * w.p.q_bs + (int64_t)(head0 + h) * w.p.q_hs;
+            // head_dim is a multiple of 8: a pair is inside or outside
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int d = ks * 16 + half * 8 + 2 * t;
-                    const bool in = h < heads && d < w.p.head_dim;  // head_dim is a multiple of 8
-                    q[ks][nt][half] = pack2<T>(in ? from[d] : zero, in ? from[d + 1] : zero);
-                }
+                for (int half = 0; half < 2; ++half) q[ks][nt][half] = 0;
+            if (w.q_vec) {
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int d = ks * 16 + half * 8 + 2 * t;
+                        if (d < w.p.head_dim) q[ks][nt][half] = *reinterpret_cast<const uint32_t *>(from + d);
+                    }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int d = ks * 16 + half * 8 + 2 * t;
+                        if (d < w.p.head_dim) q[ks][nt][half] = pack2<T>(from[d], from[d + 1]);
+                    }
+            }
         }
     }
 
@@ -124,13 +138,19 @@ struct MmaTile {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[nt][j] = s2[nt][j] = 0.0f;
+        // fragments are loaded some products ahead: the loads keep their order among themselves
+        constexpr int kBatch = DP / 16 < 8 ? DP / 16 : 8;
         const uint32_t ka = smem_addr(kt) + (lane % 16) * kRow + (lane / 16) * 16;
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) {
-            uint32_t a[4];
-            ldmatrix4(a, ka + ks * 32);
+        for (int k0 = 0; k0 < DP / 16; k0 += kBatch) {
+            uint32_t a[kBatch][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma(ks % 2 ? s2[nt] : s[nt], a, q[ks][nt][0], q[ks][nt][1], T());
+            for (int i = 0; i < kBatch; ++i) ldmatrix4(a[i], ka + (k0 + i) * 32);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma((k0 + i) % 2 ? s2[nt] : s[nt], a[i], q[k0 + i][nt][0], q[k0 + i][nt][1], T());
         }
         uint32_t hi[NT][2], lo[NT][2];
         bool moved = false;
@@ -143,26 +163,30 @@ struct MmaTile {
                 if (g + (j / 2) * 8 >= count) s[nt][j] = neg_inf();
             }
             float p[4];
+            float top[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                const float y0 = __shfl_xor_sync(~0u, top[0], x), y1 = __shfl_xor_sync(~0u, top[1], x);
+                top[0] = fmaxf(top[0], y0);
+                top[1] = fmaxf(top[1], y1);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float top = fmaxf(s[nt][j], s[nt][j + 2]);
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                top = fmaxf(top, m[nt][j]);
-                const float base = base_of(top);
+                top[j] = fmaxf(top[j], m[nt][j]);
+                const float base = base_of(top[j]);
                 fade[nt][j] = exp_neg(m[nt][j] - base);
-                moved |= top != m[nt][j];
-                m[nt][j] = top;
+                moved |= top[j] != m[nt][j];
+                m[nt][j] = top[j];
                 p[j] = exp_neg(s[nt][j] - base);
                 p[j + 2] = exp_neg(s[nt][j + 2] - base);
                 l[nt][j] = __fmaf_rn(l[nt][j], fade[nt][j], __fadd_rn(p[j], p[j + 2]));
             }
 #pragma unroll
+            for (int half = 0; half < 2; ++half) split2<T>(p[half * 2], p[half * 2 + 1], hi[nt][half], lo[nt][half]);
+#pragma unroll
             for (int half = 0; half < 2; ++half) {
-                uint32_t a, b;
-                split2<T>(p[half * 2], p[half * 2 + 1], a, b);
-                hi[nt][half] = transpose8(a);
-                lo[nt][half] = transpose8(b);
+                hi[nt][half] = transpose8(hi[nt][half]);
+                lo[nt][half] = transpose8(lo[nt][half]);
             }
         }
         // where no maximum moved every factor is 1
@@ -176,14 +200,17 @@ struct MmaTile {
         }
         const uint32_t va = smem_addr(vt) + ((lane / 16) * 8 + lane % 8) * kRow + ((lane / 8) % 2) * 16;
 #pragma unroll
-        for (int mt = 0; mt < DP / 16; ++mt) {
-            uint32_t a[4];
-            ldmatrix4_trans(a, va + mt * 32);
+        for (int m0 = 0; m0 < DP / 16; m0 += kBatch) {
+            uint32_t a[kBatch][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma(o[mt][nt], a, hi[nt][0], hi[nt][1], T());
-                mma(o[mt][nt], a, lo[nt][0], lo[nt][1], T());
-            }
+            for (int i = 0; i < kBatch; ++i) ldmatrix4_trans(a[i], va + (m0 + i) * 32);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(o[m0 + i][nt], a[i], hi[nt][0], hi[nt][1], T());
+                    mma(o[m0 + i][nt], a[i], lo[nt][0], lo[nt][1], T());
+                }
         }
     }
 
@@ -194,13 +221,16 @@ struct MmaTile {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float sum = l[nt][j];
+            for (int x = 4; x < 32; x <<= 1) {
+                const float y0 = __shfl_xor_sync(~0u, l[nt][0], x), y1 = __shfl_xor_sync(~0u, l[nt][1], x);
+                l[nt][0] = __fadd_rn(l[nt][0], y0);
+                l[nt][1] = __fadd_rn(l[nt][1], y1);
+            }
+            if (g == 0) {
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(~0u, sum, x));
-                if (g == 0) {
+                for (int j = 0; j < 2; ++j) {
                     sm[nt * 8 + 2 * t + j] = m[nt][j];
-                    sl[nt * 8 + 2 * t + j] = bad ? quiet_nan() : sum;
+                    sl[nt * 8 + 2 * t + j] = bad ? quiet_nan() : l[nt][j];
                 }
             }
 #pragma unroll
