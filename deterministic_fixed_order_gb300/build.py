@@ -10,14 +10,18 @@ The measurement probes (``csrc/probes/*.cu``, the latency floors that graphs
 of small folds are compared against) link into a library of their own,
 ``libdetfold_probes.so``, which the fold library's binding never loads. The
 decode-step attention operators (``csrc/attn/*.cu``) link into
-``libdetfold_attn.so``.
+``libdetfold_attn.so``, and the module that marshals torch tensors for them
+(``csrc/binding/attn_binding.cpp``) into ``_attn_binding.so``, with the host
+compiler against the installed torch's headers.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -30,6 +34,8 @@ PROBES_CSRC = os.path.join(CSRC, "probes")
 PROBES_LIB = os.path.join(PKG, "libdetfold_probes.so")
 ATTN_CSRC = os.path.join(CSRC, "attn")
 ATTN_LIB = os.path.join(PKG, "libdetfold_attn.so")
+BINDING_SRC = os.path.join(CSRC, "binding", "attn_binding.cpp")
+BINDING_LIB = os.path.join(PKG, "_attn_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -78,13 +84,56 @@ def build(force: bool = False, defines: dict | None = None, lib: str = LIB,
     if lib == LIB and (force or stale(PROBES_LIB, _probe_inputs())):
         _link(sorted(glob.glob(os.path.join(PROBES_CSRC, "*.cu"))), PROBES_LIB,
               os.path.join(build_dir, "probes"), [], verbose)
-    if lib == LIB and (force or stale(ATTN_LIB, _attn_inputs())):
-        _link(sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu"))), ATTN_LIB,
-              os.path.join(build_dir, "attn"), [], verbose)
+    if lib == LIB:
+        _build_attn(os.path.join(build_dir, "attn"), force, verbose)
     if not force and not defines and not stale(lib):
         return lib
     dflags = [f"-D{k}={v}" for k, v in (defines or {}).items()]
     return _link(sorted(glob.glob(os.path.join(CSRC, "*.cu"))), lib, build_dir, dflags, verbose)
+
+
+def _build_attn(build_dir: str, force: bool, verbose: bool) -> None:
+    binding_inputs = [BINDING_SRC, os.path.join(INCLUDE, "detfold.h"), os.path.join(INCLUDE, "detfold_attn.h"),
+                      os.path.abspath(__file__)]
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        obj = None
+        if force or stale(BINDING_LIB, binding_inputs):
+            obj = ex.submit(_compile_binding, build_dir)  # beside the kernels
+        if force or stale(ATTN_LIB, _attn_inputs()):
+            _link(sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu"))), ATTN_LIB, build_dir, [], verbose)
+        if obj is not None:
+            _link_binding(obj.result())
+
+
+def _torch_root() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found: the attention operators' marshalling module is built against it")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _run(cmd: list[str], what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding(build_dir: str) -> str:
+    os.makedirs(build_dir, exist_ok=True)
+    root, obj = _torch_root(), os.path.join(build_dir, "attn_binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    dirs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+            os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[f"-I{d}" for d in dirs], "-c", BINDING_SRC,
+          "-o", obj], "g++ on attn_binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    libs, tmp = os.path.join(_torch_root(), "lib"), BINDING_LIB + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libdetfold_attn.so", "-Wl,-rpath,$ORIGIN", f"-L{libs}",
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of _attn_binding.so")
+    os.replace(tmp, BINDING_LIB)
 
 
 def _link(sources: list[str], lib: str, build_dir: str, dflags: list[str], verbose: bool) -> str:
