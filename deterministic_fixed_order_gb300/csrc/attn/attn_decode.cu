@@ -9,14 +9,12 @@ cudaError_t launch_decode_f16(const DecodeWork &w, const DecodeGrid &g, cudaStre
 
 namespace {
 
-// The tile that a call takes: query heads a pair, tokens a round, CTAs an SM.
+// The call's grid: query heads a pair as the tiles take them, tokens a round.
 DecodeGrid grid_of(int dtype, int batch, int kv_heads, int group, int head_dim, int64_t max_seen)
 {
     const bool f32 = dtype == DETFOLD_F32;
     const int heads = f32 ? (group == 1 ? 1 : group <= 4 ? 4 : 8) : group > 8 && head_dim <= 128 ? 16 : 8;
-    const int round = f32 && head_dim > 128 ? 32 : 64;
-    const int resident = head_dim * (f32 ? 4 : 2) <= 256 ? 2 : 1;
-    return decode_grid(batch, kv_heads, group, head_dim, max_seen, heads, round, resident);
+    return decode_grid(batch, kv_heads, group, head_dim, max_seen, heads, tile_of(f32 ? 4 : 2, head_dim).round);
 }
 
 }  // namespace
@@ -34,6 +32,10 @@ cudaError_t launch_decode(const DecodeParams &p, int dtype, void *workspace, cud
     w.pairs = g.pairs, w.blocks = g.pairs / p.kv_heads, w.heads = g.heads;
     w.slots = g.slots, w.most_chunks = max_chunks(g.pairs);
     w.most = divide_by(w.most_chunks), w.grid = divide_by(g.ctas);
+    w.chunks = g.chunks > 0 ? g.chunks : 1, w.own = 1;
+    for (int r = g.ranks; r > 1; r /= 2) ++w.ranks_log2;
+    if (g.ranks) w.own = (g.heads * p.head_dim / 4 + g.ranks - 1) / g.ranks;
+    w.by_own = divide_by(w.own);
     w.short_line = (double)p.batch * g.pairs * (p.window / 32 + 2) < (1 << 30);
     w.pair_floats = g.pair_floats, w.slot_floats = g.slot_floats;
     w.page = divide_by(p.page_size);

@@ -27,12 +27,17 @@ namespace detfold_attn {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// CTAs: two on each of the 152 SMs of a GB300, or one where a CTA fills an SM.
+// CTAs: two on each of a GB300's 152 SMs, so that one's arithmetic goes on while the other
+// folds a chunk. Four warps with three stages of about 8.5 KB each take half an SM's
+// shared memory; its registers go round at 255 a thread.
 constexpr int kSms = 152, kMaxCtas = 2 * kSms;
 constexpr int kMinChunk = 128;  // tokens
-// Chunks a sequence: enough for one sequence to fill every CTA, within limits
-// that keep the join short.
-constexpr int kMinChunks = 32, kMaxChunks = 128;
+// Chunks a sequence: enough for one sequence to fill every CTA, within limits that keep
+// the join short.
+#ifndef MINCHUNKS
+#define MINCHUNKS 16
+#endif
+constexpr int kMinChunks = MINCHUNKS, kMaxChunks = 128;
 
 // A (key-value head, block of at most `heads` query heads) of a sequence is a
 // "pair": the unit that has a triple a query head.
@@ -50,6 +55,18 @@ inline int chunk_rounds(int rounds, int most, int round)
     return r < least ? least : r;
 }
 
+// The tile that a head dimension takes: tokens a warp has at once, so that keys and values
+// are about 8.5 KB, and tokens a round.
+struct TileShape {
+    int dims, tokens, round;
+};
+constexpr TileShape tile_of(int element_bytes, int head_dim)
+{
+    const int dims = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+    const int tokens = element_bytes == 2 ? (dims <= 128 ? 16 : 8) : dims == 64 ? 16 : dims == 128 ? 8 : 4;
+    return {dims, tokens, kWarps * tokens};
+}
+
 struct DecodeGrid {
     int ctas;    // CTAs of the main kernel
     int slots;   // workspace slots (one a CTA), 0: no sequence can be split
@@ -57,12 +74,33 @@ struct DecodeGrid {
     int pairs;   // pairs a sequence
     int heads;   // query heads a pair, at most
     int64_t pair_floats, slot_floats;  // floats of a slot's (m, l) pairs; of a slot
+    int ranks;   // CTAs a cluster where the sequences are few, else 0
 };
+
+// A few sequences: clusters of as many CTAs as a pair has chunks, within 16 a cluster and
+// FEW_WAVES an SM, as long as no CTA then has more than FEW_ROUNDS rounds.
+#ifndef FEW_WAVES
+#define FEW_WAVES 1
+#endif
+#ifndef FEW_ROUNDS
+#define FEW_ROUNDS 8
+#endif
+#ifndef MAXRANKS
+#define MAXRANKS 8
+#endif
+constexpr int kMaxRanks = MAXRANKS;
+
+inline int few_ranks(int64_t pairs_in_all, int chunks, int per)
+{
+    int ranks = 1;
+    while (ranks < kMaxRanks && ranks < chunks && pairs_in_all * ranks * 2 <= FEW_WAVES * kSms) ranks *= 2;
+    return pairs_in_all * ranks <= FEW_WAVES * kSms && (chunks + ranks - 1) / ranks * per <= FEW_ROUNDS ? ranks : 0;
+}
 
 // Workspace: `ctas` headers of four ints, then a slot a CTA: for each chunk and
 // head (m, l), then for each chunk and head the accumulator.
 inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, int64_t max_seen, int heads,
-                              int round, int resident)
+                              int round)
 {
     DecodeGrid g;
     g.heads = heads < group ? heads : group;
@@ -72,11 +110,12 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     const int per = chunk_rounds(rounds, max_chunks(g.pairs), round);
     g.chunks = (rounds + per - 1) / per;
     const int64_t units = (int64_t)batch * g.pairs * (g.chunks > 0 ? g.chunks : 1);
-    g.ctas = units < resident * kSms ? (int)units : resident * kSms;
+    g.ctas = units < kMaxCtas ? (int)units : kMaxCtas;
     // shorter sequences may have more chunks than the longest
     const int most = max_chunks(g.pairs), least = kMinChunk / round;
     const int up_to = (rounds + least - 1) / least;
     g.chunks = up_to < most ? up_to : most;
+    g.ranks = few_ranks((int64_t)batch * g.pairs, g.chunks, per);
     g.slots = g.chunks > 1 ? g.ctas : 0;
     g.pair_floats = ((int64_t)g.chunks * g.heads * 2 + 3) / 4 * 4;
     g.slot_floats = g.pair_floats + ((int64_t)g.chunks * g.heads * head_dim + 3) / 4 * 4;
@@ -95,6 +134,9 @@ struct DecodeWork {
     Divide most, grid;              // by most_chunks, by the number of CTAs
     int short_line;                 // the shares' line is shorter than 2^30
     Divide page;                    // by the page size
+    // a few sequences only: chunks a pair at most, CTAs a cluster, groups of four dimensions that a CTA folds
+    int chunks, ranks_log2, own;
+    Divide by_own;
     int out_vec;                    // four elements of out start at a multiple of their size
     int q_vec;                      // two elements of q do
     int64_t pair_floats, slot_floats;
@@ -267,6 +309,26 @@ __device__ __forceinline__ Walk<ROUND> begin_walk(const DecodeWork &w, Shares &s
     k.at += k.pair * cost(k.s);
     k.enter();
     return k;
+}
+
+// The cluster's CTAs and their shared memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t peer_addr(uint32_t at, int rank)
+{
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+    return there;
+}
+__device__ __forceinline__ void store_peer(uint32_t at, int rank, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer_addr(at, rank)), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void store_peer(uint32_t at, int rank, float2 v)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(at, rank)), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // A running triple of one element and its fold with the next chunk's.
@@ -468,11 +530,51 @@ struct DecodeKernel {
         float m[kWarps][HB], l[kWarps][HB];
         typename Tile::Shared tile;
     };
-    static constexpr int kResident = sizeof(Shared) <= 113 * 1024 ? 2 : 1;  // CTAs an SM
     static_assert(HB * kTeam <= kThreads && DP % (4 * kTeam) == 0, "every thread folds the same number of elements");
     // A warp leaves its accumulator in the stage that it has just used up: the next
     // copy into it starts after the fold.
     static_assert(HB * kPitch * 4 <= R::kStage, "the accumulator fits a stage");
+
+    // A chunk's triple, of this thread's head and dimensions, from the warps' triples.
+    static __device__ __forceinline__ void join_warps(const Shared &sh, int used, int h, int d0, float &top, float &l,
+                                                      float4 (&a)[kFours])
+    {
+        top = sh.m[0][h];
+#pragma unroll
+        for (int k = 1; k < kWarps; ++k) top = fmaxf(top, sh.m[k][h]);
+        const float base = base_of(top);
+        float f[kWarps];
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            f[k] = exp_neg(sh.m[k][h] - base);
+            l = __fmaf_rn(sh.l[k][h], f[k], l);
+        }
+#pragma unroll
+        for (int i = 0; i < kFours; ++i) {
+            a[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float4 x = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(sh.ring[k] + used * R::kStage) + h * kPitch + d0 + i * kTeam * 4);
+                a[i].x = __fmaf_rn(x.x, f[k], a[i].x);
+                a[i].y = __fmaf_rn(x.y, f[k], a[i].y);
+                a[i].z = __fmaf_rn(x.z, f[k], a[i].z);
+                a[i].w = __fmaf_rn(x.w, f[k], a[i].w);
+            }
+        }
+    }
+    // Folds a chunk's triple into the running one.
+    static __device__ __forceinline__ void fold_chunk(float &rm, float &rl, float4 (&ra)[kFours], float top, float l,
+                                                      const float4 (&a)[kFours])
+    {
+        float m, fa, fb;
+        fold_weights(rm, top, m, fa, fb);
+        rl = fold_value(rl, l, fa, fb);
+#pragma unroll
+        for (int i = 0; i < kFours; ++i) ra[i] = fold_four(ra[i], a[i], fa, fb);
+        rm = m;
+    }
 
     __device__ static void run(const DecodeWork &w)
     {
@@ -530,41 +632,18 @@ struct DecodeKernel {
                 tile.reset();
                 bad = false;
                 __syncthreads();
-                float top = sh.m[0][h];
-#pragma unroll
-                for (int k = 1; k < kWarps; ++k) top = fmaxf(top, sh.m[k][h]);
-                const float base = base_of(top);
-                float f[kWarps], l = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    f[k] = exp_neg(sh.m[k][h] - base);
-                    l = __fmaf_rn(sh.l[k][h], f[k], l);
-                }
-                float m, fa, fb;
-                fold_weights(rm, top, m, fa, fb);
-#pragma unroll
-                for (int i = 0; i < kFours; ++i) {
-                    const int d = d0 + i * kTeam * 4;
-                    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                    for (int k = 0; k < kWarps; ++k) {
-                        const float4 x = *reinterpret_cast<const float4 *>(
-                            reinterpret_cast<const float *>(sh.ring[k] + used * R::kStage) + h * kPitch + d);
-                        a.x = __fmaf_rn(x.x, f[k], a.x);
-                        a.y = __fmaf_rn(x.y, f[k], a.y);
-                        a.z = __fmaf_rn(x.z, f[k], a.z);
-                        a.w = __fmaf_rn(x.w, f[k], a.w);
-                    }
-                    if (begins)
-                        ra[i] = fold_four(ra[i], a, fa, fb);
-                    else if (folds && h < heads && d < w.p.head_dim)
-                        put_four(w, slot, chunk, h, d, a);
-                }
+                float top, l;
+                float4 a[kFours];
+                join_warps(sh, used, h, d0, top, l, a);
                 if (begins) {
-                    rl = fold_value(rl, l, fa, fb);
-                    rm = m;
-                } else if (folds && h < heads && d0 == 0) {
-                    put_pair(w, slot, chunk, h, top, l);
+                    fold_chunk(rm, rl, ra, top, l, a);
+                } else if (folds && h < heads) {
+#pragma unroll
+                    for (int i = 0; i < kFours; ++i) {
+                        const int d = d0 + i * kTeam * 4;
+                        if (d < w.p.head_dim) put_four(w, slot, chunk, h, d, a[i]);
+                    }
+                    if (d0 == 0) put_pair(w, slot, chunk, h, top, l);
                 }
                 __syncthreads();
                 ++chunk;
@@ -592,6 +671,145 @@ struct DecodeKernel {
         }
         copy_wait<0>();
         if (w.slots && threadIdx.x == 0) w.headers[blockIdx.x] = header;
+    }
+
+    // A few sequences: a cluster of CTAs a pair, each taking its part of the pair's chunks.
+    // No shares and no workspace: the CTAs push their chunks' triples straight into the
+    // shared memory of the CTA that folds the element -- each folds its part of the (head,
+    // dimension) plane -- and one cluster barrier stands where the join kernel would. The
+    // same chunks, the same folds, the same bits.
+    __device__ static void run_few(const DecodeWork &w)
+    {
+        extern __shared__ unsigned char raw[];
+        Shared &sh = *reinterpret_cast<Shared *>(raw);
+        float4 *part = reinterpret_cast<float4 *>(raw + sizeof(Shared));     // [chunks][own]
+        float2 *pairs = reinterpret_cast<float2 *>(part + w.chunks * w.own);  // [chunks][heads] (m, l)
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const bool folds = threadIdx.x < HB * kTeam;
+        const int h = folds ? threadIdx.x / kTeam : HB - 1, d0 = threadIdx.x % kTeam * 4;
+        const int rank = blockIdx.x, ranks = gridDim.x, fours = w.p.head_dim / 4;
+        if (ranks > 1) cluster_arrive();  // peers have to run before anything is pushed to them
+        enter_grid();
+        Walk<R::kRound> walk;
+        walk.b = blockIdx.z;
+        walk.pair = blockIdx.y;
+        walk.s = sequence<R::kRound>(w, walk.b);
+        walk.at = walk.lo = 0;
+        walk.hi = 1;
+        const int chunks = walk.chunks();
+        const int c0 = (rank * chunks + ranks - 1) >> w.ranks_log2, c1 = ((rank + 1) * chunks + ranks - 1) >> w.ranks_log2;
+        const int first = ((chunks + ranks - 1) >> w.ranks_log2) - 1;  // the last chunk that rank 0 folds itself
+        const bool joins = chunks > first + 1, begins = rank == 0;
+        walk.round = c0 * walk.s.per;
+        walk.end = min(c1 * walk.s.per, walk.s.rounds);
+        const int hk = walk.pair / w.blocks, block = walk.pair % w.blocks;
+        const int head0 = hk * w.p.group + block * w.heads, heads = min(w.heads, w.p.group - block * w.heads);
+        const int b = walk.b, rounds = walk.end, per = walk.s.per, n = walk.s.n;
+        const bool bad_length = walk.s.bad;
+        int g = walk.round;
+        Loader load;
+        load.start(walk, sh.ring[warp]);
+        Tile tile;
+        float rm = neg_inf(), rl = 0.0f;
+        float4 ra[kFours];
+#pragma unroll
+        for (int i = 0; i < kFours; ++i) ra[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (g < rounds) {
+            tile.load_q(w, sh.tile, b, head0, heads, warp, lane);
+#pragma unroll 1
+            for (int i = 0; i < STAGES - 1; ++i) load.issue(w, warp, lane);
+            tile.reset();
+        }
+        if (ranks > 1) cluster_wait();
+        int stage = 0, chunk = c0, left = per;
+        bool bad = false;
+        const auto push = [&](int c, float m, float l, const float4 (&a)[kFours]) {
+            if (!folds || h >= heads) return;
+#pragma unroll
+            for (int i = 0; i < kFours; ++i) {
+                const int d = d0 + i * kTeam * 4;
+                if (d >= w.p.head_dim) continue;
+                const unsigned e = h * fours + d / 4, owner = quotient(e, w.by_own);
+                store_peer(smem_addr(part + c * w.own + (e - owner * w.own)), owner, a[i]);
+            }
+            if (d0 == 0) {
+                const int from = quotient(h * fours, w.by_own), to = quotient(h * fours + fours - 1, w.by_own);
+                for (int r = from; r <= to; ++r) store_peer(smem_addr(pairs + c * w.heads + h), r, make_float2(m, l));
+            }
+        };
+        for (; g < rounds; ++g) {
+            const int count = n - (g * R::kRound + warp * TOK);
+            unsigned char *at = sh.ring[warp] + stage * R::kStage;
+            copy_wait<STAGES - 2>();
+            __syncwarp();
+            bad |= load.bad >> stage & 1;
+            load.issue(w, warp, lane);
+            if (count > 0) tile.step(w, sh.tile, at, at + R::kTile, count, warp, lane);
+            const int used = stage;
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            if (--left && g + 1 < rounds) continue;
+            __syncwarp();
+            tile.leave(reinterpret_cast<float *>(at), kPitch, sh.m[warp], sh.l[warp], bad, lane);
+            tile.reset();
+            bad = false;
+            __syncthreads();
+            float top, l;
+            float4 a[kFours];
+            join_warps(sh, used, h, d0, top, l, a);
+            if (begins)
+                fold_chunk(rm, rl, ra, top, l, a);
+            else
+                push(chunk, top, l, a);
+            __syncthreads();
+            ++chunk;
+            left = per;
+        }
+        copy_wait<0>();
+        if (begins && bad_length) {
+            rl = quiet_nan();
+            if (threadIdx.x == 0) flag_bad_index(w.p.status);
+        }
+        if (!joins) {
+            if (begins && folds && h < heads) {
+#pragma unroll
+                for (int i = 0; i < kFours; ++i) {
+                    const int d = d0 + i * kTeam * 4;
+                    if (d < w.p.head_dim) write_out<T>(w, b, head0 + h, d, rm, rl, ra[i]);
+                }
+            }
+            return;
+        }
+        if (begins) push(first, rm, rl, ra);
+        cluster_arrive();
+        cluster_wait();
+        // this CTA's part of the plane: groups of four dimensions [e0, e1)
+        const int e0 = rank * w.own, e1 = min(e0 + w.own, heads * fours), folded = chunks - first;
+        if (e0 >= e1) return;
+        const int h0 = e0 / fours, spans = (e1 - 1) / fours - h0 + 1;
+        float4 *fold = reinterpret_cast<float4 *>(raw);  // [spans][folded] (fa, fb, top, l): the rings are idle
+        for (int i = threadIdx.x; i < spans * folded; i += kThreads) {
+            const int hh = h0 + i / folded, c = i % folded;
+            float before = neg_inf();
+            for (int k = 0; k < c; ++k) before = fmaxf(before, pairs[(first + k) * w.heads + hh].x);
+            const float2 ml = pairs[(first + c) * w.heads + hh];
+            float m, fa, fb;
+            fold_weights(before, ml.x, m, fa, fb);
+            fold[i] = make_float4(fa, fb, m, ml.y);
+        }
+        __syncthreads();
+        for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
+            const int hh = e / fours;
+            float l = 0.0f, m = neg_inf();
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int c = 0; c < folded; ++c) {
+                const float4 f = fold[(hh - h0) * folded + c];
+                l = fold_value(l, f.w, f.x, f.y);
+                a = fold_four(a, part[(first + c) * w.own + e - e0], f.x, f.y);
+                m = f.z;
+            }
+            write_out<T>(w, b, head0 + hh, (e - hh * fours) * 4, m, l, a);
+        }
     }
 
     // A chunk's triple in a slot: (m, l) of each head, then the accumulators.

@@ -1,7 +1,7 @@
 // One warp's share of the attention in 16-bit types, on the matrix units.
 //
-// Scores: S^T = K Q^T, 16 tokens by 8 query heads a product, so that a group of
-// up to eight heads costs what one does. P stays in registers: S^T's layout,
+// Scores: S^T = K Q^T, 16 (or 8, the other half zeros) tokens by 8 query heads a product,
+// so that a group of up to eight heads costs what one does. P stays in registers: S^T's layout,
 // packed to 16 bits and transposed 8x8 by movmatrix, is the second product's
 // right operand, O^T = V^T P^T (V^T by transposing loads). P is split in two
 // 16-bit parts, p = hi + lo, both multiplied: one part alone would round each
@@ -50,6 +50,20 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// c += a b, 16x8x8.
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0, __nv_bfloat16)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0, __half)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(T x, T y)
 {
@@ -68,10 +82,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = pack2<T>(from_f32<T>(__fsub_rn(x, to_f32(hx))), from_f32<T>(__fsub_rn(y, to_f32(hy))));
 }
 
-template <typename T_, int DP, int NT>
+template <typename T_, int DP, int TOK, int NT>
 struct MmaTile {
     using T = T_;
-    static constexpr int kDP = DP, kTok = 16, kHeads = 8 * NT, kRow = DP * 2 + 16;
+    static constexpr int kDP = DP, kTok = TOK, kHeads = 8 * NT, kRow = DP * 2 + 16;
+    static constexpr int kHalves = TOK / 8;  // eights of tokens a tile
     struct Shared {
         int unused;
     };
@@ -126,7 +141,7 @@ struct MmaTile {
         }
     }
 
-    // One tile of `count` tokens (16 or fewer; the rest of the tile is zeros).
+    // One tile of `count` tokens (TOK or fewer; the rest of the tile is zeros).
     __device__ __forceinline__ void step(const DecodeWork &w, Shared &, const unsigned char *kt,
                                          const unsigned char *vt, int count, int, int lane)
     {
@@ -138,32 +153,41 @@ struct MmaTile {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[nt][j] = s2[nt][j] = 0.0f;
-        // fragments are loaded some products ahead: the loads keep their order among themselves
-        constexpr int kBatch = DP / 16 < 8 ? DP / 16 : 8;
-        const uint32_t ka = smem_addr(kt) + (lane % 16) * kRow + (lane / 16) * 16;
+        // four 8x8 blocks a load: of 16 tokens and 16 dimensions, or of 8 and 32. A batch of loads
+        // goes ahead of its products, since the loads keep their order among themselves.
+        constexpr int kSteps = DP / 16, kPerLoad = 2 / kHalves, kLoads = kSteps / kPerLoad;
+        constexpr int kBatch = kLoads < 8 ? kLoads : 8;
+        const uint32_t ka = smem_addr(kt) + (TOK == 16 ? (lane % 16) * kRow + (lane / 16) * 16
+                                                       : (lane % 8) * kRow + (lane / 8) * 16);
 #pragma unroll
-        for (int k0 = 0; k0 < DP / 16; k0 += kBatch) {
+        for (int k0 = 0; k0 < kLoads; k0 += kBatch) {
             uint32_t a[kBatch][4];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) ldmatrix4(a[i], ka + (k0 + i) * 32);
+            for (int i = 0; i < kBatch; ++i) ldmatrix4(a[i], ka + (k0 + i) * 32 * kPerLoad);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma((k0 + i) % 2 ? s2[nt] : s[nt], a[i], q[k0 + i][nt][0], q[k0 + i][nt][1], T());
+                for (int j = 0; j < kPerLoad; ++j) {
+                    const int ks = (k0 + i) * kPerLoad + j;
+                    const uint32_t f[4] = {TOK == 16 ? a[i][0] : a[i][2 * j], TOK == 16 ? a[i][1] : 0,
+                                           TOK == 16 ? a[i][2] : a[i][2 * j + 1], TOK == 16 ? a[i][3] : 0};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma(ks % 2 ? s2[nt] : s[nt], f, q[ks][nt][0], q[ks][nt][1], T());
+                }
         }
-        uint32_t hi[NT][2], lo[NT][2];
+        uint32_t hi[NT][kHalves], lo[NT][kHalves];
         bool moved = false;
         float fade[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            float top[2] = {neg_inf(), neg_inf()}, p[2 * kHalves];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2 * kHalves; ++j) {
                 s[nt][j] = __fmul_rn(__fadd_rn(s[nt][j], s2[nt][j]), scale);
                 if (g + (j / 2) * 8 >= count) s[nt][j] = neg_inf();
+                top[j % 2] = fmaxf(top[j % 2], s[nt][j]);
             }
-            float p[4];
-            float top[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
                 const float y0 = __shfl_xor_sync(~0u, top[0], x), y1 = __shfl_xor_sync(~0u, top[1], x);
@@ -177,14 +201,19 @@ struct MmaTile {
                 fade[nt][j] = exp_neg(m[nt][j] - base);
                 moved |= top[j] != m[nt][j];
                 m[nt][j] = top[j];
-                p[j] = exp_neg(s[nt][j] - base);
-                p[j + 2] = exp_neg(s[nt][j + 2] - base);
-                l[nt][j] = __fmaf_rn(l[nt][j], fade[nt][j], __fadd_rn(p[j], p[j + 2]));
+                float sum = 0.0f;
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half) {
+                    p[half * 2 + j] = exp_neg(s[nt][half * 2 + j] - base);
+                    sum = half ? __fadd_rn(sum, p[half * 2 + j]) : p[half * 2 + j];
+                }
+                l[nt][j] = __fmaf_rn(l[nt][j], fade[nt][j], sum);
             }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) split2<T>(p[half * 2], p[half * 2 + 1], hi[nt][half], lo[nt][half]);
+            for (int half = 0; half < kHalves; ++half)
+                split2<T>(p[half * 2], p[half * 2 + 1], hi[nt][half], lo[nt][half]);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < kHalves; ++half) {
                 hi[nt][half] = transpose8(hi[nt][half]);
                 lo[nt][half] = transpose8(lo[nt][half]);
             }
@@ -198,18 +227,28 @@ struct MmaTile {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[mt][nt][j] = __fmul_rn(o[mt][nt][j], fade[nt][j % 2]);
         }
-        const uint32_t va = smem_addr(vt) + ((lane / 16) * 8 + lane % 8) * kRow + ((lane / 8) % 2) * 16;
+        const uint32_t va = smem_addr(vt) + (TOK == 16 ? ((lane / 16) * 8 + lane % 8) * kRow + ((lane / 8) % 2) * 16
+                                                       : (lane % 8) * kRow + (lane / 8) * 16);
 #pragma unroll
-        for (int m0 = 0; m0 < DP / 16; m0 += kBatch) {
+        for (int m0 = 0; m0 < kLoads; m0 += kBatch) {
             uint32_t a[kBatch][4];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) ldmatrix4_trans(a[i], va + (m0 + i) * 32);
+            for (int i = 0; i < kBatch; ++i) ldmatrix4_trans(a[i], va + (m0 + i) * 32 * kPerLoad);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma(o[m0 + i][nt], a[i], hi[nt][0], hi[nt][1], T());
-                    mma(o[m0 + i][nt], a[i], lo[nt][0], lo[nt][1], T());
+                for (int j = 0; j < kPerLoad; ++j) {
+                    const int mt = (m0 + i) * kPerLoad + j;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (TOK == 16) {
+                            mma(o[mt][nt], a[i], hi[nt][0], hi[nt][1], T());
+                            mma(o[mt][nt], a[i], lo[nt][0], lo[nt][1], T());
+                        } else {
+                            mma8(o[mt][nt], a[i][2 * j], a[i][2 * j + 1], hi[nt][0], T());
+                            mma8(o[mt][nt], a[i][2 * j], a[i][2 * j + 1], lo[nt][0], T());
+                        }
+                    }
                 }
         }
     }
