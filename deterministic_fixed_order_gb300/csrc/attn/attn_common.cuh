@@ -71,11 +71,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
 
-// The device status word: written only where an index is out of range.
-__device__ __forceinline__ void flag_bad_index(int *status)
+// The device status word: written only where something is wrong.
+__device__ __forceinline__ void flag(int *status, int code)
 {
-    if (status) *(volatile int *)status = DETFOLD_ERR_ARG;
+    if (status) *(volatile int *)status = code;
 }
+__device__ __forceinline__ void flag_bad_index(int *status) { flag(status, DETFOLD_ERR_ARG); }
 
 // e^x for x <= 0: one product and the hardware's 2^x (2 units in the last place
 // of binary32 or so; results below 2^-126 become 0).

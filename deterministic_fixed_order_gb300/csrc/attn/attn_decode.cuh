@@ -31,7 +31,10 @@ constexpr int kThreads = kWarps * 32;
 // folds a chunk. Four warps with three stages of about 8.5 KB each take half an SM's
 // shared memory; its registers go round at 255 a thread.
 constexpr int kSms = 152, kMaxCtas = 2 * kSms;
-constexpr int kMinChunk = 128;  // tokens
+#ifndef MINCHUNK
+#define MINCHUNK 128
+#endif
+constexpr int kMinChunk = MINCHUNK;  // tokens
 // Chunks a sequence: enough for one sequence to fill every CTA, within limits that keep
 // the join short.
 #ifndef MINCHUNKS
@@ -55,15 +58,15 @@ inline int chunk_rounds(int rounds, int most, int round)
     return r < least ? least : r;
 }
 
-// The tile that a head dimension takes: tokens a warp has at once, so that keys and values
-// are about 8.5 KB, and tokens a round.
+// The tile that a head dimension takes: tokens a warp has at once, so that their keys are 8 KB
+// (4 KB at 64 16-bit dimensions), and tokens a round.
 struct TileShape {
     int dims, tokens, round;
 };
 constexpr TileShape tile_of(int element_bytes, int head_dim)
 {
     const int dims = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    const int tokens = element_bytes == 2 ? (dims <= 128 ? 16 : 8) : dims == 64 ? 16 : dims == 128 ? 8 : 4;
+    const int by_size = 8192 / (dims * element_bytes), tokens = by_size < 32 ? by_size : 32;
     return {dims, tokens, kWarps * tokens};
 }
 
@@ -106,16 +109,15 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     g.heads = heads < group ? heads : group;
     const int blocks = (group + heads - 1) / heads;
     g.pairs = kv_heads * blocks;
-    const int rounds = (int)((max_seen + round - 1) / round);
-    const int per = chunk_rounds(rounds, max_chunks(g.pairs), round);
-    g.chunks = (rounds + per - 1) / per;
-    const int64_t units = (int64_t)batch * g.pairs * (g.chunks > 0 ? g.chunks : 1);
-    g.ctas = units < kMaxCtas ? (int)units : kMaxCtas;
-    // shorter sequences may have more chunks than the longest
+    const int rounds = (int)((max_seen + round - 1) / round), per = chunk_rounds(rounds, max_chunks(g.pairs), round);
+    g.ranks = few_ranks((int64_t)batch * g.pairs, (rounds + per - 1) / per, per);
+    // shorter sequences may have more chunks than the longest: as many as there can be at all, so
+    // that a larger max_seen never needs less
     const int most = max_chunks(g.pairs), least = kMinChunk / round;
     const int up_to = (rounds + least - 1) / least;
     g.chunks = up_to < most ? up_to : most;
-    g.ranks = few_ranks((int64_t)batch * g.pairs, g.chunks, per);
+    const int64_t units = (int64_t)batch * g.pairs * (g.chunks > 0 ? g.chunks : 1);
+    g.ctas = units < kMaxCtas ? (int)units : kMaxCtas;
     g.slots = g.chunks > 1 ? g.ctas : 0;
     g.pair_floats = ((int64_t)g.chunks * g.heads * 2 + 3) / 4 * 4;
     g.slot_floats = g.pair_floats + ((int64_t)g.chunks * g.heads * head_dim + 3) / 4 * 4;
@@ -167,17 +169,18 @@ struct Seq {
     bool bad;      // its length is out of range
 };
 
-template <int ROUND>
+template <int TOK>
 __device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
 {
     Seq s;
     const int len = w.p.lens[b];
     s.bad = len < 0 || len > w.p.max_len;
+    constexpr int kRound = kWarps * TOK;
     const int n = s.bad ? 0 : len;
     s.n = n < w.p.window ? n : (int)w.p.window;
     s.first = n - s.n;
-    s.rounds = (s.n + ROUND - 1) / ROUND;
-    s.per = max(kMinChunk / ROUND, (int)quotient(s.rounds + w.most_chunks - 1, w.most));  // chunk_rounds
+    s.rounds = (s.n + kRound - 1) / kRound;
+    s.per = max(kMinChunk / kRound, (int)quotient(s.rounds + w.most_chunks - 1, w.most));  // chunk_rounds
     return s;
 }
 
@@ -187,7 +190,7 @@ __device__ __forceinline__ int64_t cost(const Seq &s) { return s.rounds + 1; }
 // Walks the pairs of a CTA's share [lo, hi) of the line on which all pairs of
 // all sequences lie, each as long as it costs. A chunk belongs to the share
 // that its first round lies in, a pair's output to the share that its start lies in.
-template <int ROUND>
+template <int TOK>
 struct Walk {
     int64_t at, lo, hi;  // start of the current pair on the line; the share
     Seq s;
@@ -216,7 +219,7 @@ struct Walk {
         at += cost(s);
         if (++pair == w.pairs) {
             pair = 0;
-            if (++b < w.p.batch) s = sequence<ROUND>(w, b);
+            if (++b < w.p.batch) s = sequence<TOK>(w, b);
         }
         if (!done(w)) enter();
     }
@@ -248,11 +251,11 @@ struct Shares {
 
 // The sequence that `at` lies in and its start, by a scan of all sequences' costs, 32 at
 // a time, and the cut of the line into shares. I holds the line's length.
-template <int ROUND, typename I>
+template <int TOK, typename I>
 __device__ __forceinline__ void find_sequence(const DecodeWork &w, Shares &shares, int64_t &lo, int &b, int64_t &at)
 {
     const int lane = threadIdx.x & 31;
-    const auto cost_of = [&](int i) { return i < w.p.batch ? (I)(cost(sequence<ROUND>(w, i)) * w.pairs) : (I)0; };
+    const auto cost_of = [&](int i) { return i < w.p.batch ? (I)(cost(sequence<TOK>(w, i)) * w.pairs) : (I)0; };
     const auto scan = [&](I up) {
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -286,22 +289,22 @@ __device__ __forceinline__ void find_sequence(const DecodeWork &w, Shares &share
 }
 
 // This CTA's share. Every warp does the same: no barrier.
-template <int ROUND>
-__device__ __forceinline__ Walk<ROUND> begin_walk(const DecodeWork &w, Shares &shares)
+template <int TOK>
+__device__ __forceinline__ Walk<TOK> begin_walk(const DecodeWork &w, Shares &shares)
 {
-    Walk<ROUND> k;
+    Walk<TOK> k;
     if (w.p.batch == 1) {
         k.b = 0;
         k.at = 0;
-        k.s = sequence<ROUND>(w, 0);
+        k.s = sequence<TOK>(w, 0);
         shares.cut(w, cost(k.s) * w.pairs);
         k.lo = shares.begin(w, blockIdx.x);
     } else {
         if (w.short_line)
-            find_sequence<ROUND, int>(w, shares, k.lo, k.b, k.at);
+            find_sequence<TOK, int>(w, shares, k.lo, k.b, k.at);
         else
-            find_sequence<ROUND, int64_t>(w, shares, k.lo, k.b, k.at);
-        k.s = sequence<ROUND>(w, k.b);
+            find_sequence<TOK, int64_t>(w, shares, k.lo, k.b, k.at);
+        k.s = sequence<TOK>(w, k.b);
     }
     k.hi = shares.begin(w, blockIdx.x + 1);
     const int64_t in = k.lo - k.at;
@@ -372,157 +375,120 @@ __device__ __forceinline__ void write_out(const DecodeWork &w, int b, int head, 
     if (d == 0 && w.p.lse) w.p.lse[(int64_t)b * w.p.q_heads + head] = __fadd_rn(base_of(m), logf(l));
 }
 
-// One warp's ring of tiles: TOK tokens of keys, then of values, rows padded by
-// 16 bytes so that eight rows' 16-byte pieces lie in different banks.
-template <typename T, int DP, int TOK, int STAGES>
+// One warp's ring: slots that hold TOK tokens of keys or of values in turn. A slot is cut into
+// columns of 128 bytes; in a column a token's eight 16-byte pieces are exchanged by the low
+// bits of the token's number, so that eight tokens' same pieces lie in different banks.
+template <typename T, int DP, int TOK, int SLOTS>
 struct Ring {
-    static constexpr int kRow = DP * (int)sizeof(T) + 16;
-    static constexpr int kTile = TOK * kRow;
-    static constexpr int kStage = 2 * kTile;
-    static constexpr int kBytes = STAGES * kStage;
-    static constexpr int kVecs = DP * (int)sizeof(T) / 16;  // 16-byte pieces a row
+    static constexpr int kRowBytes = DP * (int)sizeof(T);
+    static constexpr int kSlot = TOK * kRowBytes;
+    static constexpr int kBytes = SLOTS * kSlot;
+    static constexpr int kVecs = kRowBytes / 16;  // 16-byte pieces a row
     static constexpr int kRound = kWarps * TOK;
 };
+// The offset of piece `vec` of token `row` in a slot.
+template <int TOK>
+__device__ __forceinline__ int piece_at(int row, int vec)
+{
+    return vec / 8 * (TOK * 128) + row * 128 + (((vec & 7) ^ (row & 7)) << 4);
+}
 
-// Copies tiles ahead of their use, across chunks and pairs of the CTA's share, by
-// 16-byte pieces (cp.async); what is not copied is filled with zeros, so nothing that
-// lies in unwritten cache rows reaches the arithmetic.
+// Copies keys and values ahead of their use, across chunks and pairs of the CTA's share, by
+// 16-byte pieces (cp.async): one call a slot, keys and values in turn, and one commit group a
+// call. Each lane looks a token's page up and the lanes exchange the rows' places. Pieces that
+// are not copied are filled with zeros, so nothing that lies in unwritten cache rows reaches
+// the arithmetic.
 //
-// Pages of at least a tile's tokens: a tile lies in one page or two. The lanes hold 64
-// entries of the sequence's table row, 32 of them in use and the next 32, so a tile's
-// pages cost an exchange, not a load, and a row's address is its page's plus its place.
-// Smaller pages: each lane looks its own token's page up and the lanes exchange rows.
-//
-// Whole rows by bulk copies (a lane a row) take a tenth of the instructions, but a warp
-// starts its 32 one after the other and its arithmetic waits: 64 mixed sequences took
-// 72 us that way and 54 us by pieces.
-template <typename T, int DP, int TOK, int STAGES>
+// Measured against it, times of 64 mixed sequences and of one of 131071 tokens: bulk copies, a lane a
+// row, 72 and 113 us (a warp starts its copies one after the other); tensor copies of 16 tokens
+// by 128 bytes 57 and 86 us; pieces 53 and 86 us, the shortest path at few tokens, and any page size.
+template <typename T, int DP, int TOK, int SLOTS>
 struct Loader {
-    using R = Ring<T, DP, TOK, STAGES>;
-    static constexpr int kTimes = TOK * R::kVecs / 32;       // pieces a lane copies of keys, and of values
-    static constexpr bool kWide = R::kVecs > 32;             // a row takes more than one of them
-    static constexpr int kRows = kWide ? 1 : 32 / R::kVecs;  // rows that the lanes copy at once
+    using R = Ring<T, DP, TOK, SLOTS>;
+    static constexpr int kTimes = TOK * R::kVecs / 32;  // pieces a lane copies a slot
     static_assert(TOK * R::kVecs % 32 == 0, "every lane copies the same number of pieces");
 
-    Walk<R::kRound> walk;
-    uint32_t ring;     // shared address of this warp's ring
-    int stage;
-    unsigned bad;      // bit i: the tile in stage i needs a page outside the cache
-    int known, first;  // the sequence whose table row the lanes hold; the page that lane 0 holds
-    int now, later;    // entries of pages first + lane, first + 32 + lane
+    Walk<TOK> walk;
+    uint32_t ring;  // shared address of this warp's ring
+    int slot;
+    bool values;    // the next slot takes the values of the tile whose keys went before
+    bool any;       // there is such a tile, and it has tokens of this warp
+    unsigned bad;   // bit i: the tile looked up i tiles before the last one needs a page outside the cache
+    int64_t off;    // this lane's token's place in the cache, in elements; -1: not copied
 
-    __device__ __forceinline__ void start(const Walk<R::kRound> &k, unsigned char *at)
+    __device__ __forceinline__ void start(const Walk<TOK> &k, unsigned char *at)
     {
         walk = k;
         ring = smem_addr(at);
-        stage = 0;
+        slot = 0;
+        values = false;
         bad = 0;
-        known = -1;
     }
-    __device__ __forceinline__ int entry(const DecodeWork &w, int64_t page) const
+    __device__ __forceinline__ void look(const DecodeWork &w, int warp, int lane)
     {
-        return page < w.p.table_cols ? w.p.table[walk.b * w.p.table_stride + page] : -1;
-    }
-    // Makes `page` and the one after it part of what the lanes hold.
-    __device__ __forceinline__ void hold(const DecodeWork &w, int page, int lane)
-    {
-        if (known != walk.b || page < first || page >= first + 63) {
-            known = walk.b;
-            first = page;
-            now = entry(w, (int64_t)first + lane);
-            later = entry(w, (int64_t)first + 32 + lane);
-        } else if (page >= first + 32) {
-            first += 32;
-            now = later;
-            later = entry(w, (int64_t)first + 32 + lane);
-        }
-    }
-    __device__ __forceinline__ int held(int page) const
-    {
-        const int i = page - first;
-        const int x = __shfl_sync(~0u, now, i & 31), y = __shfl_sync(~0u, later, i & 31);
-        return i < 32 ? x : y;
-    }
-    __device__ __forceinline__ int64_t page_offset(const DecodeWork &w, int e) const
-    {
+        any = false;
+        bad <<= 1;
+        while (!walk.done(w) && walk.round >= walk.end) walk.next_pair(w);  // pairs without rounds in this share
+        if (walk.done(w)) return;
+        const int i0 = walk.round * R::kRound + warp * TOK, token = lane % TOK;
+        ++walk.round;
+        any = i0 < walk.s.n;
+        if (!any) return;
+        const bool live = i0 + token < walk.s.n;
+        const unsigned t = (unsigned)(walk.s.first + i0 + token), page = quotient(t, w.page);
+        const int e = live ? w.p.table[walk.b * w.p.table_stride + page] : 0;
+        const bool ok = e >= 0 && e < w.p.num_pages;
+        if (live && !ok) flag_bad_index(w.p.status);
+        bad |= __any_sync(~0u, live && !ok) ? 1u : 0u;
         const int hk = w.blocks == 1 ? walk.pair : walk.pair / w.blocks;
-        return e * w.p.page_stride + hk * w.p.head_stride;
+        off = live && ok ? e * w.p.page_stride + hk * w.p.head_stride +
+                               (int)(t - page * (unsigned)w.p.page_size) * w.p.token_stride
+                         : -1;
     }
-    __device__ __forceinline__ void note(const DecodeWork &w, bool out)
-    {
-        if (out) flag_bad_index(w.p.status);
-        bad = (bad & ~(1u << stage)) | ((__any_sync(~0u, out) ? 1u : 0u) << stage);
-    }
-    // One piece of a row of keys and of values, or zeros.
-    __device__ __forceinline__ void piece(const DecodeWork &w, uint32_t to, int64_t off, int row, int col, bool live)
-    {
-        live &= col * 16 < w.p.head_dim * (int)sizeof(T);
-        const int bytes = live ? 16 : 0;
-        const int64_t from = live ? off * (int64_t)sizeof(T) + col * 16 : 0;
-        const uint32_t dst = to + row * R::kRow + col * 16;
-        copy16(dst, (const char *)w.p.k + from, bytes);
-        copy16(dst + R::kTile, (const char *)w.p.v + from, bytes);
-    }
-    // Starts the copies of the next tile; a commit group a call, empty past the end.
     __device__ __forceinline__ void issue(const DecodeWork &w, int warp, int lane)
     {
-        while (!walk.done(w) && walk.round >= walk.end) walk.next_pair(w);  // pairs without rounds in this share
-        if (!walk.done(w)) {
-            const int i0 = walk.round * R::kRound + warp * TOK;
-            const int count = min(walk.s.n - i0, TOK);
-            const unsigned t0 = (unsigned)(walk.s.first + i0);
-            const uint32_t to = ring + stage * R::kStage;
-            ++walk.round;
-            if (count > 0 && w.p.page_size >= TOK) {
-                const int page = (int)quotient(t0, w.page);
-                const int row0 = (int)(t0 - (unsigned)page * (unsigned)w.p.page_size);
-                const int split = w.p.page_size - row0;  // rows of the tile that lie in `page`
-                hold(w, page, lane);
-                const int e0 = held(page), e1 = held(page + 1);
-                const bool ok0 = e0 >= 0 && e0 < w.p.num_pages, ok1 = e1 >= 0 && e1 < w.p.num_pages;
-                note(w, !ok0 || (split < count && !ok1));
-                const int have = !ok0 ? 0 : split < count && !ok1 ? split : count;
-                // element offsets of tile rows 0 .. split - 1, and of those from split on
-                const int64_t off0 = page_offset(w, e0) + row0 * w.p.token_stride;
-                const int64_t off1 = page_offset(w, e1) - split * w.p.token_stride;
+        if (!values) look(w, warp, lane);
+        if (any) {
+            const char *from = (const char *)(values ? w.p.v : w.p.k);
+            const uint32_t to = ring + slot * R::kSlot;
+            const int valid = w.p.head_dim * (int)sizeof(T) / 16;
+            // all rows' places first: the exchanges keep their order, and copies between them would wait for each
+            int64_t o[kTimes];
 #pragma unroll
-                for (int i = 0; i < kTimes; ++i) {
-                    const int row = kWide ? i * 32 / R::kVecs : i * kRows + lane / R::kVecs;
-                    const int col = kWide ? i * 32 % R::kVecs + lane : lane % R::kVecs;
-                    piece(w, to, (row < split ? off0 : off1) + row * w.p.token_stride, row, col, row < have);
-                }
-            } else if (count > 0) {
-                const unsigned t = t0 + lane % TOK, page = quotient(t, w.page);
-                const bool live = lane % TOK < count;
-                const int e = live ? w.p.table[walk.b * w.p.table_stride + page] : 0;
-                const bool ok = e >= 0 && e < w.p.num_pages;
-                note(w, live && !ok);
-                const int64_t off =
-                    live && ok ? page_offset(w, e) + (int)(t - page * (unsigned)w.p.page_size) * w.p.token_stride : -1;
-                int64_t o[kTimes];
+            for (int i = 0; i < kTimes; ++i) o[i] = __shfl_sync(~0u, off, (i * 32 + lane) / R::kVecs);
 #pragma unroll
-                for (int i = 0; i < kTimes; ++i) o[i] = __shfl_sync(~0u, off, (i * 32 + lane) / R::kVecs);
-#pragma unroll
-                for (int i = 0; i < kTimes; ++i) {
-                    const int vec = i * 32 + lane;
-                    piece(w, to, o[i], vec / R::kVecs, vec % R::kVecs, o[i] >= 0);
-                }
+            for (int i = 0; i < kTimes; ++i) {
+                const int row = (i * 32 + lane) / R::kVecs, vec = (i * 32 + lane) % R::kVecs;
+                const int bytes = o[i] >= 0 && vec < valid ? 16 : 0;
+                copy16(to + piece_at<TOK>(row, vec), from + (bytes ? o[i] * (int64_t)sizeof(T) + vec * 16 : 0), bytes);
             }
         }
         copy_commit();
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        values = !values;
+        slot = slot + 1 == SLOTS ? 0 : slot + 1;
+    }
+    // Whether the tile whose keys have just been waited for needs a page outside the cache.
+    __device__ __forceinline__ bool bad_tile() const { return bad >> ((SLOTS + 1) / 2 - 1) & 1; }
+    // Waits for the oldest slot that has not been waited for, and starts the next copy.
+    __device__ __forceinline__ void turn(const DecodeWork &w, int warp, int lane)
+    {
+        copy_wait<SLOTS - 2>();
+        __syncwarp();
+        issue(w, warp, lane);
     }
 };
 
 // The main kernel's skeleton. Tile computes one warp's triple:
-//   Tile::kHeads, kTok, kDP, T; load_q / reset / step / leave (see the users).
-template <typename Tile, int STAGES>
+//   Tile::kHeads, kTok, kDP, T; load_q / reset / scores / values / leave (see the users).
+template <typename Tile, int SLOTS>
 struct DecodeKernel {
     using T = typename Tile::T;
     static constexpr int DP = Tile::kDP, TOK = Tile::kTok, HB = Tile::kHeads;
-    using R = Ring<T, DP, TOK, STAGES>;
-    using Loader = detfold_attn::Loader<T, DP, TOK, STAGES>;
-    static constexpr int kPitch = DP + 4;  // floats a head: the lanes that store together hit different banks
+    using R = Ring<T, DP, TOK, SLOTS>;
+    using Loader = detfold_attn::Loader<T, DP, TOK, SLOTS>;
+    // Floats a head of an accumulator that a warp leaves: lanes that store together hit different
+    // banks, where a slot has room for that.
+    static constexpr int kPitch = HB * (DP + 4) * 4 <= R::kSlot ? DP + 4 : DP;
     // The fold: kTeam threads a head, each kFours groups of four dimensions.
     static constexpr int kTeam = kThreads / HB < DP / 4 ? kThreads / HB : DP / 4, kFours = DP / 4 / kTeam;
     struct Shared {
@@ -531,9 +497,9 @@ struct DecodeKernel {
         typename Tile::Shared tile;
     };
     static_assert(HB * kTeam <= kThreads && DP % (4 * kTeam) == 0, "every thread folds the same number of elements");
-    // A warp leaves its accumulator in the stage that it has just used up: the next
+    // A warp leaves its accumulator in the slot that it has just used up: the next
     // copy into it starts after the fold.
-    static_assert(HB * kPitch * 4 <= R::kStage, "the accumulator fits a stage");
+    static_assert(HB * kPitch * 4 <= R::kSlot, "the accumulator fits a slot");
 
     // A chunk's triple, of this thread's head and dimensions, from the warps' triples.
     static __device__ __forceinline__ void join_warps(const Shared &sh, int used, int h, int d0, float &top, float &l,
@@ -556,7 +522,7 @@ struct DecodeKernel {
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
                 const float4 x = *reinterpret_cast<const float4 *>(
-                    reinterpret_cast<const float *>(sh.ring[k] + used * R::kStage) + h * kPitch + d0 + i * kTeam * 4);
+                    reinterpret_cast<const float *>(sh.ring[k] + used * R::kSlot) + h * kPitch + d0 + i * kTeam * 4);
                 a[i].x = __fmaf_rn(x.x, f[k], a[i].x);
                 a[i].y = __fmaf_rn(x.y, f[k], a[i].y);
                 a[i].z = __fmaf_rn(x.z, f[k], a[i].z);
@@ -578,7 +544,7 @@ struct DecodeKernel {
 
     __device__ static void run(const DecodeWork &w)
     {
-        extern __shared__ unsigned char raw[];
+        extern __shared__ __align__(128) unsigned char raw[];
         Shared &sh = *reinterpret_cast<Shared *>(raw);
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         // this thread's head in the fold (the last one again where there are threads to spare) and first dimension
@@ -586,10 +552,10 @@ struct DecodeKernel {
         const int h = folds ? threadIdx.x / kTeam : HB - 1, d0 = threadIdx.x % kTeam * 4;
         enter_grid();
         Shares shares;
-        Walk<R::kRound> walk = begin_walk<R::kRound>(w, shares);
+        Walk<TOK> walk = begin_walk<TOK>(w, shares);
         Loader load;
         load.start(walk, sh.ring[warp]);
-        int stage = 0;
+        int slot_now = 0;
         int4 header = make_int4(0, 0, 0, 0);
         bool started = false;
         Tile tile;
@@ -606,7 +572,7 @@ struct DecodeKernel {
                 // the first copies, after the first queries are asked for
                 started = true;
 #pragma unroll 1
-                for (int i = 0; i < STAGES - 1; ++i) load.issue(w, warp, lane);
+                for (int i = 0; i < SLOTS - 1; ++i) load.issue(w, warp, lane);
             }
             tile.reset();
             float rm = neg_inf(), rl = 0.0f;
@@ -616,15 +582,15 @@ struct DecodeKernel {
             bool bad = false;
             int chunk = walk.round / walk.s.per, left = walk.s.per;
             for (int g = walk.round; g < walk.end; ++g) {
-                const int count = walk.s.n - (g * R::kRound + warp * TOK);  // tokens of this tile
-                unsigned char *at = sh.ring[warp] + stage * R::kStage;
-                copy_wait<STAGES - 2>();
-                __syncwarp();
-                bad |= load.bad >> stage & 1;
-                load.issue(w, warp, lane);
-                if (count > 0) tile.step(w, sh.tile, at, at + R::kTile, count, warp, lane);
-                const int used = stage;
-                stage = stage + 1 == STAGES ? 0 : stage + 1;
+                const int count = min(walk.s.n - (g * R::kRound + warp * TOK), TOK);  // tokens of this tile
+                const int used = slot_now + 1 == SLOTS ? 0 : slot_now + 1;
+                load.turn(w, warp, lane);
+                bad |= load.bad_tile();
+                if (count > 0) tile.scores(w, sh.tile, sh.ring[warp] + slot_now * R::kSlot, count, warp, lane);
+                load.turn(w, warp, lane);
+                unsigned char *at = sh.ring[warp] + used * R::kSlot;
+                if (count > 0) tile.values(sh.tile, at, warp, lane);
+                slot_now = used + 1 == SLOTS ? 0 : used + 1;
                 if (--left && g + 1 < walk.end) continue;
                 // the chunk's end: the warps' triples, joined in warp order
                 __syncwarp();
@@ -680,7 +646,7 @@ struct DecodeKernel {
     // same chunks, the same folds, the same bits.
     __device__ static void run_few(const DecodeWork &w)
     {
-        extern __shared__ unsigned char raw[];
+        extern __shared__ __align__(128) unsigned char raw[];
         Shared &sh = *reinterpret_cast<Shared *>(raw);
         float4 *part = reinterpret_cast<float4 *>(raw + sizeof(Shared));     // [chunks][own]
         float2 *pairs = reinterpret_cast<float2 *>(part + w.chunks * w.own);  // [chunks][heads] (m, l)
@@ -690,10 +656,10 @@ struct DecodeKernel {
         const int rank = blockIdx.x, ranks = gridDim.x, fours = w.p.head_dim / 4;
         if (ranks > 1) cluster_arrive();  // peers have to run before anything is pushed to them
         enter_grid();
-        Walk<R::kRound> walk;
+        Walk<TOK> walk;
         walk.b = blockIdx.z;
         walk.pair = blockIdx.y;
-        walk.s = sequence<R::kRound>(w, walk.b);
+        walk.s = sequence<TOK>(w, walk.b);
         walk.at = walk.lo = 0;
         walk.hi = 1;
         const int chunks = walk.chunks();
@@ -717,11 +683,11 @@ struct DecodeKernel {
         if (g < rounds) {
             tile.load_q(w, sh.tile, b, head0, heads, warp, lane);
 #pragma unroll 1
-            for (int i = 0; i < STAGES - 1; ++i) load.issue(w, warp, lane);
+            for (int i = 0; i < SLOTS - 1; ++i) load.issue(w, warp, lane);
             tile.reset();
         }
         if (ranks > 1) cluster_wait();
-        int stage = 0, chunk = c0, left = per;
+        int slot_now = 0, chunk = c0, left = per;
         bool bad = false;
         const auto push = [&](int c, float m, float l, const float4 (&a)[kFours]) {
             if (!folds || h >= heads) return;
@@ -738,15 +704,15 @@ struct DecodeKernel {
             }
         };
         for (; g < rounds; ++g) {
-            const int count = n - (g * R::kRound + warp * TOK);
-            unsigned char *at = sh.ring[warp] + stage * R::kStage;
-            copy_wait<STAGES - 2>();
-            __syncwarp();
-            bad |= load.bad >> stage & 1;
-            load.issue(w, warp, lane);
-            if (count > 0) tile.step(w, sh.tile, at, at + R::kTile, count, warp, lane);
-            const int used = stage;
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            const int count = min(n - (g * R::kRound + warp * TOK), TOK);  // tokens of this tile
+            const int used = slot_now + 1 == SLOTS ? 0 : slot_now + 1;
+            load.turn(w, warp, lane);
+            bad |= load.bad_tile();
+            if (count > 0) tile.scores(w, sh.tile, sh.ring[warp] + slot_now * R::kSlot, count, warp, lane);
+            load.turn(w, warp, lane);
+            unsigned char *at = sh.ring[warp] + used * R::kSlot;
+            if (count > 0) tile.values(sh.tile, at, warp, lane);
+            slot_now = used + 1 == SLOTS ? 0 : used + 1;
             if (--left && g + 1 < rounds) continue;
             __syncwarp();
             tile.leave(reinterpret_cast<float *>(at), kPitch, sh.m[warp], sh.l[warp], bad, lane);

@@ -11,12 +11,12 @@ cudaError_t launch_16bit(const DecodeWork &w, const DecodeGrid &g, cudaStream_t 
 {
     const bool wide = g.heads > 8;
     if (w.p.head_dim <= 64)
-        return wide ? launch_tile<MmaTile<T, 64, 16, 2>, 5>(w, g, stream)
-                    : launch_tile<MmaTile<T, 64, 16, 1>, 5>(w, g, stream);
+        return wide ? launch_tile<MmaTile<T, 64, 32, 2>, 6>(w, g, stream)
+                    : launch_tile<MmaTile<T, 64, 32, 1>, 6>(w, g, stream);
     if (w.p.head_dim <= 128)
-        return wide ? launch_tile<MmaTile<T, 128, 16, 2>, 3>(w, g, stream)
-                    : launch_tile<MmaTile<T, 128, 16, 1>, 3>(w, g, stream);
-    return launch_tile<MmaTile<T, 256, 8, 1>, 3>(w, g, stream);
+        return wide ? launch_tile<MmaTile<T, 128, 32, 2>, 3>(w, g, stream)
+                    : launch_tile<MmaTile<T, 128, 32, 1>, 3>(w, g, stream);
+    return launch_tile<MmaTile<T, 256, 16, 1>, 3>(w, g, stream);
 }
 
 }  // namespace detfold_attn

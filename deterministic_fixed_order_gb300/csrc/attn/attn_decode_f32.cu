@@ -8,9 +8,9 @@ namespace {
 template <int HB>
 cudaError_t launch_heads(const DecodeWork &w, const DecodeGrid &g, cudaStream_t stream)
 {
-    if (w.p.head_dim <= 64) return launch_tile<F32Tile<64, 16, HB>, 3>(w, g, stream);
-    if (w.p.head_dim <= 128) return launch_tile<F32Tile<128, 8, HB>, 3>(w, g, stream);
-    return launch_tile<F32Tile<256, 4, HB>, 3>(w, g, stream);
+    if (w.p.head_dim <= 64) return launch_tile<F32Tile<64, 32, HB>, 3>(w, g, stream);
+    if (w.p.head_dim <= 128) return launch_tile<F32Tile<128, 16, HB>, 3>(w, g, stream);
+    return launch_tile<F32Tile<256, 8, HB>, 3>(w, g, stream);
 }
 
 }  // namespace

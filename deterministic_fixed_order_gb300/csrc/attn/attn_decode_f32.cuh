@@ -14,7 +14,7 @@ namespace detfold_attn {
 template <int DP, int TOK, int HB>
 struct F32Tile {
     using T = float;
-    static constexpr int kDP = DP, kTok = TOK, kHeads = HB, kRow = DP * 4 + 16;
+    static constexpr int kDP = DP, kTok = TOK, kHeads = HB;
     static constexpr int kParts = 32 / TOK;  // lanes that share a token's score
     static constexpr int kOwn = DP / 32;     // dimensions a lane holds of the output
     static constexpr int kVec = kOwn >= 4 ? 4 : kOwn;
@@ -55,18 +55,18 @@ struct F32Tile {
     // The dimension of a lane's i-th output element.
     static __device__ __forceinline__ int dim(int lane, int i) { return (i / kVec) * 32 * kVec + lane * kVec + i % kVec; }
 
-    __device__ __forceinline__ void step(const DecodeWork &w, Shared &sh, const unsigned char *kt,
-                                         const unsigned char *vt, int count, int warp, int lane)
+    // The weights of a tile of `count` tokens (TOK or fewer), and what they do to the triple.
+    __device__ __forceinline__ void scores(const DecodeWork &w, Shared &sh, const unsigned char *keys, int count,
+                                           int warp, int lane)
     {
         const int token = lane % TOK, part = lane / TOK;
         float2 sum[HB];
 #pragma unroll
         for (int h = 0; h < HB; ++h) sum[h] = make_float2(0.0f, 0.0f);
-        const float4 *kr = reinterpret_cast<const float4 *>(kt + token * kRow);
         const int fours = w.p.head_dim / 4;
 #pragma unroll 4
         for (int i = part; i < fours; i += kParts) {
-            const float4 k = kr[i];
+            const float4 k = *reinterpret_cast<const float4 *>(keys + piece_at<TOK>(token, i));
 #pragma unroll
             for (int h = 0; h < HB; ++h) {
                 const float4 q = reinterpret_cast<const float4 *>(sh.q[h])[i];
@@ -103,6 +103,7 @@ struct F32Tile {
             }
         }
         __syncwarp();
+        // where no maximum moved every factor is 1
         if (__any_sync(~0u, moved)) {
 #pragma unroll
             for (int h = 0; h < HB; ++h) {
@@ -111,7 +112,11 @@ struct F32Tile {
                 for (int i = 0; i < kOwn / 2; ++i) o[h][i] = mul2(o[h][i], make_float2(f, f));
             }
         }
-        const float *v0 = reinterpret_cast<const float *>(vt);
+    }
+
+    // Adds the tile's weighted values.
+    __device__ __forceinline__ void values(Shared &sh, const unsigned char *from, int warp, int lane)
+    {
 #pragma unroll 4
         for (int t = 0; t < TOK; ++t) {
             float p[HB];
@@ -126,7 +131,7 @@ struct F32Tile {
             float2 v[kOwn / 2];
 #pragma unroll
             for (int i = 0; i < kOwn; i += kVec) {
-                const float *at = v0 + t * (kRow / 4) + dim(lane, i);
+                const unsigned char *at = from + piece_at<TOK>(t, dim(lane, i) / 4) + dim(lane, i) % 4 * 4;
                 if constexpr (kVec == 4)
                     *reinterpret_cast<float4 *>(v + i / 2) = *reinterpret_cast<const float4 *>(at);
                 else

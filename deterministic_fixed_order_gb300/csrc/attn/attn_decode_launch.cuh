@@ -7,16 +7,16 @@
 
 namespace detfold_attn {
 
-template <typename Tile, int STAGES>
+template <typename Tile, int SLOTS>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ DecodeWork w)
 {
-    DecodeKernel<Tile, STAGES>::run(w);
+    DecodeKernel<Tile, SLOTS>::run(w);
 }
 
-template <typename Tile, int STAGES>
+template <typename Tile, int SLOTS>
 __global__ void __launch_bounds__(kThreads, 2) decode_few_kernel(const __grid_constant__ DecodeWork w)
 {
-    DecodeKernel<Tile, STAGES>::run_few(w);
+    DecodeKernel<Tile, SLOTS>::run_few(w);
 }
 
 template <typename T>
@@ -42,10 +42,10 @@ inline cudaError_t allow_shared(const void *kernel, size_t bytes, std::atomic<ui
 }
 
 // The cluster launch of a few sequences.
-template <typename Tile, int STAGES>
+template <typename Tile, int SLOTS>
 cudaError_t launch_few(const DecodeWork &w, const DecodeGrid &g, size_t bytes, cudaStream_t stream)
 {
-    const auto kernel = decode_few_kernel<Tile, STAGES>;
+    const auto kernel = decode_few_kernel<Tile, SLOTS>;
     static std::atomic<uint64_t> done{0}, wide{0};
     if (cudaError_t e = allow_shared((const void *)kernel, 227 * 1024, done)) return e;
     if (g.ranks > 8)
@@ -66,19 +66,19 @@ cudaError_t launch_few(const DecodeWork &w, const DecodeGrid &g, size_t bytes, c
     return cudaLaunchKernelEx(&cfg, kernel, w);
 }
 
-template <typename Tile, int STAGES>
+template <typename Tile, int SLOTS>
 cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t stream)
 {
-    using K = DecodeKernel<Tile, STAGES>;
-    using Few = DecodeKernel<Tile, 2>;
+    using K = DecodeKernel<Tile, SLOTS>;
+    using Few = DecodeKernel<Tile, SLOTS>;
     static_assert(sizeof(typename K::Shared) <= 113 * 1024, "two CTAs an SM");
     static_assert(K::R::kRound == tile_of(sizeof(typename K::T), K::DP).round, "as the grid is sized");
     const size_t few = sizeof(typename Few::Shared) + (size_t)w.chunks * (w.own * 16 + g.heads * 8);
-    if (g.ranks && few <= 227 * 1024) return launch_few<Tile, 2>(w, g, few, stream);
+    if (g.ranks && few <= 227 * 1024) return launch_few<Tile, SLOTS>(w, g, few, stream);
     static std::atomic<uint64_t> done{0};
     const size_t bytes = sizeof(typename K::Shared);
-    if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, STAGES>, bytes, done)) return e;
-    if (cudaError_t e = launch_early(decode_kernel<Tile, STAGES>, dim3(g.ctas), kThreads, bytes, stream, w)) return e;
+    if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, SLOTS>, bytes, done)) return e;
+    if (cudaError_t e = launch_early(decode_kernel<Tile, SLOTS>, dim3(g.ctas), kThreads, bytes, stream, w)) return e;
     if (g.slots)
         return launch_early(decode_join_kernel<typename Tile::T>, dim3(g.slots, g.heads), kThreads, 0, stream, w);
     return cudaSuccess;

@@ -1,7 +1,8 @@
 // One warp's share of the attention in 16-bit types, on the matrix units.
 //
-// Scores: S^T = K Q^T, 16 (or 8, the other half zeros) tokens by 8 query heads a product,
-// so that a group of up to eight heads costs what one does. P stays in registers: S^T's layout,
+// Scores: S^T = K Q^T, 16 tokens by 8 query heads a product, so that a group of up to eight
+// heads costs what one does; a tile of 32 tokens is two of them side by side, whose chains of
+// dependent instructions overlap. P stays in registers: S^T's layout,
 // packed to 16 bits and transposed 8x8 by movmatrix, is the second product's
 // right operand, O^T = V^T P^T (V^T by transposing loads). P is split in two
 // 16-bit parts, p = hi + lo, both multiplied: one part alone would round each
@@ -50,20 +51,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// c += a b, 16x8x8.
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0, __nv_bfloat16)
-{
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b0));
-}
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0, __half)
-{
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b0));
-}
-
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(T x, T y)
 {
@@ -85,8 +72,8 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 template <typename T_, int DP, int TOK, int NT>
 struct MmaTile {
     using T = T_;
-    static constexpr int kDP = DP, kTok = TOK, kHeads = 8 * NT, kRow = DP * 2 + 16;
-    static constexpr int kHalves = TOK / 8;  // eights of tokens a tile
+    static constexpr int kDP = DP, kTok = TOK, kHeads = 8 * NT;
+    static constexpr int kSub = TOK / 16;
     struct Shared {
         int unused;
     };
@@ -94,6 +81,7 @@ struct MmaTile {
     uint32_t q[DP / 16][NT][2];  // Q^T: dims 16 ks + 2t (+1) and + 8, head 8 nt + g
     float o[DP / 16][NT][4];     // O^T: dims 16 mt + g, + 8; heads 8 nt + 2t, + 1
     float m[NT][2], l[NT][2];    // of heads 2t, 2t + 1; l of this lane's tokens only
+    uint32_t hi[kSub][NT][2], lo[kSub][NT][2];  // the tile's weights, tokens 8 half + 2t (+1), head g
 
     __device__ __forceinline__ void load_q(const DecodeWork &w, Shared &, int b, int head0, int heads, int, int lane)
     {
@@ -141,53 +129,53 @@ struct MmaTile {
         }
     }
 
-    // One tile of `count` tokens (TOK or fewer; the rest of the tile is zeros).
-    __device__ __forceinline__ void step(const DecodeWork &w, Shared &, const unsigned char *kt,
-                                         const unsigned char *vt, int count, int, int lane)
+    // The weights of a tile of `count` tokens (TOK or fewer), and what they do to the triple.
+    __device__ __forceinline__ void scores(const DecodeWork &w, Shared &, const unsigned char *keys, int count, int,
+                                           int lane)
     {
         const float scale = w.p.scale;
         const int g = lane / 4;
+        const uint32_t at = smem_addr(keys);
         // two sums a score, joined at the end: half the length of the chain of products
-        float s[NT][4], s2[NT][4];
+        float s[kSub][NT][4], s2[kSub][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[nt][j] = s2[nt][j] = 0.0f;
-        // four 8x8 blocks a load: of 16 tokens and 16 dimensions, or of 8 and 32. A batch of loads
-        // goes ahead of its products, since the loads keep their order among themselves.
-        constexpr int kSteps = DP / 16, kPerLoad = 2 / kHalves, kLoads = kSteps / kPerLoad;
-        constexpr int kBatch = kLoads < 8 ? kLoads : 8;
-        const uint32_t ka = smem_addr(kt) + (TOK == 16 ? (lane % 16) * kRow + (lane / 16) * 16
-                                                       : (lane % 8) * kRow + (lane / 8) * 16);
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k0 = 0; k0 < kLoads; k0 += kBatch) {
-            uint32_t a[kBatch][4];
+                for (int j = 0; j < 4; ++j) s[u][nt][j] = s2[u][nt][j] = 0.0f;
+        // a batch of loads goes ahead of its products, since the loads keep their order among themselves
+        constexpr int kBatch = 4;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) ldmatrix4(a[i], ka + (k0 + i) * 32 * kPerLoad);
+        for (int k0 = 0; k0 < DP / 16; k0 += kBatch) {
+            uint32_t a[kSub][kBatch][4];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-                for (int j = 0; j < kPerLoad; ++j) {
-                    const int ks = (k0 + i) * kPerLoad + j;
-                    const uint32_t f[4] = {TOK == 16 ? a[i][0] : a[i][2 * j], TOK == 16 ? a[i][1] : 0,
-                                           TOK == 16 ? a[i][2] : a[i][2 * j + 1], TOK == 16 ? a[i][3] : 0};
+                for (int u = 0; u < kSub; ++u)
+                    ldmatrix4(a[u][i], at + piece_at<TOK>(u * 16 + lane % 16, (k0 + i) * 2 + lane / 16));
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma(ks % 2 ? s2[nt] : s[nt], f, q[ks][nt][0], q[ks][nt][1], T());
-                }
+                        mma(i % 2 ? s2[u][nt] : s[u][nt], a[u][i], q[k0 + i][nt][0], q[k0 + i][nt][1], T());
         }
-        uint32_t hi[NT][kHalves], lo[NT][kHalves];
         bool moved = false;
         float fade[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float top[2] = {neg_inf(), neg_inf()}, p[2 * kHalves];
+            float top[2] = {neg_inf(), neg_inf()};
 #pragma unroll
-            for (int j = 0; j < 2 * kHalves; ++j) {
-                s[nt][j] = __fmul_rn(__fadd_rn(s[nt][j], s2[nt][j]), scale);
-                if (g + (j / 2) * 8 >= count) s[nt][j] = neg_inf();
-                top[j % 2] = fmaxf(top[j % 2], s[nt][j]);
-            }
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float &x = s[u][nt][j];
+                    x = __fmul_rn(__fadd_rn(x, s2[u][nt][j]), scale);
+                    if (u * 16 + g + (j / 2) * 8 >= count) x = neg_inf();
+                    top[j % 2] = fmaxf(top[j % 2], x);
+                }
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
                 const float y0 = __shfl_xor_sync(~0u, top[0], x), y1 = __shfl_xor_sync(~0u, top[1], x);
@@ -203,20 +191,26 @@ struct MmaTile {
                 m[nt][j] = top[j];
                 float sum = 0.0f;
 #pragma unroll
-                for (int half = 0; half < kHalves; ++half) {
-                    p[half * 2 + j] = exp_neg(s[nt][half * 2 + j] - base);
-                    sum = half ? __fadd_rn(sum, p[half * 2 + j]) : p[half * 2 + j];
+                for (int u = 0; u < kSub; ++u) {
+                    s[u][nt][j] = exp_neg(s[u][nt][j] - base);
+                    s[u][nt][j + 2] = exp_neg(s[u][nt][j + 2] - base);
+                    const float two = __fadd_rn(s[u][nt][j], s[u][nt][j + 2]);
+                    sum = u ? __fadd_rn(sum, two) : two;
                 }
                 l[nt][j] = __fmaf_rn(l[nt][j], fade[nt][j], sum);
             }
 #pragma unroll
-            for (int half = 0; half < kHalves; ++half)
-                split2<T>(p[half * 2], p[half * 2 + 1], hi[nt][half], lo[nt][half]);
+            for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int half = 0; half < kHalves; ++half) {
-                hi[nt][half] = transpose8(hi[nt][half]);
-                lo[nt][half] = transpose8(lo[nt][half]);
-            }
+                for (int half = 0; half < 2; ++half)
+                    split2<T>(s[u][nt][half * 2], s[u][nt][half * 2 + 1], hi[u][nt][half], lo[u][nt][half]);
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    hi[u][nt][half] = transpose8(hi[u][nt][half]);
+                    lo[u][nt][half] = transpose8(lo[u][nt][half]);
+                }
         }
         // where no maximum moved every factor is 1
         if (__any_sync(~0u, moved)) {
@@ -227,30 +221,31 @@ struct MmaTile {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[mt][nt][j] = __fmul_rn(o[mt][nt][j], fade[nt][j % 2]);
         }
-        const uint32_t va = smem_addr(vt) + (TOK == 16 ? ((lane / 16) * 8 + lane % 8) * kRow + ((lane / 8) % 2) * 16
-                                                       : (lane % 8) * kRow + (lane / 8) * 16);
+    }
+
+    // Adds the tile's weighted values.
+    __device__ __forceinline__ void values(Shared &, const unsigned char *from, int, int lane)
+    {
+        const uint32_t at = smem_addr(from);
+        constexpr int kBatch = 4;
 #pragma unroll
-        for (int m0 = 0; m0 < kLoads; m0 += kBatch) {
-            uint32_t a[kBatch][4];
+        for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) ldmatrix4_trans(a[i], va + (m0 + i) * 32 * kPerLoad);
+            for (int m0 = 0; m0 < DP / 16; m0 += kBatch) {
+                uint32_t a[kBatch][4];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
+                for (int i = 0; i < kBatch; ++i)
+                    ldmatrix4_trans(a[i], at + piece_at<TOK>(u * 16 + (lane / 16) * 8 + lane % 8,
+                                                            (m0 + i) * 2 + lane / 8 % 2));
 #pragma unroll
-                for (int j = 0; j < kPerLoad; ++j) {
-                    const int mt = (m0 + i) * kPerLoad + j;
+                for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (TOK == 16) {
-                            mma(o[mt][nt], a[i], hi[nt][0], hi[nt][1], T());
-                            mma(o[mt][nt], a[i], lo[nt][0], lo[nt][1], T());
-                        } else {
-                            mma8(o[mt][nt], a[i][2 * j], a[i][2 * j + 1], hi[nt][0], T());
-                            mma8(o[mt][nt], a[i][2 * j], a[i][2 * j + 1], lo[nt][0], T());
-                        }
-                    }
-                }
-        }
+                    for (int nt = 0; nt < NT; ++nt) mma(o[m0 + i][nt], a[i], hi[u][nt][0], hi[u][nt][1], T());
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma(o[m0 + i][nt], a[i], lo[u][nt][0], lo[u][nt][1], T());
+            }
     }
 
     // Leaves the triple in shared memory; a `bad` chunk's sums are NaN.
