@@ -30,12 +30,11 @@ cudaError_t launch_decode(const DecodeParams &p, int dtype, void *workspace, cud
     DecodeWork w = {};
     w.p = p;
     w.pairs = g.pairs, w.blocks = g.pairs / p.kv_heads, w.heads = g.heads;
-    w.slots = g.slots, w.most_chunks = max_chunks(g.pairs);
+    w.slots = g.slots, w.by_pair = g.by_pair, w.most_chunks = max_chunks(g.pairs);
     w.most = divide_by(w.most_chunks), w.grid = divide_by(g.ctas);
-    w.chunks = g.chunks > 0 ? g.chunks : 1, w.own = 1;
-    for (int r = g.ranks; r > 1; r /= 2) ++w.ranks_log2;
-    if (g.ranks) w.own = (g.heads * p.head_dim / 4 + g.ranks - 1) / g.ranks;
-    w.by_own = divide_by(w.own);
+    w.direct = g.direct;
+    if (g.direct) w.by_chunks = divide_by(g.direct);
+    w.by_pairs = divide_by(g.pairs);
     w.short_line = (double)p.batch * g.pairs * (p.window / 32 + 2) < (1 << 30);
     w.pair_floats = g.pair_floats, w.slot_floats = g.slot_floats;
     w.page = divide_by(p.page_size);

@@ -72,36 +72,22 @@ constexpr TileShape tile_of(int element_bytes, int head_dim)
 
 struct DecodeGrid {
     int ctas;    // CTAs of the main kernel
-    int slots;   // workspace slots (one a CTA), 0: no sequence can be split
+    int slots;   // workspace slots, 0: no sequence can be split
+    bool by_pair;  // a slot a pair, else a slot a CTA for the pair that its share breaks off in
     int chunks;  // most chunks of a sequence
     int pairs;   // pairs a sequence
     int heads;   // query heads a pair, at most
     int64_t pair_floats, slot_floats;  // floats of a slot's (m, l) pairs; of a slot
-    int ranks;   // CTAs a cluster where the sequences are few, else 0
+    int direct;  // a CTA a chunk: chunks of a pair, else 0
 };
 
-// A few sequences: clusters of as many CTAs as a pair has chunks, within 16 a cluster and
-// FEW_WAVES an SM, as long as no CTA then has more than FEW_ROUNDS rounds.
-#ifndef FEW_WAVES
-#define FEW_WAVES 1
+// Few chunks in all: a CTA a chunk, for up to DIRECT times as many CTAs as are resident.
+#ifndef DIRECT
+#define DIRECT 3
 #endif
-#ifndef FEW_ROUNDS
-#define FEW_ROUNDS 8
-#endif
-#ifndef MAXRANKS
-#define MAXRANKS 8
-#endif
-constexpr int kMaxRanks = MAXRANKS;
 
-inline int few_ranks(int64_t pairs_in_all, int chunks, int per)
-{
-    int ranks = 1;
-    while (ranks < kMaxRanks && ranks < chunks && pairs_in_all * ranks * 2 <= FEW_WAVES * kSms) ranks *= 2;
-    return pairs_in_all * ranks <= FEW_WAVES * kSms && (chunks + ranks - 1) / ranks * per <= FEW_ROUNDS ? ranks : 0;
-}
-
-// Workspace: `ctas` headers of four ints, then a slot a CTA: for each chunk and
-// head (m, l), then for each chunk and head the accumulator.
+// Workspace: a header of four ints a slot, then the slots: for each chunk and head (m, l),
+// then for each chunk and head the accumulator.
 inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, int64_t max_seen, int heads,
                               int round)
 {
@@ -109,16 +95,19 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     g.heads = heads < group ? heads : group;
     const int blocks = (group + heads - 1) / heads;
     g.pairs = kv_heads * blocks;
-    const int rounds = (int)((max_seen + round - 1) / round), per = chunk_rounds(rounds, max_chunks(g.pairs), round);
-    g.ranks = few_ranks((int64_t)batch * g.pairs, (rounds + per - 1) / per, per);
+    const int rounds = (int)((max_seen + round - 1) / round);
     // shorter sequences may have more chunks than the longest: as many as there can be at all, so
     // that a larger max_seen never needs less
     const int most = max_chunks(g.pairs), least = kMinChunk / round;
     const int up_to = (rounds + least - 1) / least;
     g.chunks = up_to < most ? up_to : most;
-    const int64_t units = (int64_t)batch * g.pairs * (g.chunks > 0 ? g.chunks : 1);
-    g.ctas = units < kMaxCtas ? (int)units : kMaxCtas;
-    g.slots = g.chunks > 1 ? g.ctas : 0;
+    const int each = g.chunks > 0 ? g.chunks : 1;
+    const int64_t pairs = (int64_t)batch * g.pairs, units = pairs * each;
+    g.direct = units <= DIRECT * kMaxCtas ? each : 0;
+    g.ctas = g.direct || units < kMaxCtas ? (int)units : kMaxCtas;
+    // at most one pair begins in a CTA's share and ends beyond it
+    g.by_pair = pairs <= g.ctas;
+    g.slots = g.chunks <= 1 ? 0 : g.by_pair ? (int)pairs : g.ctas;
     g.pair_floats = ((int64_t)g.chunks * g.heads * 2 + 3) / 4 * 4;
     g.slot_floats = g.pair_floats + ((int64_t)g.chunks * g.heads * head_dim + 3) / 4 * 4;
     return g;
@@ -131,14 +120,13 @@ inline int64_t workspace_need(const DecodeGrid &g)
 
 struct DecodeWork {
     DecodeParams p;
-    int pairs, blocks, heads, slots;
+    int pairs, blocks, heads, slots, by_pair;
     int most_chunks;                // max_chunks(pairs)
     Divide most, grid;              // by most_chunks, by the number of CTAs
     int short_line;                 // the shares' line is shorter than 2^30
     Divide page;                    // by the page size
-    // a few sequences only: chunks a pair at most, CTAs a cluster, groups of four dimensions that a CTA folds
-    int chunks, ranks_log2, own;
-    Divide by_own;
+    int direct;                     // a CTA a chunk: the most chunks of a pair, else 0
+    Divide by_chunks, by_pairs;     // by `direct` and by `pairs`
     int out_vec;                    // four elements of out start at a multiple of their size
     int q_vec;                      // two elements of q do
     int64_t pair_floats, slot_floats;
@@ -288,11 +276,23 @@ __device__ __forceinline__ void find_sequence(const DecodeWork &w, Shares &share
     }
 }
 
-// This CTA's share. Every warp does the same: no barrier.
+// This CTA's share, or its chunk of the pair that is its own. Every warp does the same: no barrier.
 template <int TOK>
 __device__ __forceinline__ Walk<TOK> begin_walk(const DecodeWork &w, Shares &shares)
 {
     Walk<TOK> k;
+    if (w.direct) {
+        const unsigned pair = quotient(blockIdx.x, w.by_chunks), c = blockIdx.x - pair * w.direct;
+        k.b = (int)quotient(pair, w.by_pairs);
+        k.pair = (int)(pair - (unsigned)k.b * (unsigned)w.pairs);
+        k.s = sequence<TOK>(w, k.b);
+        k.at = 0;
+        k.lo = c > 0;
+        k.hi = 1;
+        k.round = min((int)c * k.s.per, k.s.rounds);
+        k.end = min(k.round + k.s.per, k.s.rounds);
+        return k;
+    }
     if (w.p.batch == 1) {
         k.b = 0;
         k.at = 0;
@@ -312,26 +312,6 @@ __device__ __forceinline__ Walk<TOK> begin_walk(const DecodeWork &w, Shares &sha
     k.at += k.pair * cost(k.s);
     k.enter();
     return k;
-}
-
-// The cluster's CTAs and their shared memory.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t peer_addr(uint32_t at, int rank)
-{
-    uint32_t there;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
-    return there;
-}
-__device__ __forceinline__ void store_peer(uint32_t at, int rank, float4 v)
-{
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer_addr(at, rank)), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ void store_peer(uint32_t at, int rank, float2 v)
-{
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(at, rank)), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // A running triple of one element and its fold with the next chunk's.
@@ -566,7 +546,11 @@ struct DecodeKernel {
             const int head0 = hk * w.p.group + block * w.heads;
             const int heads = min(w.heads, w.p.group - block * w.heads);
             float *slot = nullptr;
-            if (w.slots) slot = w.slot + (begins ? (int)blockIdx.x : shares.of(w, walk.at)) * w.slot_floats;
+            if (w.slots)
+                slot = w.slot + (w.by_pair ? walk.b * w.pairs + walk.pair
+                                 : begins  ? (int)blockIdx.x
+                                           : shares.of(w, walk.at)) *
+                                    w.slot_floats;
             tile.load_q(w, sh.tile, walk.b, head0, heads, warp, lane);
             if (!started) {
                 // the first copies, after the first queries are asked for
@@ -633,149 +617,13 @@ struct DecodeKernel {
                 }
                 if (!whole && d0 == 0) put_pair(w, slot, chunk - 1, h, rm, rl);
             }
-            if (!whole) header = make_int4(walk.b, walk.pair, chunk - 1, walk.chunks());
+            if (w.slots && (w.by_pair || !whole)) {
+                header = make_int4(walk.b, walk.pair, chunk - 1, whole ? 0 : walk.chunks());
+                if (w.by_pair && threadIdx.x == 0) w.headers[walk.b * w.pairs + walk.pair] = header;
+            }
         }
         copy_wait<0>();
-        if (w.slots && threadIdx.x == 0) w.headers[blockIdx.x] = header;
-    }
-
-    // A few sequences: a cluster of CTAs a pair, each taking its part of the pair's chunks.
-    // No shares and no workspace: the CTAs push their chunks' triples straight into the
-    // shared memory of the CTA that folds the element -- each folds its part of the (head,
-    // dimension) plane -- and one cluster barrier stands where the join kernel would. The
-    // same chunks, the same folds, the same bits.
-    __device__ static void run_few(const DecodeWork &w)
-    {
-        extern __shared__ __align__(128) unsigned char raw[];
-        Shared &sh = *reinterpret_cast<Shared *>(raw);
-        float4 *part = reinterpret_cast<float4 *>(raw + sizeof(Shared));     // [chunks][own]
-        float2 *pairs = reinterpret_cast<float2 *>(part + w.chunks * w.own);  // [chunks][heads] (m, l)
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        const bool folds = threadIdx.x < HB * kTeam;
-        const int h = folds ? threadIdx.x / kTeam : HB - 1, d0 = threadIdx.x % kTeam * 4;
-        const int rank = blockIdx.x, ranks = gridDim.x, fours = w.p.head_dim / 4;
-        if (ranks > 1) cluster_arrive();  // peers have to run before anything is pushed to them
-        enter_grid();
-        Walk<TOK> walk;
-        walk.b = blockIdx.z;
-        walk.pair = blockIdx.y;
-        walk.s = sequence<TOK>(w, walk.b);
-        walk.at = walk.lo = 0;
-        walk.hi = 1;
-        const int chunks = walk.chunks();
-        const int c0 = (rank * chunks + ranks - 1) >> w.ranks_log2, c1 = ((rank + 1) * chunks + ranks - 1) >> w.ranks_log2;
-        const int first = ((chunks + ranks - 1) >> w.ranks_log2) - 1;  // the last chunk that rank 0 folds itself
-        const bool joins = chunks > first + 1, begins = rank == 0;
-        walk.round = c0 * walk.s.per;
-        walk.end = min(c1 * walk.s.per, walk.s.rounds);
-        const int hk = walk.pair / w.blocks, block = walk.pair % w.blocks;
-        const int head0 = hk * w.p.group + block * w.heads, heads = min(w.heads, w.p.group - block * w.heads);
-        const int b = walk.b, rounds = walk.end, per = walk.s.per, n = walk.s.n;
-        const bool bad_length = walk.s.bad;
-        int g = walk.round;
-        Loader load;
-        load.start(walk, sh.ring[warp]);
-        Tile tile;
-        float rm = neg_inf(), rl = 0.0f;
-        float4 ra[kFours];
-#pragma unroll
-        for (int i = 0; i < kFours; ++i) ra[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (g < rounds) {
-            tile.load_q(w, sh.tile, b, head0, heads, warp, lane);
-#pragma unroll 1
-            for (int i = 0; i < SLOTS - 1; ++i) load.issue(w, warp, lane);
-            tile.reset();
-        }
-        if (ranks > 1) cluster_wait();
-        int slot_now = 0, chunk = c0, left = per;
-        bool bad = false;
-        const auto push = [&](int c, float m, float l, const float4 (&a)[kFours]) {
-            if (!folds || h >= heads) return;
-#pragma unroll
-            for (int i = 0; i < kFours; ++i) {
-                const int d = d0 + i * kTeam * 4;
-                if (d >= w.p.head_dim) continue;
-                const unsigned e = h * fours + d / 4, owner = quotient(e, w.by_own);
-                store_peer(smem_addr(part + c * w.own + (e - owner * w.own)), owner, a[i]);
-            }
-            if (d0 == 0) {
-                const int from = quotient(h * fours, w.by_own), to = quotient(h * fours + fours - 1, w.by_own);
-                for (int r = from; r <= to; ++r) store_peer(smem_addr(pairs + c * w.heads + h), r, make_float2(m, l));
-            }
-        };
-        for (; g < rounds; ++g) {
-            const int count = min(n - (g * R::kRound + warp * TOK), TOK);  // tokens of this tile
-            const int used = slot_now + 1 == SLOTS ? 0 : slot_now + 1;
-            load.turn(w, warp, lane);
-            bad |= load.bad_tile();
-            if (count > 0) tile.scores(w, sh.tile, sh.ring[warp] + slot_now * R::kSlot, count, warp, lane);
-            load.turn(w, warp, lane);
-            unsigned char *at = sh.ring[warp] + used * R::kSlot;
-            if (count > 0) tile.values(sh.tile, at, warp, lane);
-            slot_now = used + 1 == SLOTS ? 0 : used + 1;
-            if (--left && g + 1 < rounds) continue;
-            __syncwarp();
-            tile.leave(reinterpret_cast<float *>(at), kPitch, sh.m[warp], sh.l[warp], bad, lane);
-            tile.reset();
-            bad = false;
-            __syncthreads();
-            float top, l;
-            float4 a[kFours];
-            join_warps(sh, used, h, d0, top, l, a);
-            if (begins)
-                fold_chunk(rm, rl, ra, top, l, a);
-            else
-                push(chunk, top, l, a);
-            __syncthreads();
-            ++chunk;
-            left = per;
-        }
-        copy_wait<0>();
-        if (begins && bad_length) {
-            rl = quiet_nan();
-            if (threadIdx.x == 0) flag_bad_index(w.p.status);
-        }
-        if (!joins) {
-            if (begins && folds && h < heads) {
-#pragma unroll
-                for (int i = 0; i < kFours; ++i) {
-                    const int d = d0 + i * kTeam * 4;
-                    if (d < w.p.head_dim) write_out<T>(w, b, head0 + h, d, rm, rl, ra[i]);
-                }
-            }
-            return;
-        }
-        if (begins) push(first, rm, rl, ra);
-        cluster_arrive();
-        cluster_wait();
-        // this CTA's part of the plane: groups of four dimensions [e0, e1)
-        const int e0 = rank * w.own, e1 = min(e0 + w.own, heads * fours), folded = chunks - first;
-        if (e0 >= e1) return;
-        const int h0 = e0 / fours, spans = (e1 - 1) / fours - h0 + 1;
-        float4 *fold = reinterpret_cast<float4 *>(raw);  // [spans][folded] (fa, fb, top, l): the rings are idle
-        for (int i = threadIdx.x; i < spans * folded; i += kThreads) {
-            const int hh = h0 + i / folded, c = i % folded;
-            float before = neg_inf();
-            for (int k = 0; k < c; ++k) before = fmaxf(before, pairs[(first + k) * w.heads + hh].x);
-            const float2 ml = pairs[(first + c) * w.heads + hh];
-            float m, fa, fb;
-            fold_weights(before, ml.x, m, fa, fb);
-            fold[i] = make_float4(fa, fb, m, ml.y);
-        }
-        __syncthreads();
-        for (int e = e0 + threadIdx.x; e < e1; e += kThreads) {
-            const int hh = e / fours;
-            float l = 0.0f, m = neg_inf();
-            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int c = 0; c < folded; ++c) {
-                const float4 f = fold[(hh - h0) * folded + c];
-                l = fold_value(l, f.w, f.x, f.y);
-                a = fold_four(a, part[(first + c) * w.own + e - e0], f.x, f.y);
-                m = f.z;
-            }
-            write_out<T>(w, b, head0 + hh, (e - hh * fours) * 4, m, l, a);
-        }
+        if (w.slots && !w.by_pair && threadIdx.x == 0) w.headers[blockIdx.x] = header;
     }
 
     // A chunk's triple in a slot: (m, l) of each head, then the accumulators.
@@ -794,38 +642,42 @@ struct DecodeKernel {
 // kernel's operations. The folds' factors follow from the running maxima alone
 // and are made first; the accumulators pass through shared memory so that a whole
 // batch of them is in flight at once. Bound by latency: a few tens of KB a CTA.
-template <typename T>
+template <typename T, int DP>
 __device__ __forceinline__ void join_chunks(const DecodeWork &w)
 {
-    constexpr int kBatch = 32, kPer = kBatch * DETFOLD_ATTN_MAX_HEAD_DIM / 4 / kThreads;
-    __shared__ float2 s_fold[kMaxChunks];  // fa, fb
+    constexpr int kPer = 12, kBatch = kPer * kThreads * 4 / DP;  // float4s in flight a thread, chunks a batch
+    __shared__ float4 s_fold[kMaxChunks];  // fa, fb, top, l
     __shared__ float s_top[kWarps];
-    __shared__ float4 s_acc[kBatch * DETFOLD_ATTN_MAX_HEAD_DIM / 4];
+    __shared__ float4 s_acc[kPer * kThreads];
     const int slot_index = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int fours = w.p.head_dim / 4;
+    // float4 i of a batch: chunk i / fours, group i % fours; divided once, stepped from there
+    const int step_c = kThreads / fours, step_d = kThreads % fours;
+    const int c_first = tid / fours, d_first = tid % fours;
+    const float *slot = w.slot + slot_index * w.slot_floats;
     enter_grid();
     const int4 header = w.headers[slot_index];
     if (header.w == 0) return;
     const int hk = header.y / w.blocks, block = header.y % w.blocks;
     if (h >= min(w.heads, w.p.group - block * w.heads)) return;
-    const int first = header.z, count = header.w - first, fours = w.p.head_dim / 4;
-    const float *slot = w.slot + slot_index * w.slot_floats;
+    const int first = header.z, count = header.w - first;
     const float4 *acc = reinterpret_cast<const float4 *>(slot + w.pair_floats);
     float4 x[kPer];
-    // float4 i of a batch: chunk i / fours, group i % fours
-    auto fetch = [&](int c0) {
-        const int have = min(kBatch, count - c0) * fours;
+    const auto fetch = [&](int c0) {
+        int c = c_first, d = d_first;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = tid + k * kThreads;
-            if (i < have)
-                x[k] = acc[((int64_t)(first + c0 + i / fours) * w.heads + h) * fours + i % fours];
+            if (c < kBatch && c0 + c < count) x[k] = acc[((int64_t)(first + c0 + c) * w.heads + h) * fours + d];
+            c += step_c;
+            d += step_d;
+            if (d >= fours) d -= fours, ++c;
         }
     };
-    fetch(0);
     // factors: thread c takes chunk c
     static_assert(kMaxChunks <= kThreads, "a thread a chunk");
     float2 ml = make_float2(neg_inf(), 0.0f);
     if (tid < count) ml = *reinterpret_cast<const float2 *>(slot + ((int64_t)(first + tid) * w.heads + h) * 2);
+    fetch(0);
     float top = ml.x;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
@@ -834,40 +686,35 @@ __device__ __forceinline__ void join_chunks(const DecodeWork &w)
     }
     float before = __shfl_up_sync(~0u, top, 1);
     if (lane == 0) before = neg_inf();
-    if (lane == 31) s_top[warp] = top;
-    __syncthreads();
-    for (int k = 0; k < warp; ++k) before = fmaxf(before, s_top[k]);
+    if (count > 32) {
+        if (lane == 31) s_top[warp] = top;
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) before = fmaxf(before, s_top[k]);
+    }
     float m, fa, fb;
     fold_weights(before, ml.x, m, fa, fb);
-    if (tid < count) s_fold[tid] = make_float2(fa, fb);
-    // the sums l, in order, by every thread (the same values): through shared memory
-    __shared__ float s_l[kMaxChunks];
-    __shared__ float s_m;
-    if (tid < count) s_l[tid] = ml.y;
-    if (tid == count - 1) s_m = m;
+    if (tid < count) s_fold[tid] = make_float4(fa, fb, m, ml.y);
     float l = 0.0f;
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int c0 = 0; c0 < count; c0 += kBatch) {
         const int have = min(kBatch, count - c0);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int i = tid + k * kThreads;
-            if (i < have * fours) s_acc[i] = x[k];
-        }
+        for (int k = 0; k < kPer; ++k)
+            if (tid + k * kThreads < have * fours) s_acc[tid + k * kThreads] = x[k];
         __syncthreads();
         if (c0 + kBatch < count) fetch(c0 + kBatch);
         if (tid < fours) {
-#pragma unroll 4
-            for (int c = 0; c < have; ++c) {
-                const float2 f = s_fold[c0 + c];
-                l = fold_value(l, s_l[c0 + c], f.x, f.y);
-                a = fold_four(a, s_acc[c * fours + tid], f.x, f.y);
+#pragma unroll 8
+            for (int k = 0; k < have; ++k) {
+                const float4 f = s_fold[c0 + k];
+                l = fold_value(l, f.w, f.x, f.y);
+                a = fold_four(a, s_acc[k * fours + tid], f.x, f.y);
             }
         }
         __syncthreads();
     }
     if (tid < fours)
-        write_out<T>(w, header.x, hk * w.p.group + block * w.heads + h, tid * 4, s_m, l, a);
+        write_out<T>(w, header.x, hk * w.p.group + block * w.heads + h, tid * 4, s_fold[count - 1].z, l, a);
 }
 
 #endif  // __CUDACC__
