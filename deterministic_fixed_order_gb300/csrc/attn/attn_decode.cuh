@@ -392,7 +392,7 @@ struct Loader {
     uint32_t ring;  // shared address of this warp's ring
     int slot;
     bool values;    // the next slot takes the values of the tile whose keys went before
-    bool any;       // there is such a tile, and it has tokens of this warp
+    int rows;       // its tokens of this warp, rounded up to what the arithmetic reads; 0: none
     unsigned bad;   // bit i: the tile looked up i tiles before the last one needs a page outside the cache
     int64_t off;    // this lane's token's place in the cache, in elements; -1: not copied
 
@@ -406,15 +406,16 @@ struct Loader {
     }
     __device__ __forceinline__ void look(const DecodeWork &w, int warp, int lane)
     {
-        any = false;
+        rows = 0;
         bad <<= 1;
         while (!walk.done(w) && walk.round >= walk.end) walk.next_pair(w);  // pairs without rounds in this share
         if (walk.done(w)) return;
         const int i0 = walk.round * R::kRound + warp * TOK, token = lane % TOK;
         ++walk.round;
-        any = i0 < walk.s.n;
-        if (!any) return;
-        const bool live = i0 + token < walk.s.n;
+        const int count = walk.s.n - i0;
+        if (count <= 0) return;
+        rows = min(TOK, (count + 15) & ~15);
+        const bool live = token < count;
         const unsigned t = (unsigned)(walk.s.first + i0 + token), page = quotient(t, w.page);
         const int e = live ? w.p.table[walk.b * w.p.table_stride + page] : 0;
         const bool ok = e >= 0 && e < w.p.num_pages;
@@ -428,19 +429,25 @@ struct Loader {
     __device__ __forceinline__ void issue(const DecodeWork &w, int warp, int lane)
     {
         if (!values) look(w, warp, lane);
-        if (any) {
+        if (rows) {
             const char *from = (const char *)(values ? w.p.v : w.p.k);
             const uint32_t to = ring + slot * R::kSlot;
             const int valid = w.p.head_dim * (int)sizeof(T) / 16;
-            // all rows' places first: the exchanges keep their order, and copies between them would wait for each
-            int64_t o[kTimes];
+            // all rows' places first: the exchanges keep their order, and copies between them would wait for
+            // each. A short tile's second half goes uncopied.
+            constexpr int kHalf = TOK > 16 ? kTimes / 2 : kTimes;
 #pragma unroll
-            for (int i = 0; i < kTimes; ++i) o[i] = __shfl_sync(~0u, off, (i * 32 + lane) / R::kVecs);
+            for (int i0 = 0; i0 < kTimes; i0 += kHalf) {
+                if (i0 && rows <= 16) break;
+                int64_t o[kHalf];
 #pragma unroll
-            for (int i = 0; i < kTimes; ++i) {
-                const int row = (i * 32 + lane) / R::kVecs, vec = (i * 32 + lane) % R::kVecs;
-                const int bytes = o[i] >= 0 && vec < valid ? 16 : 0;
-                copy16(to + piece_at<TOK>(row, vec), from + (bytes ? o[i] * (int64_t)sizeof(T) + vec * 16 : 0), bytes);
+                for (int i = 0; i < kHalf; ++i) o[i] = __shfl_sync(~0u, off, ((i0 + i) * 32 + lane) / R::kVecs);
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) {
+                    const int row = ((i0 + i) * 32 + lane) / R::kVecs, vec = ((i0 + i) * 32 + lane) % R::kVecs;
+                    const int bytes = o[i] >= 0 && vec < valid ? 16 : 0;
+                    copy16(to + piece_at<TOK>(row, vec), from + (bytes ? o[i] * (int64_t)sizeof(T) + vec * 16 : 0), bytes);
+                }
             }
         }
         copy_commit();
@@ -573,7 +580,7 @@ struct DecodeKernel {
                 if (count > 0) tile.scores(w, sh.tile, sh.ring[warp] + slot_now * R::kSlot, count, warp, lane);
                 load.turn(w, warp, lane);
                 unsigned char *at = sh.ring[warp] + used * R::kSlot;
-                if (count > 0) tile.values(sh.tile, at, warp, lane);
+                if (count > 0) tile.values(sh.tile, at, count, warp, lane);
                 slot_now = used + 1 == SLOTS ? 0 : used + 1;
                 if (--left && g + 1 < walk.end) continue;
                 // the chunk's end: the warps' triples, joined in warp order

@@ -64,7 +64,7 @@ struct F32Tile {
 #pragma unroll
         for (int h = 0; h < HB; ++h) sum[h] = make_float2(0.0f, 0.0f);
         const int fours = w.p.head_dim / 4;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = part; i < fours; i += kParts) {
             const float4 k = *reinterpret_cast<const float4 *>(keys + piece_at<TOK>(token, i));
 #pragma unroll
@@ -115,10 +115,11 @@ struct F32Tile {
     }
 
     // Adds the tile's weighted values.
-    __device__ __forceinline__ void values(Shared &sh, const unsigned char *from, int warp, int lane)
+    __device__ __forceinline__ void values(Shared &sh, const unsigned char *from, int count, int warp, int lane)
     {
-#pragma unroll 4
-        for (int t = 0; t < TOK; ++t) {
+        const int last = min(TOK, (count + 7) & ~7);  // zeros up to there
+#pragma unroll 8
+        for (int t = 0; t < last; ++t) {
             float p[HB];
             const float *pt = sh.p[warp][t];
             if constexpr (HB % 4 == 0) {

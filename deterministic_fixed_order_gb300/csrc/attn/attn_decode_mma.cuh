@@ -224,12 +224,13 @@ struct MmaTile {
     }
 
     // Adds the tile's weighted values.
-    __device__ __forceinline__ void values(Shared &, const unsigned char *from, int, int lane)
+    __device__ __forceinline__ void values(Shared &, const unsigned char *from, int count, int, int lane)
     {
         const uint32_t at = smem_addr(from);
         constexpr int kBatch = 4;
 #pragma unroll
-        for (int u = 0; u < kSub; ++u)
+        for (int u = 0; u < kSub; ++u) {
+            if (u * 16 >= count) break;  // not copied
 #pragma unroll
             for (int m0 = 0; m0 < DP / 16; m0 += kBatch) {
                 uint32_t a[kBatch][4];
@@ -246,6 +247,7 @@ struct MmaTile {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma(o[m0 + i][nt], a[i], lo[u][nt][0], lo[u][nt][1], T());
             }
+        }
     }
 
     // Leaves the triple in shared memory; a `bad` chunk's sums are NaN.
