@@ -14,15 +14,16 @@ namespace {
 
 constexpr int kMost = 128;  // threads a CTA, at most
 constexpr int kRanks = 8;   // ranks whose elements a thread has in flight
-// CTAs an SM, which go from row to row: registers for eight ranks' elements without spilling. 131168
-// rows of 128 bfloat16 from 8 ranks: 47.3 us (95% of the measured copy rate); 50.6 us with a CTA
-// a row's worth, 54 with a division an element, 86 with seven CTAs an SM, which spill.
-constexpr int kResident = 5;
+// CTAs an SM, which go from row to row: as many as have registers for the ranks' elements
+// without spilling. 131168 rows of 128 bfloat16 from 8 ranks: 47.2 us (96% of the measured copy
+// rate); 50.6 us with a CTA a row's worth, 54 with a division an element, 86 with seven CTAs an
+// SM, which spill.
+constexpr int resident(int ranks) { return ranks == 0 ? 5 : ranks <= 2 ? 12 : ranks <= 4 ? 8 : 5; }
 
 // W == 0: any number of ranks, kRanks at a time; else exactly W <= kRanks.
 // `places` accesses a row, `abreast` of them at a time.
 template <typename T, int N, int W>
-__global__ void __launch_bounds__(kMost, kResident) join_kernel(const __grid_constant__ JoinParams p, int places, int abreast)
+__global__ void __launch_bounds__(kMost, resident(W)) join_kernel(const __grid_constant__ JoinParams p, int places, int abreast)
 {
     using V = Pack<T, N>;
     constexpr int R = W ? W : kRanks;
@@ -98,7 +99,7 @@ template <typename T, int N>
 cudaError_t launch_packs(const JoinParams &p, cudaStream_t stream)
 {
     const int places = p.head_dim / N, abreast = places < kMost ? places : kMost, rows = kMost / abreast;
-    const int64_t need = (p.rows + rows - 1) / rows, most = 152 * kResident;
+    const int64_t need = (p.rows + rows - 1) / rows, most = 152 * resident(p.W <= kRanks ? p.W : 0);
     const dim3 grid((unsigned)(need < most ? need : most));
     static constexpr decltype(&join_kernel<T, N, 0>) kernels[kRanks + 1] = {
         join_kernel<T, N, 0>, join_kernel<T, N, 1>, join_kernel<T, N, 2>, join_kernel<T, N, 3>, join_kernel<T, N, 4>,
