@@ -11,6 +11,10 @@ size against the lengths passed) or as raw integer addresses (passed through
 unchecked). ``stream`` may be None (torch's current stream), a
 ``torch.cuda.Stream`` or a raw handle. A negative status raises
 ``DetfoldError``; the ``status_*`` variants return it instead.
+
+The decode step's attention operators (``PagedCache``, ``Rope``,
+``detfold_kv_append``, ``detfold_attn_decode``, ``detfold_attn_join``; see
+``attention.py``) are names of this module too.
 """
 from __future__ import annotations
 
@@ -500,10 +504,15 @@ def shard_plan(length: int, W: int):
 
 # ------------------------------------------------------------------ the decode step's attention
 
-from . import attention as attention  # noqa: E402  (it builds on the helpers above)
-from .attention import (  # noqa: E402
-    PagedCache, Rope, detfold_attn_decode, detfold_attn_decode_workspace_bytes, detfold_attn_join,
-    detfold_kv_append)
+# Loaded on first use: the attention binding imports torch, this module only where it is given tensors.
+_ATTENTION = ("PagedCache", "Rope", "detfold_kv_append", "detfold_attn_decode",
+              "detfold_attn_decode_workspace_bytes", "detfold_attn_join")
 
-__all__ += ["attention", "PagedCache", "Rope", "detfold_attn_decode", "detfold_attn_decode_workspace_bytes",
-            "detfold_attn_join", "detfold_kv_append"]
+
+def __getattr__(name):
+    if name == "attention" or name in _ATTENTION:
+        import importlib
+        module = importlib.import_module(".attention", __name__)
+        globals().update({n: getattr(module, n) for n in _ATTENTION})
+        return module if name == "attention" else globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

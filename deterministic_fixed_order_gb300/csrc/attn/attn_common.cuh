@@ -86,6 +86,14 @@ __device__ __forceinline__ float exp_neg(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, kLog2e)));
     return y;
 }
+// The same times 2^SHIFT.
+template <int SHIFT>
+__device__ __forceinline__ float exp_neg_scaled(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(SHIFT ? __fmaf_rn(x, kLog2e, (float)SHIFT) : __fmul_rn(x, kLog2e)));
+    return y;
+}
 // The point that exponents are taken from: the maximum, or 0 where no score is above -inf.
 __device__ __forceinline__ float base_of(float m) { return m == neg_inf() ? 0.0f : m; }
 

@@ -28,19 +28,16 @@ namespace detfold_attn {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // CTAs: two on each of a GB300's 152 SMs, so that one's arithmetic goes on while the other
-// folds a chunk. Four warps with three stages of about 8.5 KB each take half an SM's
-// shared memory; its registers go round at 255 a thread.
+// folds a chunk. Four warps with three slots of 8 KB each take under half an SM's shared
+// memory; its registers go round at 255 a thread. (One CTA of eight warps: the same for one
+// long sequence, 71 us for 54 on 64 mixed ones.)
 constexpr int kSms = 152, kMaxCtas = 2 * kSms;
-#ifndef MINCHUNK
-#define MINCHUNK 128
-#endif
-constexpr int kMinChunk = MINCHUNK;  // tokens
+// Tokens a chunk, at least: with 256 one sequence of 4093 tokens takes 10.4 us for 9.7 and 32 short ones
+// 13.2 for 12.2, while 64 long and short ones take 51.5 for 52.5.
+constexpr int kMinChunk = 128;
 // Chunks a sequence: enough for one sequence to fill every CTA, within limits that keep
 // the join short.
-#ifndef MINCHUNKS
-#define MINCHUNKS 16
-#endif
-constexpr int kMinChunks = MINCHUNKS, kMaxChunks = 128;
+constexpr int kMinChunks = 16, kMaxChunks = 128;
 
 // A (key-value head, block of at most `heads` query heads) of a sequence is a
 // "pair": the unit that has a triple a query head.
@@ -81,10 +78,11 @@ struct DecodeGrid {
     int direct;  // a CTA a chunk: chunks of a pair, else 0
 };
 
-// Few chunks in all: a CTA a chunk, for up to DIRECT times as many CTAs as are resident.
-#ifndef DIRECT
-#define DIRECT 3
-#endif
+// Few chunks in all, as the longest sequence allows: a CTA a chunk, without working shares out, for up to
+// kDirect times as many CTAs as are resident. One sequence of 4093 tokens (0.8 times) 8.1 us for 8.6 with
+// shares, 96 windows of 1024 tokens (2.5 times) 18.0 for 19.3; 32 sequences that are mostly shorter than the
+// longest (3.4 times) 11.6 for 9.9.
+constexpr int kDirect = 3;
 
 // Workspace: a header of four ints a slot, then the slots: for each chunk and head (m, l),
 // then for each chunk and head the accumulator.
@@ -103,11 +101,12 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     g.chunks = up_to < most ? up_to : most;
     const int each = g.chunks > 0 ? g.chunks : 1;
     const int64_t pairs = (int64_t)batch * g.pairs, units = pairs * each;
-    g.direct = units <= DIRECT * kMaxCtas ? each : 0;
+    // A slot a pair; where there are more pairs than CTAs, a slot a CTA, since at most one pair
+    // begins in a CTA's share and ends beyond it. So slots and their size only grow with max_seen.
+    g.by_pair = pairs <= kMaxCtas;
+    g.slots = g.chunks <= 1 ? 0 : g.by_pair ? (int)pairs : kMaxCtas;
+    g.direct = units <= kDirect * kMaxCtas && (g.by_pair || !g.slots) ? each : 0;
     g.ctas = g.direct || units < kMaxCtas ? (int)units : kMaxCtas;
-    // at most one pair begins in a CTA's share and ends beyond it
-    g.by_pair = pairs <= g.ctas;
-    g.slots = g.chunks <= 1 ? 0 : g.by_pair ? (int)pairs : g.ctas;
     g.pair_floats = ((int64_t)g.chunks * g.heads * 2 + 3) / 4 * 4;
     g.slot_floats = g.pair_floats + ((int64_t)g.chunks * g.heads * head_dim + 3) / 4 * 4;
     return g;

@@ -7,8 +7,12 @@
 // right operand, O^T = V^T P^T (V^T by transposing loads). P is split in two
 // 16-bit parts, p = hi + lo, both multiplied: one part alone would round each
 // weight to the type's 8 or 11 bits and add as much error as rounding the output
-// does. Scores, maxima, sums and O^T are binary32.
+// does. float16 has few exponents: its weights are held times 2^14, so that the weights of
+// many tokens far below the largest keep their bits too. Scores, maxima, sums and O^T are
+// binary32.
 #pragma once
+
+#include <type_traits>
 
 #include "attn_decode.cuh"
 
@@ -74,6 +78,7 @@ struct MmaTile {
     using T = T_;
     static constexpr int kDP = DP, kTok = TOK, kHeads = 8 * NT;
     static constexpr int kSub = TOK / 16;
+    static constexpr int kShift = std::is_same_v<T, __half> ? 14 : 0;  // weights, sums and O^T are times 2^kShift
     struct Shared {
         int unused;
     };
@@ -192,8 +197,8 @@ struct MmaTile {
                 float sum = 0.0f;
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
-                    s[u][nt][j] = exp_neg(s[u][nt][j] - base);
-                    s[u][nt][j + 2] = exp_neg(s[u][nt][j + 2] - base);
+                    s[u][nt][j] = exp_neg_scaled<kShift>(s[u][nt][j] - base);
+                    s[u][nt][j + 2] = exp_neg_scaled<kShift>(s[u][nt][j + 2] - base);
                     const float two = __fadd_rn(s[u][nt][j], s[u][nt][j + 2]);
                     sum = u ? __fadd_rn(sum, two) : two;
                 }
@@ -250,9 +255,10 @@ struct MmaTile {
         }
     }
 
-    // Leaves the triple in shared memory; a `bad` chunk's sums are NaN.
+    // Leaves the triple in shared memory, its scale taken out again; a `bad` chunk's sums are NaN.
     __device__ __forceinline__ void leave(float *acc, int pitch, float *sm, float *sl, bool bad, int lane)
     {
+        constexpr float kUnscale = 1.0f / (1 << kShift);
         const int g = lane / 4, t = lane % 4;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -266,14 +272,15 @@ struct MmaTile {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     sm[nt * 8 + 2 * t + j] = m[nt][j];
-                    sl[nt * 8 + 2 * t + j] = bad ? quiet_nan() : l[nt][j];
+                    sl[nt * 8 + 2 * t + j] = bad ? quiet_nan() : __fmul_rn(l[nt][j], kUnscale);
                 }
             }
 #pragma unroll
             for (int mt = 0; mt < DP / 16; ++mt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    acc[(nt * 8 + 2 * t + j % 2) * pitch + mt * 16 + g + (j / 2) * 8] = o[mt][nt][j];
+                    acc[(nt * 8 + 2 * t + j % 2) * pitch + mt * 16 + g + (j / 2) * 8] =
+                        __fmul_rn(o[mt][nt][j], kUnscale);
         }
     }
 };

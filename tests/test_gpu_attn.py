@@ -529,3 +529,140 @@ def test_split_attention_joins_to_the_whole():
     torch.cuda.synchronize()
     ref.assert_near(out, want, 4 * tol, "joined")
     ref.assert_near(lse, wlse, 4 * ltol, "joined lse")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_decode_one_token_outweighs_many(dtype):
+    # One token's weight is e^14 times each other's, but 20000 others have a fiftieth of it together,
+    # and the one's value is 0: the output is theirs, and no weight may lose its bits for being small.
+    n, width = 20000, 64
+    d = Decode(dtype, [n], 1, 1, width, 16, q_scale=0.0)
+    d.q[0, 0, 0] = 8.0
+    d.k[torch.isnan(d.k)] = 0
+    d.k[..., 0] = 0
+    page = d.table[0, 100].long()
+    d.k[page, 3, 0, 0] = 14.0  # its score: 8 x 14 / sqrt(64)
+    d.v.fill_(1.0)
+    d.v[page, 3, 0] = 0
+    out, lse = d.run()
+    others = (n - 1) * torch.exp(torch.tensor(-14.0, dtype=torch.float64))
+    want = (others / (1 + others)).expand(1, 1, width)
+    # the weights' sum and the values' sum: n / 16 + 64 roundings of 2^-23, the weights' split 2^-16, the last rounding
+    tol = want.abs() * (2 * (n / 16 + 64) * 2.0 ** -23 + 2.0 ** -15) + ref.final_round(want, dtype)
+    ref.assert_near(out, want, tol, "sink")
+
+
+def test_decode_bound_on_lengths_past_32_bits_of_work():
+    # max_len 2^30: the shares' line is longer than 32 bits hold, the lengths themselves are short
+    page, batch = 1 << 20, 40
+    lens = [int(x) for x in np.random.RandomState(3).randint(0, 3000, batch)]
+    g = gen(4)
+    k, v = (randn(g, (batch, page, 1, 8), BF16) for _ in range(2))
+    d = Decode(BF16, [1] * batch, 4, 1, 8, 16)
+    d.k, d.v, d.cache, d.lens_host, d.max_len = k, v, df.PagedCache(k, v), lens, 1 << 30
+    d.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    d.table = torch.full((batch, 1024), -1, dtype=torch.int32, device="cuda")
+    d.table[:, 0] = torch.randperm(batch, generator=g, device="cuda").to(torch.int32)
+    d.check("bound of 2^30 tokens")
+
+
+@pytest.mark.parametrize("batch,heads", [(400, 1), (456, 1), (150, 3), (305, 1), (304, 1)])
+def test_decode_workspace_suffices_whatever_the_window(batch, heads):
+    # the bytes asked for max_len hold for every window: the guard behind them stays whole
+    lens = [300 + (7 * b) % 85 for b in range(batch)]
+    d = Decode(BF16, lens, 2 * heads, heads, 8, 16)
+    need = df.detfold_attn_decode_workspace_bytes(d.cache, batch, 2 * heads, d.max_len)
+    for window in (0, 129, 200, 256, 257, 300):
+        ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(d.q)
+        df.detfold_attn_decode(out, d.q, d.cache, d.table, d.lens, d.max_len, d.scale, window=window, workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert bool((ws[need:] == 255).all()), window
+        some = [0, batch // 2, batch - 1]
+        want, _, tol, _ = ref.decode(d.q[some], d.k, d.v, d.table[some], [lens[b] for b in some], d.scale, window)
+        ref.assert_near(out[some], want, tol, f"window {window}")
+
+
+def test_workspace_bytes_never_shrink_with_max_len():
+    k = torch.empty((2, 16, 4, 64), dtype=BF16, device="cuda")
+    cache = df.PagedCache(k, torch.empty_like(k))
+    for batch in (1, 3, 76, 77, 114, 200, 1000):
+        for heads in (4, 8, 80):
+            sizes = [df.detfold_attn_decode_workspace_bytes(cache, batch, heads, n)
+                     for n in list(range(0, 700, 13)) + [1 << x for x in range(10, 31)]]
+            assert sizes == sorted(sizes), (batch, heads)
+
+
+# ------------------------------------------------------------------ what the binding refuses
+
+def test_binding_refusals_on_the_gpu():
+    d = Decode(BF16, [40, 3], 8, 2, 64, 16)
+    out = torch.empty_like(d.q)
+
+    def call(**kw):
+        a = dict(out=out, q=d.q, cache=d.cache, block_table=d.table, seq_lens=d.lens, max_len=d.max_len, scale=1.0)
+        a.update(kw)
+        df.detfold_attn_decode(**a)
+    call()
+    for kw in (dict(q=d.q.float()), dict(out=out.half()), dict(q=d.q.cpu()), dict(block_table=d.table.long()),
+               dict(seq_lens=d.lens.long()), dict(q=None), dict(lse=torch.empty((2, 8), dtype=BF16, device="cuda")),
+               dict(status=torch.zeros(1, device="cuda")), dict(max_len="40")):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(q=d.q[:1]), dict(q=d.q[:, :, :32]), dict(out=out.transpose(1, 2).contiguous().transpose(1, 2)),
+               dict(block_table=d.table[:1]), dict(block_table=d.table[0]), dict(seq_lens=d.lens[:1]),
+               dict(lse=torch.empty((2, 4), device="cuda")), dict(workspace=torch.empty(64, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            call(**kw)
+    S = df.STATUS
+    for kw, code in ((dict(max_len=1000), "DETFOLD_ERR_LEN"), (dict(window=-1), "DETFOLD_ERR_ARG"),
+                     (dict(q=d.q[:, :7], out=out[:, :7]), "DETFOLD_ERR_ARG"), (dict(out=d.q), "DETFOLD_ERR_OVERLAP")):
+        with pytest.raises(df.DetfoldError) as e:
+            call(**kw)
+        assert e.value.status == S[code], kw
+    long = Decode(BF16, [4000], 8, 2, 64, 16)
+    with pytest.raises(df.DetfoldError) as e:
+        df.detfold_attn_decode(torch.empty_like(long.q), long.q, long.cache, long.table, long.lens, 4000, 1.0)
+    assert e.value.status == S["DETFOLD_ERR_WORKSPACE"]
+
+    a = Append(BF16, 6, 4, 2, 64, 64, False)
+    q_out = torch.empty((6, 4, 64), dtype=BF16, device="cuda")
+
+    def add(**kw):
+        b = dict(cache=a.cache, k=a.nk, v=a.nv, slots=a.slots, rope=a.rope, positions=a.positions, q=a.q, q_out=q_out)
+        b.update(kw)
+        df.detfold_kv_append(**b)
+    add()
+    for kw in (dict(k=a.nk.float()), dict(slots=a.slots.int()), dict(positions=a.positions.int()), dict(q=a.q.half()),
+               dict(v=a.nv.cpu())):
+        with pytest.raises(TypeError):
+            add(**kw)
+    for kw in (dict(k=a.nk[:5]), dict(k=a.nk[:, :1]), dict(v=a.nv[:, :, :32]), dict(slots=a.slots[:5]), dict(positions=None),
+               dict(q_out=None), dict(q=None), dict(q_out=q_out[:, :3])):
+        with pytest.raises(ValueError):
+            add(**kw)
+    with pytest.raises(df.DetfoldError) as e:
+        add(rope=df.Rope(torch.zeros((10, 128), device="cuda")))  # wider than the head
+    assert e.value.status == S["DETFOLD_ERR_ARG"]
+    with pytest.raises(df.DetfoldError) as e:
+        add(k=a.k[0, :6])  # the cache's own rows
+    assert e.value.status == S["DETFOLD_ERR_OVERLAP"]
+    with pytest.raises(ValueError):
+        df.PagedCache(a.k, a.v[:, :, :1])
+    with pytest.raises(ValueError):
+        df.PagedCache(a.k.transpose(2, 3), a.v.transpose(2, 3))
+    with pytest.raises(TypeError):
+        df.PagedCache(a.k, a.v.float())
+
+    parts, lses = join_inputs(BF16, 3, (5,), 64)
+    for bad in (dict(parts=[parts[0], parts[1], parts[2].float()]), dict(lses=[lses[0], lses[1], lses[2].half()])):
+        with pytest.raises(TypeError):
+            df.detfold_attn_join(**{**dict(out=torch.empty_like(parts[0]), parts=parts, lses=lses), **bad})
+    with pytest.raises(ValueError):
+        df.detfold_attn_join(torch.empty_like(parts[0]), parts, lses[:2])
+    with pytest.raises(ValueError):
+        df.detfold_attn_join(torch.empty((4, 64), dtype=BF16, device="cuda"), parts, lses)
+    with pytest.raises(df.DetfoldError) as e:
+        df.detfold_attn_join(torch.empty_like(parts[0]), [], [])
+    assert e.value.status == S["DETFOLD_ERR_WORLD"]
+    torch.cuda.synchronize()
