@@ -66,11 +66,11 @@ __device__ __forceinline__ void rotate(T *a, T *b, const float *co, const float 
     }
 }
 
-// `units` places a head: first those of pairs, then those of single copies. `team`
-// threads take a token together.
+// `units` places a head: first those of pairs, then those of copies, which take `twos` of N
+// elements or one. `team` threads take a token together.
 template <typename T, int N, bool PAIRS>
 __global__ void __launch_bounds__(kMost, 6) append_kernel(const __grid_constant__ AppendParams p, int units,
-                                                           int team)
+                                                           int team, bool twos)
 {
     using V = Pack<T, N>;
     const detfold_kv_cache &c = p.cache;
@@ -93,10 +93,10 @@ __global__ void __launch_bounds__(kMost, 6) append_kernel(const __grid_constant_
         heads.qo = (T *)p.q_out + t * p.qo_ts;
         // one place a thread, several only in heads of more than kMost places
         for (int u = member % abreast; u < units; u += abreast) {
-            // this place's elements: [ia, ia + N) and, where they turn, [ib, ib + N)
-            const bool turns = u < turning;
-            const int ia = !turns ? half + u * N : PAIRS ? 2 * u * N : u * N;
-            const int ib = PAIRS ? ia + N : ia + half;
+            // this place's elements: [ia, ia + N) and, where they turn or are copied by twos, [ib, ib + N)
+            const bool turns = u < turning, two = turns || twos;
+            const int ia = !turns ? p.rot_dim + (u - turning) * (twos ? 2 * N : N) : PAIRS ? 2 * u * N : u * N;
+            const int ib = PAIRS || !turns ? ia + N : ia + half;
             V a[kAhead], b[kAhead];
             auto load = [&](int r0) {
 #pragma unroll
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kMost, 6) append_kernel(const __grid_constant_
                     if (r0 + j * step < rows) {
                         const T *from = heads.from(p, r0 + j * step);
                         a[j] = *reinterpret_cast<const V *>(from + ia);
-                        if (turns) b[j] = *reinterpret_cast<const V *>(from + ib);
+                        if (two) b[j] = *reinterpret_cast<const V *>(from + ib);
                     }
             };
             load(first);
@@ -145,12 +145,10 @@ __global__ void __launch_bounds__(kMost, 6) append_kernel(const __grid_constant_
                 for (int j = 0; j < kAhead; ++j) {
                     const int r = r0 + j * step;
                     if (r >= last) break;
-                    if (turns && r < p.q_heads + c.kv_heads) {
-                        rotate<T, N, PAIRS>(a[j].v, b[j].v, co, si);
-                    }
+                    if (turns && r < p.q_heads + c.kv_heads) rotate<T, N, PAIRS>(a[j].v, b[j].v, co, si);
                     T *to = heads.to(p, r);
                     *reinterpret_cast<V *>(to + ia) = a[j];
-                    if (turns) *reinterpret_cast<V *>(to + ib) = b[j];
+                    if (two) *reinterpret_cast<V *>(to + ib) = b[j];
                 }
             }
         }
@@ -177,7 +175,9 @@ template <typename T, int N>
 cudaError_t launch_packs(const AppendParams &p, cudaStream_t stream)
 {
     const detfold_kv_cache &c = p.cache;
-    const int units = p.rot_dim / 2 / N + (c.head_dim - p.rot_dim) / N;
+    const int copied = c.head_dim - p.rot_dim;
+    const bool twos = copied % (2 * N) == 0;
+    const int units = p.rot_dim / 2 / N + copied / (twos ? 2 * N : N);
     const int rows = p.q_heads + 2 * c.kv_heads;
     const int abreast = units < kMost ? units : kMost;
     // whole heads a CTA: a thread stays at its place. A few tokens spread a head a
@@ -194,8 +194,8 @@ cudaError_t launch_packs(const AppendParams &p, cudaStream_t stream)
     // as many CTAs as are resident at 80 registers a thread
     const int64_t ctas = (p.tokens + teams - 1) / teams, resident = 152 * (65536 / 80 / ((threads + 31) / 32 * 32));
     const dim3 grid((unsigned)(ctas < resident ? ctas : resident), (unsigned)across);
-    return p.interleaved ? launch_early(append_kernel<T, N, true>, grid, threads, 0, stream, p, units, team)
-                         : launch_early(append_kernel<T, N, false>, grid, threads, 0, stream, p, units, team);
+    return p.interleaved ? launch_early(append_kernel<T, N, true>, grid, threads, 0, stream, p, units, team, twos)
+                         : launch_early(append_kernel<T, N, false>, grid, threads, 0, stream, p, units, team, twos);
 }
 
 template <typename T>
