@@ -1,8 +1,11 @@
 """Run one fold row at a chosen size for a few launches (for profiler captures).
 
     python profile_case.py ROW --len N [--W W] [--launches K] [--offset E]
+    python profile_case.py operator --case NAME [--launches K]
 
-ROW is one of: stacked, ptrs, allreduce, staged, scale, small, or torch_add
+`operator` runs one of the listed cases of perf/operators.py (the decode-step
+operators) with the library's kernels. ROW is one of: stacked, ptrs, allreduce,
+staged, scale, small, or torch_add
 (torch's own elementwise add of two operands, W = 2, as a reference for a
 launch of the same size that this library does not run). Inputs are
 seeded synthetic data. --offset E starts every operand E elements past an
@@ -23,16 +26,39 @@ if _ROOT not in sys.path:
     sys.path.insert(0, _ROOT)
 
 
+def operator_case(name: str, launches: int) -> int:
+    import importlib.util
+
+    import torch
+
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(_ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    state = ops.prepare(next(c for c in ops.listed() if c["name"] == name), 1)
+    for _ in range(launches):
+        ops.run(state)
+    torch.cuda.synchronize()
+    print(f"profile_case operator {name}: {launches} passes ok")
+    return 0
+
+
 def main() -> int:
     ap = argparse.ArgumentParser()
-    ap.add_argument("row", choices=["stacked", "ptrs", "allreduce", "staged", "scale", "small", "torch_add"])
-    ap.add_argument("--len", type=int, required=True)
+    ap.add_argument("row", choices=["stacked", "ptrs", "allreduce", "staged", "scale", "small", "torch_add",
+                                    "operator"])
+    ap.add_argument("--len", type=int)
+    ap.add_argument("--case")
     ap.add_argument("--W", type=int, default=8)
     ap.add_argument("--launches", type=int, default=3)
     ap.add_argument("--offset", type=int, default=0)
     ap.add_argument("--mixed", action="store_true",
                     help="operand r at offset + (3r mod 8) elements: every rank at its own 4-byte phase")
     a = ap.parse_args()
+    if a.row == "operator":
+        return operator_case(a.case, a.launches)
+    if a.len is None:
+        ap.error("--len is needed")
     if not 0 <= a.offset < 64:
         ap.error("--offset must be in [0, 64)")
 
