@@ -623,7 +623,7 @@ struct DecodeKernel {
                 }
                 if (!whole && d0 == 0) put_pair(w, slot, chunk - 1, h, rm, rl);
             }
-            if (w.slots && (w.by_pair || !whole)) {
+            if (w.slots && !w.direct && (w.by_pair || !whole)) {
                 header = make_int4(walk.b, walk.pair, chunk - 1, whole ? 0 : walk.chunks());
                 if (w.by_pair && threadIdx.x == 0) w.headers[walk.b * w.pairs + walk.pair] = header;
             }
@@ -648,7 +648,7 @@ struct DecodeKernel {
 // kernel's operations. The folds' factors follow from the running maxima alone
 // and are made first; the accumulators pass through shared memory so that a whole
 // batch of them is in flight at once. Bound by latency: a few tens of KB a CTA.
-template <typename T, int DP>
+template <typename T, int DP, int TOK>
 __device__ __forceinline__ void join_chunks(const DecodeWork &w)
 {
     constexpr int kPer = 12, kBatch = kPer * kThreads * 4 / DP;  // float4s in flight a thread, chunks a batch
@@ -661,8 +661,19 @@ __device__ __forceinline__ void join_chunks(const DecodeWork &w)
     const int step_c = kThreads / fours, step_d = kThreads % fours;
     const int c_first = tid / fours, d_first = tid % fours;
     const float *slot = w.slot + slot_index * w.slot_floats;
-    enter_grid();
-    const int4 header = w.headers[slot_index];
+    // (sequence, pair, first stored triple, chunks; 0: whole). A CTA a chunk stores every one: then all of it
+    // follows from the length, which the main kernel's start has made readable, before the wait for its end.
+    int4 header;
+    if (w.direct) {
+        const int b = (int)quotient(slot_index, w.by_pairs);
+        const Seq s = sequence<TOK>(w, b);
+        const int chunks = (s.rounds + s.per - 1) / s.per;
+        header = make_int4(b, slot_index - b * w.pairs, 0, chunks > 1 ? chunks : 0);
+        enter_grid();
+    } else {
+        enter_grid();
+        header = w.headers[slot_index];
+    }
     if (header.w == 0) return;
     const int hk = header.y / w.blocks, block = header.y % w.blocks;
     if (h >= min(w.heads, w.p.group - block * w.heads)) return;

@@ -13,10 +13,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     DecodeKernel<Tile, SLOTS>::run(w);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int TOK>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeWork w)
 {
-    join_chunks<T, DP>(w);
+    join_chunks<T, DP, TOK>(w);
 }
 
 // Shared memory above 48 KB is allowed once a device.
@@ -42,7 +42,7 @@ cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t s
     if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, SLOTS>, bytes, done)) return e;
     if (cudaError_t e = launch_early(decode_kernel<Tile, SLOTS>, dim3(g.ctas), kThreads, bytes, stream, w)) return e;
     if (g.slots)
-        return launch_early(decode_join_kernel<typename Tile::T, K::DP>, dim3(g.slots, g.heads), kThreads, 0, stream, w);
+        return launch_early(decode_join_kernel<typename Tile::T, K::DP, K::TOK>, dim3(g.slots, g.heads), kThreads, 0, stream, w);
     return cudaSuccess;
 }
 
