@@ -338,10 +338,15 @@ __device__ __forceinline__ void write_out(const DecodeWork &w, int b, int head, 
 {
     T *to = (T *)w.p.out + b * w.p.out_bs + head * w.p.out_hs + d;
     T v[4];
-    v[0] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.x, l));
-    v[1] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.y, l));
-    v[2] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.z, l));
-    v[3] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a.w, l));
+    // 16-bit results: one reciprocal, its half unit in the last place of binary32 far below theirs
+    const float inv = sizeof(T) == 2 && l != 0.0f ? __frcp_rn(l) : 0.0f;
+    const auto quotient_of = [&](float x) {
+        return from_f32<T>(sizeof(T) == 2 ? __fmul_rn(x, inv) : l == 0.0f ? 0.0f : __fdiv_rn(x, l));
+    };
+    v[0] = quotient_of(a.x);
+    v[1] = quotient_of(a.y);
+    v[2] = quotient_of(a.z);
+    v[3] = quotient_of(a.w);
     if (w.out_vec) {
         if constexpr (sizeof(T) == 4)
             *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<uint4 *>(v);
@@ -393,7 +398,8 @@ struct Loader {
     bool values;    // the next slot takes the values of the tile whose keys went before
     int rows;       // its tokens of this warp, rounded up to what the arithmetic reads; 0: none
     unsigned bad;   // bit i: the tile looked up i tiles before the last one needs a page outside the cache
-    int64_t off;    // this lane's token's place in the cache, in elements; -1: not copied
+    unsigned mask;  // bit t: token t is copied
+    int64_t off;    // where in the cache this lane's token lies, in bytes; 0 where it is not copied
 
     __device__ __forceinline__ void start(const Walk<TOK> &k, unsigned char *at)
     {
@@ -421,17 +427,26 @@ struct Loader {
         if (live && !ok) flag_bad_index(w.p.status);
         bad |= __any_sync(~0u, live && !ok) ? 1u : 0u;
         const int hk = w.blocks == 1 ? walk.pair : walk.pair / w.blocks;
-        off = live && ok ? e * w.p.page_stride + hk * w.p.head_stride +
-                               (int)(t - page * (unsigned)w.p.page_size) * w.p.token_stride
-                         : -1;
+        mask = __ballot_sync(~0u, live && ok);
+        off = live && ok ? (e * w.p.page_stride + hk * w.p.head_stride +
+                            (int)(t - page * (unsigned)w.p.page_size) * w.p.token_stride) * (int64_t)sizeof(T)
+                         : 0;
     }
     __device__ __forceinline__ void issue(const DecodeWork &w, int warp, int lane)
     {
         if (!values) look(w, warp, lane);
         if (rows) {
-            const char *from = (const char *)(values ? w.p.v : w.p.k);
-            const uint32_t to = ring + slot * R::kSlot;
-            const int valid = w.p.head_dim * (int)sizeof(T) / 16;
+            // Turn i copies rows row_of(i) + lr, pieces from vec_of(i) + lv on: what depends on the lane alone is
+            // worked out once.
+            constexpr int kAbreast = R::kVecs < 32 ? 32 / R::kVecs : 1;
+            const int lr = lane / R::kVecs, lv = lane % R::kVecs;
+            const auto row_of = [](int i) { return R::kVecs < 32 ? i * kAbreast : i * 32 / R::kVecs; };
+            const auto vec_of = [](int i) { return R::kVecs < 32 ? 0 : i * 32 % R::kVecs; };
+            const char *from = (const char *)(values ? w.p.v : w.p.k) + lv * 16;
+            const uint32_t to = ring + slot * R::kSlot + lv / 8 * (TOK * 128) + lr * 128;
+            const uint32_t swizzle = ((lv & 7) ^ lr) << 4;
+            const int valid = w.p.head_dim * (int)sizeof(T) / 16 - lv;
+            const unsigned rows_here = mask >> lr;
             // all rows' places first: the exchanges keep their order, and copies between them would wait for
             // each. A short tile's second half goes uncopied.
             constexpr int kHalf = TOK > 16 ? kTimes / 2 : kTimes;
@@ -440,12 +455,13 @@ struct Loader {
                 if (i0 && rows <= 16) break;
                 int64_t o[kHalf];
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) o[i] = __shfl_sync(~0u, off, ((i0 + i) * 32 + lane) / R::kVecs);
+                for (int i = 0; i < kHalf; ++i) o[i] = __shfl_sync(~0u, off, row_of(i0 + i) + lr);
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) {
-                    const int row = ((i0 + i) * 32 + lane) / R::kVecs, vec = ((i0 + i) * 32 + lane) % R::kVecs;
-                    const int bytes = o[i] >= 0 && vec < valid ? 16 : 0;
-                    copy16(to + piece_at<TOK>(row, vec), from + (bytes ? o[i] * (int64_t)sizeof(T) + vec * 16 : 0), bytes);
+                    const int row = row_of(i0 + i), vec = vec_of(i0 + i);
+                    const int bytes = (rows_here >> row & 1) && vec < valid ? 16 : 0;
+                    copy16(to + vec / 8 * (TOK * 128) + row * 128 + (swizzle ^ (row & 7) << 4), from + o[i] + vec * 16,
+                           bytes);
                 }
             }
         }
@@ -548,7 +564,7 @@ struct DecodeKernel {
         for (; !walk.done(w); walk.next_pair(w)) {
             const bool begins = walk.at >= walk.lo;
             if (!begins && walk.round >= walk.end) continue;
-            const int hk = walk.pair / w.blocks, block = walk.pair % w.blocks;
+            const int hk = w.blocks == 1 ? walk.pair : walk.pair / w.blocks, block = walk.pair - hk * w.blocks;
             const int head0 = hk * w.p.group + block * w.heads;
             const int heads = min(w.heads, w.p.group - block * w.heads);
             float *slot = nullptr;
@@ -557,13 +573,15 @@ struct DecodeKernel {
                                  : begins  ? (int)blockIdx.x
                                            : shares.of(w, walk.at)) *
                                     w.slot_floats;
-            tile.load_q(w, sh.tile, walk.b, head0, heads, warp, lane);
+            // the first copies: after the first queries are asked for, where these go to registers, before them where
+            // all warps wait for them
+            if (!Tile::kSharedQueries) tile.load_q(w, sh.tile, walk.b, head0, heads, warp, lane);
             if (!started) {
-                // the first copies, after the first queries are asked for
                 started = true;
 #pragma unroll 1
                 for (int i = 0; i < SLOTS - 1; ++i) load.issue(w, warp, lane);
             }
+            if (Tile::kSharedQueries) tile.load_q(w, sh.tile, walk.b, head0, heads, warp, lane);
             tile.reset();
             float rm = neg_inf(), rl = 0.0f;
             float4 ra[kFours];

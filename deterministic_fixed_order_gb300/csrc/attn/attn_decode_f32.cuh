@@ -15,6 +15,7 @@ template <int DP, int TOK, int HB>
 struct F32Tile {
     using T = float;
     static constexpr int kDP = DP, kTok = TOK, kHeads = HB;
+    static constexpr bool kSharedQueries = true;
     static constexpr int kParts = 32 / TOK;  // lanes that share a token's score
     static constexpr int kOwn = DP / 32;     // dimensions a lane holds of the output
     static constexpr int kVec = kOwn >= 4 ? 4 : kOwn;

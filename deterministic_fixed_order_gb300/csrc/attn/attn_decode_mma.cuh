@@ -77,6 +77,7 @@ template <typename T_, int DP, int TOK, int NT>
 struct MmaTile {
     using T = T_;
     static constexpr int kDP = DP, kTok = TOK, kHeads = 8 * NT;
+    static constexpr bool kSharedQueries = false;
     static constexpr int kSub = TOK / 16;
     static constexpr int kShift = std::is_same_v<T, __half> ? 14 : 0;  // weights, sums and O^T are times 2^kShift
     struct Shared {
