@@ -221,9 +221,7 @@ int detfold_attn_join(void *out, float *lse, const void *const *parts, const flo
         if (lse && (intersects(lse, lb, parts[r], pb) || intersects(lse, lb, lses[r], lb)))
             return DETFOLD_ERR_OVERLAP;
     }
-    JoinParams p = {};
-    p.out = out, p.lse = lse, p.rows = rows, p.W = W, p.head_dim = head_dim;
-    for (int r = 0; r < W; ++r) p.parts[r] = parts[r], p.lses[r] = lses[r];
+    const JoinParams p = {out, lse, parts, lses, rows, W, head_dim};
     return cuda_status(launch_join(p, dtype, (cudaStream_t)stream));
 }
 

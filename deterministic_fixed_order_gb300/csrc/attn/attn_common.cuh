@@ -128,7 +128,8 @@ __device__ __forceinline__ unsigned quotient(unsigned t, Divide d)
 
 // A launch whose prologue may overlap the end of the launch before it.
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t shared, cudaStream_t stream, A... args)
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t shared, cudaStream_t stream,
+                         const A &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -174,8 +175,8 @@ struct DecodeParams {
 struct JoinParams {
     void *out;
     float *lse;
-    const void *parts[DETFOLD_MAX_W];
-    const float *lses[DETFOLD_MAX_W];
+    const void *const *parts;  // host arrays of the call
+    const float *const *lses;
     int64_t rows;
     int W, head_dim;
 };

@@ -7,6 +7,8 @@
 // elements of a row -- the widest access that every operand's address and the row
 // allow -- and has up to eight ranks' elements in flight; the row's weights are
 // worked out by each of its threads again (one exponential a rank and access).
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace detfold_attn {
@@ -20,10 +22,24 @@ constexpr int kRanks = 8;   // ranks whose elements a thread has in flight
 // SM, which spill.
 constexpr int resident(int ranks) { return ranks == 0 ? 5 : ranks <= 2 ? 12 : ranks <= 4 ? 8 : 5; }
 
+// What the kernel is given: with up to kRanks ranks a small table, a quarter of a microsecond less of a
+// launch's time than the largest.
+template <int MOST>
+struct Ranks {
+    void *out;
+    float *lse;
+    const void *parts[MOST];
+    const float *lses[MOST];
+    int64_t rows;
+    int W, head_dim;
+};
+constexpr int most_ranks(int W) { return W ? kRanks : DETFOLD_MAX_W; }
+
 // W == 0: any number of ranks, kRanks at a time; else exactly W <= kRanks.
 // `places` accesses a row, `abreast` of them at a time.
 template <typename T, int N, int W>
-__global__ void __launch_bounds__(kMost, resident(W)) join_kernel(const __grid_constant__ JoinParams p, int places, int abreast)
+__global__ void __launch_bounds__(kMost, resident(W)) join_kernel(const __grid_constant__ Ranks<most_ranks(W)> p,
+                                                                       int places, int abreast)
 {
     using V = Pack<T, N>;
     constexpr int R = W ? W : kRanks;
@@ -101,11 +117,24 @@ cudaError_t launch_packs(const JoinParams &p, cudaStream_t stream)
     const int places = p.head_dim / N, abreast = places < kMost ? places : kMost, rows = kMost / abreast;
     const int64_t need = (p.rows + rows - 1) / rows, most = 152 * resident(p.W <= kRanks ? p.W : 0);
     const dim3 grid((unsigned)(need < most ? need : most));
-    static constexpr decltype(&join_kernel<T, N, 0>) kernels[kRanks + 1] = {
-        join_kernel<T, N, 0>, join_kernel<T, N, 1>, join_kernel<T, N, 2>, join_kernel<T, N, 3>, join_kernel<T, N, 4>,
-        join_kernel<T, N, 5>, join_kernel<T, N, 6>, join_kernel<T, N, 7>, join_kernel<T, N, 8>};
-    const auto kernel = kernels[p.W <= kRanks ? p.W : 0];
-    return launch_early(kernel, grid, rows * abreast, 0, stream, p, places, abreast);
+    const auto launch = [&](auto world) {
+        constexpr int W = decltype(world)::value;
+        Ranks<most_ranks(W)> ranks;
+        ranks.out = p.out, ranks.lse = p.lse, ranks.rows = p.rows, ranks.W = p.W, ranks.head_dim = p.head_dim;
+        for (int r = 0; r < p.W; ++r) ranks.parts[r] = p.parts[r], ranks.lses[r] = p.lses[r];
+        return launch_early(join_kernel<T, N, W>, grid, rows * abreast, 0, stream, ranks, places, abreast);
+    };
+    switch (p.W) {
+    case 1: return launch(std::integral_constant<int, 1>());
+    case 2: return launch(std::integral_constant<int, 2>());
+    case 3: return launch(std::integral_constant<int, 3>());
+    case 4: return launch(std::integral_constant<int, 4>());
+    case 5: return launch(std::integral_constant<int, 5>());
+    case 6: return launch(std::integral_constant<int, 6>());
+    case 7: return launch(std::integral_constant<int, 7>());
+    case 8: return launch(std::integral_constant<int, 8>());
+    default: return launch(std::integral_constant<int, 0>());
+    }
 }
 
 template <typename T>
