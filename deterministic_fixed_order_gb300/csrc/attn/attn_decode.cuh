@@ -30,10 +30,11 @@ constexpr int kThreads = kWarps * 32;
 // CTAs: two on each of a GB300's 152 SMs, so that one's arithmetic goes on while the other
 // folds a chunk. Four warps with three slots of 8 KB each take under half an SM's shared
 // memory; its registers go round at 255 a thread. (One CTA of eight warps: the same for one
-// long sequence, 71 us for 54 on 64 mixed ones.)
+// long sequence, 71 us where this took 54 on 64 mixed ones.)
 constexpr int kSms = 152, kMaxCtas = 2 * kSms;
-// Tokens a chunk, at least: with 256 one sequence of 4093 tokens takes 10.4 us for 9.7 and 32 short ones
-// 13.2 for 12.2, while 64 long and short ones take 51.5 for 52.5.
+// Tokens a chunk, at least, us with 128 and with 256: one sequence of 4093 tokens 7.5 and 8.3, 32 mixed
+// sequences of one key-value head 9.3 and 10.1, float32 14.3 and 15.9; 24 windows of 1024 tokens 17.4 and
+// 15.7, 64 mixed sequences 51.9 and 51.5. 64 brings float32 to 13.1 and the windows to 19.6.
 constexpr int kMinChunk = 128;
 // Chunks a sequence: enough for one sequence to fill every CTA, within limits that keep
 // the join short.
@@ -79,9 +80,9 @@ struct DecodeGrid {
 };
 
 // Few chunks in all, as the longest sequence allows: a CTA a chunk, without working shares out, for up to
-// kDirect times as many CTAs as are resident. One sequence of 4093 tokens (0.8 times) 8.1 us for 8.6 with
-// shares, 96 windows of 1024 tokens (2.5 times) 18.0 for 19.3; 32 sequences that are mostly shorter than the
-// longest (3.4 times) 11.6 for 9.9.
+// kDirect times as many CTAs as are resident. One sequence of 4093 tokens (0.8 times) 7.5 us for 8.3 with
+// shares, 96 windows of 1024 tokens (2.5 times) 17.4 for 19.0; 32 sequences that are mostly shorter than the
+// longest (3.4 times) 10.3 for 9.3.
 constexpr int kDirect = 3;
 
 // Workspace: a header of four ints a slot, then the slots: for each chunk and head (m, l),
@@ -171,7 +172,8 @@ __device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
     return s;
 }
 
-// A pair's share of the work: its rounds, and one for what each pair costs anyway.
+// A pair's share of the work: its rounds, and one for what each pair costs anyway (53.3 us for 51.8 on 64 mixed
+// sequences without the one).
 __device__ __forceinline__ int64_t cost(const Seq &s) { return s.rounds + 1; }
 
 // Walks the pairs of a CTA's share [lo, hi) of the line on which all pairs of
