@@ -14,7 +14,7 @@ DecodeGrid grid_of(int dtype, int batch, int kv_heads, int group, int head_dim, 
 {
     const bool f32 = dtype == DETFOLD_F32;
     const int heads = f32 ? (group == 1 ? 1 : group <= 4 ? 4 : 8) : group > 8 && head_dim <= 128 ? 16 : 8;
-    return decode_grid(batch, kv_heads, group, head_dim, max_seen, heads, tile_of(f32 ? 4 : 2, head_dim).round);
+    return decode_grid(batch, kv_heads, group, head_dim, max_seen, heads, tile_of(f32 ? 4 : 2, head_dim, heads));
 }
 
 }  // namespace
@@ -30,7 +30,7 @@ cudaError_t launch_decode(const DecodeParams &p, int dtype, void *workspace, cud
     DecodeWork w = {};
     w.p = p;
     w.pairs = g.pairs, w.blocks = g.pairs / p.kv_heads, w.heads = g.heads;
-    w.slots = g.slots, w.by_pair = g.by_pair, w.most_chunks = max_chunks(g.pairs);
+    w.slots = g.slots, w.by_pair = g.by_pair, w.most_chunks = g.most;
     w.most = divide_by(w.most_chunks), w.grid = divide_by(g.ctas);
     w.direct = g.direct;
     if (g.direct) w.by_chunks = divide_by(g.direct);

@@ -8,7 +8,7 @@
 //     m' = max(m, m_i), l' = l e^(m - m') + l_i e^(m_i - m'), a' likewise.
 //
 // Fixed order. A sequence's tokens are cut into chunks; the cut follows from
-// its length and the head counts alone (chunk_rounds). Within a chunk warp w
+// its length and the head counts alone (sequence). Within a chunk warp w
 // takes tiles w, w + 4, ... and the four warps' triples join in warp order; the
 // chunks' triples are folded in ascending order. Which CTA takes which chunks is
 // free: a CTA that begins a sequence folds in registers, any other leaves its
@@ -27,11 +27,7 @@ namespace detfold_attn {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// CTAs: two on each of a GB300's 152 SMs, so that one's arithmetic goes on while the other
-// folds a chunk. Four warps with three slots of 8 KB each take under half an SM's shared
-// memory; its registers go round at 255 a thread. (One CTA of eight warps: the same for one
-// long sequence, 71 us where this took 54 on 64 mixed ones.)
-constexpr int kSms = 152, kMaxCtas = 2 * kSms;
+constexpr int kSms = 152;
 // Tokens a chunk, at least, us with 128 and with 256: one sequence of 4093 tokens 7.5 and 8.3, 32 mixed
 // sequences of one key-value head 9.3 and 10.1, float32 14.3 and 15.9; 24 windows of 1024 tokens 17.4 and
 // 15.7, 64 mixed sequences 51.9 and 51.5. 64 brings float32 to 13.1 and the windows to 19.6.
@@ -41,35 +37,38 @@ constexpr int kMinChunk = 128;
 constexpr int kMinChunks = 16, kMaxChunks = 128;
 
 // A (key-value head, block of at most `heads` query heads) of a sequence is a
-// "pair": the unit that has a triple a query head.
-__host__ __device__ inline int max_chunks(int pairs)
+// "pair": the unit that has a triple a query head. `resident`: CTAs that the GPU holds.
+inline int max_chunks(int pairs, int resident)
 {
-    const int c = kMaxCtas / pairs;
+    const int c = resident / pairs;
     return c < kMinChunks ? kMinChunks : c > kMaxChunks ? kMaxChunks : c;
 }
 
-// Rounds (of `round` tokens) a chunk, for a sequence of `rounds` rounds and at most `most` chunks.
-inline int chunk_rounds(int rounds, int most, int round)
-{
-    const int least = kMinChunk / round;
-    const int r = (rounds + most - 1) / most;
-    return r < least ? least : r;
-}
-
 // The tile that a head dimension takes: tokens a warp has at once, so that their keys are 8 KB
-// (4 KB at 64 16-bit dimensions), and tokens a round.
+// (4 KB at 64 16-bit dimensions), and tokens a round; and the CTAs that an SM holds.
+//
+// Two, so that one's arithmetic goes on while the other folds a chunk: four warps with three slots of
+// 8 KB take under half an SM's shared memory, and its registers go round at 255 a thread. (One CTA of eight
+// warps: the same for one long sequence, 71 us where this took 54 on 64 mixed ones. Three CTAs with slots of
+// 4 KB at 128 16-bit dimensions: 82.5 us for 84.1 on one sequence of 131071 tokens, 63.0 for 51.9 on 64 mixed ones.)
+// At 64 16-bit dimensions a tile has half the bytes and takes nearly as long, and half the registers: four, with
+// three slots of 4 KB. 64 mixed sequences of 16 heads 60.4 us for 65.5, one of 131071 tokens 48.6 for
+// 51.6, 100 of 64 tokens 8.4 for 11.5; 32 mixed ones of one head 9.5 for 8.9. Of more than eight query heads
+// three, with four slots: 64 mixed sequences of 4 key-value heads 32.9 us, 36.3 with two CTAs and 40.1 with four,
+// which spill.
 struct TileShape {
-    int dims, tokens, round;
+    int dims, tokens, round, ctas;
 };
-constexpr TileShape tile_of(int element_bytes, int head_dim)
+constexpr TileShape tile_of(int element_bytes, int head_dim, int heads)
 {
     const int dims = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     const int by_size = 8192 / (dims * element_bytes), tokens = by_size < 32 ? by_size : 32;
-    return {dims, tokens, kWarps * tokens};
+    return {dims, tokens, kWarps * tokens, dims > 64 || element_bytes > 2 ? 2 : heads > 8 ? 3 : 4};
 }
 
 struct DecodeGrid {
     int ctas;    // CTAs of the main kernel
+    int most;    // max_chunks
     int slots;   // workspace slots, 0: no sequence can be split
     bool by_pair;  // a slot a pair, else a slot a CTA for the pair that its share breaks off in
     int chunks;  // most chunks of a sequence
@@ -88,8 +87,9 @@ constexpr int kDirect = 3;
 // Workspace: a header of four ints a slot, then the slots: for each chunk and head (m, l),
 // then for each chunk and head the accumulator.
 inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, int64_t max_seen, int heads,
-                              int round)
+                              const TileShape &tile)
 {
+    const int round = tile.round, resident = kSms * tile.ctas;
     DecodeGrid g;
     g.heads = heads < group ? heads : group;
     const int blocks = (group + heads - 1) / heads;
@@ -97,17 +97,17 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     const int rounds = (int)((max_seen + round - 1) / round);
     // shorter sequences may have more chunks than the longest: as many as there can be at all, so
     // that a larger max_seen never needs less
-    const int most = max_chunks(g.pairs), least = kMinChunk / round;
-    const int up_to = (rounds + least - 1) / least;
-    g.chunks = up_to < most ? up_to : most;
+    g.most = max_chunks(g.pairs, resident);
+    const int least = kMinChunk / round, up_to = (rounds + least - 1) / least;
+    g.chunks = up_to < g.most ? up_to : g.most;
     const int each = g.chunks > 0 ? g.chunks : 1;
     const int64_t pairs = (int64_t)batch * g.pairs, units = pairs * each;
     // A slot a pair; where there are more pairs than CTAs, a slot a CTA, since at most one pair
     // begins in a CTA's share and ends beyond it. So slots and their size only grow with max_seen.
-    g.by_pair = pairs <= kMaxCtas;
-    g.slots = g.chunks <= 1 ? 0 : g.by_pair ? (int)pairs : kMaxCtas;
-    g.direct = units <= kDirect * kMaxCtas && (g.by_pair || !g.slots) ? each : 0;
-    g.ctas = g.direct || units < kMaxCtas ? (int)units : kMaxCtas;
+    g.by_pair = pairs <= resident;
+    g.slots = g.chunks <= 1 ? 0 : g.by_pair ? (int)pairs : resident;
+    g.direct = units <= kDirect * resident && (g.by_pair || !g.slots) ? each : 0;
+    g.ctas = g.direct || units < resident ? (int)units : resident;
     g.pair_floats = ((int64_t)g.chunks * g.heads * 2 + 3) / 4 * 4;
     g.slot_floats = g.pair_floats + ((int64_t)g.chunks * g.heads * head_dim + 3) / 4 * 4;
     return g;
@@ -121,7 +121,7 @@ inline int64_t workspace_need(const DecodeGrid &g)
 struct DecodeWork {
     DecodeParams p;
     int pairs, blocks, heads, slots, by_pair;
-    int most_chunks;                // max_chunks(pairs)
+    int most_chunks;                // max_chunks
     Divide most, grid;              // by most_chunks, by the number of CTAs
     int short_line;                 // the shares' line is shorter than 2^30
     Divide page;                    // by the page size
@@ -152,8 +152,8 @@ __device__ __forceinline__ void copy_wait()
 
 // A sequence as the kernel sees it.
 struct Seq {
-    int n, first;  // attended tokens, the first one's index
-    int rounds, per;
+    int n, first;     // attended tokens, the first one's index
+    int rounds, per;  // rounds, and rounds a chunk: kMinChunk tokens, or more where that made too many chunks
     bool bad;      // its length is out of range
 };
 
@@ -168,7 +168,7 @@ __device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
     s.n = n < w.p.window ? n : (int)w.p.window;
     s.first = n - s.n;
     s.rounds = (s.n + kRound - 1) / kRound;
-    s.per = max(kMinChunk / kRound, (int)quotient(s.rounds + w.most_chunks - 1, w.most));  // chunk_rounds
+    s.per = max(kMinChunk / kRound, (int)quotient(s.rounds + w.most_chunks - 1, w.most));
     return s;
 }
 

@@ -11,8 +11,8 @@ cudaError_t launch_16bit(const DecodeWork &w, const DecodeGrid &g, cudaStream_t 
 {
     const bool wide = g.heads > 8;
     if (w.p.head_dim <= 64)
-        return wide ? launch_tile<MmaTile<T, 64, 32, 2>, 6>(w, g, stream)
-                    : launch_tile<MmaTile<T, 64, 32, 1>, 6>(w, g, stream);
+        return wide ? launch_tile<MmaTile<T, 64, 32, 2>, 4>(w, g, stream)
+                    : launch_tile<MmaTile<T, 64, 32, 1>, 3>(w, g, stream);
     if (w.p.head_dim <= 128)
         return wide ? launch_tile<MmaTile<T, 128, 32, 2>, 3>(w, g, stream)
                     : launch_tile<MmaTile<T, 128, 32, 1>, 3>(w, g, stream);

@@ -7,8 +7,11 @@
 
 namespace detfold_attn {
 
+template <typename Tile>
+inline constexpr TileShape kShape = tile_of(sizeof(typename Tile::T), Tile::kDP, Tile::kHeads);
+
 template <typename Tile, int SLOTS>
-__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ DecodeWork w)
+__global__ void __launch_bounds__(kThreads, kShape<Tile>.ctas) decode_kernel(const __grid_constant__ DecodeWork w)
 {
     DecodeKernel<Tile, SLOTS>::run(w);
 }
@@ -35,8 +38,9 @@ template <typename Tile, int SLOTS>
 cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t stream)
 {
     using K = DecodeKernel<Tile, SLOTS>;
-    static_assert(sizeof(typename K::Shared) <= 113 * 1024, "two CTAs an SM");
-    static_assert(K::R::kRound == tile_of(sizeof(typename K::T), K::DP).round, "as the grid is sized");
+    // of an SM's 228 KB the system keeps 1 KB a CTA
+    static_assert((sizeof(typename K::Shared) + 1024) * kShape<Tile>.ctas <= 228 * 1024, "CTAs an SM");
+    static_assert(K::R::kRound == kShape<Tile>.round, "as the grid is sized");
     static std::atomic<uint64_t> done{0};
     const size_t bytes = sizeof(typename K::Shared);
     if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, SLOTS>, bytes, done)) return e;
