@@ -142,6 +142,20 @@ def test_decode_workspace(df):
         assert decode(df, c=big, **big_call, **place, ws=far) == S["DETFOLD_ERR_OVERLAP"]
 
 
+@no_gpu_only
+def test_workspace_grows_with_every_size(df):
+    # no GPU needed: every type, tile and grouping, lengths around the chunk's and large ones
+    F = df.attention.lib.detfold_attn_decode_workspace_bytes
+    for dtype in (0, 1, 2):
+        for head_dim in (8, 64, 80, 128, 256):
+            c = cache(df, dtype=dtype, head_dim=head_dim, kv_heads=2, num_pages=1 << 20)
+            for group in (1, 4, 9):
+                for batch in (1, 152, 153, 229, 304, 305, 1000):
+                    got = [F(ctypes.addressof(c), batch, 2 * group, n)
+                           for n in (0, 1, 127, 128, 129, 256, 257, 384, 385, 1000, 1 << 14, 1 << 24)]
+                    assert got == sorted(got) and got[0] >= 0, (dtype, head_dim, group, batch)
+
+
 def append(df, c=None, rope="default", **kw):
     a = dict(k=Q, kt=128, kh=64, v=Q + (1 << 20), vt=128, vh=64, slots=TAB, tokens=3, pos=LEN, qo=OUT, ot=512, oh=64,
              q=WS, qt=512, qh=64, heads=8, status=None)

@@ -583,6 +583,31 @@ def test_decode_workspace_suffices_whatever_the_window(batch, heads):
         ref.assert_near(out[some], want, tol, f"window {window}")
 
 
+@pytest.mark.parametrize("batch,heads,group,head_dim", [
+    (608, 1, 2, 64), (609, 1, 2, 64), (203, 3, 2, 64), (1900, 1, 2, 8),        # four CTAs an SM
+    (456, 1, 16, 64), (457, 1, 16, 64), (1400, 1, 9, 8), (153, 3, 12, 64),     # three
+    (304, 1, 12, 128), (305, 1, 2, 128), (153, 2, 8, 200), (920, 1, 1, 136)])  # two
+def test_decode_at_the_counts_of_resident_ctas(batch, heads, group, head_dim):
+    # slots by pairs and by CTAs, a CTA a chunk and shares, on both sides of each change; garbage in the workspace
+    lens = [0 if b % 11 == 5 else 140 + (53 * b) % 250 for b in range(batch)]
+    d = Decode(BF16, lens, group * heads, heads, head_dim, 16)
+    need = df.detfold_attn_decode_workspace_bytes(d.cache, batch, group * heads, d.max_len)
+    some = [0, 5, batch // 2, batch - 1]
+    want, _, tol, _ = ref.decode(d.q[some], d.k, d.v, d.table[some], [lens[b] for b in some], d.scale)
+    alone = torch.empty_like(d.q[:1])
+    for fill in (0, 255):
+        ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(d.q)
+        df.detfold_attn_decode(out, d.q, d.cache, d.table, d.lens, d.max_len, d.scale, workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert bool((ws[need:] == fill).all())
+        ref.assert_near(out[some], want, tol, f"workspace of {fill}")
+        for b in (some[2], some[3]):
+            df.detfold_attn_decode(alone, d.q[b:b + 1].contiguous(), d.cache, d.table[b:b + 1].contiguous(),
+                                   d.lens[b:b + 1].contiguous(), d.max_len, d.scale, workspace=ws[:need])
+            assert torch.equal(alone[0], out[b]), b
+
+
 def test_workspace_bytes_never_shrink_with_max_len():
     k = torch.empty((2, 16, 4, 64), dtype=BF16, device="cuda")
     cache = df.PagedCache(k, torch.empty_like(k))
