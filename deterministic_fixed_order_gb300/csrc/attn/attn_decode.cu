@@ -30,7 +30,7 @@ cudaError_t launch_decode(const DecodeParams &p, int dtype, void *workspace, cud
     DecodeWork w = {};
     w.p = p;
     w.pairs = g.pairs, w.blocks = g.pairs / p.kv_heads, w.heads = g.heads;
-    w.slots = g.slots, w.by_pair = g.by_pair, w.most_chunks = g.most;
+    w.slots = g.direct == 1 ? 0 : g.slots, w.by_pair = g.by_pair, w.most_chunks = g.most, w.slot_chunks = g.chunks;
     w.most = divide_by(w.most_chunks), w.grid = divide_by(g.ctas);
     w.direct = g.direct;
     if (g.direct) w.by_chunks = divide_by(g.direct);

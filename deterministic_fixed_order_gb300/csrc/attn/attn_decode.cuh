@@ -75,7 +75,7 @@ struct DecodeGrid {
     int pairs;   // pairs a sequence
     int heads;   // query heads a pair, at most
     int64_t pair_floats, slot_floats;  // floats of a slot's (m, l) pairs; of a slot
-    int direct;  // a CTA a chunk: chunks of a pair, else 0
+    int direct;  // CTAs a pair: a CTA a chunk, or 1: a CTA has it all; else 0
 };
 
 // Few chunks in all, as the longest sequence allows: a CTA a chunk, without working shares out, for up to
@@ -83,6 +83,10 @@ struct DecodeGrid {
 // shares, 96 windows of 1024 tokens (2.5 times) 17.4 for 19.0; 32 sequences that are mostly shorter than the
 // longest (3.4 times) 10.3 for 9.3.
 constexpr int kDirect = 3;
+// More chunks than resident CTAs, none of a pair of over kWhole rounds, at most kDirect pairs a resident CTA: a CTA a
+// pair, and no join. 300 sequences of 288 tokens, one key-value head: 13.3 us for 26.0 in chunks; 600 of them
+// 24.6 for 31.4 in shares; 300 mixed ones of up to 480 tokens 12.1 for 16.0, 16 of 8 heads 10.6 for 7.9.
+constexpr int kWhole = 4;
 
 // Workspace: a header of four ints a slot, then the slots: for each chunk and head (m, l),
 // then for each chunk and head the accumulator.
@@ -106,8 +110,9 @@ inline DecodeGrid decode_grid(int batch, int kv_heads, int group, int head_dim, 
     // begins in a CTA's share and ends beyond it. So slots and their size only grow with max_seen.
     g.by_pair = pairs <= resident;
     g.slots = g.chunks <= 1 ? 0 : g.by_pair ? (int)pairs : resident;
-    g.direct = units <= kDirect * resident && (g.by_pair || !g.slots) ? each : 0;
-    g.ctas = g.direct || units < resident ? (int)units : resident;
+    const bool whole = units > resident && pairs <= kDirect * resident && rounds <= kWhole;
+    g.direct = whole ? 1 : units <= kDirect * resident && (g.by_pair || !g.slots) ? each : 0;
+    g.ctas = g.direct ? (int)(pairs * g.direct) : units < resident ? (int)units : resident;
     g.pair_floats = ((int64_t)g.chunks * g.heads * 2 + 3) / 4 * 4;
     g.slot_floats = g.pair_floats + ((int64_t)g.chunks * g.heads * head_dim + 3) / 4 * 4;
     return g;
@@ -121,11 +126,12 @@ inline int64_t workspace_need(const DecodeGrid &g)
 struct DecodeWork {
     DecodeParams p;
     int pairs, blocks, heads, slots, by_pair;
+    int slot_chunks;                // a slot has room for
     int most_chunks;                // max_chunks
     Divide most, grid;              // by most_chunks, by the number of CTAs
     int short_line;                 // the shares' line is shorter than 2^30
     Divide page;                    // by the page size
-    int direct;                     // a CTA a chunk: the most chunks of a pair, else 0
+    int direct;                     // CTAs a pair, else 0
     Divide by_chunks, by_pairs;     // by `direct` and by `pairs`
     int out_vec;                    // four elements of out start at a multiple of their size
     int q_vec;                      // two elements of q do
@@ -158,10 +164,9 @@ struct Seq {
 };
 
 template <int TOK>
-__device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
+__device__ __forceinline__ Seq sequence_of(const DecodeWork &w, int len)
 {
     Seq s;
-    const int len = w.p.lens[b];
     s.bad = len < 0 || len > w.p.max_len;
     constexpr int kRound = kWarps * TOK;
     const int n = s.bad ? 0 : len;
@@ -170,6 +175,12 @@ __device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
     s.rounds = (s.n + kRound - 1) / kRound;
     s.per = max(kMinChunk / kRound, (int)quotient(s.rounds + w.most_chunks - 1, w.most));
     return s;
+}
+
+template <int TOK>
+__device__ __forceinline__ Seq sequence(const DecodeWork &w, int b)
+{
+    return sequence_of<TOK>(w, w.p.lens[b]);
 }
 
 // A pair's share of the work: its rounds, and one for what each pair costs anyway (53.3 us for 51.8 on 64 mixed
@@ -238,13 +249,14 @@ struct Shares {
     }
 };
 
-// The sequence that `at` lies in and its start, by a scan of all sequences' costs, 32 at
-// a time, and the cut of the line into shares. I holds the line's length.
+// The sequence that this CTA's share begins in and its start, and the cut of the line into shares: each lane
+// adds up the costs of a block of sequences, and the block that the share begins in is looked through. I
+// holds the line's length. (608 mixed sequences of up to 900 tokens, 64 wide, one key-value head: 20.2 us, 23.7 where all
+// sequences were looked through 32 at a time.)
 template <int TOK, typename I>
 __device__ __forceinline__ void find_sequence(const DecodeWork &w, Shares &shares, int64_t &lo, int &b, int64_t &at)
 {
-    const int lane = threadIdx.x & 31;
-    const auto cost_of = [&](int i) { return i < w.p.batch ? (I)(cost(sequence<TOK>(w, i)) * w.pairs) : (I)0; };
+    const int lane = threadIdx.x & 31, block = (w.p.batch + 31) / 32;
     const auto scan = [&](I up) {
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -253,28 +265,43 @@ __device__ __forceinline__ void find_sequence(const DecodeWork &w, Shares &share
         }
         return up;
     };
-    const I mine = cost_of(lane);
-    I rest = 0;
-    for (int i = lane + 32; i < w.p.batch; i += 32) rest += cost_of(i);
+    I mine = 0;
+    constexpr int kAhead = 4;  // lengths asked for at once
+    const int end = min(lane * block + block, w.p.batch);
+    for (int i = lane * block; i < end; i += kAhead) {
+        int len[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) len[k] = i + k < end ? w.p.lens[i + k] : 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i + k < end) mine += (I)cost(sequence_of<TOK>(w, len[k])) * w.pairs;
+    }
+    __syncwarp();
     I up = scan(mine);
-    I total = __shfl_sync(~0u, up, 31);
-    if (w.p.batch > 32) total += __shfl_sync(~0u, scan(rest), 31);
-    shares.cut(w, total);
+    shares.cut(w, __shfl_sync(~0u, up, 31));
     lo = shares.begin(w, blockIdx.x);
-    I before = 0, c = mine;
-    for (int b0 = 0;;) {
+    int i = __ffs(__ballot_sync(~0u, up > (I)lo)) - 1;
+    I before = __shfl_sync(~0u, up - mine, i);
+    if (block == 1) {
+        b = i;
+        at = before;
+        return;
+    }
+    for (int b0 = i * block; b0 < w.p.batch; b0 += 32) {
+        const I c = b0 + lane < w.p.batch ? (I)cost(sequence<TOK>(w, b0 + lane)) * w.pairs : (I)0;
+        up = scan(c);
         const unsigned past = __ballot_sync(~0u, before + up > (I)lo);
         if (past) {
-            const int i = __ffs(past) - 1;
+            i = __ffs(past) - 1;
             b = b0 + i;
             at = before + __shfl_sync(~0u, up - c, i);
             return;
         }
         before += __shfl_sync(~0u, up, 31);
-        b0 += 32;
-        c = cost_of(b0 + lane);
-        up = scan(c);
     }
+    // lengths that changed meanwhile: any place that is one
+    b = w.p.batch - 1;
+    at = lo;
 }
 
 // This CTA's share, or its chunk of the pair that is its own. Every warp does the same: no barrier.
@@ -291,7 +318,7 @@ __device__ __forceinline__ Walk<TOK> begin_walk(const DecodeWork &w, Shares &sha
         k.lo = c > 0;
         k.hi = 1;
         k.round = min((int)c * k.s.per, k.s.rounds);
-        k.end = min(k.round + k.s.per, k.s.rounds);
+        k.end = w.direct == 1 ? k.s.rounds : min(k.round + k.s.per, k.s.rounds);
         return k;
     }
     if (w.p.batch == 1) {
@@ -310,6 +337,7 @@ __device__ __forceinline__ Walk<TOK> begin_walk(const DecodeWork &w, Shares &sha
     k.hi = shares.begin(w, blockIdx.x + 1);
     const int64_t in = k.lo - k.at;
     k.pair = w.pairs == 1 ? 0 : (int)(in >> 32 ? in / cost(k.s) : (unsigned)in / (unsigned)cost(k.s));
+    k.pair = min(k.pair, w.pairs - 1);
     k.at += k.pair * cost(k.s);
     k.enter();
     return k;
@@ -693,6 +721,10 @@ __device__ __forceinline__ void join_chunks(const DecodeWork &w)
     } else {
         enter_grid();
         header = w.headers[slot_index];
+        // written by one CTA's share, unless lengths changed under the call
+        if ((unsigned)header.x >= (unsigned)w.p.batch || (unsigned)header.y >= (unsigned)w.pairs || header.z < 0 ||
+            header.z >= header.w || header.w > w.slot_chunks)
+            return;
     }
     if (header.w == 0) return;
     const int hk = header.y / w.blocks, block = header.y % w.blocks;

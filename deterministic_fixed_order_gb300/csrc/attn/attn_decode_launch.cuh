@@ -45,7 +45,7 @@ cudaError_t launch_tile(const DecodeWork &w, const DecodeGrid &g, cudaStream_t s
     const size_t bytes = sizeof(typename K::Shared);
     if (cudaError_t e = allow_shared((const void *)decode_kernel<Tile, SLOTS>, bytes, done)) return e;
     if (cudaError_t e = launch_early(decode_kernel<Tile, SLOTS>, dim3(g.ctas), kThreads, bytes, stream, w)) return e;
-    if (g.slots)
+    if (w.slots)
         return launch_early(decode_join_kernel<typename Tile::T, K::DP, K::TOK>, dim3(g.slots, g.heads), kThreads, 0, stream, w);
     return cudaSuccess;
 }

@@ -608,6 +608,25 @@ def test_decode_at_the_counts_of_resident_ctas(batch, heads, group, head_dim):
             assert torch.equal(alone[0], out[b]), b
 
 
+@pytest.mark.parametrize("longest", [129, 256, 300, 384, 512, 513, 700])
+@pytest.mark.parametrize("dtype,head_dim,batches", [(BF16, 128, (100, 304, 650, 930)), (F16, 64, (300, 640, 1850)),
+                                                    (F32, 128, (160, 320)), (BF16, 256, (160, 320))])
+def test_decode_gives_the_bits_of_one_sequence_in_any_batch(dtype, head_dim, batches, longest):
+    # a CTA a chunk, a pair or a share, as the batch grows: one sequence's bits stay
+    for batch in batches:
+        lens = [(longest * (1 + (7 * b) % 10)) // 10 for b in range(batch)]
+        lens[batch // 3] = longest
+        d = Decode(dtype, lens, 2, 1, head_dim, 16)
+        out, lse = d.run()
+        for b in (0, batch // 3, batch - 1):
+            alone, alone_lse = d.run(q=d.q[b:b + 1].contiguous(), table=d.table[b:b + 1].contiguous(),
+                                     lens=d.lens[b:b + 1].contiguous())
+            assert torch.equal(alone[0], out[b]) and torch.equal(alone_lse[0], lse[b]), (batch, b)
+        some = [0, batch // 3]
+        want, _, tol, _ = ref.decode(d.q[some], d.k, d.v, d.table[some], [lens[b] for b in some], d.scale)
+        ref.assert_near(out[some], want, tol, f"{batch} sequences")
+
+
 def test_workspace_bytes_never_shrink_with_max_len():
     k = torch.empty((2, 16, 4, 64), dtype=BF16, device="cuda")
     cache = df.PagedCache(k, torch.empty_like(k))
