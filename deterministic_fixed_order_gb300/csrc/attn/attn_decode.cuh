@@ -251,8 +251,8 @@ struct Shares {
 
 // The sequence that this CTA's share begins in and its start, and the cut of the line into shares: each lane
 // adds up the costs of a block of sequences, and the block that the share begins in is looked through. I
-// holds the line's length. (608 mixed sequences of up to 900 tokens, 64 wide, one key-value head: 20.2 us, 23.7 where all
-// sequences were looked through 32 at a time.)
+// holds the line's length. (608 mixed sequences of up to 900 tokens, 64 wide, one key-value head: 20.2 us,
+// 23.7 where all sequences were looked through 32 at a time.)
 template <int TOK, typename I>
 __device__ __forceinline__ void find_sequence(const DecodeWork &w, Shares &shares, int64_t &lo, int &b, int64_t &at)
 {
