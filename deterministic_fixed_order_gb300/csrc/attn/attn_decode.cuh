@@ -709,17 +709,18 @@ __device__ __forceinline__ void join_chunks(const DecodeWork &w)
     const int step_c = kThreads / fours, step_d = kThreads % fours;
     const int c_first = tid / fours, d_first = tid % fours;
     const float *slot = w.slot + slot_index * w.slot_floats;
-    // (sequence, pair, first stored triple, chunks; 0: whole). A CTA a chunk stores every one: then all of it
-    // follows from the length, which the main kernel's start has made readable, before the wait for its end.
+    // Every kernel that may start early waits before it reads anything, the lengths too: what earlier launches wrote is
+    // visible after this wait only.
+    enter_grid();
+    // (sequence, pair, first stored triple, chunks; 0: whole). A CTA a chunk stores every one: all of it follows from
+    // the length.
     int4 header;
     if (w.direct) {
         const int b = (int)quotient(slot_index, w.by_pairs);
         const Seq s = sequence<TOK>(w, b);
         const int chunks = (s.rounds + s.per - 1) / s.per;
         header = make_int4(b, slot_index - b * w.pairs, 0, chunks > 1 ? chunks : 0);
-        enter_grid();
     } else {
-        enter_grid();
         header = w.headers[slot_index];
         // written by one CTA's share, unless lengths changed under the call
         if ((unsigned)header.x >= (unsigned)w.p.batch || (unsigned)header.y >= (unsigned)w.pairs || header.z < 0 ||
