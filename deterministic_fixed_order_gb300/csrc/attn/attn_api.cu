@@ -88,12 +88,13 @@ int detfold_kv_append(const detfold_kv_cache *cache, const void *k, int64_t k_to
                       int64_t q_head_stride, int q_heads, int *d_status, void *stream)
 {
     if (int rc = check_cache_shape(cache)) return rc;
-    if (!cache->k || !cache->v || !k || !v || !slots) return DETFOLD_ERR_NULL;
+    // operands without elements may have no address
+    if (!cache->k || !cache->v || (tokens != 0 && (!k || !v || !slots))) return DETFOLD_ERR_NULL;
     if (q_heads < 0 || q_heads > DETFOLD_ATTN_MAX_COUNT) return DETFOLD_ERR_ARG;
-    if (q_heads > 0 && (!q || !q_out)) return DETFOLD_ERR_NULL;
+    if (q_heads > 0 && tokens != 0 && (!q || !q_out)) return DETFOLD_ERR_NULL;
     if (q_heads == 0 && (q || q_out)) return DETFOLD_ERR_ARG;
     if (rope) {
-        if (!rope->cos_sin || !positions) return DETFOLD_ERR_NULL;
+        if (!rope->cos_sin || (tokens != 0 && !positions)) return DETFOLD_ERR_NULL;
         if (rope->rot_dim < 2 || rope->rot_dim > cache->head_dim || rope->rot_dim % 2 || rope->positions < 1 ||
             (rope->interleaved != 0 && rope->interleaved != 1))
             return DETFOLD_ERR_ARG;
@@ -156,7 +157,8 @@ int detfold_attn_decode(void *out, int64_t out_batch_stride, int64_t out_head_st
                         void *stream)
 {
     if (int rc = check_decode_sizes(cache, batch, q_heads, max_len)) return rc;
-    if (!out || !q || !cache->k || !cache->v || !block_table || !seq_lens) return DETFOLD_ERR_NULL;
+    if (!cache->k || !cache->v) return DETFOLD_ERR_NULL;
+    if (batch > 0 && (!out || !q || !seq_lens || (table_cols > 0 && !block_table))) return DETFOLD_ERR_NULL;
     if (window < 0 || table_cols < 0 || table_stride < 0) return DETFOLD_ERR_ARG;
     if (max_len > 0 && (max_len - 1) / cache->page_size >= table_cols) return DETFOLD_ERR_LEN;
     const int es = esize(cache->dtype), per16 = 16 / es;
@@ -202,9 +204,9 @@ int detfold_attn_decode(void *out, int64_t out_batch_stride, int64_t out_head_st
 int detfold_attn_join(void *out, float *lse, const void *const *parts, const float *const *lses, int W,
                       int64_t rows, int head_dim, int dtype, void *stream)
 {
-    if (!out || !parts || !lses) return DETFOLD_ERR_NULL;
+    if (!parts || !lses || (rows != 0 && !out)) return DETFOLD_ERR_NULL;
     if (W < 1 || W > DETFOLD_MAX_W) return DETFOLD_ERR_WORLD;
-    for (int r = 0; r < W; ++r)
+    for (int r = 0; rows != 0 && r < W; ++r)
         if (!parts[r] || !lses[r]) return DETFOLD_ERR_NULL;
     if (!known(dtype) || head_dim < 1 || head_dim > DETFOLD_ATTN_MAX_COUNT) return DETFOLD_ERR_ARG;
     if (rows < 0 || rows > DETFOLD_MAX_LEN / head_dim) return DETFOLD_ERR_LEN;

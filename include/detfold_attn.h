@@ -24,6 +24,8 @@
  *     parts' type in detfold_attn_join). Sums, maxima and accumulators are
  *     binary32; each output is rounded once.
  *   - Strides are in elements. The head dimension is always contiguous.
+ *   - A call whose count (tokens, batch, rows) is 0 is a no-op, and operands that
+ *     have no elements then may be NULL.
  *   - `d_status` is an optional DEVICE int (NULL = none) that the caller sets
  *     to DETFOLD_OK. It is written only when a kernel meets an index out of
  *     range in device memory (a slot, a position, a page, a length), and then
@@ -134,7 +136,8 @@ DETFOLD_API int64_t detfold_attn_decode_workspace_bytes(const detfold_kv_cache *
  *   cache       head_dim <= DETFOLD_ATTN_MAX_HEAD_DIM; its pointers and, in
  *               bytes, its strides and head_dim must be multiples of 16
  *               (DETFOLD_ERR_ALIGN).
- *   block_table device int32, row b at b * table_stride, table_cols entries each.
+ *   block_table device int32, row b at b * table_stride, table_cols entries each
+ *               (NULL when table_cols == 0).
  *   seq_lens    device int32 [batch].
  *   max_len     no length is larger; max_len <= table_cols * page_size.
  *   workspace   device, >= detfold_attn_decode_workspace_bytes bytes, 16-byte

@@ -1,0 +1,69 @@
+"""How the decode-step operators are called from Python: empty calls."""
+import pytest
+import torch
+
+import deterministic_fixed_order_gb300 as df
+from test_gpu_attn import BF16, F16, F32, gen, randn
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+S = df.STATUS
+
+
+def empty(*shape, dtype=BF16):
+    return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+# ------------------------------------------------------------------ nothing to do
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_calls_without_rows_do_nothing(dtype):
+    cache = df.PagedCache(empty(4, 16, 2, 64, dtype=dtype), empty(4, 16, 2, 64, dtype=dtype))
+    k0 = cache.k.fill_(3).clone()
+    cache.v.fill_(4)
+    rope = df.Rope(torch.ones((10, 64), device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    long = empty(0, dtype=torch.int64)
+    df.detfold_kv_append(cache, empty(0, 2, 64, dtype=dtype), empty(0, 2, 64, dtype=dtype), long)
+    df.detfold_kv_append(cache, empty(0, 2, 64, dtype=dtype), empty(0, 2, 64, dtype=dtype), long, rope=rope,
+                         positions=long, q=empty(0, 8, 64, dtype=dtype), q_out=empty(0, 8, 64, dtype=dtype),
+                         status=status)
+    for cols in (0, 4):
+        df.detfold_attn_decode(empty(0, 8, 64, dtype=dtype), empty(0, 8, 64, dtype=dtype), cache,
+                               empty(0, cols, dtype=torch.int32), empty(0, dtype=torch.int32), 0, 0.125, status=status)
+    df.detfold_attn_decode(empty(0, 8, 64, dtype=dtype), empty(0, 8, 64, dtype=dtype), cache,
+                           empty(0, 4, dtype=torch.int32), empty(0, dtype=torch.int32), 64, 0.125, window=7,
+                           lse=empty(0, 8, dtype=F32), status=status)
+    for shape in ((0,), (0, 5), (5, 0)):
+        df.detfold_attn_join(empty(*shape, 64, dtype=dtype), [empty(*shape, 64, dtype=dtype) for _ in range(3)],
+                             [empty(*shape, dtype=F32) for _ in range(3)], lse=empty(*shape, dtype=F32))
+    torch.cuda.synchronize()
+    assert int(status) == 0 and torch.equal(cache.k, k0) and bool((cache.v == 4).all())
+
+
+def test_sequences_without_a_table():
+    # max_len 0: no page is looked up, so the table may have no columns
+    cache = df.PagedCache(empty(4, 16, 2, 64), empty(4, 16, 2, 64))
+    q, out, lse = randn(gen(1), (3, 8, 64), BF16), empty(3, 8, 64), empty(3, 8, dtype=F32)
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    df.detfold_attn_decode(out, q, cache, empty(3, 0, dtype=torch.int32), lens, 0, 0.125, lse=lse)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+
+
+def test_what_is_wrong_without_rows_is_refused_all_the_same():
+    cache = df.PagedCache(empty(4, 16, 2, 64), empty(4, 16, 2, 64))
+    none = empty(0, dtype=torch.int32)
+    for kw, code in ((dict(heads=7), "DETFOLD_ERR_ARG"), (dict(window=-1), "DETFOLD_ERR_ARG"),
+                     (dict(max_len=65), "DETFOLD_ERR_LEN"), (dict(max_len=-1), "DETFOLD_ERR_LEN")):
+        a = {**dict(heads=8, window=0, max_len=64), **kw}
+        with pytest.raises(df.DetfoldError) as e:
+            df.detfold_attn_decode(empty(0, a["heads"], 64), empty(0, a["heads"], 64), cache,
+                                   empty(0, 4, dtype=torch.int32), none, a["max_len"], 0.125, window=a["window"])
+        assert e.value.status == S[code], kw
+    with pytest.raises(ValueError):
+        df.detfold_kv_append(cache, empty(0, 2, 64), empty(0, 3, 64), empty(0, dtype=torch.int64))
+    with pytest.raises(df.DetfoldError) as e:
+        df.detfold_attn_join(empty(0, 64), [], [])
+    assert e.value.status == S["DETFOLD_ERR_WORLD"]
