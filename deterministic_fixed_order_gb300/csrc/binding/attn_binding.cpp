@@ -86,6 +86,17 @@ void *flat(PyObject *x, at::ScalarType type, int device, int64_t count, const ch
     return t.data_ptr();
 }
 
+// Address of a contiguous tensor of this type and shape.
+void *packed(PyObject *x, at::ScalarType type, int device, at::IntArrayRef shape, const char *what)
+{
+    const at::Tensor &t = tensor(x, what);
+    check_kind(t, type, device, what);
+    if (!t.is_contiguous() || t.sizes() != shape)
+        raise(PyExc_ValueError, std::string(what) + ": expected a contiguous tensor of shape " + shape_text(shape) +
+                                    ", got shape " + shape_text(t.sizes()) + ", strides " + shape_text(t.strides()));
+    return t.data_ptr();
+}
+
 int *status_word(PyObject *x, int device)
 {
     if (x == Py_None) return nullptr;
@@ -235,7 +246,8 @@ PyObject *attn_decode(PyObject *const *a)
     const int64_t max_len = integer(a[5]), window = integer(a[7]);
     const double scale = PyFloat_AsDouble(a[6]);
     if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
-    float *lse = a[8] == Py_None ? nullptr : (float *)flat(a[8], at::kFloat, c.device, batch * heads, "lse");
+    const int64_t rows_heads[2] = {batch, heads};
+    float *lse = a[8] == Py_None ? nullptr : (float *)packed(a[8], at::kFloat, c.device, rows_heads, "lse");
     void *ws = nullptr;
     int64_t bytes = 0;
     if (a[9] != Py_None) {
@@ -272,16 +284,19 @@ PyObject *attn_join(PyObject *const *a)
         raise(PyExc_ValueError, std::to_string(world) + " parts, " + std::to_string(PySequence_Fast_GET_SIZE(lses)) + " lses");
     if (!out.is_cuda()) raise(PyExc_TypeError, "out: expected a CUDA tensor, got " + out.device().str());
     const int device = out.get_device();
-    const int64_t count = out.numel(), width = out.dim() ? out.size(-1) : 0, n = width ? count / width : 0;
+    if (!out.dim()) raise(PyExc_ValueError, "out: expected rows of a head, got shape []");
+    // every operand has out's shape, log-sums without the head's dimension
+    const at::IntArrayRef shape = out.sizes(), shape_rows = shape.slice(0, shape.size() - 1);
+    const int64_t width = shape.back(), n = c10::multiply_integers(shape_rows);
     if (width > DETFOLD_ATTN_MAX_COUNT) raise(PyExc_ValueError, "out: shape " + shape_text(out.sizes()) + " is too large");
     const void *p[DETFOLD_MAX_W];
     const float *l[DETFOLD_MAX_W];
     for (Py_ssize_t r = 0; r < world && r < DETFOLD_MAX_W; ++r) {
-        p[r] = flat(PySequence_Fast_GET_ITEM(parts, r), type, device, count, "parts");
-        l[r] = (const float *)flat(PySequence_Fast_GET_ITEM(lses, r), at::kFloat, device, n, "lses");
+        p[r] = packed(PySequence_Fast_GET_ITEM(parts, r), type, device, shape, "parts");
+        l[r] = (const float *)packed(PySequence_Fast_GET_ITEM(lses, r), at::kFloat, device, shape_rows, "lses");
     }
-    void *to = flat(a[0], type, device, count, "out");
-    float *lse = a[3] == Py_None ? nullptr : (float *)flat(a[3], at::kFloat, device, n, "lse");
+    void *to = packed(a[0], type, device, shape, "out");
+    float *lse = a[3] == Py_None ? nullptr : (float *)packed(a[3], at::kFloat, device, shape_rows, "lse");
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
     return PyLong_FromLong(detfold_attn_join(to, lse, p, l, world > DETFOLD_MAX_W ? DETFOLD_MAX_W + 1 : (int)world, n,
                                              (int)width, code, stream_of(a[4], device)));

@@ -1,9 +1,10 @@
-"""How the decode-step operators are called from Python: empty calls."""
+"""How the decode-step operators are called from Python: empty calls, shapes that are
+refused."""
 import pytest
 import torch
 
 import deterministic_fixed_order_gb300 as df
-from test_gpu_attn import BF16, F16, F32, gen, randn
+from test_gpu_attn import BF16, F16, F32, Decode, gen, join_inputs, randn
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
@@ -67,3 +68,29 @@ def test_what_is_wrong_without_rows_is_refused_all_the_same():
     with pytest.raises(df.DetfoldError) as e:
         df.detfold_attn_join(empty(0, 64), [], [])
     assert e.value.status == S["DETFOLD_ERR_WORLD"]
+
+
+# ------------------------------------------------------------------ shapes
+
+def test_join_takes_parts_of_its_output_s_shape_only():
+    parts, lses = join_inputs(BF16, 3, (6, 4), 8)
+    out, lse = torch.empty_like(parts[0]), torch.empty_like(lses[0])
+    df.detfold_attn_join(out, parts, lses, lse=lse)
+    for name, bad in (("parts", dict(parts=[parts[0], parts[1].view(4, 6, 8), parts[2]])),
+                      ("parts", dict(parts=[parts[0], parts[1], parts[2].view(6, 8, 4)])),
+                      ("parts", dict(parts=[parts[0].view(24, 8)] + parts[1:])),
+                      ("lses", dict(lses=[lses[0].view(4, 6)] + lses[1:])),
+                      ("lses", dict(lses=lses[:2] + [lses[2].view(24)])),
+                      ("lse", dict(lse=torch.empty((4, 6), device="cuda")))):
+        with pytest.raises(ValueError, match="^" + name + ":"):
+            df.detfold_attn_join(**{**dict(out=out, parts=parts, lses=lses, lse=lse), **bad})
+
+
+def test_decode_takes_an_lse_of_a_value_a_query_head_only():
+    d = Decode(BF16, [40, 3], 8, 2, 64, 16)
+    out = torch.empty_like(d.q)
+    df.detfold_attn_decode(out, d.q, d.cache, d.table, d.lens, d.max_len, 1.0, lse=torch.empty((2, 8), device="cuda"))
+    for shape in ((8, 2), (16,), (2, 8, 1)):
+        with pytest.raises(ValueError, match="^lse:"):
+            df.detfold_attn_decode(out, d.q, d.cache, d.table, d.lens, d.max_len, 1.0,
+                                   lse=torch.empty(shape, device="cuda"))
