@@ -42,7 +42,11 @@ if not os.path.exists(ATTN_LIB_PATH):
 
 lib = ctypes.CDLL(ATTN_LIB_PATH)
 
-from . import _attn_binding as _binding  # noqa: E402  (built and linked beside the library)
+try:
+    from . import _attn_binding as _binding  # noqa: E402  (built and linked beside the library)
+except ImportError as e:
+    raise ImportError(f"the attention operators' binding does not load ({e}); "
+                      "`python -c 'import __graft_entry__ as g; g.build()'` builds it and says what it lacks") from e
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64

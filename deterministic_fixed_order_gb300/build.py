@@ -22,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -67,6 +68,11 @@ def _attn_inputs() -> list[str]:
                      os.path.abspath(__file__)])
 
 
+def _binding_inputs() -> list[str]:
+    return [BINDING_SRC, os.path.join(INCLUDE, "detfold.h"), os.path.join(INCLUDE, "detfold_attn.h"),
+            os.path.abspath(__file__)]
+
+
 def stale(lib: str = LIB, inputs=None) -> bool:
     if not os.path.exists(lib):
         return True
@@ -77,32 +83,36 @@ def stale(lib: str = LIB, inputs=None) -> bool:
 def build(force: bool = False, defines: dict | None = None, lib: str = LIB,
           build_dir: str = BUILD_DIR, verbose: bool = False) -> str:
     """Compile and link libdetfold.so (and, for the default library path, the
-    probes and attention libraries); returns the fold library's path.
+    probes and attention libraries and the latter's Python binding); returns the
+    fold library's path.
 
     ``defines`` adds -D macros (launch-shape knobs of csrc/detfold_launch.cuh).
+    The C libraries do not depend on torch: a binding that cannot be built is a
+    RuntimeWarning, and importing ``attention`` then fails.
     """
-    if lib == LIB and (force or stale(PROBES_LIB, _probe_inputs())):
-        _link(sorted(glob.glob(os.path.join(PROBES_CSRC, "*.cu"))), PROBES_LIB,
-              os.path.join(build_dir, "probes"), [], verbose)
-    if lib == LIB:
-        _build_attn(os.path.join(build_dir, "attn"), force, verbose)
-    if not force and not defines and not stale(lib):
-        return lib
+    default = lib == LIB
     dflags = [f"-D{k}={v}" for k, v in (defines or {}).items()]
-    return _link(sorted(glob.glob(os.path.join(CSRC, "*.cu"))), lib, build_dir, dflags, verbose)
-
-
-def _build_attn(build_dir: str, force: bool, verbose: bool) -> None:
-    binding_inputs = [BINDING_SRC, os.path.join(INCLUDE, "detfold.h"), os.path.join(INCLUDE, "detfold_attn.h"),
-                      os.path.abspath(__file__)]
     with ThreadPoolExecutor(max_workers=1) as ex:
-        obj = None
-        if force or stale(BINDING_LIB, binding_inputs):
-            obj = ex.submit(_compile_binding, build_dir)  # beside the kernels
-        if force or stale(ATTN_LIB, _attn_inputs()):
-            _link(sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu"))), ATTN_LIB, build_dir, [], verbose)
-        if obj is not None:
-            _link_binding(obj.result())
+        binding = None
+        if default and (force or stale(BINDING_LIB, _binding_inputs())):
+            binding = ex.submit(_compile_binding, os.path.join(build_dir, "attn"))  # beside the kernels
+        if force or defines or stale(lib):
+            _link(sorted(glob.glob(os.path.join(CSRC, "*.cu"))), lib, build_dir, dflags, verbose)
+        if default and (force or stale(PROBES_LIB, _probe_inputs())):
+            _link(sorted(glob.glob(os.path.join(PROBES_CSRC, "*.cu"))), PROBES_LIB,
+                  os.path.join(build_dir, "probes"), [], verbose)
+        if default and (force or stale(ATTN_LIB, _attn_inputs())):
+            _link(sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu"))), ATTN_LIB,
+                  os.path.join(build_dir, "attn"), [], verbose)
+        if binding is not None:
+            try:
+                _link_binding(binding.result())
+            except (RuntimeError, OSError) as e:
+                if os.path.exists(BINDING_LIB):
+                    os.remove(BINDING_LIB)  # of older sources: not to be loaded
+                warnings.warn(f"the attention operators' Python binding was not built: {e}", RuntimeWarning,
+                              stacklevel=2)
+    return lib
 
 
 def _torch_root() -> str:
