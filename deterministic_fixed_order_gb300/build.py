@@ -21,6 +21,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 import warnings
 from concurrent.futures import ThreadPoolExecutor
@@ -91,11 +92,13 @@ def build(force: bool = False, defines: dict | None = None, lib: str = LIB,
     RuntimeWarning, and importing ``attention`` then fails.
     """
     default = lib == LIB
+    attn_dir = os.path.join(build_dir, "attn")
+    stamp = os.path.join(attn_dir, "binding.for")
     dflags = [f"-D{k}={v}" for k, v in (defines or {}).items()]
     with ThreadPoolExecutor(max_workers=1) as ex:
         binding = None
-        if default and (force or stale(BINDING_LIB, _binding_inputs())):
-            binding = ex.submit(_compile_binding, os.path.join(build_dir, "attn"))  # beside the kernels
+        if default and (force or _binding_stale(stamp)):
+            binding = ex.submit(_compile_binding, attn_dir)  # beside the kernels
         if force or defines or stale(lib):
             _link(sorted(glob.glob(os.path.join(CSRC, "*.cu"))), lib, build_dir, dflags, verbose)
         if default and (force or stale(PROBES_LIB, _probe_inputs())):
@@ -103,16 +106,35 @@ def build(force: bool = False, defines: dict | None = None, lib: str = LIB,
                   os.path.join(build_dir, "probes"), [], verbose)
         if default and (force or stale(ATTN_LIB, _attn_inputs())):
             _link(sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu"))), ATTN_LIB,
-                  os.path.join(build_dir, "attn"), [], verbose)
+                  attn_dir, [], verbose)
         if binding is not None:
             try:
                 _link_binding(binding.result())
+                with open(stamp, "w") as f:
+                    f.write(_binding_target())
             except (RuntimeError, OSError) as e:
                 if os.path.exists(BINDING_LIB):
                     os.remove(BINDING_LIB)  # of older sources: not to be loaded
                 warnings.warn(f"the attention operators' Python binding was not built: {e}", RuntimeWarning,
                               stacklevel=2)
     return lib
+
+
+def _binding_target() -> str:
+    """The torch and the Python that the binding is compiled against."""
+    root = _torch_root()
+    with open(os.path.join(root, "version.py")) as f:
+        return "\n".join([sys.version, str(sysconfig.get_config_var("SOABI")), root, f.read()])
+
+
+def _binding_stale(stamp: str) -> bool:
+    if stale(BINDING_LIB, _binding_inputs()) or not os.path.exists(stamp):
+        return True
+    try:
+        with open(stamp) as f:
+            return f.read() != _binding_target()
+    except (RuntimeError, OSError):
+        return True
 
 
 def _torch_root() -> str:

@@ -80,3 +80,32 @@ def test_a_c_library_that_does_not_compile_fails_the_build(build, monkeypatch):
         warnings.simplefilter("error")
         with pytest.raises(RuntimeError, match="nvcc failed"):
             build.run()
+
+
+def test_the_binding_is_built_again_for_another_torch_or_python(build, tmp_path, monkeypatch):
+    # its code is compiled against one torch's headers and one Python's
+    root = tmp_path / "torch"
+    root.mkdir()
+    (root / "version.py").write_text("__version__ = '2.9.1+cu130'\n")
+    monkeypatch.setattr(build, "_torch_root", lambda: str(root))
+    both = ["attn_binding.o", "_attn_binding.so"]
+
+    def again():
+        build.made.clear()
+        build.run()
+        return [n for n in build.made if n in both]
+
+    assert again() == both
+    assert again() == []
+    (root / "version.py").write_text("__version__ = '2.11.0+cu130'\n")
+    assert again() == both and not C_LIBRARIES & set(build.made)
+    assert again() == []
+    other = tmp_path / "elsewhere"
+    other.mkdir()
+    (other / "version.py").write_text("__version__ = '2.11.0+cu130'\n")
+    monkeypatch.setattr(build, "_torch_root", lambda: str(other))
+    assert again() == both
+    assert again() == []
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399")
+    assert again() == both
+    assert again() == []
