@@ -42,6 +42,9 @@ int64_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64
     return e > kMaxElems ? -1 : (int64_t)e;
 }
 
+// Whether neighbours of `n` blocks of `inner` elements share some: they may not where they are written.
+bool shares(int64_t n, int64_t stride, int64_t inner) { return n > 1 && stride < inner; }
+
 // A cache's shape; its pointers are checked by the calls that use them.
 int check_cache_shape(const detfold_kv_cache *c)
 {
@@ -108,7 +111,10 @@ int detfold_kv_append(const detfold_kv_cache *cache, const void *k, int64_t k_to
     if (tokens == 0) return DETFOLD_OK;
     const int64_t kb = extent(tokens, k_token_stride, cache->kv_heads, k_head_stride, 1, 0, cache->head_dim) * es;
     const int64_t vb = extent(tokens, v_token_stride, cache->kv_heads, v_head_stride, 1, 0, cache->head_dim) * es;
-    if (kb < 0 || vb < 0) return DETFOLD_ERR_ARG;
+    if (kb < 0 || vb < 0 || shares(cache->num_pages, cache->page_stride, cache->head_dim) ||
+        shares(cache->page_size, cache->token_stride, cache->head_dim) ||
+        shares(cache->kv_heads, cache->head_stride, cache->head_dim))
+        return DETFOLD_ERR_ARG;
     const int64_t cb = cache_bytes(cache);
     for (const void *c : {cache->k, cache->v})
         if (intersects(c, cb, k, kb) || intersects(c, cb, v, vb)) return DETFOLD_ERR_OVERLAP;
@@ -116,7 +122,9 @@ int detfold_kv_append(const detfold_kv_cache *cache, const void *k, int64_t k_to
         const int64_t qb = extent(tokens, q_token_stride, q_heads, q_head_stride, 1, 0, cache->head_dim) * es;
         const int64_t ob =
             extent(tokens, q_out_token_stride, q_heads, q_out_head_stride, 1, 0, cache->head_dim) * es;
-        if (qb < 0 || ob < 0) return DETFOLD_ERR_ARG;
+        if (qb < 0 || ob < 0 || shares(tokens, q_out_token_stride, cache->head_dim) ||
+            shares(q_heads, q_out_head_stride, cache->head_dim))
+            return DETFOLD_ERR_ARG;
         for (const void *c : {cache->k, cache->v})
             if (intersects(c, cb, q, qb) || intersects(c, cb, q_out, ob)) return DETFOLD_ERR_OVERLAP;
         // In place the layouts are one; elsewhere q_out meets nothing that is read.
@@ -171,7 +179,9 @@ int detfold_attn_decode(void *out, int64_t out_batch_stride, int64_t out_head_st
     const int64_t ob = extent(batch, out_batch_stride, q_heads, out_head_stride, 1, 0, cache->head_dim) * es;
     const int64_t qb = extent(batch, q_batch_stride, q_heads, q_head_stride, 1, 0, cache->head_dim) * es;
     const int64_t tb = extent(batch, table_stride, 1, 0, 1, 0, table_cols > 0 ? table_cols : 1) * 4;
-    if (ob < 0 || qb < 0 || tb < 0) return DETFOLD_ERR_ARG;
+    if (ob < 0 || qb < 0 || tb < 0 || shares(batch, out_batch_stride, cache->head_dim) ||
+        shares(q_heads, out_head_stride, cache->head_dim))
+        return DETFOLD_ERR_ARG;
     const int64_t need = detfold_attn_decode_workspace_bytes(cache, batch, q_heads, max_len);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return DETFOLD_ERR_WORKSPACE;

@@ -23,7 +23,9 @@
  *     operand of a call that is not otherwise typed has the cache's type (the
  *     parts' type in detfold_attn_join). Sums, maxima and accumulators are
  *     binary32; each output is rounded once.
- *   - Strides are in elements. The head dimension is always contiguous.
+ *   - Strides are in elements. The head dimension is always contiguous. Where
+ *     an operand is written, neighbours (two heads, rows, tokens or pages) are at
+ *     least head_dim elements apart (DETFOLD_ERR_ARG).
  *   - A call whose count (tokens, batch, rows) is 0 is a no-op, and operands that
  *     have no elements then may be NULL.
  *   - `d_status` is an optional DEVICE int (NULL = none) that the caller sets
@@ -59,13 +61,13 @@ extern "C" {
  * either lies at page * page_stride + row * token_stride + head * head_stride + d,
  * so pages may be stored token by token, head by head, or inside one buffer
  * that holds both. Pages of keys and of values have the same strides. No two
- * elements may share an address.
+ * elements that are written may share an address. A stride whose count is 1 is not used.
  */
 typedef struct detfold_kv_cache {
     void *k;             /* device */
     void *v;             /* device */
     int64_t num_pages;   /* >= 1 */
-    int64_t page_stride; /* >= 1 */
+    int64_t page_stride;
     int64_t token_stride;
     int64_t head_stride;
     int dtype;     /* DETFOLD_F32, DETFOLD_BF16 or DETFOLD_F16 */

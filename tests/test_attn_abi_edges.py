@@ -41,3 +41,24 @@ def test_what_is_wrong_without_elements_is_refused(df):  # noqa: F811
     assert F(None, None, tab(0, 0), tab(0, 0), 2, 4, 64, 1, None) == S["DETFOLD_ERR_NULL"]
     assert F(OUT, None, tab(A, 0), tab(LEN, WS), 2, 4, 64, 1, None) == S["DETFOLD_ERR_NULL"]
     assert F(OUT, None, tab(A, Q), tab(0, TAB), 2, 4, 64, 1, None) == S["DETFOLD_ERR_NULL"]
+
+
+@no_gpu_only
+def test_written_operands_whose_elements_share_addresses_are_refused(df):  # noqa: F811
+    # two neighbours less than a head apart: their elements would be written twice, in any order
+    S = df.STATUS
+    for bad in (dict(ob=0), dict(ob=56), dict(oh=0), dict(oh=32), dict(oh=63)):
+        assert decode(df, **bad) == S["DETFOLD_ERR_ARG"], bad
+    for bad in (dict(page_stride=0), dict(token_stride=0), dict(head_stride=0), dict(page_stride=56), dict(token_stride=8),
+                dict(head_stride=48)):
+        assert append(df, c=cache(df, **bad)) == S["DETFOLD_ERR_ARG"], bad
+    for bad in (dict(ot=0), dict(oh=0), dict(ot=63), dict(oh=1)):
+        assert append(df, **bad) == S["DETFOLD_ERR_ARG"], bad
+    assert append(df, qo=WS, ot=0, qt=0) == S["DETFOLD_ERR_ARG"]  # in place
+    # one of a kind has no neighbour, whatever its stride; what is only read may be broadcast
+    OK = (S["DETFOLD_OK"], S["DETFOLD_ERR_CUDA"])  # past the checks: no device to launch on
+    assert decode(df, batch=1, ob=0) in OK and decode(df, qb=0, qh=0) in OK
+    assert decode(df, c=cache(df, kv_heads=1, head_stride=0), heads=1, oh=0) in OK
+    assert decode(df, c=cache(df, page_stride=0)) in OK
+    assert append(df, c=cache(df, num_pages=1, page_stride=0)) in OK
+    assert append(df, kt=0, kh=0, vt=0, qt=0) in OK and append(df, tokens=1, ot=0) in OK
