@@ -1,14 +1,17 @@
 """How the decode-step operators are called from Python: empty calls, shapes that are
-refused."""
+refused, the status-returning forms, several streams and several host threads."""
+import threading
+
 import pytest
 import torch
 
 import deterministic_fixed_order_gb300 as df
-from test_gpu_attn import BF16, F16, F32, Decode, gen, join_inputs, randn
+from test_gpu_attn import BF16, F16, F32, Append, Decode, gen, join_inputs, randn
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
 
+A = df.attention
 S = df.STATUS
 
 
@@ -94,3 +97,100 @@ def test_decode_takes_an_lse_of_a_value_a_query_head_only():
         with pytest.raises(ValueError, match="^lse:"):
             df.detfold_attn_decode(out, d.q, d.cache, d.table, d.lens, d.max_len, 1.0,
                                    lse=torch.empty(shape, device="cuda"))
+
+
+# ------------------------------------------------------------------ the status-returning forms
+
+def test_status_forms_return_what_the_others_raise():
+    d = Decode(BF16, [40, 3], 8, 2, 64, 16)
+    want, wlse = d.run()
+    out, lse = torch.empty_like(d.q), torch.empty((2, 8), device="cuda")
+    args = (d.q, d.cache, d.table, d.lens)
+    assert A.status_attn_decode(out, *args, d.max_len, d.scale, lse=lse) == S["DETFOLD_OK"]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    assert A.status_attn_decode(out, *args, 1000, d.scale) == S["DETFOLD_ERR_LEN"]
+    assert A.status_attn_decode(d.q, *args, d.max_len, d.scale) == S["DETFOLD_ERR_OVERLAP"]
+    with pytest.raises(TypeError):
+        A.status_attn_decode(out.half(), *args, d.max_len, d.scale)
+
+    a, b = Append(BF16, 20, 4, 2, 64, 64, False), Append(BF16, 20, 4, 2, 64, 64, False)
+    qa, qb = torch.empty((20, 4, 64), dtype=BF16, device="cuda"), torch.empty((20, 4, 64), dtype=BF16, device="cuda")
+    df.detfold_kv_append(a.cache, a.nk, a.nv, a.slots, rope=a.rope, positions=a.positions, q=a.q, q_out=qa)
+    assert A.status_kv_append(b.cache, b.nk, b.nv, b.slots, rope=b.rope, positions=b.positions, q=b.q, q_out=qb) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(qa, qb) and torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+    assert A.status_kv_append(a.cache, a.k[0, :6], a.nv[:6], a.slots[:6]) == S["DETFOLD_ERR_OVERLAP"]
+
+    parts, lses = join_inputs(BF16, 3, (5,), 64)
+    one, two = torch.empty_like(parts[0]), torch.empty_like(parts[0])
+    df.detfold_attn_join(one, parts, lses)
+    assert A.status_attn_join(two, parts, lses) == S["DETFOLD_OK"]
+    torch.cuda.synchronize()
+    assert torch.equal(one, two)
+    assert A.status_attn_join(two, [], []) == S["DETFOLD_ERR_WORLD"]
+
+
+# ------------------------------------------------------------------ at the same time
+
+def test_calls_at_the_same_time_on_two_streams():
+    # a workspace and outputs each; every call's bits are those of the call alone
+    jobs = [Decode(BF16, [9000, 40, 1200], 32, 8, 128, 16, seed=1), Decode(F32, [2500, 0, 700, 90], 8, 8, 64, 16, seed=2)]
+    want = [d.run() for d in jobs]
+    spaces = [torch.empty(df.detfold_attn_decode_workspace_bytes(d.cache, d.q.shape[0], d.q.shape[1], d.max_len) + 16,
+                          dtype=torch.uint8, device="cuda") for d in jobs]
+    outs = [[(torch.empty_like(d.q), torch.empty(d.q.shape[:2], device="cuda")) for _ in range(25)] for d in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()  # what the streams use is there
+    for i in range(25):
+        for d, ws, out, stream in zip(jobs, spaces, outs, streams):
+            df.detfold_attn_decode(out[i][0], d.q, d.cache, d.table, d.lens, d.max_len, d.scale, lse=out[i][1],
+                                   workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for got, (o, s) in zip(outs, want):
+        assert all(torch.equal(a, o) and torch.equal(b, s) for a, b in got)
+
+
+def test_calls_from_several_host_threads():
+    # a step of each thread's own: append, attention and join, on a stream of its own
+    def job(seed):
+        d = Decode(BF16, [1500, 40 + seed], 8, 2, 64, 16, seed=seed)
+        a = Append(BF16, 33, 8, 2, 64, 64, False, seed=seed)
+        parts, lses = join_inputs(BF16, 3, (50,), 64, seed=seed)
+        ws = torch.empty(df.detfold_attn_decode_workspace_bytes(d.cache, 2, 8, d.max_len) + 16, dtype=torch.uint8,
+                         device="cuda")
+        return d, a, parts, lses, ws
+
+    def step(j, stream):
+        d, a, parts, lses, ws = j
+        with torch.cuda.stream(stream):
+            out, q_out, joined = torch.empty_like(d.q), torch.empty(a.q.shape, dtype=BF16, device="cuda"), torch.empty_like(parts[0])
+            df.detfold_kv_append(a.cache, a.nk, a.nv, a.slots, rope=a.rope, positions=a.positions, q=a.q, q_out=q_out)
+            df.detfold_attn_decode(out, d.q, d.cache, d.table, d.lens, d.max_len, d.scale, workspace=ws)
+            df.detfold_attn_join(joined, parts, lses)
+        return out, q_out, joined
+
+    jobs = [job(1 + t) for t in range(4)]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    want = [step(j, s) for j, s in zip(jobs, streams)]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def work(t):
+        try:
+            got[t] = [step(jobs[t], streams[t]) for _ in range(20)]
+            streams[t].synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for t in range(4):
+        for one in got[t]:
+            assert all(torch.equal(x, y) for x, y in zip(one, want[t])), t
