@@ -78,15 +78,18 @@ __device__ __forceinline__ void flag(int *status, int code)
 }
 __device__ __forceinline__ void flag_bad_index(int *status) { flag(status, DETFOLD_ERR_ARG); }
 
-// e^x for x <= 0: one product and the hardware's 2^x (2 units in the last place
-// of binary32 or so; results below 2^-126 become 0).
+// e^x for x <= 0: one product and the hardware's 2^x (2 units in the last place). The roundings
+// of the product and of log2 e become relative errors that grow with |x|: 3.6 units more for |x| up
+// to 4, 15 up to 16, 62 up to 80. The scores whose difference x is bring as much by their own
+// rounding. Results below 2^-126 become 0.
 __device__ __forceinline__ float exp_neg(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, kLog2e)));
     return y;
 }
-// The same times 2^SHIFT.
+// The same times 2^SHIFT by one fused multiply-add. A SHIFT of 14 rounds the exponent at 2^-21, the
+// weight by 3e-7; the weights' sum is taken of the same weights.
 template <int SHIFT>
 __device__ __forceinline__ float exp_neg_scaled(float x)
 {

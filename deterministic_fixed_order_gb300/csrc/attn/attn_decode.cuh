@@ -15,10 +15,12 @@
 // chunks' triples in the workspace for the join kernel, which goes on with the
 // same operations on the same values. So the bits do not depend on the batch.
 //
-// Bound. Each cached key and value is read once for all the query heads that
-// share it: 4 x group flops an element pair, so memory bound while the
+// Bound. Each cached key and value is read once for all the query heads of a tile (8,
+// or 16 in 16-bit types up to 128 dimensions): 4 x group flops an element pair, so memory bound while the
 // arithmetic keeps up. One pass; nothing but the triples of split sequences
-// goes back to memory.
+// goes back to memory. A wider group is several blocks of heads, and each reads the cache again: 16 sequences
+// of 8192 tokens, 2 key-value heads, groups of 8, 16 and 32: 33.7, 40.9 and 73.1 us for bfloat16 of 128, 58.8, 100
+// and 176 for 256, 63.3, 115 and 209 for float32 of 128.
 #pragma once
 
 #include "attn_common.cuh"
@@ -28,9 +30,10 @@ namespace detfold_attn {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSms = 152;
-// Tokens a chunk, at least, us with 128 and with 256: one sequence of 4093 tokens 7.5 and 8.3, 32 mixed
-// sequences of one key-value head 9.3 and 10.1, float32 14.3 and 15.9; 24 windows of 1024 tokens 17.4 and
-// 15.7, 64 mixed sequences 51.9 and 51.5. 64 brings float32 to 13.1 and the windows to 19.6.
+// Tokens a chunk, at least, us with 128 and with 256: one sequence of 4093 tokens 7.7 and 8.6, 32 mixed
+// sequences of one key-value head 9.4 and 10.3, float32 14.6 and 15.9; 24 windows of 1024 tokens of 256-wide heads 17.6 and
+// 15.9, 64 mixed sequences 51.4 and 51.1. 64 brings float32 to 13.1 and the windows to 19.7. One length for every
+// tile: a length by type and width would take both gains.
 constexpr int kMinChunk = 128;
 // Chunks a sequence: enough for one sequence to fill every CTA, within limits that keep
 // the join short.
@@ -79,9 +82,9 @@ struct DecodeGrid {
 };
 
 // Few chunks in all, as the longest sequence allows: a CTA a chunk, without working shares out, for up to
-// kDirect times as many CTAs as are resident. One sequence of 4093 tokens (0.8 times) 7.5 us for 8.3 with
-// shares, 96 windows of 1024 tokens (2.5 times) 17.4 for 19.0; 32 sequences that are mostly shorter than the
-// longest (3.4 times) 10.3 for 9.3.
+// kDirect times as many CTAs as are resident. One sequence of 4093 tokens (0.8 times) 7.7 us for 8.4 with
+// shares, 96 windows of 1024 tokens (2.5 times) 17.6 for 19.1; 32 sequences that are mostly shorter than the
+// longest (3.4 times) 10.6 for 9.4.
 constexpr int kDirect = 3;
 // More chunks than resident CTAs, none of a pair of over kWhole rounds, at most kDirect pairs a resident CTA: a CTA a
 // pair, and no join. 300 sequences of 288 tokens, one key-value head: 13.3 us for 26.0 in chunks; 600 of them

@@ -16,10 +16,10 @@ namespace {
 
 constexpr int kMost = 128;  // threads a CTA, at most
 constexpr int kRanks = 8;   // ranks whose elements a thread has in flight
-// CTAs an SM, which go from row to row: as many as have registers for the ranks' elements
-// without spilling. 131168 rows of 128 bfloat16 from 8 ranks: 47.2 us (96% of the measured copy
-// rate); 50.6 us with a CTA a row's worth, 54 with a division an element, 86 with seven CTAs an
-// SM, which spill.
+// CTAs an SM, which go from row to row: as many as have registers for the ranks' elements (but
+// for 4 bytes of spills at two ranks of bfloat16 and 12 at one of float32). 131168 rows of 128
+// bfloat16 from 8 ranks: 47.2 us (96% of the measured copy rate); 50.6 us with a CTA a row's
+// worth, 54 with a division an element, 86 with seven CTAs an SM, which spill more.
 constexpr int resident(int ranks) { return ranks == 0 ? 5 : ranks <= 2 ? 12 : ranks <= 4 ? 8 : 5; }
 
 // Keeps the widening of 16-bit elements here: done as they arrive it takes twice their registers, which
