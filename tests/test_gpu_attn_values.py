@@ -97,3 +97,24 @@ def test_infinite_values_of_one_sequence_stay_there(dtype, n):
     # of the other key-value head's queries neither
     assert torch.equal(out[0, 4:], good[0, 4:])
     assert bool((out[0, :4] == INF).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("hq,hk,width", CASES)
+@pytest.mark.parametrize("score", [NAN, INF])
+@pytest.mark.parametrize("n", [1, 100, 3000])
+def test_scores_that_have_no_weight_make_their_heads_nan(dtype, hq, hk, width, score, n):
+    # m = inf gives inf - inf for the token itself, NaN a NaN weight: the sum is NaN, in its key-value head's queries only
+    d, at, places, s, first = make(dtype, n, hq, hk, width)
+    good, good_lse = d.run()
+    for p in {0, n // 2, n - 1}:
+        k = d.k[at].clone()
+        k[p, 0, 0] = score
+        before = d.k[at].clone()
+        d.k[at] = k
+        out, lse = d.run()
+        d.k[at] = before
+        group = hq // hk
+        assert bool(torch.isnan(out[0, :group]).all()) and bool(torch.isnan(lse[0, :group]).all()), p
+        assert torch.equal(out[0, group:], good[0, group:]) and torch.equal(lse[0, group:], good_lse[0, group:]), p
+        assert torch.equal(out[1], good[1]) and torch.equal(lse[1], good_lse[1]), p
