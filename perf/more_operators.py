@@ -481,9 +481,9 @@ def _plain_pages(s):
     cnt = s["refs"].long()
     cnt.index_add_(0, table[old], -one.expand(int(old.sum())))
     cnt.index_add_(0, from_row[kept], one.expand(int(kept.sum())))
-    # a page that a row does not fill is its own, or is copied
+    # a page that a row goes on writing into is its own, or is copied
     last = up(keep) - 1
-    partial = keep % page != 0
+    partial = (keep % page != 0) & (want > keep)
     held = from_row.gather(1, last.clamp_min(0)[:, None])[:, 0]
     copies = partial & (cnt[held.clamp_min(0)] > 1)
     need = up(want) - up(keep) + copies
