@@ -14,7 +14,9 @@ unchecked). ``stream`` may be None (torch's current stream), a
 
 The decode step's attention operators (``PagedCache``, ``Rope``,
 ``detfold_kv_append``, ``detfold_attn_decode``, ``detfold_attn_join``; see
-``attention.py``) are names of this module too.
+``attention.py``) and those of a step with drafted tokens (``detfold_tree_plan``,
+``detfold_attn_tree``, ``detfold_kv_compact``, ``detfold_kv_copy_pages``,
+``detfold_pages_step``; see ``tree.py``) are names of this module too.
 """
 from __future__ import annotations
 
@@ -509,10 +511,15 @@ _ATTENTION = ("PagedCache", "Rope", "detfold_kv_append", "detfold_attn_decode",
               "detfold_attn_decode_workspace_bytes", "detfold_attn_join")
 
 
+_TREE = ("detfold_tree_plan", "detfold_attn_tree", "detfold_attn_tree_workspace_bytes", "detfold_kv_compact",
+         "detfold_kv_copy_pages", "detfold_pages_step")
+
+
 def __getattr__(name):
-    if name == "attention" or name in _ATTENTION:
-        import importlib
-        module = importlib.import_module(".attention", __name__)
-        globals().update({n: getattr(module, n) for n in _ATTENTION})
-        return module if name == "attention" else globals()[name]
+    import importlib
+    for where, names in (("attention", _ATTENTION), ("tree", _TREE)):
+        if name == where or name in names:
+            module = importlib.import_module("." + where, __name__)
+            globals().update({n: getattr(module, n) for n in names})
+            return module if name == where else globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -10,7 +10,8 @@ The measurement probes (``csrc/probes/*.cu``, the latency floors that graphs
 of small folds are compared against) link into a library of their own,
 ``libdetfold_probes.so``, which the fold library's binding never loads. The
 decode-step attention operators (``csrc/attn/*.cu``) link into
-``libdetfold_attn.so``, and the module that marshals torch tensors for them
+``libdetfold_attn.so``, those of a step with drafted tokens (``csrc/tree/*.cu``)
+into ``libdetfold_tree.so``, and the module that marshals torch tensors for both
 (``csrc/binding/attn_binding.cpp``) into ``_attn_binding.so``, with the host
 compiler against the installed torch's headers.
 """
@@ -36,6 +37,8 @@ PROBES_CSRC = os.path.join(CSRC, "probes")
 PROBES_LIB = os.path.join(PKG, "libdetfold_probes.so")
 ATTN_CSRC = os.path.join(CSRC, "attn")
 ATTN_LIB = os.path.join(PKG, "libdetfold_attn.so")
+TREE_CSRC = os.path.join(CSRC, "tree")
+TREE_LIB = os.path.join(PKG, "libdetfold_tree.so")
 BINDING_SRC = os.path.join(CSRC, "binding", "attn_binding.cpp")
 BINDING_LIB = os.path.join(PKG, "_attn_binding.so")
 
@@ -69,8 +72,16 @@ def _attn_inputs() -> list[str]:
                      os.path.abspath(__file__)])
 
 
+def _tree_inputs() -> list[str]:
+    return sorted(glob.glob(os.path.join(TREE_CSRC, "*.cu")) + glob.glob(os.path.join(TREE_CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(ATTN_CSRC, "*.cuh"))
+                  + [os.path.join(INCLUDE, h) for h in ("detfold.h", "detfold_attn.h", "detfold_tree.h")]
+                  + [os.path.abspath(__file__)])
+
+
 def _binding_inputs() -> list[str]:
-    return [BINDING_SRC, os.path.join(INCLUDE, "detfold.h"), os.path.join(INCLUDE, "detfold_attn.h"),
+    return [BINDING_SRC, *sorted(glob.glob(os.path.join(CSRC, "binding", "*.h"))),
+            *[os.path.join(INCLUDE, h) for h in ("detfold.h", "detfold_attn.h", "detfold_tree.h")],
             os.path.abspath(__file__)]
 
 
@@ -84,8 +95,8 @@ def stale(lib: str = LIB, inputs=None) -> bool:
 def build(force: bool = False, defines: dict | None = None, lib: str = LIB,
           build_dir: str = BUILD_DIR, verbose: bool = False) -> str:
     """Compile and link libdetfold.so (and, for the default library path, the
-    probes and attention libraries and the latter's Python binding); returns the
-    fold library's path.
+    probes, attention and drafted-token libraries and the latter two's Python
+    binding); returns the fold library's path.
 
     ``defines`` adds -D macros (launch-shape knobs of csrc/detfold_launch.cuh).
     The C libraries do not depend on torch: a binding that cannot be built is a
@@ -107,6 +118,9 @@ def build(force: bool = False, defines: dict | None = None, lib: str = LIB,
         if default and (force or stale(ATTN_LIB, _attn_inputs())):
             _link(sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu"))), ATTN_LIB,
                   attn_dir, [], verbose)
+        if default and (force or stale(TREE_LIB, _tree_inputs())):
+            _link(sorted(glob.glob(os.path.join(TREE_CSRC, "*.cu"))), TREE_LIB,
+                  os.path.join(build_dir, "tree"), [], verbose)
         if binding is not None:
             try:
                 _link_binding(binding.result())
@@ -163,7 +177,7 @@ def _compile_binding(build_dir: str) -> str:
 
 def _link_binding(obj: str) -> None:
     libs, tmp = os.path.join(_torch_root(), "lib"), BINDING_LIB + f".tmp{os.getpid()}"
-    _run(["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libdetfold_attn.so", "-Wl,-rpath,$ORIGIN", f"-L{libs}",
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libdetfold_attn.so", "-l:libdetfold_tree.so", "-Wl,-rpath,$ORIGIN", f"-L{libs}",
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "link of _attn_binding.so")
     os.replace(tmp, BINDING_LIB)
 

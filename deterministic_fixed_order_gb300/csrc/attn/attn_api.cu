@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "attn_checks.cuh"
 #include "attn_common.cuh"
 
 namespace {
@@ -18,52 +19,6 @@ int cuda_status(cudaError_t e)
     g_last_cuda_error = (int)e;
     (void)cudaGetLastError();  // clear a non-sticky launch error
     return DETFOLD_ERR_CUDA;
-}
-
-int esize(int dtype) { return dtype == DETFOLD_F32 ? 4 : 2; }
-bool known(int dtype) { return dtype == DETFOLD_F32 || dtype == DETFOLD_BF16 || dtype == DETFOLD_F16; }
-bool aligned(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
-
-// Half-open byte ranges [a, a+na) and [b, b+nb) intersect.
-bool intersects(const void *a, int64_t na, const void *b, int64_t nb)
-{
-    const uintptr_t ua = (uintptr_t)a, ub = (uintptr_t)b;
-    return ua < ub + (uintptr_t)nb && ub < ua + (uintptr_t)na;
-}
-
-constexpr int64_t kMaxElems = (int64_t)1 << 48;
-
-// Elements from the first to the last of a strided block, or -1 when a count
-// or stride is negative or the block is too large to address.
-int64_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t inner)
-{
-    if (s0 < 0 || s1 < 0 || s2 < 0 || n0 < 1 || n1 < 1 || n2 < 1 || inner < 1) return -1;
-    const __int128 e = (__int128)(n0 - 1) * s0 + (__int128)(n1 - 1) * s1 + (__int128)(n2 - 1) * s2 + inner;
-    return e > kMaxElems ? -1 : (int64_t)e;
-}
-
-// Whether neighbours of `n` blocks of `inner` elements share some: they may not where they are written.
-bool shares(int64_t n, int64_t stride, int64_t inner) { return n > 1 && stride < inner; }
-
-// A cache's shape; its pointers are checked by the calls that use them.
-int check_cache_shape(const detfold_kv_cache *c)
-{
-    if (!c) return DETFOLD_ERR_NULL;
-    if (!known(c->dtype)) return DETFOLD_ERR_ARG;
-    if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1) return DETFOLD_ERR_ARG;
-    if (c->page_size > DETFOLD_ATTN_MAX_COUNT || c->kv_heads > DETFOLD_ATTN_MAX_COUNT ||
-        c->head_dim > DETFOLD_ATTN_MAX_COUNT || c->num_pages > kMaxElems)
-        return DETFOLD_ERR_ARG;
-    if (extent(c->num_pages, c->page_stride, c->page_size, c->token_stride, c->kv_heads, c->head_stride,
-               c->head_dim) < 0)
-        return DETFOLD_ERR_ARG;
-    return DETFOLD_OK;
-}
-
-int64_t cache_bytes(const detfold_kv_cache *c)
-{
-    return extent(c->num_pages, c->page_stride, c->page_size, c->token_stride, c->kv_heads, c->head_stride,
-                  c->head_dim) * esize(c->dtype);
 }
 
 // The decode call's sizes, as far as they do not concern pointers.

@@ -1,0 +1,182 @@
+// Rows and pages of a paged cache moved in place: an accepted path's rows to the end of the
+// committed tokens, and whole pages. Copies of bytes, bound by memory: what moves is read and
+// written once, by the widest accesses that pointers and strides allow.
+#include "tree_common.cuh"
+
+namespace detfold_tree {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kFlight = 8;  // rows that a thread has in flight
+
+// Elements of B bytes that are moved at once.
+template <int B>
+struct Bytes;
+template <>
+struct Bytes<2> { using type = uint16_t; };
+template <>
+struct Bytes<4> { using type = uint32_t; };
+template <>
+struct Bytes<8> { using type = uint2; };
+template <>
+struct Bytes<16> { using type = uint4; };
+
+// A cache in units of B bytes.
+struct Units {
+    char *k, *v;
+    int64_t page, token, head;  // strides in bytes
+    int64_t a_head, a_row;      // units a head, units a row of all heads
+};
+Units units_of(const detfold_kv_cache &c, int es, int bytes)
+{
+    const int64_t a = (int64_t)c.head_dim * es / bytes;
+    return {(char *)c.k, (char *)c.v, c.page_stride * es, c.token_stride * es, c.head_stride * es, a, a * c.kv_heads};
+}
+
+// The widest unit that divides a head and every address: a stride whose count is 1 is not used.
+int widest(const detfold_kv_cache &c, int es)
+{
+    uint64_t all = (uint64_t)(uintptr_t)c.k | (uint64_t)(uintptr_t)c.v | (uint64_t)c.head_dim * es | 16;
+    if (c.num_pages > 1) all |= (uint64_t)c.page_stride * es;
+    if (c.page_size > 1) all |= (uint64_t)c.token_stride * es;
+    if (c.kv_heads > 1) all |= (uint64_t)c.head_stride * es;
+    return (int)(all & (0 - all));
+}
+
+// Row n + path[i] goes to row n + i, i ascending. A thread takes one place of the rows and all
+// of the path there. Within a group of kFlight all are read before one is written; an earlier group wrote
+// rows under n + i, and path[j] >= j >= i for the later ones, so every row is read as it was.
+template <int B>
+__global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactParams p, const Units u)
+{
+    using T = typename Bytes<B>::type;
+    __shared__ int64_t s_from[DETFOLD_TREE_MAX_NODES], s_to[DETFOLD_TREE_MAX_NODES];
+    enter_grid();
+    const int b = blockIdx.x, tid = threadIdx.x;
+    const int n = p.lens[b], count = p.path_lens[b];
+    bool bad = n < 0 || n > DETFOLD_ATTN_MAX_LEN - DETFOLD_TREE_MAX_NODES || count < 0 || count > p.max_path;
+    if (!bad && tid < count) {
+        const int32_t *path = p.path + b * p.path_stride;
+        const int j = path[tid], before = tid ? path[tid - 1] : -1;
+        bad = j <= before || j >= DETFOLD_TREE_MAX_NODES;
+        int64_t at[2] = {0, 0};
+        if (!bad && j != tid) {
+            const unsigned t[2] = {(unsigned)(n + j), (unsigned)(n + tid)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const unsigned col = t[k] / (unsigned)p.cache.page_size;
+                const int page = col < p.table_cols ? p.table[b * p.table_stride + col] : -1;
+                if (page < 0 || page >= p.cache.num_pages) bad = true;
+                at[k] = page * u.page + (int64_t)(t[k] - col * (unsigned)p.cache.page_size) * u.token;
+            }
+        }
+        s_from[tid] = at[0], s_to[tid] = at[1];
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && blockIdx.y == 0) flag_bad_index(p.status);
+        return;
+    }
+    // ascending from 0 on: what stays comes first
+    int first = 0;
+    while (first < count && s_from[first] == s_to[first]) ++first;
+    for (int64_t place = (int64_t)blockIdx.y * kThreads + tid; place < 2 * u.a_row; place += (int64_t)gridDim.y * kThreads) {
+        const bool value = place >= u.a_row;
+        const int64_t in = place - (value ? u.a_row : 0), h = in / u.a_head;
+        char *base = (value ? u.v : u.k) + h * u.head + (in - h * u.a_head) * B;
+        for (int i0 = first; i0 < count; i0 += kFlight) {
+            T x[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i)
+                if (i0 + i < count) x[i] = *reinterpret_cast<const T *>(base + s_from[i0 + i]);
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i)
+                if (i0 + i < count) *reinterpret_cast<T *>(base + s_to[i0 + i]) = x[i];
+        }
+    }
+}
+
+// Page src to page dst. A CTA takes a part of one pair's keys or values; threads go
+// along the rows that lie side by side in memory.
+template <int B>
+__global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyParams p, const Units u, int parts,
+                                                        bool by_head)
+{
+    using T = typename Bytes<B>::type;
+    enter_grid();
+    const int64_t units = p.count * 2 * parts;
+    for (int64_t w = blockIdx.x; w < units; w += gridDim.x) {
+        const int64_t i = w / (2 * parts);
+        const int rest = (int)(w - i * 2 * parts), part = rest >> 1;
+        const int src = p.src[i], dst = p.dst[i], rows = p.rows ? p.rows[i] : p.cache.page_size;
+        if (src < 0 || dst < 0 || src == dst) continue;
+        if (src >= p.cache.num_pages || dst >= p.cache.num_pages || rows < 0 || rows > p.cache.page_size) {
+            if (threadIdx.x == 0 && rest == 0) flag_bad_index(p.status);
+            continue;
+        }
+        const char *from = (rest & 1 ? u.v : u.k) + src * u.page;
+        char *to = (rest & 1 ? u.v : u.k) + dst * u.page;
+        const unsigned total = (unsigned)rows * (unsigned)u.a_row;  // units of this pair
+        const auto place = [&](unsigned x) {
+            const unsigned t = x / (unsigned)u.a_head, piece = x - t * (unsigned)u.a_head;
+            const unsigned lines = by_head ? (unsigned)rows : (unsigned)p.cache.kv_heads;
+            const unsigned outer = t / lines, inner = t - outer * lines;
+            return (by_head ? outer * u.head + inner * u.token : outer * u.token + inner * u.head) + (int64_t)piece * B;
+        };
+        const unsigned step = parts * kThreads;
+        for (unsigned x0 = part * kThreads + threadIdx.x; x0 < total; x0 += step * kFlight) {
+            T x[kFlight];
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j)
+                if (x0 + j * step < total) x[j] = *reinterpret_cast<const T *>(from + place(x0 + j * step));
+#pragma unroll
+            for (int j = 0; j < kFlight; ++j)
+                if (x0 + j * step < total) *reinterpret_cast<T *>(to + place(x0 + j * step)) = x[j];
+        }
+    }
+}
+
+template <int B>
+cudaError_t compact(const CompactParams &p, int es, cudaStream_t stream)
+{
+    const Units u = units_of(p.cache, es, B);
+    const int64_t across = (2 * u.a_row + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)p.batch, (unsigned)(across < 65535 ? across : 65535));
+    return launch_early(compact_kernel<B>, grid, kThreads, 0, stream, p, u);
+}
+
+template <int B>
+cudaError_t copy(const CopyParams &p, int es, cudaStream_t stream)
+{
+    const Units u = units_of(p.cache, es, B);
+    const bool by_head = p.cache.token_stride < p.cache.head_stride;
+    const int64_t page = (int64_t)p.cache.page_size * u.a_row;
+    int parts = (int)((page + kThreads * kFlight - 1) / (kThreads * kFlight));
+    const int64_t need = p.count * 2 * parts, most = kSms * 8;
+    return launch_early(copy_kernel<B>, dim3((unsigned)(need < most ? need : most)), kThreads, 0, stream, p, u, parts, by_head);
+}
+
+}  // namespace
+
+cudaError_t launch_compact(const CompactParams &p, cudaStream_t stream)
+{
+    const int es = p.cache.dtype == DETFOLD_F32 ? 4 : 2;
+    switch (widest(p.cache, es)) {
+    case 16: return compact<16>(p, es, stream);
+    case 8: return compact<8>(p, es, stream);
+    case 4: return compact<4>(p, es, stream);
+    default: return compact<2>(p, es, stream);
+    }
+}
+
+cudaError_t launch_copy(const CopyParams &p, cudaStream_t stream)
+{
+    const int es = p.cache.dtype == DETFOLD_F32 ? 4 : 2;
+    switch (widest(p.cache, es)) {
+    case 16: return copy<16>(p, es, stream);
+    case 8: return copy<8>(p, es, stream);
+    case 4: return copy<4>(p, es, stream);
+    default: return copy<2>(p, es, stream);
+    }
+}
+
+}  // namespace detfold_tree

@@ -1,0 +1,243 @@
+// The C ABI of libdetfold_tree (declared in include/detfold_tree.h): argument
+// checks and dispatch. Nothing here allocates, synchronizes or touches device
+// memory other than through stream-ordered launches.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "attn/attn_checks.cuh"
+#include "tree_common.cuh"
+
+namespace {
+
+using namespace detfold_tree;
+
+thread_local int g_last_cuda_error = 0;
+
+int cuda_status(cudaError_t e)
+{
+    if (e == cudaSuccess) return DETFOLD_OK;
+    g_last_cuda_error = (int)e;
+    (void)cudaGetLastError();  // clear a non-sticky launch error
+    return DETFOLD_ERR_CUDA;
+}
+
+// What a call reads or writes, as byte ranges.
+struct Range {
+    const void *at;
+    int64_t bytes;
+};
+bool meets(const Range &a, const Range &b)
+{
+    return a.at && b.at && a.bytes > 0 && b.bytes > 0 && intersects(a.at, a.bytes, b.at, b.bytes);
+}
+// Whether something written meets something read, or something else written.
+template <size_t W, size_t R>
+bool conflicts(const Range (&written)[W], const Range (&read)[R])
+{
+    for (size_t i = 0; i < W; ++i) {
+        for (size_t j = 0; j < R; ++j)
+            if (meets(written[i], read[j])) return true;
+        for (size_t j = i + 1; j < W; ++j)
+            if (meets(written[i], written[j])) return true;
+    }
+    return false;
+}
+
+int64_t table_bytes(int64_t rows, int64_t stride, int64_t cols)
+{
+    return extent(rows, stride, 1, 0, 1, 0, cols > 0 ? cols : 1) * 4;
+}
+
+// A cache that is written: its pointers, alignment and strides.
+int check_written_cache(const detfold_kv_cache *c)
+{
+    if (!c->k || !c->v) return DETFOLD_ERR_NULL;
+    const int es = esize(c->dtype);
+    if (!aligned(c->k, es) || !aligned(c->v, es)) return DETFOLD_ERR_ALIGN;
+    if (c->num_pages > INT32_MAX || shares(c->num_pages, c->page_stride, c->head_dim) ||
+        shares(c->page_size, c->token_stride, c->head_dim) || shares(c->kv_heads, c->head_stride, c->head_dim))
+        return DETFOLD_ERR_ARG;
+    // a page's elements are counted in 32 bits
+    const __int128 page = (__int128)c->page_size * c->kv_heads * c->head_dim;
+    return page > (1 << 30) ? DETFOLD_ERR_ARG : DETFOLD_OK;
+}
+
+int check_tree_sizes(const detfold_kv_cache *c, int batch, int nodes, int q_heads, int64_t max_len)
+{
+    if (int rc = check_cache_shape(c)) return rc;
+    if (c->head_dim > DETFOLD_ATTN_MAX_HEAD_DIM) return DETFOLD_ERR_ARG;
+    if (batch < 0 || batch > DETFOLD_ATTN_MAX_COUNT || nodes < 0 || nodes > DETFOLD_TREE_MAX_NODES || q_heads < 1 ||
+        q_heads > DETFOLD_ATTN_MAX_COUNT || q_heads % c->kv_heads != 0)
+        return DETFOLD_ERR_ARG;
+    if ((int64_t)batch * nodes * q_heads > ((int64_t)1 << 30)) return DETFOLD_ERR_ARG;
+    if (max_len < 0 || max_len > DETFOLD_ATTN_MAX_LEN) return DETFOLD_ERR_LEN;
+    return DETFOLD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int detfold_tree_plan(int64_t *mask, int64_t *positions, int64_t *slots, const int32_t *parents,
+                      const int32_t *seq_lens, const int32_t *node_counts, const int32_t *block_table,
+                      int64_t table_stride, int64_t table_cols, int page_size, int64_t num_pages, int batch, int nodes,
+                      int *d_status, void *stream)
+{
+    if (batch < 0 || batch > DETFOLD_ATTN_MAX_COUNT || nodes < 0 || nodes > DETFOLD_TREE_MAX_NODES)
+        return DETFOLD_ERR_ARG;
+    const bool none = batch == 0 || nodes == 0;
+    if (!none && (!mask || !parents || !seq_lens || (slots && table_cols > 0 && !block_table))) return DETFOLD_ERR_NULL;
+    if (slots && (page_size < 1 || page_size > DETFOLD_ATTN_MAX_COUNT || num_pages < 0 || table_stride < 0 || table_cols < 0))
+        return DETFOLD_ERR_ARG;
+    if (!aligned(mask, 8) || !aligned(positions, 8) || !aligned(slots, 8) || !aligned(parents, 4) ||
+        !aligned(seq_lens, 4) || !aligned(node_counts, 4) || !aligned(block_table, 4) || !aligned(d_status, 4))
+        return DETFOLD_ERR_ALIGN;
+    if (none) return DETFOLD_OK;
+    const int64_t per = (int64_t)batch * nodes, tb = slots ? table_bytes(batch, table_stride, table_cols) : 0;
+    if (tb < 0) return DETFOLD_ERR_ARG;
+    const Range written[] = {{mask, per * DETFOLD_TREE_WORDS(nodes) * 8}, {positions, per * 8}, {slots, per * 8}};
+    const Range read[] = {{parents, per * 4}, {seq_lens, (int64_t)batch * 4}, {node_counts, (int64_t)batch * 4},
+                          {slots ? block_table : nullptr, tb}};
+    if (conflicts(written, read)) return DETFOLD_ERR_OVERLAP;
+    const PlanParams p = {mask,         positions,  slots,     parents,   seq_lens, node_counts, block_table,
+                          table_stride, table_cols, num_pages, page_size, batch,    nodes,       d_status};
+    return cuda_status(launch_plan(p, (cudaStream_t)stream));
+}
+
+int64_t detfold_attn_tree_workspace_bytes(const detfold_kv_cache *cache, int batch, int nodes, int q_heads,
+                                          int64_t max_len)
+{
+    if (int rc = check_tree_sizes(cache, batch, nodes, q_heads, max_len)) return rc;
+    if (batch == 0 || nodes == 0) return 0;
+    return tree_workspace(cache->dtype, batch, nodes, cache->kv_heads, q_heads / cache->kv_heads, cache->head_dim,
+                          max_len);
+}
+
+int detfold_attn_tree(void *out, int64_t out_batch_stride, int64_t out_node_stride, int64_t out_head_stride, float *lse,
+                      const void *q, int64_t q_batch_stride, int64_t q_node_stride, int64_t q_head_stride,
+                      const detfold_kv_cache *cache, const int32_t *block_table, int64_t table_stride,
+                      int64_t table_cols, const int32_t *seq_lens, const int32_t *node_counts, const int64_t *mask,
+                      int batch, int nodes, int q_heads, int64_t max_len, float scale, int64_t window, void *workspace,
+                      int64_t workspace_bytes, int *d_status, void *stream)
+{
+    if (int rc = check_tree_sizes(cache, batch, nodes, q_heads, max_len)) return rc;
+    const bool none = batch == 0 || nodes == 0;
+    if (!cache->k || !cache->v) return DETFOLD_ERR_NULL;
+    if (!none && (!out || !q || !seq_lens || !mask || (table_cols > 0 && !block_table))) return DETFOLD_ERR_NULL;
+    if (window < 0 || (window != 0 && window < nodes) || table_cols < 0 || table_stride < 0) return DETFOLD_ERR_ARG;
+    if (max_len > 0 && (max_len - 1) / cache->page_size >= table_cols) return DETFOLD_ERR_LEN;
+    const int es = esize(cache->dtype), per16 = 16 / es;
+    if (!aligned(out, es) || !aligned(q, es) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(node_counts, 4) || !aligned(mask, 8) || !aligned(d_status, 4) || !aligned(cache->k, 16) ||
+        !aligned(cache->v, 16) || cache->page_stride % per16 || cache->token_stride % per16 ||
+        cache->head_stride % per16 || cache->head_dim % per16)
+        return DETFOLD_ERR_ALIGN;
+    if (none) return DETFOLD_OK;
+    const int d = cache->head_dim;
+    const int64_t ob = extent(batch, out_batch_stride, nodes, out_node_stride, q_heads, out_head_stride, d) * es;
+    const int64_t qb = extent(batch, q_batch_stride, nodes, q_node_stride, q_heads, q_head_stride, d) * es;
+    const int64_t tb = table_bytes(batch, table_stride, table_cols);
+    if (ob < 0 || qb < 0 || tb < 0 || shares(batch, out_batch_stride, d) || shares(nodes, out_node_stride, d) ||
+        shares(q_heads, out_head_stride, d))
+        return DETFOLD_ERR_ARG;
+    const int64_t need = detfold_attn_tree_workspace_bytes(cache, batch, nodes, q_heads, max_len);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return DETFOLD_ERR_WORKSPACE;
+    const int64_t cb = cache_bytes(cache), rows = (int64_t)batch * nodes;
+    const Range written[] = {{out, ob}, {lse, rows * q_heads * 4}, {need > 0 ? workspace : nullptr, need}};
+    const Range read[] = {{q, qb}, {cache->k, cb}, {cache->v, cb}, {block_table, tb}, {seq_lens, (int64_t)batch * 4},
+                          {node_counts, (int64_t)batch * 4}, {mask, rows * DETFOLD_TREE_WORDS(nodes) * 8}};
+    if (conflicts(written, read)) return DETFOLD_ERR_OVERLAP;
+    TreeParams p = {};
+    p.out = out, p.lse = lse, p.q = q;
+    p.out_bs = out_batch_stride, p.out_ns = out_node_stride, p.out_hs = out_head_stride;
+    p.q_bs = q_batch_stride, p.q_ns = q_node_stride, p.q_hs = q_head_stride;
+    p.k = cache->k, p.v = cache->v, p.num_pages = cache->num_pages;
+    p.page_stride = cache->page_stride, p.token_stride = cache->token_stride, p.head_stride = cache->head_stride;
+    p.table = block_table, p.lens = seq_lens, p.counts = node_counts, p.mask = mask, p.table_stride = table_stride;
+    p.page_size = cache->page_size, p.kv_heads = cache->kv_heads, p.head_dim = d, p.group = q_heads / cache->kv_heads;
+    p.batch = batch, p.nodes = nodes, p.words = DETFOLD_TREE_WORDS(nodes), p.q_heads = q_heads;
+    p.max_len = (int)max_len, p.window = window > max_len ? 0 : (int)window;
+    p.scale = scale, p.status = d_status;
+    return cuda_status(launch_tree(p, cache->dtype, workspace, (cudaStream_t)stream));
+}
+
+int detfold_kv_compact(const detfold_kv_cache *cache, const int32_t *block_table, int64_t table_stride,
+                       int64_t table_cols, const int32_t *seq_lens, const int32_t *path, int64_t path_stride,
+                       const int32_t *path_lens, int batch, int max_path, int *d_status, void *stream)
+{
+    if (int rc = check_cache_shape(cache)) return rc;
+    if (int rc = check_written_cache(cache)) return rc;
+    if (batch < 0 || batch > DETFOLD_ATTN_MAX_COUNT || max_path < 0 || max_path > DETFOLD_TREE_MAX_NODES ||
+        table_stride < 0 || table_cols < 0 || path_stride < 0)
+        return DETFOLD_ERR_ARG;
+    const bool none = batch == 0 || max_path == 0;
+    if (!none && (!seq_lens || !path || !path_lens || (table_cols > 0 && !block_table))) return DETFOLD_ERR_NULL;
+    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(path, 4) || !aligned(path_lens, 4) ||
+        !aligned(d_status, 4))
+        return DETFOLD_ERR_ALIGN;
+    if (none) return DETFOLD_OK;
+    const int64_t tb = table_bytes(batch, table_stride, table_cols), pb = table_bytes(batch, path_stride, max_path);
+    if (tb < 0 || pb < 0) return DETFOLD_ERR_ARG;
+    const int64_t cb = cache_bytes(cache), lb = (int64_t)batch * 4;
+    const Range read[] = {{block_table, tb}, {seq_lens, lb}, {path, pb}, {path_lens, lb}};
+    for (const void *c : {(const void *)cache->k, (const void *)cache->v})
+        for (const Range &r : read)
+            if (meets({c, cb}, r)) return DETFOLD_ERR_OVERLAP;
+    const CompactParams p = {*cache,     block_table, seq_lens, path,     path_lens, table_stride,
+                             table_cols, path_stride, batch,    max_path, d_status};
+    return cuda_status(launch_compact(p, (cudaStream_t)stream));
+}
+
+int detfold_kv_copy_pages(const detfold_kv_cache *cache, const int32_t *src, const int32_t *dst, const int32_t *rows,
+                          int64_t count, int *d_status, void *stream)
+{
+    if (int rc = check_cache_shape(cache)) return rc;
+    if (int rc = check_written_cache(cache)) return rc;
+    if (count < 0 || count > DETFOLD_ATTN_MAX_LEN) return DETFOLD_ERR_LEN;
+    if (count != 0 && (!src || !dst)) return DETFOLD_ERR_NULL;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(rows, 4) || !aligned(d_status, 4)) return DETFOLD_ERR_ALIGN;
+    if (count == 0) return DETFOLD_OK;
+    const int64_t cb = cache_bytes(cache);
+    const Range read[] = {{src, count * 4}, {dst, count * 4}, {rows, count * 4}};
+    for (const void *c : {(const void *)cache->k, (const void *)cache->v})
+        for (const Range &r : read)
+            if (meets({c, cb}, r)) return DETFOLD_ERR_OVERLAP;
+    const CopyParams p = {*cache, src, dst, rows, count, d_status};
+    return cuda_status(launch_copy(p, (cudaStream_t)stream));
+}
+
+int detfold_pages_step(int32_t *refs_out, int32_t *table_out, int64_t table_out_stride, int32_t *lens_out,
+                       int32_t *copy_src, int32_t *copy_dst, int32_t *copy_rows, const int32_t *refs,
+                       const int32_t *table, int64_t table_stride, const int32_t *lens, const int32_t *origin,
+                       const int32_t *keep, const int32_t *want, int64_t num_pages, int64_t table_cols, int page_size,
+                       int rows_in, int rows_out, int *d_status, void *stream)
+{
+    if (num_pages < 1 || num_pages > DETFOLD_ATTN_MAX_LEN || table_cols < 0 || table_cols > DETFOLD_ATTN_MAX_COUNT ||
+        page_size < 1 || page_size > DETFOLD_ATTN_MAX_COUNT || rows_in < 0 || rows_in > DETFOLD_PAGES_MAX_ROWS ||
+        rows_out < 0 || rows_out > DETFOLD_PAGES_MAX_ROWS || table_stride < 0 || table_out_stride < 0)
+        return DETFOLD_ERR_ARG;
+    if (!refs_out || !refs || (rows_in > 0 && (!lens || (table_cols > 0 && !table)))) return DETFOLD_ERR_NULL;
+    if (rows_out > 0 && (!lens_out || !copy_src || !copy_dst || !copy_rows || !origin || !keep || !want ||
+                         (table_cols > 0 && !table_out)))
+        return DETFOLD_ERR_NULL;
+    for (const void *x : {(const void *)refs_out, (const void *)table_out, (const void *)lens_out, (const void *)copy_src,
+                          (const void *)copy_dst, (const void *)copy_rows, (const void *)refs, (const void *)table,
+                          (const void *)lens, (const void *)origin, (const void *)keep, (const void *)want,
+                          (const void *)d_status})
+        if (!aligned(x, 4)) return DETFOLD_ERR_ALIGN;
+    const int64_t rb = num_pages * 4, ib = (int64_t)rows_in * 4, ob = (int64_t)rows_out * 4;
+    const int64_t tb = rows_in > 0 && table_cols > 0 ? table_bytes(rows_in, table_stride, table_cols) : 0;
+    const int64_t sb = rows_out > 0 && table_cols > 0 ? table_bytes(rows_out, table_out_stride, table_cols) : 0;
+    if (tb < 0 || sb < 0 || shares(rows_out, table_out_stride, table_cols)) return DETFOLD_ERR_ARG;
+    const Range written[] = {{refs_out, rb}, {table_out, sb}, {lens_out, ob}, {copy_src, ob}, {copy_dst, ob}, {copy_rows, ob}};
+    const Range read[] = {{refs == refs_out ? nullptr : refs, rb}, {table, tb}, {lens, ib}, {origin, ob}, {keep, ob}, {want, ob}};
+    if (conflicts(written, read)) return DETFOLD_ERR_OVERLAP;
+    const PagesParams p = {refs_out, table_out, lens_out, copy_src, copy_dst, copy_rows, refs, table, lens, origin,
+                           keep, want, table_out_stride, table_stride, (int)num_pages, (int)table_cols, page_size,
+                           rows_in, rows_out, d_status};
+    return cuda_status(launch_pages(p, (cudaStream_t)stream));
+}
+
+int detfold_tree_last_cuda_error(void) { return g_last_cuda_error; }
+
+}  // extern "C"

@@ -1,0 +1,198 @@
+// Attention of trees of drafted tokens: the pieces that every element type shares -- how a
+// sequence's work is cut, the masks, the fold of partial results and the join.
+//
+// Mathematics. A row is a (node, query head) pair. Over the tokens that its node attends to,
+// s_t = scale (q . k_t), m >= max s_t about, l = sum exp(s_t - m), a = sum exp(s_t - m) v_t; the
+// output is a / l, whatever m is. Two triples (m, l, a) join to
+//     m' = max(m, m_i), l' = l e^(m - m') + l_i e^(m_i - m'), a' likewise.
+//
+// Fixed order. The rows of one key-value head go by blocks ("pairs" of a sequence and such a
+// block); the tokens of a sequence, the committed ones that a root sees and then the drafted ones, by
+// chunks of tiles, and chunks by groups. All of it follows from the sequence's own length, tree and the head
+// counts. A group's triple is the fold of its chunks' in ascending order, the pair's the fold of its groups'.
+// The unit of work that a CTA takes is a chunk, or a whole group that it folds by itself where there is
+// work enough: the call's choice, which the bits do not depend on. Units of pairs that are
+// more than one leave their triples in the workspace for the join kernel.
+#pragma once
+
+#include "tree_common.cuh"
+
+namespace detfold_tree {
+
+// How sequences are cut, for one element type and head dimension.
+struct TreeRule {
+    int tok;    // tokens a tile
+    int rows;   // rows a pair's block, at most
+    int wide;   // rows of the widest block of this type: a call whose trees have fewer may take narrower ones,
+                // which are then one block a key-value head either way
+    int least;  // tiles a chunk, at least, for up to half of the widest block's rows; twice as many for more
+    int group;  // tiles a group, at least; 0: a group is a chunk
+};
+
+// CTAs that a sequence's chunks are to fill when it is alone.
+constexpr int kFill = kSms;
+
+struct TreeWork {
+    TreeParams p;
+    TreeRule rule;
+    int by_group;     // units are groups, else chunks
+    int slots;        // workspace slots a sequence, 0: no pair has more than one unit
+    int slot_rows;    // rows of a slot
+    Divide page;      // by the page size
+    float2 *ml;       // [batch][slots][slot_rows] (m, l)
+    float *acc;       // [batch][slots][slot_rows][head_dim]
+    int q_vec, out_vec;  // 16 bytes of q, of out, start at a multiple of 16
+};
+
+// Slots of one sequence: pairs x units never pass these, and they only grow with max_len. (There are at most
+// kFill / pairs chunks, or one.)
+inline int64_t slots_of(const TreeRule &r, int kv_heads, int group, int nodes, int64_t max_len)
+{
+    const int64_t blocks = ((int64_t)nodes * group + r.rows - 1) / r.rows, pairs = kv_heads * blocks;
+    const int64_t tiles = (max_len + r.tok - 1) / r.tok, chunks = (tiles + r.least - 1) / r.least;
+    if (chunks <= 1) return 0;
+    const int64_t full = pairs > kFill ? pairs : kFill;
+    return full < pairs * chunks ? full : pairs * chunks;
+}
+inline int slot_rows_of(const TreeRule &r, int group, int nodes)
+{
+    const int64_t rows = (int64_t)nodes * group;
+    return (int)(rows < r.rows ? rows : r.rows);
+}
+inline int64_t tree_need(const TreeRule &r, int batch, int kv_heads, int group, int nodes, int head_dim, int64_t max_len)
+{
+    const int64_t rows = (int64_t)batch * slots_of(r, kv_heads, group, nodes, max_len) * slot_rows_of(r, group, nodes);
+    return rows == 0 ? 0 : (rows * 8 + 15) / 16 * 16 + rows * head_dim * 4;
+}
+inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *workspace)
+{
+    TreeWork w = {};
+    w.p = p, w.rule = r;
+    w.slots = (int)slots_of(r, p.kv_heads, p.group, p.nodes, p.max_len);
+    w.slot_rows = slot_rows_of(r, p.group, p.nodes);
+    w.page = divide_by(p.page_size);
+    const int64_t rows = (int64_t)p.batch * w.slots * w.slot_rows;
+    w.ml = (float2 *)workspace;
+    w.acc = (float *)((char *)workspace + (rows * 8 + 15) / 16 * 16);
+    const int per = 16 / es;
+    w.q_vec = (uintptr_t)p.q % 16 == 0 && p.q_bs % per == 0 && p.q_ns % per == 0 && p.q_hs % per == 0;
+    w.out_vec = (uintptr_t)p.out % 16 == 0 && p.out_bs % per == 0 && p.out_ns % per == 0 && p.out_hs % per == 0;
+    return w;
+}
+cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream);
+
+#ifdef __CUDACC__
+
+// A sequence as the kernels see it.
+struct TreeSeq {
+    int n, c;       // committed tokens, nodes
+    int first;      // first token that a root sees
+    int end;        // n + c
+    int tiles, per; // tiles, and tiles a chunk
+    int chunks, each, units;  // chunks; chunks a unit; units a pair
+    int fold;       // chunks a group
+    int blocks, pairs;
+    bool bad;
+};
+
+// `n`, `c` as read. A sequence that cannot be attended to has one unit a pair and no tokens.
+__device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
+{
+    TreeSeq s;
+    const TreeParams &p = w.p;
+    const bool bad_count = c < 0 || c > p.nodes;
+    s.c = bad_count ? p.nodes : c;
+    s.bad = bad_count || n < 0 || n > p.max_len - s.c;
+    s.n = s.bad ? 0 : n;
+    s.first = p.window && s.n + 1 > p.window ? s.n + 1 - p.window : 0;
+    s.end = s.bad ? 0 : s.n + s.c;
+    const int rows = s.c * p.group;
+    s.blocks = (rows + w.rule.rows - 1) / w.rule.rows;
+    s.pairs = s.blocks * p.kv_heads;
+    s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) / w.rule.tok;
+    const int least = 2 * rows > w.rule.wide ? 2 * w.rule.least : w.rule.least;
+    const int most = s.pairs < kFill ? kFill / max(s.pairs, 1) : 1;
+    s.per = max(least, (s.tiles + most - 1) / most);
+    s.chunks = s.c == 0 ? 0 : max(1, (s.tiles + s.per - 1) / s.per);
+    s.fold = max(1, (w.rule.group + s.per - 1) / s.per);
+    s.each = w.by_group ? s.fold : 1;
+    s.units = (s.chunks + s.each - 1) / s.each;
+    return s;
+}
+__device__ __forceinline__ TreeSeq tree_seq_of(const TreeWork &w, int b)
+{
+    return tree_seq(w, w.p.lens[b], w.p.counts ? w.p.counts[b] : w.p.nodes);
+}
+
+// What a row's node sees: its mask without the bits behind the last node, and the first committed token.
+struct RowMask {
+    uint64_t bits[kMaxWords];
+    int from;
+};
+__device__ __forceinline__ RowMask row_mask(const TreeParams &p, int b, int node, const TreeSeq &s)
+{
+    RowMask m;
+    const int64_t *at = p.mask + ((int64_t)b * p.nodes + node) * p.words;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxWords; ++i) {
+        const int have = s.c - 64 * i;
+        m.bits[i] = i < p.words && have > 0 ? (uint64_t)at[i] & (have >= 64 ? ~0ull : (1ull << have) - 1) : 0;
+        count += __popcll(m.bits[i]);
+    }
+    m.from = p.window ? max(0, s.n + max(count, 1) - p.window) : 0;
+    return m;
+}
+// Bits for the 64 tokens from t on: the node sees them.
+__device__ __forceinline__ uint64_t seen_from(const RowMask &m, int n, int t)
+{
+    const int off = t - n;  // bit `off` of the mask comes first
+    uint64_t x = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxWords; ++i) {
+        const int sh = 64 * i - off;  // word i's first bit, from t on
+        if (sh >= 0 && sh < 64) x |= m.bits[i] << sh;
+        if (sh < 0 && sh > -64) x |= m.bits[i] >> -sh;
+    }
+    if (off < 0) {  // committed ones: from `from` on, before n
+        uint64_t before = off <= -64 ? ~0ull : (1ull << -off) - 1;
+        const int skip = m.from - t;
+        if (skip > 0) before = skip >= 64 ? 0 : before >> skip << skip;
+        x |= before;
+    }
+    return x;
+}
+
+// The factors of a fold of two triples whose maxima are in units of log 2, or of the natural logarithm.
+template <bool LOG2>
+__device__ __forceinline__ float fade(float x)
+{
+    if constexpr (LOG2) {
+        float y;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+        return y;
+    } else {
+        return exp_neg(x);
+    }
+}
+template <bool LOG2>
+__device__ __forceinline__ void fold_factors(float m, float mi, float &top, float &fa, float &fb)
+{
+    top = fmaxf(m, mi);
+    const float base = base_of(top);
+    fa = fade<LOG2>(__fsub_rn(m, base));
+    fb = fade<LOG2>(__fsub_rn(mi, base));
+}
+__device__ __forceinline__ float fold_in(float x, float y, float fa, float fb) { return __fmaf_rn(x, fa, __fmul_rn(y, fb)); }
+
+// The log-sum of a row.
+template <bool LOG2>
+__device__ __forceinline__ float log_sum(float m, float l)
+{
+    if (LOG2) return __fmul_rn(__fadd_rn(base_of(m), log2f(l)), kLn2);
+    return __fadd_rn(base_of(m), logf(l));
+}
+
+#endif  // __CUDACC__
+
+}  // namespace detfold_tree

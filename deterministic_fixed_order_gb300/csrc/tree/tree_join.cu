@@ -1,0 +1,104 @@
+// Joins the partial results of rows whose tokens lie in several units of work: a warp a row. The units'
+// triples are folded as the fixed order has it, chunks to groups and groups to the row, each in
+// ascending order. Bound by memory and latency: each accumulator is read once, several in flight.
+#include "tree_attn.cuh"
+
+namespace detfold_tree {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kAhead = 8;  // units whose accumulators a warp has in flight
+
+template <typename T, int PER, bool LOG2>
+__global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_constant__ TreeWork w)
+{
+    const TreeParams &p = w.p;
+    const int lane = threadIdx.x % 32;
+    enter_grid();
+    const int64_t rows = (int64_t)p.batch * p.nodes * p.q_heads;
+    for (int64_t row = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; row < rows; row += (int64_t)gridDim.x * kWarps) {
+        const int b = (int)(row / (p.nodes * p.q_heads)), in = (int)(row - (int64_t)b * p.nodes * p.q_heads);
+        const int node = in / p.q_heads, head = in - node * p.q_heads;
+        const TreeSeq s = tree_seq_of(w, b);
+        if (node >= s.c || s.units <= 1) continue;
+        const int kv = head / p.group, r = node * p.group + head - kv * p.group, block = r / w.rule.rows;
+        const int pair = kv * s.blocks + block;
+        const int64_t first = ((int64_t)b * w.slots + pair) * w.slot_rows + (r - block * w.rule.rows);
+        const int64_t step = (int64_t)s.pairs * w.slot_rows;
+        // lengths that change under the call: no unit past the workspace
+        const int units = min(s.units, w.slots / max(s.pairs, 1)), group = w.by_group ? 1 : s.fold;
+        float m = neg_inf(), l = 0.0f, a[PER], gm = neg_inf(), gl = 0.0f, ga[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) a[i] = ga[i] = 0.0f;
+        int left = group;
+        for (int u0 = 0; u0 < units; u0 += kAhead) {
+            float2 ml[kAhead];
+            float x[kAhead][PER];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (u0 + k >= units) continue;
+                const int64_t at = first + (u0 + k) * step;
+                ml[k] = w.ml[at];
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (lane + 32 * i < p.head_dim) x[k][i] = w.acc[at * p.head_dim + lane + 32 * i];
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (u0 + k >= units) continue;
+                float top, fa, fb;
+                if (left == group) {  // a group's first
+                    gm = ml[k].x, gl = ml[k].y;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) ga[i] = x[k][i];
+                } else {
+                    fold_factors<LOG2>(gm, ml[k].x, top, fa, fb);
+                    gm = top, gl = fold_in(gl, ml[k].y, fa, fb);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) ga[i] = fold_in(ga[i], x[k][i], fa, fb);
+                }
+                if (--left && u0 + k + 1 < units) continue;
+                if (u0 + k < group) {  // the first group
+                    m = gm, l = gl;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) a[i] = ga[i];
+                } else {
+                    fold_factors<LOG2>(m, gm, top, fa, fb);
+                    m = top, l = fold_in(l, gl, fa, fb);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) a[i] = fold_in(a[i], ga[i], fa, fb);
+                }
+                left = group;
+            }
+        }
+        T *out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane + 32 * i < p.head_dim) out[lane + 32 * i] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a[i], l));
+        if (lane == 0 && p.lse) p.lse[row] = log_sum<LOG2>(m, l);
+    }
+}
+
+template <typename T, bool LOG2>
+cudaError_t launch_type(const TreeWork &w, cudaStream_t stream)
+{
+    const int64_t need = ((int64_t)w.p.batch * w.p.nodes * w.p.q_heads + kWarps - 1) / kWarps, most = kSms * 8;
+    const dim3 grid((unsigned)(need < most ? need : most));
+    const auto kernel = w.p.head_dim <= 64    ? tree_join_kernel<T, 2, LOG2>
+                        : w.p.head_dim <= 128 ? tree_join_kernel<T, 4, LOG2>
+                                              : tree_join_kernel<T, 8, LOG2>;
+    return launch_early(kernel, grid, kWarps * 32, 0, stream, w);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream)
+{
+    switch (dtype) {
+    case DETFOLD_F32: return launch_type<float, false>(w, stream);
+    case DETFOLD_BF16: return launch_type<__nv_bfloat16, false>(w, stream);
+    default: return launch_type<__half, false>(w, stream);
+    }
+}
+
+}  // namespace detfold_tree

@@ -1,0 +1,270 @@
+// Attention of trees on the ordinary units: rows by blocks of four warps, a chunk of tokens a CTA.
+//
+// A tile of 32 tokens: a lane takes a token for the scores, of each of its warp's rows, then places of the
+// head for the weighted values; the weights pass through shared memory within the warp. Tiles come by
+// 16-byte asynchronous copies, one ahead.
+#include <atomic>
+
+#include "tree_attn.cuh"
+
+namespace detfold_tree {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32, kTok = 32;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void widen16(const void *at, float (&x)[16 / sizeof(T)])
+{
+    const Pack<T, 16 / sizeof(T)> y = *reinterpret_cast<const Pack<T, 16 / sizeof(T)> *>(at);
+#pragma unroll
+    for (int i = 0; i < 16 / (int)sizeof(T); ++i) x[i] = to_f32(y.v[i]);
+}
+
+// RW rows a warp; DP: the head dimension, rounded up.
+template <typename T, int DP, int RW>
+struct Simt {
+    static constexpr int kRows = kWarps * RW, kPer = 16 / sizeof(T), kPitch = DP * sizeof(T) + 16, kPlaces = DP / 32;
+    struct Shared {
+        float q[kRows][DP];
+        float weights[kWarps][RW][kTok];
+        RowMask masks[kRows];
+        alignas(16) unsigned char k[2][kTok * kPitch], v[2][kTok * kPitch];
+    };
+
+    static __device__ __forceinline__ void run(const TreeWork &w)
+    {
+        extern __shared__ __align__(128) unsigned char raw[];
+        Shared &sh = *reinterpret_cast<Shared *>(raw);
+        const TreeParams &p = w.p;
+        const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+        enter_grid();
+        for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
+            const TreeSeq s = tree_seq_of(w, b);
+            for (int64_t u = blockIdx.x; u < (int64_t)s.units * s.pairs; u += gridDim.x) {
+                const int chunk = (int)(u / s.pairs), pair = (int)(u - (int64_t)chunk * s.pairs);
+                const int kv = pair / s.blocks, row0 = (pair - kv * s.blocks) * w.rule.rows;
+                unit(w, sh, b, s, chunk, pair, kv, row0, warp, lane);
+                __syncthreads();
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void unit(const TreeWork &w, Shared &sh, int b, const TreeSeq &s, int chunk, int pair,
+                                                int kv, int row0, int warp, int lane)
+    {
+        const TreeParams &p = w.p;
+        const int tid = threadIdx.x, rows = min(w.rule.rows, s.c * p.group - row0);
+        const int t_lo = s.first + chunk * s.per * kTok, t_hi = min(s.end, t_lo + s.per * kTok);
+        for (int i = tid; i < kRows * DP; i += kThreads) {
+            const int r = i / DP, d = i - r * DP;
+            float x = 0.0f;
+            if (r < rows && d < p.head_dim) {
+                const int node = (row0 + r) / p.group, head = kv * p.group + (row0 + r) - node * p.group;
+                x = to_f32(((const T *)p.q)[b * p.q_bs + node * p.q_ns + head * p.q_hs + d]);
+            }
+            sh.q[r][d] = x;
+        }
+        if (tid < rows) sh.masks[tid] = row_mask(p, b, (row0 + tid) / p.group, s);
+        bool bad = s.bad;
+        const int pieces = p.head_dim / kPer, tiles = (t_hi - t_lo + kTok - 1) / kTok;
+        const auto fetch = [&](int tile) {
+            const int t = t_lo + tile * kTok + lane;
+            int64_t at = -1;
+            if (tile < tiles && t < t_hi) {
+                const unsigned col = quotient(t, w.page);
+                const int page = p.table[b * p.table_stride + col];
+                if (page >= 0 && page < p.num_pages)
+                    at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + kv * p.head_stride;
+                else
+                    bad = true;
+            }
+            unsigned char *k = sh.k[tile & 1], *v = sh.v[tile & 1];
+            if (tile < tiles)
+                for (int i = tid; i < kTok * (DP / kPer); i += kThreads) {
+                    const int r = i / (DP / kPer), d = i - r * (DP / kPer);
+                    const int64_t from = __shfl_sync(~0u, at, r);
+                    if (d >= pieces) continue;
+                    const int bytes = from < 0 ? 0 : 16;
+                    const int64_t el = from < 0 ? 0 : from + d * kPer;
+                    copy16((uint32_t)__cvta_generic_to_shared(k + r * kPitch + d * 16), (const T *)p.k + el, bytes);
+                    copy16((uint32_t)__cvta_generic_to_shared(v + r * kPitch + d * 16), (const T *)p.v + el, bytes);
+                }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        fetch(0);
+        float m[RW], l[RW], o[RW][kPlaces];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            m[r] = neg_inf(), l[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPlaces; ++i) o[r][i] = 0.0f;
+        }
+        for (int tile = 0; tile < tiles; ++tile) {
+            fetch(tile + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            const unsigned char *k = sh.k[tile & 1], *v = sh.v[tile & 1];
+            const int t0 = t_lo + tile * kTok, t = t0 + lane;
+            // every row sees every token here
+            const bool whole = t0 + kTok <= s.n && (!p.window || t0 >= s.n + s.c - p.window);
+            float x[RW];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) x[r] = 0.0f;
+            for (int d = 0; d < p.head_dim; d += kPer) {
+                float kk[kPer];
+                widen16<T>(k + lane * kPitch + d * sizeof(T), kk);
+#pragma unroll
+                for (int r = 0; r < RW; ++r)
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) x[r] = __fmaf_rn(sh.q[warp * RW + r][d + i], kk[i], x[r]);
+            }
+            uint32_t seen[RW];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) {
+                const int row = warp * RW + r;
+                seen[r] = ~0u;
+                x[r] = __fmul_rn(x[r], p.scale);
+                if (!whole) {
+                    bool here = false;
+                    if (row < rows && t < t_hi) {
+                        const RowMask &mk = sh.masks[row];
+                        const int j = t - s.n;
+                        here = j < 0 ? t >= mk.from : (mk.bits[j >> 6] >> (j & 63)) & 1;
+                    }
+                    if (!here) x[r] = neg_inf();
+                    seen[r] = __ballot_sync(~0u, here);
+                }
+                float top = x[r];
+#pragma unroll
+                for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
+                const float next = fmaxf(m[r], top), base = base_of(next), f = exp_neg(__fsub_rn(m[r], base));
+                const float y = (seen[r] >> lane) & 1 ? exp_neg(__fsub_rn(x[r], base)) : 0.0f;
+                l[r] = __fmaf_rn(l[r], f, y);
+                if (f != 1.0f) {
+#pragma unroll
+                    for (int i = 0; i < kPlaces; ++i) o[r][i] = __fmul_rn(o[r][i], f);
+                }
+                m[r] = next;
+                sh.weights[warp][r][lane] = y;
+            }
+            __syncwarp();
+            for (int j = 0; j < kTok; ++j) {
+                float vv[kPlaces];
+#pragma unroll
+                for (int i = 0; i < kPlaces; ++i) vv[i] = to_f32(*reinterpret_cast<const T *>(v + j * kPitch + (lane + 32 * i) * sizeof(T)));
+#pragma unroll
+                for (int r = 0; r < RW; ++r) {
+                    const float y = sh.weights[warp][r][j];
+                    if (whole || ((seen[r] >> j) & 1)) {
+#pragma unroll
+                        for (int i = 0; i < kPlaces; ++i) o[r][i] = __fmaf_rn(y, vv[i], o[r][i]);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        bad = __syncthreads_or(bad);
+        if (bad && tid == 0) flag_bad_index(p.status);
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const int row = warp * RW + r;
+            float sum = l[r];
+#pragma unroll
+            for (int i = 16; i; i >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(~0u, sum, i));
+            if (bad) sum = quiet_nan();
+            if (row >= rows) continue;
+            if (s.units > 1) {
+                const int64_t at = ((int64_t)b * w.slots + (int64_t)chunk * s.pairs + pair) * w.slot_rows + row;
+                if ((int64_t)chunk * s.pairs + pair >= w.slots) continue;  // lengths that change under the call
+                if (lane == 0) w.ml[at] = make_float2(m[r], sum);
+#pragma unroll
+                for (int i = 0; i < kPlaces; ++i)
+                    if (lane + 32 * i < p.head_dim) w.acc[at * p.head_dim + lane + 32 * i] = o[r][i];
+            } else {
+                const int node = (row0 + row) / p.group, head = kv * p.group + (row0 + row) - node * p.group;
+                T *out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
+#pragma unroll
+                for (int i = 0; i < kPlaces; ++i)
+                    if (lane + 32 * i < p.head_dim)
+                        out[lane + 32 * i] = from_f32<T>(sum == 0.0f ? 0.0f : __fdiv_rn(o[r][i], sum));
+                if (lane == 0 && p.lse)
+                    p.lse[((int64_t)b * p.nodes + node) * p.q_heads + head] = log_sum<false>(m[r], sum);
+            }
+        }
+    }
+};
+
+template <typename T, int DP, int RW>
+__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_constant__ TreeWork w)
+{
+    Simt<T, DP, RW>::run(w);
+}
+
+TreeRule simt_rule(int rows)
+{
+    return {kTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 0};
+}
+
+template <typename T, int DP, int RW>
+cudaError_t launch_rows(const TreeWork &w, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    using K = Simt<T, DP, RW>;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (!(dev < 64 && (done.load() & (1ull << dev)))) {
+        if (cudaError_t e = cudaFuncSetAttribute((const void *)tree_simt_kernel<T, DP, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)sizeof(typename K::Shared)))
+            return e;
+        done.fetch_or(1ull << (dev & 63));
+    }
+    const TreeParams &p = w.p;
+    const int64_t blocks = ((int64_t)p.nodes * p.group + w.rule.rows - 1) / w.rule.rows, pairs = p.kv_heads * blocks;
+    const int64_t need = w.slots ? (w.slots > pairs ? w.slots : pairs) : pairs;
+    const dim3 grid((unsigned)(need < (1 << 20) ? need : 1 << 20), (unsigned)(p.batch < 65535 ? p.batch : 65535));
+    if (cudaError_t e = launch_early(tree_simt_kernel<T, DP, RW>, grid, kThreads, sizeof(typename K::Shared), stream, w)) return e;
+    return cudaSuccess;
+}
+
+template <typename T, int DP>
+cudaError_t launch_dims(const TreeWork &w, cudaStream_t stream)
+{
+    switch (w.rule.rows) {
+    case 8: return launch_rows<T, DP, 2>(w, stream);
+    case 16: return launch_rows<T, DP, 4>(w, stream);
+    default: return launch_rows<T, DP, 8>(w, stream);
+    }
+}
+
+template <typename T>
+cudaError_t launch_type(const TreeWork &w, cudaStream_t stream)
+{
+    const int d = w.p.head_dim;
+    return d <= 64 ? launch_dims<T, 64>(w, stream) : d <= 128 ? launch_dims<T, 128>(w, stream) : launch_dims<T, 256>(w, stream);
+}
+
+}  // namespace
+
+int64_t tree_workspace(int dtype, int batch, int nodes, int kv_heads, int group, int head_dim, int64_t max_len)
+{
+    (void)dtype;
+    return tree_need(simt_rule(nodes * group), batch, kv_heads, group, nodes, head_dim, max_len);
+}
+
+cudaError_t launch_tree(const TreeParams &p, int dtype, void *workspace, cudaStream_t stream)
+{
+    const TreeWork w = tree_work(p, simt_rule(p.nodes * p.group), dtype == DETFOLD_F32 ? 4 : 2, workspace);
+    cudaError_t e = dtype == DETFOLD_F32    ? launch_type<float>(w, stream)
+                    : dtype == DETFOLD_BF16 ? launch_type<__nv_bfloat16>(w, stream)
+                                            : launch_type<__half>(w, stream);
+    if (e != cudaSuccess || !w.slots) return e;
+    return launch_tree_join(w, dtype, stream);
+}
+
+}  // namespace detfold_tree

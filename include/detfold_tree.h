@@ -1,0 +1,220 @@
+/*
+ * libdetfold_tree -- a step with drafted tokens over the paged key-value cache of
+ * detfold_attn.h, for GB300 (sm_103a).
+ *
+ * A draft gives every sequence a tree of tokens; one pass of the model answers all
+ * of them, and the tokens of one path are kept:
+ *   detfold_tree_plan      the trees' ancestor bits, positions and cache slots, from
+ *                          the nodes' parents;
+ *   detfold_attn_tree      attention of the trees' nodes over the cache: the committed
+ *                          tokens and the node's own ancestors;
+ *   detfold_kv_compact     move the accepted path's rows of the cache together;
+ *   detfold_kv_copy_pages  copy pages of the cache (a fork's last page, a pool that
+ *                          is packed before it shrinks);
+ *   detfold_pages_step     the bookkeeping of pages between steps: sequences begin,
+ *                          grow, fork, are cut back and end.
+ * Between the plan and the attention the drafted tokens' keys and values go to the
+ * cache with detfold_kv_append, at the plan's slots and positions. Partial
+ * attentions of ranks that hold parts of a cache join with detfold_attn_join, a node a
+ * row (a rank without drafted tokens passes nodes whose mask is empty).
+ *
+ * Fixed order: as for detfold_attn_decode, a sequence's attention is cut by its own
+ * length, tree and head counts alone, and the parts are folded in a fixed order, so a
+ * sequence gives the same bits alone or in any batch, in any pages. The bookkeeping
+ * gives pages out in ascending order.
+ *
+ * Conventions are those of detfold_attn.h: element types, strides in elements, no
+ * allocation, no synchronisation, stream-ordered work, host structures read only
+ * during the call, nothing enqueued on an error, calls without rows are no-ops,
+ * `d_status` written only when a kernel meets an index out of range in device
+ * memory, which is never used as an address. `d_status` then becomes
+ * DETFOLD_ERR_ARG; it becomes DETFOLD_ERR_SCRATCH_LIMIT where a pool has too few free
+ * pages, and DETFOLD_ERR_CUDA where a wait inside a kernel ran out (a fault of the
+ * device or of this library: the outputs are not valid).
+ */
+#ifndef DETFOLD_TREE_H
+#define DETFOLD_TREE_H
+
+#include "detfold_attn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Most nodes of a tree. */
+#define DETFOLD_TREE_MAX_NODES 256
+/* Words of 64 bits that hold one node's ancestors. */
+#define DETFOLD_TREE_WORDS(nodes) (((nodes) + 63) / 64)
+/* Most sequences (rows of a block table) of detfold_pages_step, before and after. */
+#define DETFOLD_PAGES_MAX_ROWS 4096
+
+/*
+ * Trees: for sequence b with n = seq_lens[b] committed tokens and the first
+ * c = node_counts[b] of its `nodes` nodes (all, when node_counts is NULL):
+ *     mask      bit j of words mask[b][i]: node j is node i or an ancestor of it
+ *     positions positions[b][i] = n + (number of ancestors of i)
+ *     slots     slots[b][i] = the cache slot of token n + i: row (n + i) % page_size of
+ *               page block_table[b][(n + i) / page_size]
+ * as detfold_attn_tree and detfold_kv_append take them. Nodes from c on have an empty
+ * mask, position 0 and slot -1.
+ *   mask        device int64 [batch][nodes][DETFOLD_TREE_WORDS(nodes)].
+ *   positions   device int64 [batch][nodes], or NULL.
+ *   slots       device int64 [batch][nodes], or NULL.
+ *   parents     device int32 [batch][nodes]: the node's parent, before it in
+ *               number, or -1 for a node that follows the committed tokens.
+ *   seq_lens    device int32 [batch].
+ *   node_counts device int32 [batch], or NULL.
+ *   block_table device int32, row b at b * table_stride, table_cols entries each;
+ *               needed with slots.
+ * A sequence whose length is negative or over DETFOLD_ATTN_MAX_LEN - nodes, whose count is
+ * out of range, or with a parent that is neither -1 nor an earlier node, is laid out as if
+ * it had no nodes (d_status). A token without a page (past the table's columns, or an
+ * entry outside [0, num_pages)) has slot -1 (d_status).
+ */
+DETFOLD_API int detfold_tree_plan(int64_t *mask, int64_t *positions, int64_t *slots, const int32_t *parents,
+                                  const int32_t *seq_lens, const int32_t *node_counts,
+                                  const int32_t *block_table, int64_t table_stride, int64_t table_cols,
+                                  int page_size, int64_t num_pages, int batch, int nodes, int *d_status,
+                                  void *stream);
+
+/*
+ * Bytes of device workspace that detfold_attn_tree needs for these sizes (cache: host,
+ * its pointers are not looked at). Never less for a larger max_len. Returns a negative
+ * status for invalid sizes.
+ */
+DETFOLD_API int64_t detfold_attn_tree_workspace_bytes(const detfold_kv_cache *cache, int batch, int nodes,
+                                                      int q_heads, int64_t max_len);
+
+/*
+ * Attention of trees: sequence b has n = seq_lens[b] committed tokens (rows 0 .. n - 1 of
+ * its cache) and c = node_counts[b] drafted ones (rows n .. n + c - 1; all `nodes` when
+ * node_counts is NULL). Node i attends to the drafted tokens n + j whose bit j < c its
+ * mask has, and to the committed tokens t -- with a window, to those of them with
+ * t > p - window, where p = n + max(1, bits of its mask below c) - 1 is its position. Over these, for
+ * query head h, which reads key-value head h / (q_heads / kv_heads):
+ *     s_t = scale * (q . k_t),  m = max s_t,  l = sum exp(s_t - m)
+ *     out = (sum exp(s_t - m) v_t) / l,  lse = m + ln l
+ * A node that attends to nothing gives out = 0 and lse = -inf. Keys and values that a node
+ * does not attend to have no part in its output, whatever they hold. Rows of out
+ * and lse of nodes from c on are left as they were.
+ *   out         device, element (b, i, h, d) at b * out_batch_stride + i * out_node_stride
+ *               + h * out_head_stride + d.
+ *   lse         device f32 [batch][nodes][q_heads], or NULL.
+ *   q           device, strides as out's.
+ *   cache       as for detfold_attn_decode (head_dim, alignment).
+ *   block_table, table_stride, table_cols, workspace  as for detfold_attn_decode.
+ *               Table entries of pages that hold no attended token are not read.
+ *   seq_lens    device int32 [batch].
+ *   node_counts device int32 [batch], or NULL.
+ *   mask        device int64 [batch][nodes][DETFOLD_TREE_WORDS(nodes)]. Any bits: a tree's
+ *               (detfold_tree_plan), a chain's, or others.
+ *   nodes       0 .. DETFOLD_TREE_MAX_NODES.
+ *   max_len     no n + c is larger; max_len <= table_cols * page_size.
+ *   window      0: no window; else at least `nodes`, since drafted tokens are not
+ *               windowed (DETFOLD_ERR_ARG).
+ * A sequence with n or c out of range, with n + c over max_len, or that needs a page outside
+ * the cache, gives NaN in out and lse (d_status): in the rows of all `nodes` where c is
+ * out of range, else of its c nodes. q_heads must be a multiple of kv_heads. batch == 0 or
+ * nodes == 0 is a no-op.
+ */
+DETFOLD_API int detfold_attn_tree(void *out, int64_t out_batch_stride, int64_t out_node_stride,
+                                  int64_t out_head_stride, float *lse, const void *q, int64_t q_batch_stride,
+                                  int64_t q_node_stride, int64_t q_head_stride, const detfold_kv_cache *cache,
+                                  const int32_t *block_table, int64_t table_stride, int64_t table_cols,
+                                  const int32_t *seq_lens, const int32_t *node_counts, const int64_t *mask,
+                                  int batch, int nodes, int q_heads, int64_t max_len, float scale,
+                                  int64_t window, void *workspace, int64_t workspace_bytes, int *d_status,
+                                  void *stream);
+
+/*
+ * Keep an accepted path: for sequence b with n = seq_lens[b] committed tokens, row
+ * n + path[b][i] of its cache goes to row n + i for i < path_lens[b], keys and values of
+ * every head. Rows are as before the call where they are read. The other rows stay as they were.
+ *   cache       written; element alignment is enough, wide accesses are used where
+ *               pointers and strides are 16-byte aligned.
+ *   block_table, table_stride, table_cols  as above; sequences share none of the rows
+ *               that are read or written.
+ *   seq_lens    device int32 [batch].
+ *   path        device int32, row b at b * path_stride, max_path entries each: node
+ *               numbers in ascending order.
+ *   path_lens   device int32 [batch].
+ *   max_path    0 .. DETFOLD_TREE_MAX_NODES.
+ * A sequence is left as it was (d_status) if its length or path length is out of range, its path
+ * does not ascend or has a number outside [0, DETFOLD_TREE_MAX_NODES), or a row that
+ * moves has no page. batch == 0 or max_path == 0 is a no-op.
+ */
+DETFOLD_API int detfold_kv_compact(const detfold_kv_cache *cache, const int32_t *block_table,
+                                   int64_t table_stride, int64_t table_cols, const int32_t *seq_lens,
+                                   const int32_t *path, int64_t path_stride, const int32_t *path_lens, int batch,
+                                   int max_path, int *d_status, void *stream);
+
+/*
+ * Copy pages: the first rows[i] rows (all, when rows is NULL) of page src[i] go to page
+ * dst[i], keys and values of every head. A pair with a negative page is skipped, and so is one whose
+ * pages are the same.
+ *   cache  written; alignment as for detfold_kv_compact.
+ *   src    device int32 [count].
+ *   dst    device int32 [count]: no page twice, and none that is also in src.
+ *   rows   device int32 [count], each 0 .. page_size, or NULL.
+ * A pair with a page past the cache or rows out of range is skipped (d_status).
+ * count == 0 is a no-op.
+ */
+DETFOLD_API int detfold_kv_copy_pages(const detfold_kv_cache *cache, const int32_t *src, const int32_t *dst,
+                                      const int32_t *rows, int64_t count, int *d_status, void *stream);
+
+/*
+ * Pages between steps. A pool of num_pages pages has a reference count a page (0: free).
+ * Row f of the block table before the step holds the pages of lens[f] tokens; row b after
+ * it keeps the first keep[b] tokens of row origin[b] (-1: none, keep[b] = 0) and has room
+ * for want[b] >= keep[b]:
+ *   a sequence that grows or is cut back  origin[b] = b, keep[b] = what stays;
+ *   one that begins or has ended          origin[b] = -1, keep[b] = 0, want[b] = its room or 0;
+ *   forks                                 several rows with the same origin.
+ * Rows of the old table that no row goes on from are released. With up(x) = ceil(x / page_size):
+ *   1. count = refs - (pages of old rows, up(lens[f]) each) + (pages that new rows
+ *      keep, up(keep[b]) each).
+ *   2. A row that gets room (want[b] > keep[b]) behind a last kept page that is not full (keep[b] %
+ *      page_size != 0), and that is not alone on that page (count > 1), needs a copy of it. So
+ *      the pages that a row may write to are its own.
+ *   3. A row needs up(want[b]) - up(keep[b]) pages, and one for the copy. Rows are served
+ *      in ascending order while the free pages (count == 0) last: a row that needs pages
+ *      is served if it and the rows before it need no more than there are.
+ *   4. Served rows get the free pages in ascending order, the copy's first, then those of
+ *      ascending columns.
+ * Pages that are released in a step can be given out in it.
+ *   refs_out    device int32 [num_pages]: the counts after the step (a copied page's less
+ *               its leaving rows, a new page's 1). It may be refs itself.
+ *   table_out   device int32, row b at b * table_out_stride, table_cols entries each; -1 where a row
+ *               holds no page.
+ *   lens_out    device int32 [rows_out]: want[b], or keep[b] where the row was not served
+ *               (d_status = DETFOLD_ERR_SCRATCH_LIMIT), which is less: such a row has only the
+ *               pages that it keeps.
+ *   copy_src, copy_dst, copy_rows  device int32 [rows_out]: for detfold_kv_copy_pages, to be run before
+ *               the next step; -1, -1 and 0 where nothing is to be copied.
+ *   refs        device int32 [num_pages].
+ *   table       device int32, row f at f * table_stride, table_cols entries each. A page is
+ *               held once by a row.
+ *   lens        device int32 [rows_in].
+ *   origin, keep, want  device int32 [rows_out].
+ * An old row whose length is out of range counts as empty (d_status). So does a new row whose origin is
+ * out of range, or whose keep is over that row's length, or want under keep or over the
+ * table's columns; its lens_out is 0. A held table entry outside the pool is passed over, and
+ * kept as -1 (d_status). rows_in and rows_out are 0 .. DETFOLD_PAGES_MAX_ROWS; with rows_out == 0 every
+ * row is released.
+ */
+DETFOLD_API int detfold_pages_step(int32_t *refs_out, int32_t *table_out, int64_t table_out_stride,
+                                   int32_t *lens_out, int32_t *copy_src, int32_t *copy_dst, int32_t *copy_rows,
+                                   const int32_t *refs, const int32_t *table, int64_t table_stride,
+                                   const int32_t *lens, const int32_t *origin, const int32_t *keep,
+                                   const int32_t *want, int64_t num_pages, int64_t table_cols, int page_size,
+                                   int rows_in, int rows_out, int *d_status, void *stream);
+
+/* The cudaError_t value of the last DETFOLD_ERR_CUDA that this library
+ * returned on the calling thread (0 if none). */
+DETFOLD_API int detfold_tree_last_cuda_error(void);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DETFOLD_TREE_H */
