@@ -79,6 +79,10 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
     w.out_vec = (uintptr_t)p.out % 16 == 0 && p.out_bs % per == 0 && p.out_ns % per == 0 && p.out_hs % per == 0;
     return w;
 }
+// The float32 kernel's: a block of as many rows as four warps take.
+constexpr int kSimtTok = 32;
+inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 0}; }
+
 cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream);
 
 #ifdef __CUDACC__
@@ -184,6 +188,16 @@ __device__ __forceinline__ void fold_factors(float m, float mi, float &top, floa
     fb = fade<LOG2>(__fsub_rn(mi, base));
 }
 __device__ __forceinline__ float fold_in(float x, float y, float fa, float fb) { return __fmaf_rn(x, fa, __fmul_rn(y, fb)); }
+
+// What a row's accumulator is multiplied by in the end, everywhere: in 16-bit types the reciprocal, its half unit in the last
+// place of binary32 far below theirs; in float32 the sum is divided by.
+__device__ __forceinline__ float inverse_of(float l) { return l == 0.0f ? 0.0f : __frcp_rn(l); }
+template <typename T>
+__device__ __forceinline__ T quotient_of(float a, float l, float inverse)
+{
+    if constexpr (sizeof(T) == 2) return from_f32<T>(__fmul_rn(a, inverse));
+    return from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a, l));
+}
 
 // The log-sum of a row.
 template <bool LOG2>

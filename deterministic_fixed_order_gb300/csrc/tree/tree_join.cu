@@ -72,9 +72,10 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
             }
         }
         T *out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
+        const float inverse = inverse_of(l);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (lane + 32 * i < p.head_dim) out[lane + 32 * i] = from_f32<T>(l == 0.0f ? 0.0f : __fdiv_rn(a[i], l));
+            if (lane + 32 * i < p.head_dim) out[lane + 32 * i] = quotient_of<T>(a[i], l, inverse);
         if (lane == 0 && p.lse) p.lse[row] = log_sum<LOG2>(m, l);
     }
 }
@@ -96,8 +97,8 @@ cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream)
 {
     switch (dtype) {
     case DETFOLD_F32: return launch_type<float, false>(w, stream);
-    case DETFOLD_BF16: return launch_type<__nv_bfloat16, false>(w, stream);
-    default: return launch_type<__half, false>(w, stream);
+    case DETFOLD_BF16: return launch_type<__nv_bfloat16, true>(w, stream);
+    default: return launch_type<__half, true>(w, stream);
     }
 }
 

@@ -1,0 +1,822 @@
+// Attention of trees in 16-bit types on the matrix units (tcgen05): 128 rows a CTA.
+//
+// S = Q K^T and O += P V are products of 128 rows by a tile's tokens: with a tree's nodes and a group's query heads
+// side by side a tile of keys and values is read once for all of them. The accumulators, S (two, in turn) and O,
+// lie in tensor memory, and P goes back there in the place of its S, so that the second product takes it
+// from there. P is split in two 16-bit parts (split2), both multiplied.
+//
+// Warps 0 to 3 have a row a thread: they mask, take the maximum, make the weights and, where a chunk ends, fold its
+// triple or write it. O is multiplied by the change of the maximum only where that grew by more than kSlack
+// (a power of two's exponent; weights stay below 2^(kShift + kSlack)). Warp 4 issues the products: a tile's scores ahead of the
+// weighted values of the tile before. Warps 5 and 6 copy: pages may be one token long and end inside a tile, so a
+// thread copies 16 bytes of a row at a time to where the swizzled operand has them, and writes by the generic
+// proxy are fenced before the products read them. One CTA an SM goes from unit to unit; the copies run ahead
+// over their ends. (Seven warps, two an SM's quarter, may have 255 registers a thread; a ninth would make that 168.)
+//
+// Tiles whose tokens are not seen by every row (the drafted ones, a window's edge) are masked by bits. There a value
+// that is not finite must not meet a weight of 0: such values are looked for, taken out of the tile, and added
+// by the rows that see them.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "attn/attn_split.cuh"
+#include "tree_attn.cuh"
+
+namespace detfold_tree {
+
+// NS: slabs of 64 elements of a head.
+template <typename T_, int NS>
+struct MmaShape {
+    using T = T_;
+    static constexpr int kTok = NS <= 2 ? 128 : 64;
+    static constexpr int kRows = 128;
+    static constexpr int kSlab = kTok * 128;        // bytes of a tile's slab: 128 a token
+    static constexpr int kSlot = NS * kSlab;
+    static constexpr int kQ = NS * kRows * 128;
+    static constexpr int kSlots = NS == 1 ? 8 : 5;  // tiles of keys or values in shared memory
+    static constexpr int kQs = NS == 4 ? 1 : 2;
+    static constexpr bool kFolds = NS <= 3;         // tensor memory has room for a second accumulator
+    static constexpr int kColO = 2 * kTok, kColF = kColO + NS * 64;
+    static constexpr int kShift = std::is_same_v<T, __half> ? 14 : 0, kSlack = std::is_same_v<T, __half> ? 1 : 8;
+    static constexpr int kBytes = kSlots * kSlot + kQs * kQ + 1024 + 1024;
+    // chunks of 256 tokens at least, groups of 1024
+    static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kFolds ? 1024 / kTok : 0}; }
+};
+
+#ifdef __CUDACC__
+
+// More units of a chunk each, as the longest sequence allows, than this many an SM: units are groups.
+constexpr int kByGroup = 4;
+constexpr int kSoftmax = 128, kCopy = 64, kMmaThreads = kSoftmax + 32 + kCopy;
+
+// ------------------------------------------------------------------ instructions
+
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t bar, int count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, int parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// Bounded: two seconds, or until another wait of this CTA has run out.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, int parity, volatile int *dead)
+{
+    if (bar_try(bar, parity)) return true;
+    long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (int i = 0; i < (1 << 24); ++i) {
+        if (bar_try(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (*dead || t - t0 > 2000000000LL) break;
+    }
+    *dead = 1;
+    return false;
+}
+// By a whole warp, with one verdict.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, int parity, volatile int *dead)
+{
+    return __all_sync(~0u, bar_wait(bar, parity, dead));
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void mma_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mma_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on `bar` when the products that this thread has issued are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+                 : "memory");
+}
+// An operand in shared memory in rows of 128 bytes, swizzled by 128 bytes, eight rows 1024 bytes on. `slab`: bytes
+// between blocks of 64 elements where these go along the rows that are not summed over.
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t slab)
+{
+    return (uint64_t)((at & 0x3ffff) >> 4) | (uint64_t)(slab >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// Accumulators binary32, 128 rows by n columns; the right operand by rows of what is summed over, or not.
+template <typename T>
+__device__ __forceinline__ uint32_t product(int n, bool right_along)
+{
+    const uint32_t type = std::is_same_v<T, __nv_bfloat16> ? 1 : 0;
+    return 1u << 4 | type << 7 | type << 10 | (uint32_t)right_along << 16 | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tm_load(float *x, uint32_t at)
+{
+    uint32_t *r = reinterpret_cast<uint32_t *>(x);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+                 "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tm_load_one(uint32_t &x, uint32_t at)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(at));
+}
+__device__ __forceinline__ void tm_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_store32(uint32_t at, const float *x)
+{
+    const uint32_t *r = reinterpret_cast<const uint32_t *>(x);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+                 "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+                 "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+                 "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+__device__ __forceinline__ void tm_store16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tm_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{ .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// ------------------------------------------------------------------ units of work
+
+// A unit: tiles [tile, end) of a pair.
+struct Unit {
+    TreeSeq s;
+    int b, pair, index, tile, end;
+};
+
+// A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By whole warps.
+struct Units {
+    int64_t next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
+    int b0, n, c;
+
+    __device__ __forceinline__ void load(const TreeWork &w)
+    {
+        const int lane = threadIdx.x % 32, b = b0 + lane;
+        upto = 0, n = 0, c = 0;
+        if (b < w.p.batch) {
+            n = w.p.lens[b], c = w.p.counts ? w.p.counts[b] : w.p.nodes;
+            const TreeSeq s = tree_seq(w, n, c);
+            upto = (int64_t)s.units * s.pairs;
+        }
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int64_t y = __shfl_up_sync(~0u, (long long)upto, k);
+            if (lane >= k) upto += y;
+        }
+    }
+    __device__ __forceinline__ void start(const TreeWork &w)
+    {
+        next = blockIdx.x, base = 0, b0 = 0;
+        load(w);
+    }
+    __device__ __forceinline__ bool take(const TreeWork &w, Unit &u)
+    {
+        int64_t all;
+        while ((all = __shfl_sync(~0u, (long long)upto, 31)) <= next - base) {
+            base += all;
+            b0 += 32;
+            if (b0 >= w.p.batch) return false;
+            load(w);
+        }
+        const int64_t at = next - base;
+        const int lane = __ffs(__ballot_sync(~0u, upto > at)) - 1;
+        u.b = b0 + lane;
+        u.s = tree_seq(w, __shfl_sync(~0u, n, lane), __shfl_sync(~0u, c, lane));
+        const int local = (int)(at - (__shfl_sync(~0u, (long long)upto, lane) - (int64_t)u.s.units * u.s.pairs));
+        u.index = local / u.s.pairs;
+        u.pair = local - u.index * u.s.pairs;
+        u.tile = u.index * u.s.each * u.s.per;
+        u.end = min(u.s.tiles, u.tile + u.s.each * u.s.per);
+        next += gridDim.x;
+        return true;
+    }
+};
+
+// ------------------------------------------------------------------ the kernel
+
+template <typename Shape>
+struct TreeMma {
+    using T = typename Shape::T;
+    static constexpr int kTok = Shape::kTok, kSlots = Shape::kSlots, kQs = Shape::kQs, kNS = Shape::kSlot / Shape::kSlab;
+
+    struct Control {
+        uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2], met, end;
+        uint32_t tmem;
+        int dead, keep_o;
+        int bad[16];         // the unit (counted from 1) that has a page outside the cache, by its last bits
+        uint32_t odd[2][4];  // tokens of a tile with values that are not finite, by turns
+    };
+
+    static __device__ __forceinline__ void run(const TreeWork &w)
+    {
+        extern __shared__ unsigned char raw[];
+        unsigned char *smem = raw + ((1024 - (smem_at(raw) & 1023)) & 1023);
+        const uint32_t ring = smem_at(smem), q = ring + kSlots * Shape::kSlot;
+        Control &ct = *reinterpret_cast<Control *>(smem + kSlots * Shape::kSlot + kQs * Shape::kQ);
+        static_assert(sizeof(Control) <= 1024, "as kBytes has it");
+        const int tid = threadIdx.x, warp = tid / 32;
+        if (tid == 0) {
+            for (int i = 0; i < kSlots; ++i) bar_init(smem_at(&ct.full[i]), kCopy), bar_init(smem_at(&ct.empty[i]), 1);
+            for (int i = 0; i < kQs; ++i) bar_init(smem_at(&ct.q_full[i]), kCopy), bar_init(smem_at(&ct.q_empty[i]), 1);
+            for (int i = 0; i < 2; ++i) {
+                bar_init(smem_at(&ct.s_full[i]), 1);
+                bar_init(smem_at(&ct.p_ready[i]), kSoftmax);
+                bar_init(smem_at(&ct.o_done[i]), 1);
+            }
+            bar_init(smem_at(&ct.met), 4);
+            bar_init(smem_at(&ct.end), 1);
+            ct.dead = 0, ct.keep_o = 0;
+            for (int i = 0; i < 16; ++i) ct.bad[i] = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        enter_grid();
+        if (warp == 4) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(&ct.tmem)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+            mma_before();
+        }
+        __syncthreads();
+        mma_after();
+        const uint32_t tmem = *(volatile uint32_t *)&ct.tmem;
+        if (warp < 4)
+            softmax(w, ct, smem, tmem + ((uint32_t)(warp * 32) << 16));
+        else if (warp == 4)
+            products(w, ct, ring, q, tmem);
+        else
+            copies(w, ct, ring, q);
+        __syncwarp();
+        mma_before();
+        __syncthreads();
+        mma_after();
+        if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        if (tid == 0 && ct.dead) flag(w.p.status, DETFOLD_ERR_CUDA);
+    }
+
+    // ---------------------------------------------------------- copies
+
+    // Copies that were started, in order, and whose barriers are still to be told: two at most, so that the
+    // products never wait for a copy that is told only after a slot that they hold is free again.
+    struct Told {
+        uint32_t first = 0, second = 0;
+        __device__ __forceinline__ void all()
+        {
+            if (!first) return;
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            fence_async();
+            bar_arrive(first);
+            if (second) bar_arrive(second);
+            first = second = 0;
+        }
+        __device__ __forceinline__ void add(uint32_t bar)
+        {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (!first) {
+                first = bar;
+            } else if (!second) {
+                second = bar;
+            } else {
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                fence_async();
+                bar_arrive(first);
+                first = second, second = bar;
+            }
+        }
+    };
+
+    static __device__ __forceinline__ void copy16(uint32_t dst, const T *src, bool some)
+    {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+    }
+
+    static __device__ __forceinline__ void copies(const TreeWork &w, Control &ct, uint32_t ring, uint32_t q)
+    {
+        constexpr int kLanes = kNS == 1 ? 8 : kNS == 2 ? 16 : 32;          // threads a row
+        constexpr int kTogether = kCopy / kLanes, kPasses = kTok / kTogether;  // rows at a time, times
+        constexpr int kOwn = 32 / kLanes;                                      // of them a warp's
+        constexpr int kHold = kPasses * kOwn / 32;                             // places that a lane looks up
+        const TreeParams &p = w.p;
+        const int tid = threadIdx.x - kSoftmax - 32, warp = tid / 32, lane = tid % 32;
+        const int piece = tid % kLanes, pieces = p.head_dim / 8, padded = (pieces + 1) / 2 * 2;
+        const int row0 = tid / kLanes, slab = piece / 8, chunk = piece % 8;
+        Told told;
+        Units units;
+        units.start(w);
+        Unit u;
+        int fill = 0, count = 0;
+        bool alive = true;
+        while (alive && units.take(w, u)) {
+            if (u.tile >= u.end) continue;
+            const int kv = u.pair / u.s.blocks, first_row = (u.pair - kv * u.s.blocks) * Shape::kRows;
+            const int rows = min(Shape::kRows, u.s.c * p.group - first_row);
+            const int seq = ++count;
+            const auto free = [&](uint32_t bar, int parity) {
+                if (bar_try(bar, parity)) return true;
+                told.all();
+                return bar_wait(bar, parity, &ct.dead);
+            };
+            const auto free_warp = [&](uint32_t bar, int parity) { return __all_sync(~0u, free(bar, parity)); };
+            // a tile's places: looked up a tile ahead
+            const auto look = [&](int tile, int h) {
+                const int mine = h * 32 + lane, row = mine / kOwn * kTogether + warp * kOwn + mine % kOwn;
+                const int t = u.s.first + tile * kTok + row;
+                int64_t at = -1;
+                if (tile < u.end && t < u.s.end) {
+                    const unsigned col = quotient(t, w.page);
+                    const int page = p.table[u.b * p.table_stride + col];
+                    if (page >= 0 && page < p.num_pages)
+                        at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + kv * p.head_stride;
+                    else
+                        ((volatile int *)ct.bad)[seq & 15] = seq;
+                }
+                return at;
+            };
+            int64_t places[kHold];
+#pragma unroll
+            for (int h = 0; h < kHold; ++h) places[h] = look(u.tile, h);
+            // queries: rows behind the last are zeros
+            const int qi = (seq - 1) % kQs, q_round = (seq - 1) / kQs;
+            if (!(alive = free_warp(smem_at(&ct.q_empty[qi]), (q_round & 1) ^ 1))) break;
+            if (piece < padded) {
+                for (int r = row0; r < Shape::kRows; r += kTogether) {
+                    const uint32_t dst = q + qi * Shape::kQ + slab * (Shape::kRows * 128) + r * 128 + ((chunk ^ (r & 7)) << 4);
+                    const T *src = (const T *)p.q;
+                    const bool some = r < rows && piece < pieces;
+                    if (some) {
+                        const int node = (first_row + r) / p.group, head = kv * p.group + first_row + r - node * p.group;
+                        src += u.b * p.q_bs + node * p.q_ns + head * p.q_hs + piece * 8;
+                    }
+                    if (w.q_vec || !some) {
+                        copy16(dst, src, some);
+                    } else {
+                        Pack<T, 8> x;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x.v[i] = src[i];
+                        const uint4 y = *reinterpret_cast<const uint4 *>(&x);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+                    }
+                }
+            }
+            told.add(smem_at(&ct.q_full[qi]));
+            for (int tile = u.tile; alive && tile < u.end; ++tile) {
+                int64_t now[kHold];
+#pragma unroll
+                for (int h = 0; h < kHold; ++h) now[h] = places[h], places[h] = look(tile + 1, h);
+#pragma unroll 1
+                for (int value = 0; value < 2; ++value) {
+                    const int slot = fill % kSlots;
+                    if (!(alive = free_warp(smem_at(&ct.empty[slot]), (fill / kSlots & 1) ^ 1))) break;
+                    const T *src = (const T *)(value ? p.v : p.k);
+                    const uint32_t to = ring + slot * Shape::kSlot + slab * Shape::kSlab;
+#pragma unroll
+                    for (int i = 0; i < kPasses; ++i) {
+                        const int r = row0 + i * kTogether;
+                        const int64_t at = __shfl_sync(~0u, (long long)now[i * kOwn / 32], (i * kOwn + lane / kLanes) % 32);
+                        const bool some = at >= 0 && piece < pieces;
+                        if (piece < padded) copy16(to + r * 128 + ((chunk ^ (r & 7)) << 4), src + (some ? at + piece * 8 : 0), some);
+                    }
+                    told.add(smem_at(&ct.full[slot]));
+                    ++fill;
+                }
+            }
+        }
+        told.all();
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+
+    // ---------------------------------------------------------- products
+
+    static __device__ __forceinline__ void products(const TreeWork &w, Control &ct, uint32_t ring, uint32_t q, uint32_t tmem)
+    {
+        const int d16 = (w.p.head_dim + 15) / 16 * 16, lane = threadIdx.x % 32;
+        const uint32_t scores = product<T>(kTok, false), values = product<T>(d16, true);
+        Units ahead, behind;
+        ahead.start(w);
+        behind = ahead;
+        Unit a, v;
+        bool more_a, more_v;
+        // units without tokens have no products
+        const auto next = [&](Units &units, Unit &u) {
+            do
+                if (!units.take(w, u)) return false;
+            while (u.tile >= u.end);
+            return true;
+        };
+        more_a = next(ahead, a);
+        more_v = next(behind, v);
+        bool fresh = true;  // the first tile of unit a
+        int ga = 0, gv = 0, unit = 0;
+        while (more_v) {
+            if (more_a) {
+                const int slot = 2 * ga % kSlots;
+                const int qi = unit % kQs;
+                if (fresh && !warp_wait(smem_at(&ct.q_full[qi]), unit / kQs & 1, &ct.dead)) break;
+                if (!warp_wait(smem_at(&ct.full[slot]), 2 * ga / kSlots & 1, &ct.dead)) break;
+                // the weights that lay here have been multiplied
+                if (ga >= 2 && !warp_wait(smem_at(&ct.o_done[ga & 1]), (ga - 2) / 2 & 1, &ct.dead)) break;
+                mma_after();
+                if (lane == 0) {
+                    const uint32_t left = q + qi * Shape::kQ, right = ring + slot * Shape::kSlot;
+                    for (int k = 0; k < d16 / 16; ++k) {
+                        const uint32_t in = (k & 3) * 32;
+                        mma_ss(tmem + (ga & 1) * kTok, operand(left + (k >> 2) * (Shape::kRows * 128) + in, 16),
+                               operand(right + (k >> 2) * Shape::kSlab + in, 16), scores, k > 0);
+                    }
+                    mma_commit(smem_at(&ct.empty[slot]));
+                    mma_commit(smem_at(&ct.s_full[ga & 1]));
+                    if (a.tile + 1 == a.end) mma_commit(smem_at(&ct.q_empty[qi]));
+                }
+                __syncwarp();
+                ++ga;
+                fresh = false;
+                if (++a.tile == a.end) {
+                    more_a = next(ahead, a);
+                    fresh = true;
+                    ++unit;
+                }
+                if (ga == 1 && more_a) continue;  // one tile ahead
+            }
+            const int fill = 2 * gv + 1, slot = fill % kSlots;
+            if (!warp_wait(smem_at(&ct.p_ready[gv & 1]), gv / 2 & 1, &ct.dead)) break;
+            if (!warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) break;
+            mma_after();
+            if (lane == 0) {
+                const bool first = (v.tile % v.s.per) == 0;
+                bool add = !first || *(volatile int *)&ct.keep_o;
+                const uint32_t right = ring + slot * Shape::kSlot, weights = tmem + (gv & 1) * kTok;
+                for (int part = 0; part < 2; ++part)
+                    for (int k = 0; k < kTok / 16; ++k) {
+                        mma_ts(tmem + Shape::kColO, weights + part * (kTok / 2) + k * 8, operand(right + k * 2048, Shape::kSlab), values, add);
+                        add = true;
+                    }
+                mma_commit(smem_at(&ct.empty[slot]));
+                mma_commit(smem_at(&ct.o_done[gv & 1]));
+            }
+            __syncwarp();
+            ++gv;
+            if (++v.tile == v.end) more_v = next(behind, v);
+        }
+        // whatever was issued is done before the tensor memory goes back
+        if (lane == 0) mma_commit(smem_at(&ct.end));
+        __syncwarp();
+        warp_wait(smem_at(&ct.end), 0, &ct.dead);
+    }
+
+    // ---------------------------------------------------------- softmax
+
+    // The four softmax warps meet; bounded like every wait.
+    static __device__ __forceinline__ bool meet(Control &ct, int &meetings)
+    {
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) bar_arrive(smem_at(&ct.met));
+        return warp_wait(smem_at(&ct.met), meetings++ & 1, &ct.dead);
+    }
+    // Where 16 bytes of a tile's row lie.
+    static __device__ __forceinline__ uint4 *piece_of(unsigned char *slot, int row, int piece)
+    {
+        return reinterpret_cast<uint4 *>(slot + (piece >> 3) * Shape::kSlab + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+    }
+    // Above the largest finite number, as 16 bits without the sign.
+    static constexpr uint32_t kInf = std::is_same_v<T, __nv_bfloat16> ? 0x7f80 : 0x7c00;
+
+    static __device__ __forceinline__ bool row_is_odd(unsigned char *slot, int row, int pieces)
+    {
+        uint32_t top = 0;
+        for (int i = 0; i < pieces; ++i) {
+            const uint4 x = *piece_of(slot, row, i);
+            top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fff), x.y & 0x7fff7fff);
+            top = __vmaxu2(__vmaxu2(top, x.z & 0x7fff7fff), x.w & 0x7fff7fff);
+        }
+        return (top & 0xffff) >= kInf || (top >> 16) >= kInf;
+    }
+
+    // Values that are not finite, in a tile that not every row sees: added by the rows that see them, then zeros.
+    static __device__ __noinline__ bool odd_values(Control &ct, const volatile uint32_t *odd, int &meetings, unsigned char *slot,
+                                                   uint32_t weights, uint32_t o, int d, bool first, bool works)
+    {
+        const int tid = threadIdx.x, blocks = (d + 31) / 32, pieces = d / 8;
+        for (int cb = 0; works && cb < blocks; ++cb) {
+            float x[32];
+            if (first) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+            } else {
+                tm_load(x, o + cb * 32);
+                tm_loaded();
+            }
+            for (int word = 0; word < kTok / 32; ++word)
+                for (uint32_t left = odd[word]; left; left &= left - 1) {
+                    const int j = word * 32 + __ffs(left) - 1;
+                    uint32_t hi, lo;
+                    tm_load_one(hi, weights + j / 2);
+                    tm_load_one(lo, weights + kTok / 2 + j / 2);
+                    tm_loaded();
+                    if (j & 1) hi >>= 16, lo >>= 16;
+                    T h, l;
+                    const uint16_t h16 = (uint16_t)hi, l16 = (uint16_t)lo;
+                    memcpy(&h, &h16, 2), memcpy(&l, &l16, 2);
+                    const float weight = __fadd_rn(to_f32(h), to_f32(l));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (weight == 0.0f || cb * 4 + k >= pieces) continue;  // not seen
+                        const Pack<T, 8> y = *reinterpret_cast<const Pack<T, 8> *>(piece_of(slot, j, cb * 4 + k));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float z = to_f32(y.v[i]);
+                            if (!(fabsf(z) < __int_as_float(0x7f800000))) x[k * 8 + i] = __fmaf_rn(weight, z, x[k * 8 + i]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            tm_store32(o + cb * 32, x);
+        }
+        tm_stored();
+        if (!meet(ct, meetings)) return false;
+        if (tid < kTok && (odd[tid / 32] >> (tid % 32)) & 1)
+            for (int i = 0; i < pieces; ++i) {
+                Pack<T, 8> y = *reinterpret_cast<const Pack<T, 8> *>(piece_of(slot, tid, i));
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (!(fabsf(to_f32(y.v[k])) < __int_as_float(0x7f800000))) y.v[k] = from_f32<T>(0.0f);
+                *piece_of(slot, tid, i) = *reinterpret_cast<const uint4 *>(&y);
+            }
+        fence_async();
+        if (tid == 0 && first) *(volatile int *)&ct.keep_o = 1;
+        return true;
+    }
+
+    // A row's result, or its triple, 32 places of the head at a time.
+    static __device__ __forceinline__ void put(const TreeWork &w, const float (&x)[32], int d0, T *out, float *acc, float inverse)
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (d0 + 8 * k >= w.p.head_dim) continue;
+            if (out) {
+                Pack<T, 8> y;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y.v[i] = quotient_of<T>(x[8 * k + i], 0.0f, inverse);
+                if (w.out_vec) {
+                    *reinterpret_cast<Pack<T, 8> *>(out + d0 + 8 * k) = y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) out[d0 + 8 * k + i] = y.v[i];
+                }
+            } else {
+                float4 *to = reinterpret_cast<float4 *>(acc + d0 + 8 * k);
+                to[0] = make_float4(x[8 * k], x[8 * k + 1], x[8 * k + 2], x[8 * k + 3]);
+                to[1] = make_float4(x[8 * k + 4], x[8 * k + 5], x[8 * k + 6], x[8 * k + 7]);
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void softmax(const TreeWork &w, Control &ct, unsigned char *smem, uint32_t tmem)
+    {
+        const TreeParams &p = w.p;
+        const int tid = threadIdx.x, warp = tid / 32, blocks = (p.head_dim + 31) / 32;
+        const float scale = __fmul_rn(p.scale, kLog2e);
+        const uint32_t o = tmem + Shape::kColO, f = tmem + Shape::kColF;
+        Units units;
+        units.start(w);
+        Unit u;
+        int g = 0, count = 0, meetings = 0;
+        while (units.take(w, u)) {
+            const TreeSeq &s = u.s;
+            const int kv = u.pair / s.blocks, first_row = (u.pair - kv * s.blocks) * Shape::kRows;
+            const int rows = min(Shape::kRows, s.c * p.group - first_row);
+            const bool live = tid < rows, works = warp * 32 < rows;
+            const int node = live ? (first_row + tid) / p.group : 0;
+            const int head = live ? kv * p.group + first_row + tid - node * p.group : 0;
+            T *out = nullptr;
+            float *acc = nullptr;
+            int64_t slot_row = -1;
+            if (s.units == 1) {
+                out = (T *)p.out + u.b * p.out_bs + node * p.out_ns + head * p.out_hs;
+            } else {
+                const int64_t at = (int64_t)u.index * s.pairs + u.pair;
+                // lengths that change under the call: nothing past the workspace
+                if (at < w.slots) slot_row = ((int64_t)u.b * w.slots + at) * w.slot_rows + tid, acc = w.acc + slot_row * p.head_dim;
+            }
+            const bool puts = live && (out || acc);
+            const auto finish = [&](float m, float l) {
+                if (!puts) return;
+                if (!out)
+                    w.ml[slot_row] = make_float2(m, l);
+                else if (p.lse)
+                    p.lse[((int64_t)u.b * p.nodes + node) * p.q_heads + head] = log_sum<true>(m, l);
+            };
+            if (u.tile >= u.end) {  // a sequence that cannot be attended to
+                float x[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = quiet_nan();
+                for (int cb = 0; puts && cb < blocks; ++cb) put(w, x, cb * 32, out, acc, 1.0f);
+                finish(0.0f, quiet_nan());
+                if (tid == 0) flag_bad_index(p.status);
+                continue;
+            }
+            const RowMask mask = row_mask(p, u.b, node, s);
+            ++count;
+            bool bad = false;
+            float fm = neg_inf(), fl = 0.0f;  // of the chunks before
+            for (int t0 = u.tile; t0 < u.end; t0 += s.per) {
+                const int t1 = min(u.end, t0 + s.per);
+                float m = neg_inf(), l = 0.0f;
+                for (int tile = t0; tile < t1; ++tile, ++g) {
+                    const int at = s.first + tile * kTok;
+                    const bool whole = at + kTok <= s.n && (!p.window || at >= s.n + s.c - p.window);
+                    const uint32_t here = tmem + (g & 1) * kTok;
+                    if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
+                    mma_after();
+                    bool waited = tile == t0;  // for the tile before, whose product O may still change
+                    const auto settle = [&]() {
+                        if (waited) return true;
+                        waited = true;
+                        if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return false;
+                        mma_after();
+                        return true;
+                    };
+                    if (works) {
+                        float x[kTok];
+#pragma unroll
+                        for (int i = 0; i < kTok; i += 32) tm_load(x + i, here + i);
+                        tm_loaded();
+#pragma unroll
+                        for (int i = 0; i < kTok; i += 2) {
+                            const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(scale, scale));
+                            x[i] = y.x, x[i + 1] = y.y;
+                        }
+                        if (!whole) {
+#pragma unroll
+                            for (int half = 0; half < kTok / 64; ++half) {
+                                const uint64_t seen = seen_from(mask, s.n, at + half * 64);
+#pragma unroll
+                                for (int i = 0; i < 64; ++i)
+                                    if (!((seen >> i) & 1)) x[half * 64 + i] = neg_inf();
+                            }
+                        }
+                        float top4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                        for (int i = 4; i < kTok; ++i) top4[i & 3] = fmaxf(top4[i & 3], x[i]);
+                        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                        const bool moves = top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack));
+                        if (__any_sync(~0u, moves)) {
+                            const float next = moves ? __fsub_rn(top, (float)Shape::kShift) : m;
+                            const float fall = moves ? fade<true>(__fsub_rn(m, base_of(next))) : 1.0f;
+                            m = next;
+                            l = __fmul_rn(l, fall);
+                            if (tile != t0) {
+                                if (!settle()) return;
+                                for (int cb = 0; cb < blocks; ++cb) {
+                                    float y[32];
+                                    tm_load(y, o + cb * 32);
+                                    tm_loaded();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], fall);
+                                    tm_store32(o + cb * 32, y);
+                                }
+                            }
+                        }
+                        const float base = base_of(m);
+                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                        for (int i = 0; i < kTok; i += 32) {
+                            uint32_t hi[16], lo[16];
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 e = add2(make_float2(x[i + k], x[i + k + 1]), make_float2(-base, -base));
+                                const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
+                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
+                                split2(y.x, y.y, hi[k / 2], lo[k / 2], T());
+                            }
+                            tm_store16(here + i / 2, hi);
+                            tm_store16(here + kTok / 2 + i / 2, lo);
+                        }
+                        l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
+                        tm_stored();
+                    }
+                    if (tid == 0 && tile == t0) *(volatile int *)&ct.keep_o = 0;
+                    // The values have come, and are not given up before the weights below are told.
+                    const int fill = 2 * g + 1, slot = fill % kSlots;
+                    if ((!whole || tile + 1 == u.end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
+                    // every copy of this unit has been told: what it found is known
+                    if (tile + 1 == u.end) bad = ((volatile int *)ct.bad)[count & 15] == count;
+                    if (!whole) {
+                        unsigned char *values = smem + slot * Shape::kSlot;
+                        const uint32_t word = __ballot_sync(~0u, tid < kTok && row_is_odd(values, tid, p.head_dim / 8));
+                        volatile uint32_t *odd = ct.odd[meetings & 1];
+                        if (tid % 32 == 0) odd[warp] = word;
+                        if (!meet(ct, meetings)) return;
+                        if (odd[0] | odd[1] | odd[2] | odd[3]) {
+                            if (!settle() || !odd_values(ct, odd, meetings, values, here, o, p.head_dim, tile == t0, works)) return;
+                        }
+                    }
+                    mma_before();
+                    bar_arrive(smem_at(&ct.p_ready[g & 1]));
+                }
+                // the chunk's end: O is whole
+                if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return;
+                mma_after();
+                const bool last = t1 == u.end;
+                if (last && bad) {
+                    l = quiet_nan();
+                    if (tid == 0) flag_bad_index(p.status);
+                }
+                if (!works) continue;
+                const bool before = t0 != u.tile;
+                float top = m, fa = 0.0f, fb = 1.0f, sum = l;
+                if (before) {
+                    fold_factors<true>(fm, m, top, fa, fb);
+                    sum = fold_in(fl, l, fa, fb);
+                }
+                const float inverse = inverse_of(sum);
+                for (int cb = 0; cb < blocks; ++cb) {
+                    float x[32];
+                    tm_load(x, o + cb * 32);
+                    if (Shape::kFolds && before) {
+                        float y[32];
+                        tm_load(y, f + cb * 32);
+                        tm_loaded();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = fold_in(y[i], x[i], fa, fb);
+                    } else {
+                        tm_loaded();
+                    }
+                    if (!last) {
+                        if (Shape::kFolds) tm_store32(f + cb * 32, x);
+                    } else if (puts) {
+                        put(w, x, cb * 32, out, acc, inverse);
+                    }
+                }
+                __syncwarp();
+                if (!last)
+                    tm_stored();
+                else
+                    finish(top, sum);
+                fm = top, fl = sum;
+            }
+        }
+    }
+};
+
+template <typename Shape>
+__global__ void __launch_bounds__(kMmaThreads, 1) tree_mma_kernel(const __grid_constant__ TreeWork w)
+{
+    TreeMma<Shape>::run(w);
+}
+
+template <typename Shape>
+cudaError_t launch_mma(TreeWork w, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = tree_mma_kernel<Shape>;
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (!(dev < 64 && (done.load(std::memory_order_acquire) & (1ull << dev)))) {
+        if (cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes))
+            return e;
+        done.fetch_or(1ull << (dev & 63), std::memory_order_release);
+    }
+    const TreeParams &p = w.p;
+    const int64_t pairs = p.kv_heads * (((int64_t)p.nodes * p.group + w.rule.rows - 1) / w.rule.rows);
+    const int64_t units = p.batch * (w.slots > pairs ? w.slots : pairs);
+    w.by_group = Shape::kFolds && units > kByGroup * kSms;
+    const dim3 grid((unsigned)(units < kSms ? units : kSms));
+    if (cudaError_t e = launch_early(kernel, grid, kMmaThreads, Shape::kBytes, stream, w)) return e;
+    const int dtype = std::is_same_v<typename Shape::T, __nv_bfloat16> ? DETFOLD_BF16 : DETFOLD_F16;
+    return w.slots ? launch_tree_join(w, dtype, stream) : cudaSuccess;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace detfold_tree

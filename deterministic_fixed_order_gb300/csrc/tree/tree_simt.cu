@@ -1,4 +1,4 @@
-// Attention of trees on the ordinary units: rows by blocks of four warps, a chunk of tokens a CTA.
+// Attention of trees in float32, on the ordinary units: rows by blocks of four warps, a chunk of tokens a CTA.
 //
 // A tile of 32 tokens: a lane takes a token for the scores, of each of its warp's rows, then places of the
 // head for the weighted values; the weights pass through shared memory within the warp. Tiles come by
@@ -10,7 +10,7 @@
 namespace detfold_tree {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32, kTok = 32;
+constexpr int kWarps = 4, kThreads = kWarps * 32, kTok = kSimtTok;
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
 {
@@ -192,7 +192,7 @@ struct Simt {
 #pragma unroll
                 for (int i = 0; i < kPlaces; ++i)
                     if (lane + 32 * i < p.head_dim)
-                        out[lane + 32 * i] = from_f32<T>(sum == 0.0f ? 0.0f : __fdiv_rn(o[r][i], sum));
+                        out[lane + 32 * i] = quotient_of<T>(o[r][i], sum, 0.0f);
                 if (lane == 0 && p.lse)
                     p.lse[((int64_t)b * p.nodes + node) * p.q_heads + head] = log_sum<false>(m[r], sum);
             }
@@ -204,11 +204,6 @@ template <typename T, int DP, int RW>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const __grid_constant__ TreeWork w)
 {
     Simt<T, DP, RW>::run(w);
-}
-
-TreeRule simt_rule(int rows)
-{
-    return {kTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 0};
 }
 
 template <typename T, int DP, int RW>
@@ -229,7 +224,7 @@ cudaError_t launch_rows(const TreeWork &w, cudaStream_t stream)
     const int64_t need = w.slots ? (w.slots > pairs ? w.slots : pairs) : pairs;
     const dim3 grid((unsigned)(need < (1 << 20) ? need : 1 << 20), (unsigned)(p.batch < 65535 ? p.batch : 65535));
     if (cudaError_t e = launch_early(tree_simt_kernel<T, DP, RW>, grid, kThreads, sizeof(typename K::Shared), stream, w)) return e;
-    return cudaSuccess;
+    return w.slots ? launch_tree_join(w, DETFOLD_F32, stream) : cudaSuccess;
 }
 
 template <typename T, int DP>
@@ -251,20 +246,6 @@ cudaError_t launch_type(const TreeWork &w, cudaStream_t stream)
 
 }  // namespace
 
-int64_t tree_workspace(int dtype, int batch, int nodes, int kv_heads, int group, int head_dim, int64_t max_len)
-{
-    (void)dtype;
-    return tree_need(simt_rule(nodes * group), batch, kv_heads, group, nodes, head_dim, max_len);
-}
-
-cudaError_t launch_tree(const TreeParams &p, int dtype, void *workspace, cudaStream_t stream)
-{
-    const TreeWork w = tree_work(p, simt_rule(p.nodes * p.group), dtype == DETFOLD_F32 ? 4 : 2, workspace);
-    cudaError_t e = dtype == DETFOLD_F32    ? launch_type<float>(w, stream)
-                    : dtype == DETFOLD_BF16 ? launch_type<__nv_bfloat16>(w, stream)
-                                            : launch_type<__half>(w, stream);
-    if (e != cudaSuccess || !w.slots) return e;
-    return launch_tree_join(w, dtype, stream);
-}
+cudaError_t launch_simt(const TreeWork &w, cudaStream_t stream) { return launch_type<float>(w, stream); }
 
 }  // namespace detfold_tree
