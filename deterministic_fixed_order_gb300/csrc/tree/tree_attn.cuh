@@ -21,8 +21,8 @@ namespace detfold_tree {
 
 // How sequences are cut, for one element type and head dimension.
 struct TreeRule {
-    int tok;    // tokens a tile
-    int rows;   // rows a pair's block, at most
+    int tok;    // tokens a tile: a power of two
+    int rows;   // rows a pair's block, at most: a power of two
     int wide;   // rows of the widest block of this type: a call whose trees have fewer may take narrower ones,
                 // which are then one block a key-value head either way
     int least;  // tiles a chunk, at least, for up to half of the widest block's rows; twice as many for more
@@ -39,6 +39,7 @@ struct TreeWork {
     int slots;        // workspace slots a sequence, 0: no pair has more than one unit
     int slot_rows;    // rows of a slot
     Divide page;      // by the page size
+    Divide by_heads;  // by the query heads a key-value head
     float2 *ml;       // [batch][slots][slot_rows] (m, l)
     float *acc;       // [batch][slots][slot_rows][head_dim]
     int q_vec, out_vec;  // 16 bytes of q, of out, start at a multiple of 16
@@ -70,7 +71,7 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
     w.p = p, w.rule = r;
     w.slots = (int)slots_of(r, p.kv_heads, p.group, p.nodes, p.max_len);
     w.slot_rows = slot_rows_of(r, p.group, p.nodes);
-    w.page = divide_by(p.page_size);
+    w.page = divide_by(p.page_size), w.by_heads = divide_by(p.group);
     const int64_t rows = (int64_t)p.batch * w.slots * w.slot_rows;
     w.ml = (float2 *)workspace;
     w.acc = (float *)((char *)workspace + (rows * 8 + 15) / 16 * 16);
@@ -99,6 +100,18 @@ struct TreeSeq {
     bool bad;
 };
 
+// x / y for x >= 0, y >= 1. Below 2^23 by the reciprocal, whose product with x is off by less than one.
+__device__ __forceinline__ int over(int x, int y)
+{
+    if (x >> 23) return x / y;
+    int q = (int)__fmul_rn((float)x, __frcp_rn((float)y));
+    const int r = x - q * y;
+    if (r < 0) --q;
+    if (r >= y) ++q;
+    return q;
+}
+__device__ __forceinline__ int over_up(int x, int y) { return over(x + y - 1, y); }
+
 // `n`, `c` as read. A sequence that cannot be attended to has one unit a pair and no tokens.
 __device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
 {
@@ -111,16 +124,16 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
     s.first = p.window && s.n + 1 > p.window ? s.n + 1 - p.window : 0;
     s.end = s.bad ? 0 : s.n + s.c;
     const int rows = s.c * p.group;
-    s.blocks = (rows + w.rule.rows - 1) / w.rule.rows;
+    s.blocks = (rows + w.rule.rows - 1) >> (31 - __clz(w.rule.rows));  // powers of two, and tiles
     s.pairs = s.blocks * p.kv_heads;
-    s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) / w.rule.tok;
+    s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) >> (31 - __clz(w.rule.tok));
     const int least = 2 * rows > w.rule.wide ? 2 * w.rule.least : w.rule.least;
-    const int most = s.pairs < kFill ? kFill / max(s.pairs, 1) : 1;
-    s.per = max(least, (s.tiles + most - 1) / most);
-    s.chunks = s.c == 0 ? 0 : max(1, (s.tiles + s.per - 1) / s.per);
-    s.fold = max(1, (w.rule.group + s.per - 1) / s.per);
+    const int most = s.pairs < kFill ? over(kFill, max(s.pairs, 1)) : 1;
+    s.per = s.tiles <= least * most ? least : max(least, over_up(s.tiles, most));
+    s.chunks = s.c == 0 ? 0 : max(1, over_up(s.tiles, s.per));
+    s.fold = max(1, over_up(w.rule.group, s.per));
     s.each = w.by_group ? s.fold : 1;
-    s.units = (s.chunks + s.each - 1) / s.each;
+    s.units = over_up(s.chunks, s.each);
     return s;
 }
 __device__ __forceinline__ TreeSeq tree_seq_of(const TreeWork &w, int b)

@@ -8,10 +8,10 @@
 // Warps 0 to 3 have a row a thread: they mask, take the maximum, make the weights and, where a chunk ends, fold its
 // triple or write it. O is multiplied by the change of the maximum only where that grew by more than kSlack
 // (a power of two's exponent; weights stay below 2^(kShift + kSlack)). Warp 4 issues the products: a tile's scores ahead of the
-// weighted values of the tile before. Warps 5 and 6 copy: pages may be one token long and end inside a tile, so a
+// weighted values of the tile before. Warps 5 to 8 copy: pages may be one token long and end inside a tile, so a
 // thread copies 16 bytes of a row at a time to where the swizzled operand has them, and writes by the generic
 // proxy are fenced before the products read them. One CTA an SM goes from unit to unit; the copies run ahead
-// over their ends. (Seven warps, two an SM's quarter, may have 255 registers a thread; a ninth would make that 168.)
+// over their ends.
 //
 // Tiles whose tokens are not seen by every row (the drafted ones, a window's edge) are masked by bits. There a value
 // that is not finite must not meet a weight of 0: such values are looked for, taken out of the tile, and added
@@ -39,8 +39,8 @@ struct MmaShape {
     static constexpr int kQs = NS == 4 ? 1 : 2;
     static constexpr bool kFolds = NS <= 3;         // tensor memory has room for a second accumulator
     static constexpr int kColO = 2 * kTok, kColF = kColO + NS * 64;
-    static constexpr int kShift = std::is_same_v<T, __half> ? 14 : 0, kSlack = std::is_same_v<T, __half> ? 1 : 8;
-    static constexpr int kBytes = kSlots * kSlot + kQs * kQ + 1024 + 1024;
+    static constexpr int kShift = std::is_same_v<T, __half> ? 8 : 0, kSlack = std::is_same_v<T, __half> ? 7 : 8;
+    static constexpr int kBytes = kSlots * kSlot + kQs * kQ + 2048;
     // chunks of 256 tokens at least, groups of 1024
     static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kFolds ? 1024 / kTok : 0}; }
 };
@@ -49,7 +49,7 @@ struct MmaShape {
 
 // More units of a chunk each, as the longest sequence allows, than this many an SM: units are groups.
 constexpr int kByGroup = 4;
-constexpr int kSoftmax = 128, kCopy = 64, kMmaThreads = kSoftmax + 32 + kCopy;
+constexpr int kSoftmax = 128, kCopy = 128, kMmaThreads = kSoftmax + 32 + kCopy;
 
 // ------------------------------------------------------------------ instructions
 
@@ -71,10 +71,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, int parity)
                  : "memory");
     return ok != 0;
 }
-// Bounded: two seconds, or until another wait of this CTA has run out.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, int parity, volatile int *dead)
+// Bounded: two seconds, or until another wait of this CTA has run out. Out of line: there are a dozen waits, and the
+// warps' different loops share one instruction cache.
+static __device__ __noinline__ bool bar_wait_on(uint32_t bar, int parity, volatile int *dead)
 {
-    if (bar_try(bar, parity)) return true;
     long long t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     for (int i = 0; i < (1 << 24); ++i) {
@@ -84,6 +84,10 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, int parity, volatile int 
     }
     *dead = 1;
     return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, int parity, volatile int *dead)
+{
+    return bar_try(bar, parity) || bar_wait_on(bar, parity, dead);
 }
 // By a whole warp, with one verdict.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, int parity, volatile int *dead)
@@ -97,6 +101,19 @@ __device__ __forceinline__ void mma_after() { asm volatile("tcgen05.fence::after
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A value that a warp's lanes share, said so that the compiler knows it: the products' operands have to be in uniform registers.
+__device__ __forceinline__ uint32_t shared_by_all(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+__device__ __forceinline__ uint64_t shared_by_all(uint64_t x)
+{
+    return (uint64_t)shared_by_all((uint32_t)(x >> 32)) << 32 | shared_by_all((uint32_t)x);
+}
+// One lane of a whole warp.
+__device__ __forceinline__ bool one_lane()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add)
 {
@@ -174,7 +191,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 // A unit: tiles [tile, end) of a pair.
 struct Unit {
     TreeSeq s;
-    int b, pair, index, tile, end;
+    int b, pair, index, tile, end, chunk;  // `chunk`: the first tile of the chunk at hand
 };
 
 // A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By whole warps.
@@ -182,7 +199,7 @@ struct Units {
     int64_t next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
     int b0, n, c;
 
-    __device__ __forceinline__ void load(const TreeWork &w)
+    __device__ __noinline__ void load(const TreeWork &w)
     {
         const int lane = threadIdx.x % 32, b = b0 + lane;
         upto = 0, n = 0, c = 0;
@@ -202,7 +219,7 @@ struct Units {
         next = blockIdx.x, base = 0, b0 = 0;
         load(w);
     }
-    __device__ __forceinline__ bool take(const TreeWork &w, Unit &u)
+    __device__ __noinline__ bool take(const TreeWork &w, Unit &u)
     {
         int64_t all;
         while ((all = __shfl_sync(~0u, (long long)upto, 31)) <= next - base) {
@@ -216,10 +233,11 @@ struct Units {
         u.b = b0 + lane;
         u.s = tree_seq(w, __shfl_sync(~0u, n, lane), __shfl_sync(~0u, c, lane));
         const int local = (int)(at - (__shfl_sync(~0u, (long long)upto, lane) - (int64_t)u.s.units * u.s.pairs));
-        u.index = local / u.s.pairs;
+        u.index = over(local, u.s.pairs);
         u.pair = local - u.index * u.s.pairs;
         u.tile = u.index * u.s.each * u.s.per;
         u.end = min(u.s.tiles, u.tile + u.s.each * u.s.per);
+        u.chunk = u.tile;
         next += gridDim.x;
         return true;
     }
@@ -233,6 +251,7 @@ struct TreeMma {
     static constexpr int kTok = Shape::kTok, kSlots = Shape::kSlots, kQs = Shape::kQs, kNS = Shape::kSlot / Shape::kSlab;
 
     struct Control {
+        int64_t places[kTok];  // where a tile's rows begin in the cache, by warps that copy them
         uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2], met, end;
         uint32_t tmem;
         int dead, keep_o;
@@ -242,11 +261,10 @@ struct TreeMma {
 
     static __device__ __forceinline__ void run(const TreeWork &w)
     {
-        extern __shared__ unsigned char raw[];
-        unsigned char *smem = raw + ((1024 - (smem_at(raw) & 1023)) & 1023);
+        extern __shared__ __align__(1024) unsigned char smem[];
         const uint32_t ring = smem_at(smem), q = ring + kSlots * Shape::kSlot;
         Control &ct = *reinterpret_cast<Control *>(smem + kSlots * Shape::kSlot + kQs * Shape::kQ);
-        static_assert(sizeof(Control) <= 1024, "as kBytes has it");
+        static_assert(sizeof(Control) <= 2048, "as kBytes has it");
         const int tid = threadIdx.x, warp = tid / 32;
         if (tid == 0) {
             for (int i = 0; i < kSlots; ++i) bar_init(smem_at(&ct.full[i]), kCopy), bar_init(smem_at(&ct.empty[i]), 1);
@@ -325,21 +343,30 @@ struct TreeMma {
     {
         constexpr int kLanes = kNS == 1 ? 8 : kNS == 2 ? 16 : 32;          // threads a row
         constexpr int kTogether = kCopy / kLanes, kPasses = kTok / kTogether;  // rows at a time, times
-        constexpr int kOwn = 32 / kLanes;                                      // of them a warp's
-        constexpr int kHold = kPasses * kOwn / 32;                             // places that a lane looks up
+        constexpr int kOwn = 32 / kLanes, kWarpRows = kPasses * kOwn;          // of them a warp's; a warp's rows of a tile
+        static_assert(kWarpRows <= 32 && kTogether * kPasses == kTok, "a lane looks up a row at most");
         const TreeParams &p = w.p;
         const int tid = threadIdx.x - kSoftmax - 32, warp = tid / 32, lane = tid % 32;
         const int piece = tid % kLanes, pieces = p.head_dim / 8, padded = (pieces + 1) / 2 * 2;
         const int row0 = tid / kLanes, slab = piece / 8, chunk = piece % 8;
+        // Where this thread's piece of row row0 + i kTogether lies: a place a row's last three bits, and 128 bytes a row. The
+        // rows go by eights, or by fours.
+        const uint32_t even = slab * Shape::kSlab + row0 * 128 + ((chunk ^ (row0 & 7)) << 4);
+        const uint32_t odd = slab * Shape::kSlab + row0 * 128 + ((chunk ^ ((row0 + kTogether) & 7)) << 4);
+        static_assert(kTogether % 4 == 0, "two places");
+        // the row that this lane looks up
+        const int held = lane / kOwn * kTogether + warp * kOwn + lane % kOwn;
+        int64_t *mine = ct.places + warp * kWarpRows;
+        const int64_t *read = mine + lane / kLanes;
         Told told;
         Units units;
         units.start(w);
         Unit u;
-        int fill = 0, count = 0;
+        int slot = 0, slot_round = 0, count = 0;
         bool alive = true;
         while (alive && units.take(w, u)) {
             if (u.tile >= u.end) continue;
-            const int kv = u.pair / u.s.blocks, first_row = (u.pair - kv * u.s.blocks) * Shape::kRows;
+            const int kv = over(u.pair, u.s.blocks), first_row = (u.pair - kv * u.s.blocks) * Shape::kRows;
             const int rows = min(Shape::kRows, u.s.c * p.group - first_row);
             const int seq = ++count;
             const auto free = [&](uint32_t bar, int parity) {
@@ -348,34 +375,34 @@ struct TreeMma {
                 return bar_wait(bar, parity, &ct.dead);
             };
             const auto free_warp = [&](uint32_t bar, int parity) { return __all_sync(~0u, free(bar, parity)); };
-            // a tile's places: looked up a tile ahead
-            const auto look = [&](int tile, int h) {
-                const int mine = h * 32 + lane, row = mine / kOwn * kTogether + warp * kOwn + mine % kOwn;
-                const int t = u.s.first + tile * kTok + row;
+            const int32_t *table = p.table + u.b * p.table_stride;
+            const int64_t in_row = kv * p.head_stride;
+            // a row's place, or -1: looked up a tile ahead
+            const auto look = [&](int tile) {
+                const int t = u.s.first + tile * kTok + held;
                 int64_t at = -1;
-                if (tile < u.end && t < u.s.end) {
+                if (held < kTok && tile < u.end && t < u.s.end) {
                     const unsigned col = quotient(t, w.page);
-                    const int page = p.table[u.b * p.table_stride + col];
+                    const int page = table[col];
                     if (page >= 0 && page < p.num_pages)
-                        at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + kv * p.head_stride;
+                        at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + in_row;
                     else
                         ((volatile int *)ct.bad)[seq & 15] = seq;
                 }
                 return at;
             };
-            int64_t places[kHold];
-#pragma unroll
-            for (int h = 0; h < kHold; ++h) places[h] = look(u.tile, h);
+            int64_t next = look(u.tile);
             // queries: rows behind the last are zeros
             const int qi = (seq - 1) % kQs, q_round = (seq - 1) / kQs;
             if (!(alive = free_warp(smem_at(&ct.q_empty[qi]), (q_round & 1) ^ 1))) break;
             if (piece < padded) {
+#pragma unroll 4
                 for (int r = row0; r < Shape::kRows; r += kTogether) {
                     const uint32_t dst = q + qi * Shape::kQ + slab * (Shape::kRows * 128) + r * 128 + ((chunk ^ (r & 7)) << 4);
                     const T *src = (const T *)p.q;
                     const bool some = r < rows && piece < pieces;
                     if (some) {
-                        const int node = (first_row + r) / p.group, head = kv * p.group + first_row + r - node * p.group;
+                        const int node = (int)quotient(first_row + r, w.by_heads), head = kv * p.group + first_row + r - node * p.group;
                         src += u.b * p.q_bs + node * p.q_ns + head * p.q_hs + piece * 8;
                     }
                     if (w.q_vec || !some) {
@@ -391,24 +418,30 @@ struct TreeMma {
             }
             told.add(smem_at(&ct.q_full[qi]));
             for (int tile = u.tile; alive && tile < u.end; ++tile) {
-                int64_t now[kHold];
-#pragma unroll
-                for (int h = 0; h < kHold; ++h) now[h] = places[h], places[h] = look(tile + 1, h);
+                __syncwarp();
+                if (kWarpRows == 32 || lane < kWarpRows) mine[lane] = next;
+                const bool every = __all_sync(~0u, next >= 0 || held >= kTok);
+                next = look(tile + 1);
+                __syncwarp();
 #pragma unroll 1
                 for (int value = 0; value < 2; ++value) {
-                    const int slot = fill % kSlots;
-                    if (!(alive = free_warp(smem_at(&ct.empty[slot]), (fill / kSlots & 1) ^ 1))) break;
-                    const T *src = (const T *)(value ? p.v : p.k);
-                    const uint32_t to = ring + slot * Shape::kSlot + slab * Shape::kSlab;
+                    if (!(alive = free_warp(smem_at(&ct.empty[slot]), (slot_round & 1) ^ 1))) break;
+                    const T *src = (const T *)(value ? p.v : p.k) + (piece < pieces ? piece * 8 : 0);
+                    const uint32_t to = ring + slot * Shape::kSlot;
+                    if (every && piece < pieces) {
 #pragma unroll
-                    for (int i = 0; i < kPasses; ++i) {
-                        const int r = row0 + i * kTogether;
-                        const int64_t at = __shfl_sync(~0u, (long long)now[i * kOwn / 32], (i * kOwn + lane / kLanes) % 32);
-                        const bool some = at >= 0 && piece < pieces;
-                        if (piece < padded) copy16(to + r * 128 + ((chunk ^ (r & 7)) << 4), src + (some ? at + piece * 8 : 0), some);
+                        for (int i = 0; i < kPasses; ++i)
+                            copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), src + read[i * kOwn], true);
+                    } else if (piece < padded) {
+#pragma unroll 2
+                        for (int i = 0; i < kPasses; ++i) {
+                            const int64_t at = read[i * kOwn];
+                            const bool some = at >= 0 && piece < pieces;
+                            copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), some ? src + at : src, some);
+                        }
                     }
                     told.add(smem_at(&ct.full[slot]));
-                    ++fill;
+                    if (++slot == kSlots) slot = 0, ++slot_round;
                 }
             }
         }
@@ -420,13 +453,12 @@ struct TreeMma {
 
     static __device__ __forceinline__ void products(const TreeWork &w, Control &ct, uint32_t ring, uint32_t q, uint32_t tmem)
     {
-        const int d16 = (w.p.head_dim + 15) / 16 * 16, lane = threadIdx.x % 32;
-        const uint32_t scores = product<T>(kTok, false), values = product<T>(d16, true);
+        const int steps = (w.p.head_dim + 15) / 16;
+        const uint32_t scores = product<T>(kTok, false), values = product<T>(steps * 16, true);
         Units ahead, behind;
         ahead.start(w);
         behind = ahead;
         Unit a, v;
-        bool more_a, more_v;
         // units without tokens have no products
         const auto next = [&](Units &units, Unit &u) {
             do
@@ -434,62 +466,74 @@ struct TreeMma {
             while (u.tile >= u.end);
             return true;
         };
-        more_a = next(ahead, a);
-        more_v = next(behind, v);
+        bool more_a = next(ahead, a), more_v = more_a;
+        if (more_a) {
+            v = a;
+            behind = ahead;
+        }
         bool fresh = true;  // the first tile of unit a
-        int ga = 0, gv = 0, unit = 0;
+        int ga = 0, gv = 0, qi = 0, q_round = 0;
+        int slot_a = 0, round_a = 0, slot_v = 1, round_v = 0;  // slots go keys, values, keys, ...
+        const auto past = [&](int &slot, int &round) {
+            if ((slot += 2) >= kSlots) slot -= kSlots, ++round;
+        };
         while (more_v) {
             if (more_a) {
-                const int slot = 2 * ga % kSlots;
-                const int qi = unit % kQs;
-                if (fresh && !warp_wait(smem_at(&ct.q_full[qi]), unit / kQs & 1, &ct.dead)) break;
-                if (!warp_wait(smem_at(&ct.full[slot]), 2 * ga / kSlots & 1, &ct.dead)) break;
+                if (fresh && !warp_wait(smem_at(&ct.q_full[qi]), q_round & 1, &ct.dead)) break;
+                if (!warp_wait(smem_at(&ct.full[slot_a]), round_a & 1, &ct.dead)) break;
                 // the weights that lay here have been multiplied
                 if (ga >= 2 && !warp_wait(smem_at(&ct.o_done[ga & 1]), (ga - 2) / 2 & 1, &ct.dead)) break;
                 mma_after();
-                if (lane == 0) {
-                    const uint32_t left = q + qi * Shape::kQ, right = ring + slot * Shape::kSlot;
-                    for (int k = 0; k < d16 / 16; ++k) {
-                        const uint32_t in = (k & 3) * 32;
-                        mma_ss(tmem + (ga & 1) * kTok, operand(left + (k >> 2) * (Shape::kRows * 128) + in, 16),
-                               operand(right + (k >> 2) * Shape::kSlab + in, 16), scores, k > 0);
-                    }
-                    mma_commit(smem_at(&ct.empty[slot]));
+                const uint64_t left = shared_by_all(operand(q + qi * Shape::kQ, 16));
+                const uint64_t right = shared_by_all(operand(ring + slot_a * Shape::kSlot, 16));
+                const uint32_t to = shared_by_all(tmem + (ga & 1) * kTok);
+                const bool ends = a.tile + 1 == a.end;
+                if (one_lane()) {
+#pragma unroll
+                    for (int k = 0; k < kNS * 4; ++k)  // 32 bytes on, in the next slab after four
+                        if (k < steps)
+                            mma_ss(to, left + ((k >> 2) * (Shape::kRows * 8) + (k & 3) * 2),
+                                   right + ((k >> 2) * (Shape::kSlab / 16) + (k & 3) * 2), scores, k > 0);
+                    mma_commit(smem_at(&ct.empty[slot_a]));
                     mma_commit(smem_at(&ct.s_full[ga & 1]));
-                    if (a.tile + 1 == a.end) mma_commit(smem_at(&ct.q_empty[qi]));
+                    if (ends) mma_commit(smem_at(&ct.q_empty[qi]));
                 }
                 __syncwarp();
                 ++ga;
+                past(slot_a, round_a);
                 fresh = false;
                 if (++a.tile == a.end) {
                     more_a = next(ahead, a);
                     fresh = true;
-                    ++unit;
+                    if (++qi == kQs) qi = 0, ++q_round;
                 }
                 if (ga == 1 && more_a) continue;  // one tile ahead
             }
-            const int fill = 2 * gv + 1, slot = fill % kSlots;
             if (!warp_wait(smem_at(&ct.p_ready[gv & 1]), gv / 2 & 1, &ct.dead)) break;
-            if (!warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) break;
+            if (!warp_wait(smem_at(&ct.full[slot_v]), round_v & 1, &ct.dead)) break;
             mma_after();
-            if (lane == 0) {
-                const bool first = (v.tile % v.s.per) == 0;
-                bool add = !first || *(volatile int *)&ct.keep_o;
-                const uint32_t right = ring + slot * Shape::kSlot, weights = tmem + (gv & 1) * kTok;
-                for (int part = 0; part < 2; ++part)
-                    for (int k = 0; k < kTok / 16; ++k) {
-                        mma_ts(tmem + Shape::kColO, weights + part * (kTok / 2) + k * 8, operand(right + k * 2048, Shape::kSlab), values, add);
-                        add = true;
-                    }
-                mma_commit(smem_at(&ct.empty[slot]));
+            const bool first = v.tile == v.chunk && !*(volatile int *)&ct.keep_o;
+            const uint64_t right = shared_by_all(operand(ring + slot_v * Shape::kSlot, Shape::kSlab));
+            const uint32_t weights = shared_by_all(tmem + (gv & 1) * kTok), to = shared_by_all(tmem + Shape::kColO);
+            if (one_lane()) {
+                // weights of 32 tokens: 16 columns of upper parts, 16 of lower ones; 2048 bytes of values
+#pragma unroll
+                for (int k = 0; k < kTok / 16; ++k)
+                    mma_ts(to, weights + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, k > 0 || !first);
+#pragma unroll
+                for (int k = 0; k < kTok / 16; ++k)
+                    mma_ts(to, weights + 16 + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, true);
+                mma_commit(smem_at(&ct.empty[slot_v]));
                 mma_commit(smem_at(&ct.o_done[gv & 1]));
             }
             __syncwarp();
             ++gv;
-            if (++v.tile == v.end) more_v = next(behind, v);
+            past(slot_v, round_v);
+            if (++v.tile == v.chunk + v.s.per) v.chunk = v.tile;
+            if (v.tile == v.end) more_v = next(behind, v);
         }
         // whatever was issued is done before the tensor memory goes back
-        if (lane == 0) mma_commit(smem_at(&ct.end));
+        if (one_lane()) mma_commit(smem_at(&ct.end));
         __syncwarp();
         warp_wait(smem_at(&ct.end), 0, &ct.dead);
     }
@@ -514,6 +558,7 @@ struct TreeMma {
     static __device__ __forceinline__ bool row_is_odd(unsigned char *slot, int row, int pieces)
     {
         uint32_t top = 0;
+#pragma unroll 4
         for (int i = 0; i < pieces; ++i) {
             const uint4 x = *piece_of(slot, row, i);
             top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fff), x.y & 0x7fff7fff);
@@ -527,6 +572,7 @@ struct TreeMma {
                                                    uint32_t weights, uint32_t o, int d, bool first, bool works)
     {
         const int tid = threadIdx.x, blocks = (d + 31) / 32, pieces = d / 8;
+#pragma unroll 1
         for (int cb = 0; works && cb < blocks; ++cb) {
             float x[32];
             if (first) {
@@ -540,8 +586,8 @@ struct TreeMma {
                 for (uint32_t left = odd[word]; left; left &= left - 1) {
                     const int j = word * 32 + __ffs(left) - 1;
                     uint32_t hi, lo;
-                    tm_load_one(hi, weights + j / 2);
-                    tm_load_one(lo, weights + kTok / 2 + j / 2);
+                    tm_load_one(hi, weights + (j & ~31) + (j & 31) / 2);
+                    tm_load_one(lo, weights + (j & ~31) + 16 + (j & 31) / 2);
                     tm_loaded();
                     if (j & 1) hi >>= 16, lo >>= 16;
                     T h, l;
@@ -613,10 +659,10 @@ struct TreeMma {
         int g = 0, count = 0, meetings = 0;
         while (units.take(w, u)) {
             const TreeSeq &s = u.s;
-            const int kv = u.pair / s.blocks, first_row = (u.pair - kv * s.blocks) * Shape::kRows;
+            const int kv = over(u.pair, s.blocks), first_row = (u.pair - kv * s.blocks) * Shape::kRows;
             const int rows = min(Shape::kRows, s.c * p.group - first_row);
             const bool live = tid < rows, works = warp * 32 < rows;
-            const int node = live ? (first_row + tid) / p.group : 0;
+            const int node = live ? (int)quotient(first_row + tid, w.by_heads) : 0;
             const int head = live ? kv * p.group + first_row + tid - node * p.group : 0;
             T *out = nullptr;
             float *acc = nullptr;
@@ -640,6 +686,7 @@ struct TreeMma {
                 float x[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = quiet_nan();
+#pragma unroll 1
                 for (int cb = 0; puts && cb < blocks; ++cb) put(w, x, cb * 32, out, acc, 1.0f);
                 finish(0.0f, quiet_nan());
                 if (tid == 0) flag_bad_index(p.status);
@@ -667,28 +714,37 @@ struct TreeMma {
                         return true;
                     };
                     if (works) {
-                        float x[kTok];
-#pragma unroll
-                        for (int i = 0; i < kTok; i += 32) tm_load(x + i, here + i);
-                        tm_loaded();
-#pragma unroll
-                        for (int i = 0; i < kTok; i += 2) {
-                            const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(scale, scale));
-                            x[i] = y.x, x[i + 1] = y.y;
-                        }
+                        uint64_t seen[kTok / 64];
                         if (!whole) {
 #pragma unroll
-                            for (int half = 0; half < kTok / 64; ++half) {
-                                const uint64_t seen = seen_from(mask, s.n, at + half * 64);
-#pragma unroll
-                                for (int i = 0; i < 64; ++i)
-                                    if (!((seen >> i) & 1)) x[half * 64 + i] = neg_inf();
-                            }
+                            for (int half = 0; half < kTok / 64; ++half) seen[half] = seen_from(mask, s.n, at + half * 64);
                         }
-                        float top4[4] = {x[0], x[1], x[2], x[3]};
+                        // 32 tokens of the tile: scores times the scale, -inf where they are not seen
+                        const auto scores = [&](float (&x)[32], int i) {
+                            tm_load(x, here + i);
+                            tm_loaded();
 #pragma unroll
-                        for (int i = 4; i < kTok; ++i) top4[i & 3] = fmaxf(top4[i & 3], x[i]);
-                        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 y = mul2(make_float2(x[k], x[k + 1]), make_float2(scale, scale));
+                                x[k] = y.x, x[k + 1] = y.y;
+                            }
+                            if (!whole) {
+                                const uint32_t bits = (uint32_t)(seen[kTok > 64 ? i >> 6 : 0] >> (i & 32));
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!((bits >> k) & 1)) x[k] = neg_inf();
+                            }
+                        };
+                        float top = neg_inf();
+#pragma unroll 1
+                        for (int i = 0; i < kTok; i += 32) {
+                            float x[32];
+                            scores(x, i);
+                            float t4[4] = {top, x[0], x[1], x[2]};
+#pragma unroll
+                            for (int k = 3; k < 32; ++k) t4[k & 3] = fmaxf(t4[k & 3], x[k]);
+                            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                        }
                         const bool moves = top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack));
                         if (__any_sync(~0u, moves)) {
                             const float next = moves ? __fsub_rn(top, (float)Shape::kShift) : m;
@@ -697,6 +753,7 @@ struct TreeMma {
                             l = __fmul_rn(l, fall);
                             if (tile != t0) {
                                 if (!settle()) return;
+#pragma unroll 1
                                 for (int cb = 0; cb < blocks; ++cb) {
                                     float y[32];
                                     tm_load(y, o + cb * 32);
@@ -709,18 +766,20 @@ struct TreeMma {
                         }
                         const float base = base_of(m);
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < kTok; i += 32) {
+                            float x[32];
+                            scores(x, i);
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
-                                const float2 e = add2(make_float2(x[i + k], x[i + k + 1]), make_float2(-base, -base));
+                                const float2 e = add2(make_float2(x[k], x[k + 1]), make_float2(-base, -base));
                                 const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
                                 sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
                                 split2(y.x, y.y, hi[k / 2], lo[k / 2], T());
                             }
-                            tm_store16(here + i / 2, hi);
-                            tm_store16(here + kTok / 2 + i / 2, lo);
+                            tm_store16(here + i, hi);
+                            tm_store16(here + i + 16, lo);
                         }
                         l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
                         tm_stored();
@@ -760,6 +819,7 @@ struct TreeMma {
                     sum = fold_in(fl, l, fa, fb);
                 }
                 const float inverse = inverse_of(sum);
+#pragma unroll 1
                 for (int cb = 0; cb < blocks; ++cb) {
                     float x[32];
                     tm_load(x, o + cb * 32);
