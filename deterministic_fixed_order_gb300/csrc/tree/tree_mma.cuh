@@ -5,13 +5,13 @@
 // lie in tensor memory, and P goes back there in the place of its S, so that the second product takes it
 // from there. P is split in two 16-bit parts (split2), both multiplied.
 //
-// Warps 0 to 3 have a row a thread: they mask, take the maximum, make the weights and, where a chunk ends, fold its
-// triple or write it. O is multiplied by the change of the maximum only where that grew by more than kSlack
-// (a power of two's exponent; weights stay below 2^(kShift + kSlack)). Warp 4 issues the products: a tile's scores ahead of the
-// weighted values of the tile before. Warps 5 to 8 copy: pages may be one token long and end inside a tile, so a
-// thread copies 16 bytes of a row at a time to where the swizzled operand has them, and writes by the generic
-// proxy are fenced before the products read them. One CTA an SM goes from unit to unit; the copies run ahead
-// over their ends.
+// Warps 0 to 7, by halves, have a tile in turn and a row a thread: they mask, take the maximum, make the weights, and finish
+// chunks. O is multiplied by the change of the maximum only where that grew by more than kSlack (a power of
+// two's exponent; weights stay below 2^(kShift + kSlack)). Warp 8 issues the products: scores up to a tile ahead of weighted
+// values. Warps 9 to 12 copy: pages may be one token long and end inside a tile, so a thread copies 16
+// bytes of a row at a time to where the swizzled operand has them, and writes by the generic proxy are fenced before the
+// products read them. Warp 13 works out what the CTA does next. One CTA an SM goes from unit to unit; copies and
+// products run ahead over their ends.
 //
 // Tiles whose tokens are not seen by every row (the drafted ones, a window's edge) are masked by bits. There a value
 // that is not finite must not meet a weight of 0: such values are looked for, taken out of the tile, and added
@@ -40,7 +40,7 @@ struct MmaShape {
     static constexpr bool kFolds = NS <= 3;         // tensor memory has room for a second accumulator
     static constexpr int kColO = 2 * kTok, kColF = kColO + NS * 64;
     static constexpr int kShift = std::is_same_v<T, __half> ? 8 : 0, kSlack = std::is_same_v<T, __half> ? 7 : 8;
-    static constexpr int kBytes = kSlots * kSlot + kQs * kQ + 2048;
+    static constexpr int kControl = 3072, kBytes = kSlots * kSlot + kQs * kQ + kControl;
     // chunks of 256 tokens at least, groups of 1024
     static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kFolds ? 1024 / kTok : 0}; }
 };
@@ -49,7 +49,7 @@ struct MmaShape {
 
 // More units of a chunk each, as the longest sequence allows, than this many an SM: units are groups.
 constexpr int kByGroup = 4;
-constexpr int kSoftmax = 128, kCopy = 128, kMmaThreads = kSoftmax + 32 + kCopy;
+constexpr int kSoftmax = 256, kCopy = 128, kMmaThreads = kSoftmax + 32 + kCopy + 32;
 
 // ------------------------------------------------------------------ instructions
 
@@ -66,6 +66,15 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, int parity)
 {
     uint32_t ok;
     asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_test(uint32_t bar, int parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
                  : "=r"(ok)
                  : "r"(bar), "r"(parity)
                  : "memory");
@@ -186,20 +195,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // ------------------------------------------------------------------ units of work
 
-// A unit: tiles [tile, end) of a pair.
+// A unit as the warps of a CTA are told it: tiles [tile, end) of a block of rows.
 struct Unit {
-    TreeSeq s;
-    int b, pair, index, tile, end, chunk;  // `chunk`: the first tile of the chunk at hand
+    int b, n, c, first, stop;      // the sequence: committed tokens, nodes, first token seen, end of its tokens
+    int kv, first_row, rows;       // key-value head; rows of it
+    int tile, end, per;            // tiles; tiles a chunk
+    int slot;                      // where its triple goes, or -1: the outputs
 };
 
-// A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By whole warps.
+// A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By a whole warp.
 struct Units {
     int64_t next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
     int b0, n, c;
 
-    __device__ __noinline__ void load(const TreeWork &w)
+    __device__ __forceinline__ void load(const TreeWork &w)
     {
         const int lane = threadIdx.x % 32, b = b0 + lane;
         upto = 0, n = 0, c = 0;
@@ -214,30 +232,30 @@ struct Units {
             if (lane >= k) upto += y;
         }
     }
-    __device__ __forceinline__ void start(const TreeWork &w)
-    {
-        next = blockIdx.x, base = 0, b0 = 0;
-        load(w);
-    }
-    __device__ __noinline__ bool take(const TreeWork &w, Unit &u)
+    __device__ __forceinline__ bool take(const TreeWork &w, Unit &u)
     {
         int64_t all;
-        while ((all = __shfl_sync(~0u, (long long)upto, 31)) <= next - base) {
-            base += all;
-            b0 += 32;
+        while (b0 < 0 || (all = __shfl_sync(~0u, (long long)upto, 31)) <= next - base) {
+            if (b0 >= 0) base += all;
+            b0 = b0 < 0 ? 0 : b0 + 32;
             if (b0 >= w.p.batch) return false;
             load(w);
         }
         const int64_t at = next - base;
         const int lane = __ffs(__ballot_sync(~0u, upto > at)) - 1;
         u.b = b0 + lane;
-        u.s = tree_seq(w, __shfl_sync(~0u, n, lane), __shfl_sync(~0u, c, lane));
-        const int local = (int)(at - (__shfl_sync(~0u, (long long)upto, lane) - (int64_t)u.s.units * u.s.pairs));
-        u.index = over(local, u.s.pairs);
-        u.pair = local - u.index * u.s.pairs;
-        u.tile = u.index * u.s.each * u.s.per;
-        u.end = min(u.s.tiles, u.tile + u.s.each * u.s.per);
-        u.chunk = u.tile;
+        const TreeSeq s = tree_seq(w, __shfl_sync(~0u, n, lane), __shfl_sync(~0u, c, lane));
+        const int local = (int)(at - (__shfl_sync(~0u, (long long)upto, lane) - (int64_t)s.units * s.pairs));
+        const int index = over(local, s.pairs), pair = local - index * s.pairs;
+        u.n = s.n, u.c = s.c, u.first = s.first, u.stop = s.end;
+        u.kv = over(pair, s.blocks);
+        u.first_row = (pair - u.kv * s.blocks) * w.rule.rows;
+        u.rows = min(w.rule.rows, s.c * w.p.group - u.first_row);
+        u.tile = index * s.each * s.per;
+        u.end = min(s.tiles, u.tile + s.each * s.per);
+        u.per = s.per;
+        // lengths that change under the call: nothing past the workspace
+        u.slot = s.units == 1 ? -1 : local < w.slots ? local : -2;
         next += gridDim.x;
         return true;
     }
@@ -245,18 +263,24 @@ struct Units {
 
 // ------------------------------------------------------------------ the kernel
 
+constexpr int kUnits = 4;  // units that the warps are told ahead
+
 template <typename Shape>
 struct TreeMma {
     using T = typename Shape::T;
     static constexpr int kTok = Shape::kTok, kSlots = Shape::kSlots, kQs = Shape::kQs, kNS = Shape::kSlot / Shape::kSlab;
+    static constexpr int kSoftmaxWarps = kSoftmax / 32, kCopyWarps = kCopy / 32;
 
     struct Control {
-        int64_t places[kTok];  // where a tile's rows begin in the cache, by warps that copy them
-        uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2], met, end;
+        uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2], o_free;
+        uint64_t met[2], agree[4], both[4], unit_full[kUnits], unit_empty[kUnits], end;
+        Unit units[kUnits];  // b = -1: no more
         uint32_t tmem;
         int dead, keep_o;
-        int bad[16];         // the unit (counted from 1) that has a page outside the cache, by its last bits
-        uint32_t odd[2][4];  // tokens of a tile with values that are not finite, by turns
+        int bad[16];             // the unit (counted from 1) that has a page outside the cache, by its last bits
+        uint32_t odd[2][2][4];   // tokens of a tile with values that are not finite: of either half of the softmax warps, by turns
+        float top[128];          // a row's maximum, as the last tile left it
+        float sums[2][128];      // a row's sums of weights of either half
     };
 
     static __device__ __forceinline__ void run(const TreeWork &w)
@@ -264,24 +288,24 @@ struct TreeMma {
         extern __shared__ __align__(1024) unsigned char smem[];
         const uint32_t ring = smem_at(smem), q = ring + kSlots * Shape::kSlot;
         Control &ct = *reinterpret_cast<Control *>(smem + kSlots * Shape::kSlot + kQs * Shape::kQ);
-        static_assert(sizeof(Control) <= 2048, "as kBytes has it");
+        static_assert(sizeof(Control) <= Shape::kControl, "as kBytes has it");
         const int tid = threadIdx.x, warp = tid / 32;
         if (tid == 0) {
-            for (int i = 0; i < kSlots; ++i) bar_init(smem_at(&ct.full[i]), kCopy), bar_init(smem_at(&ct.empty[i]), 1);
-            for (int i = 0; i < kQs; ++i) bar_init(smem_at(&ct.q_full[i]), kCopy), bar_init(smem_at(&ct.q_empty[i]), 1);
-            for (int i = 0; i < 2; ++i) {
-                bar_init(smem_at(&ct.s_full[i]), 1);
-                bar_init(smem_at(&ct.p_ready[i]), kSoftmax);
-                bar_init(smem_at(&ct.o_done[i]), 1);
-            }
-            bar_init(smem_at(&ct.met), 4);
-            bar_init(smem_at(&ct.end), 1);
+            const auto set = [](uint64_t *bars, int n, int count) {
+                for (int i = 0; i < n; ++i) bar_init(smem_at(bars + i), count);
+            };
+            set(ct.full, kSlots, kCopy), set(ct.empty, kSlots, 1), set(ct.q_full, kQs, kCopy), set(ct.q_empty, kQs, 1);
+            set(ct.s_full, 2, 1), set(ct.p_ready, 2, kSoftmax / 2), set(ct.o_done, 2, 1), set(&ct.o_free, 1, kSoftmax);
+            set(ct.met, 2, kSoftmaxWarps / 2), set(ct.agree, 4, 1), set(ct.both, 4, 2), set(&ct.end, 1, 1);
+            set(ct.unit_full, kUnits, 1), set(ct.unit_empty, kUnits, kSoftmaxWarps + kCopyWarps + 1);
             ct.dead = 0, ct.keep_o = 0;
             for (int i = 0; i < 16; ++i) ct.bad[i] = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
+        // tensor memory is taken after the wait: a kernel that is waited for may need it
         enter_grid();
-        if (warp == 4) {
+        constexpr int kProducts = kSoftmaxWarps, kScheduler = kProducts + 1 + kCopyWarps;
+        if (warp == kProducts) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(&ct.tmem)) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
             mma_before();
@@ -289,34 +313,81 @@ struct TreeMma {
         __syncthreads();
         mma_after();
         const uint32_t tmem = *(volatile uint32_t *)&ct.tmem;
-        if (warp < 4)
-            softmax(w, ct, smem, tmem + ((uint32_t)(warp * 32) << 16));
-        else if (warp == 4)
+        if (warp < kProducts)
+            softmax(w, ct, smem, tmem + ((uint32_t)(warp % 4 * 32) << 16));
+        else if (warp == kProducts)
             products(w, ct, ring, q, tmem);
-        else
+        else if (warp < kScheduler)
             copies(w, ct, ring, q);
+        else
+            schedule(w, ct);
         __syncwarp();
         mma_before();
         __syncthreads();
         mma_after();
-        if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        if (warp == kProducts) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
         if (tid == 0 && ct.dead) flag(w.p.status, DETFOLD_ERR_CUDA);
     }
 
+    // ---------------------------------------------------------- units
+
+    static __device__ __forceinline__ void schedule(const TreeWork &w, Control &ct)
+    {
+        Units units;
+        units.next = blockIdx.x, units.base = 0, units.b0 = -1;
+        bool more = true;
+        for (int i = 0, round = 0; more; ) {
+            Unit u;
+            more = units.take(w, u);
+            if (!warp_wait(smem_at(&ct.unit_empty[i]), (round & 1) ^ 1, &ct.dead)) break;
+            if (threadIdx.x % 32 == 0) {
+                if (!more) u.b = -1;
+                ct.units[i] = u;
+                bar_arrive(smem_at(&ct.unit_full[i]));
+            }
+            __syncwarp();
+            if (++i == kUnits) i = 0, ++round;
+        }
+    }
+
+    // A warp's way through them.
+    struct Way {
+        int i = 0, round = 0;
+        __device__ __forceinline__ void past(Control &ct)
+        {
+            __syncwarp();
+            if (threadIdx.x % 32 == 0) bar_arrive(smem_at(&ct.unit_empty[i]));
+            skip();
+        }
+        __device__ __forceinline__ void skip()
+        {
+            if (++i == kUnits) i = 0, ++round;
+        }
+        __device__ __forceinline__ bool here(Control &ct)
+        {
+            return warp_wait(smem_at(&ct.unit_full[i]), round & 1, &ct.dead) && *(volatile int *)&ct.units[i].b >= 0;
+        }
+    };
+
     // ---------------------------------------------------------- copies
 
-    // Copies that were started, in order, and whose barriers are still to be told: two at most, so that the
-    // products never wait for a copy that is told only after a slot that they hold is free again.
+    // Copies that were started, in order, and whose barriers are still to be told.
     struct Told {
         uint32_t first = 0, second = 0;
-        __device__ __forceinline__ void all()
+        __device__ __forceinline__ void tell()
         {
-            if (!first) return;
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
             fence_async();
             bar_arrive(first);
-            if (second) bar_arrive(second);
-            first = second = 0;
+            first = second, second = 0;
+        }
+        // The oldest, once it has come.
+        __device__ __forceinline__ void one()
+        {
+            if (second)
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            tell();
         }
         __device__ __forceinline__ void add(uint32_t bar)
         {
@@ -327,9 +398,8 @@ struct TreeMma {
                 second = bar;
             } else {
                 asm volatile("cp.async.wait_group 2;" ::: "memory");
-                fence_async();
-                bar_arrive(first);
-                first = second, second = bar;
+                tell();
+                second = bar;
             }
         }
     };
@@ -356,32 +426,34 @@ struct TreeMma {
         static_assert(kTogether % 4 == 0, "two places");
         // the row that this lane looks up
         const int held = lane / kOwn * kTogether + warp * kOwn + lane % kOwn;
-        int64_t *mine = ct.places + warp * kWarpRows;
-        const int64_t *read = mine + lane / kLanes;
+        const bool mine = piece < pieces;
         Told told;
-        Units units;
-        units.start(w);
-        Unit u;
+        Way way;
         int slot = 0, slot_round = 0, count = 0;
+        // Waits for a barrier, telling what has come meanwhile: nobody waits for a copy that is only told after this.
+        const auto wait = [&](uint64_t &b, int parity) {
+            const uint32_t bar = smem_at(&b);
+            bool ok = bar_test(bar, parity);
+            while (!ok && told.first) {
+                told.one();
+                ok = bar_test(bar, parity);
+            }
+            return __all_sync(~0u, ok || bar_wait(bar, parity, &ct.dead));
+        };
         bool alive = true;
-        while (alive && units.take(w, u)) {
-            if (u.tile >= u.end) continue;
-            const int kv = over(u.pair, u.s.blocks), first_row = (u.pair - kv * u.s.blocks) * Shape::kRows;
-            const int rows = min(Shape::kRows, u.s.c * p.group - first_row);
+        for (; (alive = wait(ct.unit_full[way.i], way.round & 1)) && *(volatile int *)&ct.units[way.i].b >= 0; way.past(ct)) {
+            const Unit &u = ct.units[way.i];
+            const int end = u.end, stop = u.stop, first = u.first, kv = u.kv;
+            if (u.tile >= end) continue;
+            const int first_row = u.first_row, rows = u.rows;
             const int seq = ++count;
-            const auto free = [&](uint32_t bar, int parity) {
-                if (bar_try(bar, parity)) return true;
-                told.all();
-                return bar_wait(bar, parity, &ct.dead);
-            };
-            const auto free_warp = [&](uint32_t bar, int parity) { return __all_sync(~0u, free(bar, parity)); };
             const int32_t *table = p.table + u.b * p.table_stride;
             const int64_t in_row = kv * p.head_stride;
             // a row's place, or -1: looked up a tile ahead
             const auto look = [&](int tile) {
-                const int t = u.s.first + tile * kTok + held;
+                const int t = first + tile * kTok + held;
                 int64_t at = -1;
-                if (held < kTok && tile < u.end && t < u.s.end) {
+                if (held < kTok && tile < end && t < stop) {
                     const unsigned col = quotient(t, w.page);
                     const int page = table[col];
                     if (page >= 0 && page < p.num_pages)
@@ -394,16 +466,17 @@ struct TreeMma {
             int64_t next = look(u.tile);
             // queries: rows behind the last are zeros
             const int qi = (seq - 1) % kQs, q_round = (seq - 1) / kQs;
-            if (!(alive = free_warp(smem_at(&ct.q_empty[qi]), (q_round & 1) ^ 1))) break;
+            if (!(alive = wait(ct.q_empty[qi], (q_round & 1) ^ 1))) break;
             if (piece < padded) {
-#pragma unroll 4
+                const T *queries = (const T *)p.q + u.b * p.q_bs + piece * 8;
+#pragma unroll 1
                 for (int r = row0; r < Shape::kRows; r += kTogether) {
                     const uint32_t dst = q + qi * Shape::kQ + slab * (Shape::kRows * 128) + r * 128 + ((chunk ^ (r & 7)) << 4);
                     const T *src = (const T *)p.q;
-                    const bool some = r < rows && piece < pieces;
+                    const bool some = r < rows && mine;
                     if (some) {
                         const int node = (int)quotient(first_row + r, w.by_heads), head = kv * p.group + first_row + r - node * p.group;
-                        src += u.b * p.q_bs + node * p.q_ns + head * p.q_hs + piece * 8;
+                        src = queries + node * p.q_ns + head * p.q_hs;
                     }
                     if (w.q_vec || !some) {
                         copy16(dst, src, some);
@@ -417,35 +490,38 @@ struct TreeMma {
                 }
             }
             told.add(smem_at(&ct.q_full[qi]));
-            for (int tile = u.tile; alive && tile < u.end; ++tile) {
-                __syncwarp();
-                if (kWarpRows == 32 || lane < kWarpRows) mine[lane] = next;
+            for (int tile = u.tile; alive && tile < end; ++tile) {
+                const int64_t places = next;
                 const bool every = __all_sync(~0u, next >= 0 || held >= kTok);
                 next = look(tile + 1);
-                __syncwarp();
 #pragma unroll 1
                 for (int value = 0; value < 2; ++value) {
-                    if (!(alive = free_warp(smem_at(&ct.empty[slot]), (slot_round & 1) ^ 1))) break;
-                    const T *src = (const T *)(value ? p.v : p.k) + (piece < pieces ? piece * 8 : 0);
+                    if (!(alive = wait(ct.empty[slot], (slot_round & 1) ^ 1))) break;
+                    const T *src = (const T *)(value ? p.v : p.k) + (mine ? piece * 8 : 0);
                     const uint32_t to = ring + slot * Shape::kSlot;
-                    if (every && piece < pieces) {
+                    if (every) {
 #pragma unroll
-                        for (int i = 0; i < kPasses; ++i)
-                            copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), src + read[i * kOwn], true);
-                    } else if (piece < padded) {
-#pragma unroll 2
                         for (int i = 0; i < kPasses; ++i) {
-                            const int64_t at = read[i * kOwn];
-                            const bool some = at >= 0 && piece < pieces;
-                            copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), some ? src + at : src, some);
+                            const int64_t at = __shfl_sync(~0u, (long long)places, i * kOwn + lane / kLanes);
+                            if (mine) copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), src + at, true);
+                        }
+                    }
+                    if (!every || pieces != padded) {
+#pragma unroll 1
+                        for (int i = 0; i < kPasses; ++i) {
+                            const int64_t at = __shfl_sync(~0u, (long long)places, i * kOwn + lane / kLanes);
+                            const bool some = at >= 0 && mine;
+                            if (piece < padded && !(every && mine))
+                                copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), some ? src + at : src, some);
                         }
                     }
                     told.add(smem_at(&ct.full[slot]));
                     if (++slot == kSlots) slot = 0, ++slot_round;
                 }
             }
+            if (!alive) break;
         }
-        told.all();
+        while (told.first) told.one();
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 
@@ -455,82 +531,111 @@ struct TreeMma {
     {
         const int steps = (w.p.head_dim + 15) / 16;
         const uint32_t scores = product<T>(kTok, false), values = product<T>(steps * 16, true);
-        Units ahead, behind;
-        ahead.start(w);
-        behind = ahead;
-        Unit a, v;
-        // units without tokens have no products
-        const auto next = [&](Units &units, Unit &u) {
-            do
-                if (!units.take(w, u)) return false;
-            while (u.tile >= u.end);
-            return true;
+        const auto ready = [&](uint64_t &bar, int parity) { return __all_sync(~0u, bar_test(smem_at(&bar), parity & 1)); };
+        // The unit whose scores are next, and the one whose weighted values are: 0 not known, 1 known, 2 no more.
+        Way way_a, way_v;
+        int know_a = 0, know_v = 0, tile_a = 0, end_a = 0, tile_v = 0, end_v = 0, chunk_v = 0, per_v = 0;
+        const auto look = [&](Way &way, bool frees, int &know, int &tile, int &end, int &per) {
+            while (know == 0 && ready(ct.unit_full[way.i], way.round)) {
+                const volatile Unit &u = ct.units[way.i];
+                tile = u.tile, end = u.end, per = u.per;
+                if (u.b < 0)
+                    know = 2;
+                else if (tile < end)  // units without tokens have no products
+                    know = 1;
+                else if (frees)
+                    way.past(ct);
+                else
+                    way.skip();
+            }
         };
-        bool more_a = next(ahead, a), more_v = more_a;
-        if (more_a) {
-            v = a;
-            behind = ahead;
-        }
-        bool fresh = true;  // the first tile of unit a
-        int ga = 0, gv = 0, qi = 0, q_round = 0;
+        bool fresh = true;  // the first tile of scores of a unit
+        int ga = 0, gv = 0, qi = 0, q_round = 0, idle = 0, chunks = 0, per = 0;
         int slot_a = 0, round_a = 0, slot_v = 1, round_v = 0;  // slots go keys, values, keys, ...
         const auto past = [&](int &slot, int &round) {
             if ((slot += 2) >= kSlots) slot -= kSlots, ++round;
         };
-        while (more_v) {
-            if (more_a) {
-                if (fresh && !warp_wait(smem_at(&ct.q_full[qi]), q_round & 1, &ct.dead)) break;
-                if (!warp_wait(smem_at(&ct.full[slot_a]), round_a & 1, &ct.dead)) break;
-                // the weights that lay here have been multiplied
-                if (ga >= 2 && !warp_wait(smem_at(&ct.o_done[ga & 1]), (ga - 2) / 2 & 1, &ct.dead)) break;
+        long long t0 = 0;
+        // Whichever product can be made: a tile's scores once the weights that lay in their place have been multiplied, at
+        // most a tile ahead; a tile's weighted values once the weights are there, and what O held before has been read.
+        while (true) {
+            bool did = false;
+            look(way_a, false, know_a, tile_a, end_a, per);
+            if (know_v == 0) {
+                look(way_v, true, know_v, tile_v, end_v, per_v);
+                chunk_v = tile_v;
+            }
+            if (know_v == 2) break;
+            if (know_a == 1 && ga < gv + 2 && (!fresh || ready(ct.q_full[qi], q_round)) && ready(ct.full[slot_a], round_a) &&
+                (ga < 2 || ready(ct.o_done[ga & 1], (ga - 2) / 2))) {
+                did = true;
                 mma_after();
                 const uint64_t left = shared_by_all(operand(q + qi * Shape::kQ, 16));
                 const uint64_t right = shared_by_all(operand(ring + slot_a * Shape::kSlot, 16));
                 const uint32_t to = shared_by_all(tmem + (ga & 1) * kTok);
-                const bool ends = a.tile + 1 == a.end;
+                const bool ends = tile_a + 1 == end_a;
                 if (one_lane()) {
 #pragma unroll
                     for (int k = 0; k < kNS * 4; ++k)  // 32 bytes on, in the next slab after four
                         if (k < steps)
                             mma_ss(to, left + ((k >> 2) * (Shape::kRows * 8) + (k & 3) * 2),
                                    right + ((k >> 2) * (Shape::kSlab / 16) + (k & 3) * 2), scores, k > 0);
-                    mma_commit(smem_at(&ct.empty[slot_a]));
                     mma_commit(smem_at(&ct.s_full[ga & 1]));
+                    mma_commit(smem_at(&ct.empty[slot_a]));
                     if (ends) mma_commit(smem_at(&ct.q_empty[qi]));
                 }
                 __syncwarp();
                 ++ga;
                 past(slot_a, round_a);
-                fresh = false;
-                if (++a.tile == a.end) {
-                    more_a = next(ahead, a);
-                    fresh = true;
+                fresh = ends;
+                ++tile_a;
+                if (ends) {
+                    know_a = 0;
+                    way_a.skip();
                     if (++qi == kQs) qi = 0, ++q_round;
                 }
-                if (ga == 1 && more_a) continue;  // one tile ahead
             }
-            if (!warp_wait(smem_at(&ct.p_ready[gv & 1]), gv / 2 & 1, &ct.dead)) break;
-            if (!warp_wait(smem_at(&ct.full[slot_v]), round_v & 1, &ct.dead)) break;
-            mma_after();
-            const bool first = v.tile == v.chunk && !*(volatile int *)&ct.keep_o;
-            const uint64_t right = shared_by_all(operand(ring + slot_v * Shape::kSlot, Shape::kSlab));
-            const uint32_t weights = shared_by_all(tmem + (gv & 1) * kTok), to = shared_by_all(tmem + Shape::kColO);
-            if (one_lane()) {
-                // weights of 32 tokens: 16 columns of upper parts, 16 of lower ones; 2048 bytes of values
+            if (gv < ga && ready(ct.p_ready[gv & 1], gv / 2) && ready(ct.full[slot_v], round_v) &&
+                (tile_v != chunk_v || chunks == 0 || ready(ct.o_free, chunks - 1))) {
+                did = true;
+                mma_after();
+                const bool first = tile_v == chunk_v && !*(volatile int *)&ct.keep_o;
+                const uint64_t right = shared_by_all(operand(ring + slot_v * Shape::kSlot, Shape::kSlab));
+                const uint32_t weights = shared_by_all(tmem + (gv & 1) * kTok), to = shared_by_all(tmem + Shape::kColO);
+                if (one_lane()) {
+                    // weights of 32 tokens: 16 columns of upper parts, 16 of lower ones; 2048 bytes of values
 #pragma unroll
-                for (int k = 0; k < kTok / 16; ++k)
-                    mma_ts(to, weights + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, k > 0 || !first);
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_ts(to, weights + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, k > 0 || !first);
 #pragma unroll
-                for (int k = 0; k < kTok / 16; ++k)
-                    mma_ts(to, weights + 16 + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, true);
-                mma_commit(smem_at(&ct.empty[slot_v]));
-                mma_commit(smem_at(&ct.o_done[gv & 1]));
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_ts(to, weights + 16 + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, true);
+                    mma_commit(smem_at(&ct.o_done[gv & 1]));
+                    mma_commit(smem_at(&ct.empty[slot_v]));
+                }
+                __syncwarp();
+                ++gv;
+                past(slot_v, round_v);
+                if (tile_v == chunk_v) ++chunks;
+                if (++tile_v == end_v) {
+                    know_v = 0;
+                    way_v.past(ct);
+                } else if (tile_v == chunk_v + per_v) {
+                    chunk_v = tile_v;
+                }
             }
-            __syncwarp();
-            ++gv;
-            past(slot_v, round_v);
-            if (++v.tile == v.chunk + v.s.per) v.chunk = v.tile;
-            if (v.tile == v.end) more_v = next(behind, v);
+            // bounded, as every wait
+            if (did) {
+                idle = 0;
+            } else if ((++idle & 1023) == 0) {
+                long long t;
+                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+                if (idle == 1024) t0 = t;
+                if (__any_sync(~0u, *(volatile int *)&ct.dead || t - t0 > 2000000000LL || idle > (1 << 28))) {
+                    *(volatile int *)&ct.dead = 1;
+                    break;
+                }
+            }
         }
         // whatever was issued is done before the tensor memory goes back
         if (one_lane()) mma_commit(smem_at(&ct.end));
@@ -540,12 +645,13 @@ struct TreeMma {
 
     // ---------------------------------------------------------- softmax
 
-    // The four softmax warps meet; bounded like every wait.
+    // The four warps of one half meet; bounded like every wait.
     static __device__ __forceinline__ bool meet(Control &ct, int &meetings)
     {
+        const int half = threadIdx.x / 128;
         __syncwarp();
-        if (threadIdx.x % 32 == 0) bar_arrive(smem_at(&ct.met));
-        return warp_wait(smem_at(&ct.met), meetings++ & 1, &ct.dead);
+        if (threadIdx.x % 32 == 0) bar_arrive(smem_at(&ct.met[half]));
+        return warp_wait(smem_at(&ct.met[half]), meetings++ & 1, &ct.dead);
     }
     // Where 16 bytes of a tile's row lie.
     static __device__ __forceinline__ uint4 *piece_of(unsigned char *slot, int row, int piece)
@@ -558,7 +664,7 @@ struct TreeMma {
     static __device__ __forceinline__ bool row_is_odd(unsigned char *slot, int row, int pieces)
     {
         uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < pieces; ++i) {
             const uint4 x = *piece_of(slot, row, i);
             top = __vmaxu2(__vmaxu2(top, x.x & 0x7fff7fff), x.y & 0x7fff7fff);
@@ -571,7 +677,7 @@ struct TreeMma {
     static __device__ __noinline__ bool odd_values(Control &ct, const volatile uint32_t *odd, int &meetings, unsigned char *slot,
                                                    uint32_t weights, uint32_t o, int d, bool first, bool works)
     {
-        const int tid = threadIdx.x, blocks = (d + 31) / 32, pieces = d / 8;
+        const int row = threadIdx.x % 128, blocks = (d + 31) / 32, pieces = d / 8;
 #pragma unroll 1
         for (int cb = 0; works && cb < blocks; ++cb) {
             float x[32];
@@ -610,16 +716,16 @@ struct TreeMma {
         }
         tm_stored();
         if (!meet(ct, meetings)) return false;
-        if (tid < kTok && (odd[tid / 32] >> (tid % 32)) & 1)
+        if (row < kTok && (odd[row / 32] >> (row % 32)) & 1)
             for (int i = 0; i < pieces; ++i) {
-                Pack<T, 8> y = *reinterpret_cast<const Pack<T, 8> *>(piece_of(slot, tid, i));
+                Pack<T, 8> y = *reinterpret_cast<const Pack<T, 8> *>(piece_of(slot, row, i));
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (!(fabsf(to_f32(y.v[k])) < __int_as_float(0x7f800000))) y.v[k] = from_f32<T>(0.0f);
-                *piece_of(slot, tid, i) = *reinterpret_cast<const uint4 *>(&y);
+                *piece_of(slot, row, i) = *reinterpret_cast<const uint4 *>(&y);
             }
         fence_async();
-        if (tid == 0 && first) *(volatile int *)&ct.keep_o = 1;
+        if (row == 0 && first) *(volatile int *)&ct.keep_o = 1;
         return true;
     }
 
@@ -647,61 +753,68 @@ struct TreeMma {
         }
     }
 
+    // Two halves of four warps, each with the tiles of one parity: while one makes weights the other takes a maximum. A tile's
+    // maximum follows from the one that the tile before has left (ct.top); each half sums its own tiles' weights, and both
+    // finish a chunk together, a half of the head each.
     static __device__ __forceinline__ void softmax(const TreeWork &w, Control &ct, unsigned char *smem, uint32_t tmem)
     {
         const TreeParams &p = w.p;
-        const int tid = threadIdx.x, warp = tid / 32, blocks = (p.head_dim + 31) / 32;
-        const float scale = __fmul_rn(p.scale, kLog2e);
+        const int tid = threadIdx.x, row = tid % 128, half = tid / 128, warp = row / 32, blocks = (p.head_dim + 31) / 32;
+        // a positive scale goes into the exponent's product; another one is multiplied in first
+        const float factor = __fmul_rn(p.scale, kLog2e), scale = factor > 0.0f ? factor : 1.0f;
         const uint32_t o = tmem + Shape::kColO, f = tmem + Shape::kColF;
-        Units units;
-        units.start(w);
-        Unit u;
-        int g = 0, count = 0, meetings = 0;
-        while (units.take(w, u)) {
-            const TreeSeq &s = u.s;
-            const int kv = over(u.pair, s.blocks), first_row = (u.pair - kv * s.blocks) * Shape::kRows;
-            const int rows = min(Shape::kRows, s.c * p.group - first_row);
-            const bool live = tid < rows, works = warp * 32 < rows;
-            const int node = live ? (int)quotient(first_row + tid, w.by_heads) : 0;
-            const int head = live ? kv * p.group + first_row + tid - node * p.group : 0;
+        volatile float *left = ct.top;
+        int g = 0, count = 0, meetings = 0, ends = 0, tiles_of = 0;  // tiles_of: tiles of units that this warp worked in
+        for (Way way; way.here(ct); way.past(ct)) {
+            const Unit &u = ct.units[way.i];
+            const int rows = u.rows, first_row = u.first_row, b = u.b, end = u.end, per = u.per, c = u.c;
+            const bool live = row < rows, works = warp * 32 < rows;
+            const int node = live ? (int)quotient(first_row + row, w.by_heads) : 0;
+            const int head = live ? u.kv * p.group + first_row + row - node * p.group : 0;
             T *out = nullptr;
             float *acc = nullptr;
             int64_t slot_row = -1;
-            if (s.units == 1) {
-                out = (T *)p.out + u.b * p.out_bs + node * p.out_ns + head * p.out_hs;
-            } else {
-                const int64_t at = (int64_t)u.index * s.pairs + u.pair;
-                // lengths that change under the call: nothing past the workspace
-                if (at < w.slots) slot_row = ((int64_t)u.b * w.slots + at) * w.slot_rows + tid, acc = w.acc + slot_row * p.head_dim;
+            if (u.slot == -1) {
+                out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
+            } else if (u.slot >= 0) {
+                slot_row = ((int64_t)b * w.slots + u.slot) * w.slot_rows + row;
+                acc = w.acc + slot_row * p.head_dim;
             }
             const bool puts = live && (out || acc);
             const auto finish = [&](float m, float l) {
-                if (!puts) return;
+                if (!puts || half) return;
                 if (!out)
                     w.ml[slot_row] = make_float2(m, l);
                 else if (p.lse)
-                    p.lse[((int64_t)u.b * p.nodes + node) * p.q_heads + head] = log_sum<true>(m, l);
+                    p.lse[((int64_t)b * p.nodes + node) * p.q_heads + head] = log_sum<true>(m, l);
             };
-            if (u.tile >= u.end) {  // a sequence that cannot be attended to
+            if (u.tile >= end) {  // a sequence that cannot be attended to
                 float x[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = quiet_nan();
 #pragma unroll 1
-                for (int cb = 0; puts && cb < blocks; ++cb) put(w, x, cb * 32, out, acc, 1.0f);
+                for (int cb = half; puts && cb < blocks; cb += 2) put(w, x, cb * 32, out, acc, 1.0f);
                 finish(0.0f, quiet_nan());
                 if (tid == 0) flag_bad_index(p.status);
                 continue;
             }
-            const RowMask mask = row_mask(p, u.b, node, s);
+            const int n = u.n, first = u.first;
+            RowMask mask;
+            {
+                TreeSeq s;
+                s.n = n, s.c = c;
+                mask = row_mask(p, b, node, s);
+            }
             ++count;
             bool bad = false;
             float fm = neg_inf(), fl = 0.0f;  // of the chunks before
-            for (int t0 = u.tile; t0 < u.end; t0 += s.per) {
-                const int t1 = min(u.end, t0 + s.per);
-                float m = neg_inf(), l = 0.0f;
-                for (int tile = t0; tile < t1; ++tile, ++g) {
-                    const int at = s.first + tile * kTok;
-                    const bool whole = at + kTok <= s.n && (!p.window || at >= s.n + s.c - p.window);
+            for (int t0 = u.tile; t0 < end; t0 += per) {
+                const int t1 = min(end, t0 + per);
+                float m = neg_inf(), l = 0.0f;  // as this half's last tile left them
+                for (int tile = t0; tile < t1; ++tile, ++g, ++tiles_of) {
+                    if ((g & 1) != half) continue;
+                    const int at = first + tile * kTok;
+                    const bool whole = at + kTok <= n && (!p.window || at >= n + c - p.window);
                     const uint32_t here = tmem + (g & 1) * kTok;
                     if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
                     mma_after();
@@ -717,16 +830,15 @@ struct TreeMma {
                         uint64_t seen[kTok / 64];
                         if (!whole) {
 #pragma unroll
-                            for (int half = 0; half < kTok / 64; ++half) seen[half] = seen_from(mask, s.n, at + half * 64);
+                            for (int i = 0; i < kTok / 64; ++i) seen[i] = seen_from(mask, n, at + i * 64);
                         }
-                        // 32 tokens of the tile: scores times the scale, -inf where they are not seen
+                        // 32 tokens of the tile, -inf where they are not seen
                         const auto scores = [&](float (&x)[32], int i) {
                             tm_load(x, here + i);
                             tm_loaded();
+                            if (!(factor > 0.0f)) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float2 y = mul2(make_float2(x[k], x[k + 1]), make_float2(scale, scale));
-                                x[k] = y.x, x[k + 1] = y.y;
+                                for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], factor);
                             }
                             if (!whole) {
                                 const uint32_t bits = (uint32_t)(seen[kTok > 64 ? i >> 6 : 0] >> (i & 32));
@@ -740,31 +852,44 @@ struct TreeMma {
                         for (int i = 0; i < kTok; i += 32) {
                             float x[32];
                             scores(x, i);
-                            float t4[4] = {top, x[0], x[1], x[2]};
+                            float t4[4] = {fmaxf(top, x[0]), x[1], x[2], x[3]};
 #pragma unroll
-                            for (int k = 3; k < 32; ++k) t4[k & 3] = fmaxf(t4[k & 3], x[k]);
-                            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                            for (int k = 4; k < 28; k += 8) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) t4[j] = max3(t4[j], x[k + j], x[k + 4 + j]);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) t4[j] = fmaxf(t4[j], x[28 + j]);
+                            top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
                         }
-                        const bool moves = top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack));
-                        if (__any_sync(~0u, moves)) {
-                            const float next = moves ? __fsub_rn(top, (float)Shape::kShift) : m;
-                            const float fall = moves ? fade<true>(__fsub_rn(m, base_of(next))) : 1.0f;
-                            m = next;
-                            l = __fmul_rn(l, fall);
-                            if (tile != t0) {
-                                if (!settle()) return;
+                        top = __fmul_rn(top, scale);
+                        // what the tile before left
+                        const float mine = m;
+                        if (tile != t0) {
+                            if (!warp_wait(smem_at(&ct.agree[warp]), (tiles_of - 1) & 1, &ct.dead)) return;
+                            m = left[row];
+                        }
+                        const float before = m;
+                        if (top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack))) m = __fsub_rn(top, (float)Shape::kShift);
+                        left[row] = m;
+                        __syncwarp();
+                        if (tid % 32 == 0) bar_arrive(smem_at(&ct.agree[warp]));
+                        const float base = base_of(m);
+                        if (__any_sync(~0u, mine != m)) l = __fmul_rn(l, mine == m ? 1.0f : fade<true>(__fsub_rn(mine, base)));
+                        if (tile != t0 && __any_sync(~0u, before != m)) {
+                            const float fall = before == m ? 1.0f : fade<true>(__fsub_rn(before, base));
+                            if (!settle()) return;
 #pragma unroll 1
-                                for (int cb = 0; cb < blocks; ++cb) {
-                                    float y[32];
-                                    tm_load(y, o + cb * 32);
-                                    tm_loaded();
+                            for (int cb = 0; cb < blocks; ++cb) {
+                                float y[32];
+                                tm_load(y, o + cb * 32);
+                                tm_loaded();
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], fall);
-                                    tm_store32(o + cb * 32, y);
-                                }
+                                for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], fall);
+                                tm_store32(o + cb * 32, y);
                             }
                         }
-                        const float base = base_of(m);
+                        const float2 by = make_float2(scale, scale), less = make_float2(-base, -base);
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
                         for (int i = 0; i < kTok; i += 32) {
@@ -773,7 +898,7 @@ struct TreeMma {
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
-                                const float2 e = add2(make_float2(x[k], x[k + 1]), make_float2(-base, -base));
+                                const float2 e = fma2(make_float2(x[k], x[k + 1]), by, less);
                                 const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
                                 sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
                                 split2(y.x, y.y, hi[k / 2], lo[k / 2], T());
@@ -784,16 +909,16 @@ struct TreeMma {
                         l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
                         tm_stored();
                     }
-                    if (tid == 0 && tile == t0) *(volatile int *)&ct.keep_o = 0;
+                    if (row == 0 && tile == t0) *(volatile int *)&ct.keep_o = 0;
                     // The values have come, and are not given up before the weights below are told.
                     const int fill = 2 * g + 1, slot = fill % kSlots;
-                    if ((!whole || tile + 1 == u.end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
+                    if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
                     // every copy of this unit has been told: what it found is known
-                    if (tile + 1 == u.end) bad = ((volatile int *)ct.bad)[count & 15] == count;
+                    if (tile + 1 == end) bad = ((volatile int *)ct.bad)[count & 15] == count;
                     if (!whole) {
                         unsigned char *values = smem + slot * Shape::kSlot;
-                        const uint32_t word = __ballot_sync(~0u, tid < kTok && row_is_odd(values, tid, p.head_dim / 8));
-                        volatile uint32_t *odd = ct.odd[meetings & 1];
+                        const uint32_t word = __ballot_sync(~0u, row < kTok && row_is_odd(values, row, p.head_dim / 8));
+                        volatile uint32_t *odd = ct.odd[half][meetings & 1];
                         if (tid % 32 == 0) odd[warp] = word;
                         if (!meet(ct, meetings)) return;
                         if (odd[0] | odd[1] | odd[2] | odd[3]) {
@@ -806,45 +931,56 @@ struct TreeMma {
                 // the chunk's end: O is whole
                 if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return;
                 mma_after();
-                const bool last = t1 == u.end;
-                if (last && bad) {
-                    l = quiet_nan();
-                    if (tid == 0) flag_bad_index(p.status);
-                }
-                if (!works) continue;
-                const bool before = t0 != u.tile;
-                float top = m, fa = 0.0f, fb = 1.0f, sum = l;
-                if (before) {
-                    fold_factors<true>(fm, m, top, fa, fb);
-                    sum = fold_in(fl, l, fa, fb);
-                }
-                const float inverse = inverse_of(sum);
+                if (works) {
+                    // the last maximum, and the other half's sum
+                    if (!warp_wait(smem_at(&ct.agree[warp]), (tiles_of - 1) & 1, &ct.dead)) return;
+                    const float last_m = left[row];
+                    if (last_m != m) l = __fmul_rn(l, fade<true>(__fsub_rn(m, base_of(last_m))));
+                    m = last_m;
+                    ct.sums[half][row] = bad ? quiet_nan() : l;
+                    __syncwarp();
+                    if (tid % 32 == 0) bar_arrive(smem_at(&ct.both[warp]));
+                    if (!warp_wait(smem_at(&ct.both[warp]), ends++ & 1, &ct.dead)) return;
+                    l = __fadd_rn(((volatile float *)ct.sums[0])[row], ((volatile float *)ct.sums[1])[row]);
+                    const bool last = t1 == end, before = t0 != u.tile;
+                    float top = m, fa = 0.0f, fb = 1.0f, sum = l;
+                    if (before) {
+                        fold_factors<true>(fm, m, top, fa, fb);
+                        sum = fold_in(fl, l, fa, fb);
+                    }
+                    const float inverse = inverse_of(sum);
 #pragma unroll 1
-                for (int cb = 0; cb < blocks; ++cb) {
-                    float x[32];
-                    tm_load(x, o + cb * 32);
-                    if (Shape::kFolds && before) {
-                        float y[32];
-                        tm_load(y, f + cb * 32);
-                        tm_loaded();
+                    for (int cb = half; cb < blocks; cb += 2) {
+                        float x[32];
+                        tm_load(x, o + cb * 32);
+                        if (Shape::kFolds && before) {
+                            float y[32];
+                            tm_load(y, f + cb * 32);
+                            tm_loaded();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = fold_in(y[i], x[i], fa, fb);
-                    } else {
-                        tm_loaded();
+                            for (int i = 0; i < 32; ++i) x[i] = fold_in(y[i], x[i], fa, fb);
+                        } else {
+                            tm_loaded();
+                        }
+                        if (!last) {
+                            if (Shape::kFolds) tm_store32(f + cb * 32, x);
+                        } else if (puts) {
+                            put(w, x, cb * 32, out, acc, inverse);
+                        }
+                        __syncwarp();
                     }
                     if (!last) {
-                        if (Shape::kFolds) tm_store32(f + cb * 32, x);
-                    } else if (puts) {
-                        put(w, x, cb * 32, out, acc, inverse);
+                        tm_stored();
+                    } else {
+                        finish(top, sum);
+                        if (bad && row == 0) flag_bad_index(p.status);
                     }
+                    fm = top, fl = sum;
                 }
-                __syncwarp();
-                if (!last)
-                    tm_stored();
-                else
-                    finish(top, sum);
-                fm = top, fl = sum;
+                mma_before();
+                bar_arrive(smem_at(&ct.o_free));
             }
+            if (!works) tiles_of -= end - u.tile;
         }
     }
 };
