@@ -5,7 +5,7 @@
 // lie in tensor memory, and P goes back there in the place of its S, so that the second product takes it
 // from there. P is split in two 16-bit parts (split2), both multiplied.
 //
-// Warps 0 to 7, by halves, have a tile in turn and a row a thread: they mask, take the maximum, make the weights, and finish
+// Warps 0 to 7 have two threads a row, half of a tile's tokens each: they mask, take the maximum, make the weights, and finish
 // chunks. O is multiplied by the change of the maximum only where that grew by more than kSlack (a power of
 // two's exponent; weights stay below 2^(kShift + kSlack)). Warp 8 issues the products: scores up to a tile ahead of weighted
 // values. Warps 9 to 12 copy: pages may be one token long and end inside a tile, so a thread copies 16
@@ -272,15 +272,14 @@ struct TreeMma {
     static constexpr int kSoftmaxWarps = kSoftmax / 32, kCopyWarps = kCopy / 32;
 
     struct Control {
-        uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2], o_free;
-        uint64_t met[2], agree[4], both[4], unit_full[kUnits], unit_empty[kUnits], end;
+        uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2];
+        uint64_t met, agree[4], unit_full[kUnits], unit_empty[kUnits], end;
         Unit units[kUnits];  // b = -1: no more
         uint32_t tmem;
         int dead, keep_o;
         int bad[16];             // the unit (counted from 1) that has a page outside the cache, by its last bits
-        uint32_t odd[2][2][4];   // tokens of a tile with values that are not finite: of either half of the softmax warps, by turns
-        float top[128];          // a row's maximum, as the last tile left it
-        float sums[2][128];      // a row's sums of weights of either half
+        uint32_t odd[2][4];      // tokens of a tile with values that are not finite, by turns
+        float given[2][2][128];  // what the two warps of a row hand each other, by turns
     };
 
     static __device__ __forceinline__ void run(const TreeWork &w)
@@ -295,8 +294,8 @@ struct TreeMma {
                 for (int i = 0; i < n; ++i) bar_init(smem_at(bars + i), count);
             };
             set(ct.full, kSlots, kCopy), set(ct.empty, kSlots, 1), set(ct.q_full, kQs, kCopy), set(ct.q_empty, kQs, 1);
-            set(ct.s_full, 2, 1), set(ct.p_ready, 2, kSoftmax / 2), set(ct.o_done, 2, 1), set(&ct.o_free, 1, kSoftmax);
-            set(ct.met, 2, kSoftmaxWarps / 2), set(ct.agree, 4, 1), set(ct.both, 4, 2), set(&ct.end, 1, 1);
+            set(ct.s_full, 2, 1), set(ct.p_ready, 2, kSoftmax), set(ct.o_done, 2, 1);
+            set(&ct.met, 1, kSoftmaxWarps), set(ct.agree, 4, 2), set(&ct.end, 1, 1);
             set(ct.unit_full, kUnits, 1), set(ct.unit_empty, kUnits, kSoftmaxWarps + kCopyWarps + 1);
             ct.dead = 0, ct.keep_o = 0;
             for (int i = 0; i < 16; ++i) ct.bad[i] = 0;
@@ -550,14 +549,14 @@ struct TreeMma {
             }
         };
         bool fresh = true;  // the first tile of scores of a unit
-        int ga = 0, gv = 0, qi = 0, q_round = 0, idle = 0, chunks = 0, per = 0;
+        int ga = 0, gv = 0, qi = 0, q_round = 0, idle = 0, per = 0;
         int slot_a = 0, round_a = 0, slot_v = 1, round_v = 0;  // slots go keys, values, keys, ...
         const auto past = [&](int &slot, int &round) {
             if ((slot += 2) >= kSlots) slot -= kSlots, ++round;
         };
         long long t0 = 0;
         // Whichever product can be made: a tile's scores once the weights that lay in their place have been multiplied, at
-        // most a tile ahead; a tile's weighted values once the weights are there, and what O held before has been read.
+        // most a tile ahead; a tile's weighted values once the weights are there.
         while (true) {
             bool did = false;
             look(way_a, false, know_a, tile_a, end_a, per);
@@ -595,8 +594,7 @@ struct TreeMma {
                     if (++qi == kQs) qi = 0, ++q_round;
                 }
             }
-            if (gv < ga && ready(ct.p_ready[gv & 1], gv / 2) && ready(ct.full[slot_v], round_v) &&
-                (tile_v != chunk_v || chunks == 0 || ready(ct.o_free, chunks - 1))) {
+            if (gv < ga && ready(ct.p_ready[gv & 1], gv / 2) && ready(ct.full[slot_v], round_v)) {
                 did = true;
                 mma_after();
                 const bool first = tile_v == chunk_v && !*(volatile int *)&ct.keep_o;
@@ -616,7 +614,6 @@ struct TreeMma {
                 __syncwarp();
                 ++gv;
                 past(slot_v, round_v);
-                if (tile_v == chunk_v) ++chunks;
                 if (++tile_v == end_v) {
                     know_v = 0;
                     way_v.past(ct);
@@ -645,13 +642,27 @@ struct TreeMma {
 
     // ---------------------------------------------------------- softmax
 
-    // The four warps of one half meet; bounded like every wait.
+    // The softmax warps meet; bounded like every wait. What each wrote to tensor memory is there for the others.
     static __device__ __forceinline__ bool meet(Control &ct, int &meetings)
     {
-        const int half = threadIdx.x / 128;
+        mma_before();
         __syncwarp();
-        if (threadIdx.x % 32 == 0) bar_arrive(smem_at(&ct.met[half]));
-        return warp_wait(smem_at(&ct.met[half]), meetings++ & 1, &ct.dead);
+        if (threadIdx.x % 32 == 0) bar_arrive(smem_at(&ct.met));
+        const bool ok = warp_wait(smem_at(&ct.met), meetings++ & 1, &ct.dead);
+        mma_after();
+        return ok;
+    }
+    // The two warps of the same rows hand each other a number a row.
+    static __device__ __forceinline__ bool hand(Control &ct, int &handed, float &x)
+    {
+        const int row = threadIdx.x % 128, half = threadIdx.x / 128, bar = row / 32;
+        volatile float(*at)[128] = ct.given[handed & 1];
+        at[half][row] = x;
+        __syncwarp();
+        if (row % 32 == 0) bar_arrive(smem_at(&ct.agree[bar]));
+        const bool ok = warp_wait(smem_at(&ct.agree[bar]), handed++ & 1, &ct.dead);
+        x = at[half ^ 1][row];
+        return ok;
     }
     // Where 16 bytes of a tile's row lie.
     static __device__ __forceinline__ uint4 *piece_of(unsigned char *slot, int row, int piece)
@@ -677,9 +688,9 @@ struct TreeMma {
     static __device__ __noinline__ bool odd_values(Control &ct, const volatile uint32_t *odd, int &meetings, unsigned char *slot,
                                                    uint32_t weights, uint32_t o, int d, bool first, bool works)
     {
-        const int row = threadIdx.x % 128, blocks = (d + 31) / 32, pieces = d / 8;
+        const int tid = threadIdx.x, half = tid / 128, blocks = (d + 31) / 32, pieces = d / 8;
 #pragma unroll 1
-        for (int cb = 0; works && cb < blocks; ++cb) {
+        for (int cb = half; works && cb < blocks; cb += 2) {
             float x[32];
             if (first) {
 #pragma unroll
@@ -716,16 +727,16 @@ struct TreeMma {
         }
         tm_stored();
         if (!meet(ct, meetings)) return false;
-        if (row < kTok && (odd[row / 32] >> (row % 32)) & 1)
+        if (tid < kTok && (odd[tid / 32] >> (tid % 32)) & 1)
             for (int i = 0; i < pieces; ++i) {
-                Pack<T, 8> y = *reinterpret_cast<const Pack<T, 8> *>(piece_of(slot, row, i));
+                Pack<T, 8> y = *reinterpret_cast<const Pack<T, 8> *>(piece_of(slot, tid, i));
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (!(fabsf(to_f32(y.v[k])) < __int_as_float(0x7f800000))) y.v[k] = from_f32<T>(0.0f);
-                *piece_of(slot, row, i) = *reinterpret_cast<const uint4 *>(&y);
+                *piece_of(slot, tid, i) = *reinterpret_cast<const uint4 *>(&y);
             }
         fence_async();
-        if (row == 0 && first) *(volatile int *)&ct.keep_o = 1;
+        if (tid == 0 && first) *(volatile int *)&ct.keep_o = 1;
         return true;
     }
 
@@ -753,18 +764,16 @@ struct TreeMma {
         }
     }
 
-    // Two halves of four warps, each with the tiles of one parity: while one makes weights the other takes a maximum. A tile's
-    // maximum follows from the one that the tile before has left (ct.top); each half sums its own tiles' weights, and both
-    // finish a chunk together, a half of the head each.
+    // Two threads a row, each with half of a tile's tokens and, of the accumulator, every other 32 places of the head.
     static __device__ __forceinline__ void softmax(const TreeWork &w, Control &ct, unsigned char *smem, uint32_t tmem)
     {
+        constexpr int kOwn = kTok / 2;
         const TreeParams &p = w.p;
         const int tid = threadIdx.x, row = tid % 128, half = tid / 128, warp = row / 32, blocks = (p.head_dim + 31) / 32;
         // a positive scale goes into the exponent's product; another one is multiplied in first
         const float factor = __fmul_rn(p.scale, kLog2e), scale = factor > 0.0f ? factor : 1.0f;
         const uint32_t o = tmem + Shape::kColO, f = tmem + Shape::kColF;
-        volatile float *left = ct.top;
-        int g = 0, count = 0, meetings = 0, ends = 0, tiles_of = 0;  // tiles_of: tiles of units that this warp worked in
+        int g = 0, count = 0, meetings = 0, handed = 0;
         for (Way way; way.here(ct); way.past(ct)) {
             const Unit &u = ct.units[way.i];
             const int rows = u.rows, first_row = u.first_row, b = u.b, end = u.end, per = u.per, c = u.c;
@@ -810,12 +819,11 @@ struct TreeMma {
             float fm = neg_inf(), fl = 0.0f;  // of the chunks before
             for (int t0 = u.tile; t0 < end; t0 += per) {
                 const int t1 = min(end, t0 + per);
-                float m = neg_inf(), l = 0.0f;  // as this half's last tile left them
-                for (int tile = t0; tile < t1; ++tile, ++g, ++tiles_of) {
-                    if ((g & 1) != half) continue;
+                float m = neg_inf(), l = 0.0f;  // l: of this thread's tokens
+                for (int tile = t0; tile < t1; ++tile, ++g) {
                     const int at = first + tile * kTok;
                     const bool whole = at + kTok <= n && (!p.window || at >= n + c - p.window);
-                    const uint32_t here = tmem + (g & 1) * kTok;
+                    const uint32_t here = tmem + (g & 1) * kTok + half * kOwn;
                     if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
                     mma_after();
                     bool waited = tile == t0;  // for the tile before, whose product O may still change
@@ -827,78 +835,60 @@ struct TreeMma {
                         return true;
                     };
                     if (works) {
-                        uint64_t seen[kTok / 64];
+                        float x[kOwn];
+#pragma unroll
+                        for (int i = 0; i < kOwn; i += 32) tm_load(x + i, here + i);
+                        tm_loaded();
+                        if (!(factor > 0.0f)) {
+#pragma unroll
+                            for (int i = 0; i < kOwn; ++i) x[i] = __fmul_rn(x[i], factor);
+                        }
                         if (!whole) {
+                            const uint64_t seen = seen_from(mask, n, at + half * kOwn);
 #pragma unroll
-                            for (int i = 0; i < kTok / 64; ++i) seen[i] = seen_from(mask, n, at + i * 64);
+                            for (int i = 0; i < kOwn; ++i)
+                                if (!((seen >> i) & 1)) x[i] = neg_inf();
                         }
-                        // 32 tokens of the tile, -inf where they are not seen
-                        const auto scores = [&](float (&x)[32], int i) {
-                            tm_load(x, here + i);
-                            tm_loaded();
-                            if (!(factor > 0.0f)) {
+                        float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], factor);
-                            }
-                            if (!whole) {
-                                const uint32_t bits = (uint32_t)(seen[kTok > 64 ? i >> 6 : 0] >> (i & 32));
+                        for (int i = 4; i < kOwn - 4; i += 8) {
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!((bits >> k) & 1)) x[k] = neg_inf();
-                            }
-                        };
-                        float top = neg_inf();
+                            for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], x[i + k], x[i + 4 + k]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], x[kOwn - 4 + k]);
+                        const float mine = __fmul_rn(fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]), scale);
+                        float top = mine;
+                        if (!hand(ct, handed, top)) return;
+                        top = fmaxf(top, mine);
+                        const bool moves = top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack));
+                        if (__any_sync(~0u, moves)) {
+                            const float next = moves ? __fsub_rn(top, (float)Shape::kShift) : m;
+                            const float fall = moves ? fade<true>(__fsub_rn(m, base_of(next))) : 1.0f;
+                            m = next;
+                            l = __fmul_rn(l, fall);
+                            if (tile != t0) {
+                                if (!settle()) return;
 #pragma unroll 1
-                        for (int i = 0; i < kTok; i += 32) {
-                            float x[32];
-                            scores(x, i);
-                            float t4[4] = {fmaxf(top, x[0]), x[1], x[2], x[3]};
+                                for (int cb = half; cb < blocks; cb += 2) {
+                                    float y[32];
+                                    tm_load(y, o + cb * 32);
+                                    tm_loaded();
 #pragma unroll
-                            for (int k = 4; k < 28; k += 8) {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) t4[j] = max3(t4[j], x[k + j], x[k + 4 + j]);
+                                    for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], fall);
+                                    tm_store32(o + cb * 32, y);
+                                }
                             }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) t4[j] = fmaxf(t4[j], x[28 + j]);
-                            top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
                         }
-                        top = __fmul_rn(top, scale);
-                        // what the tile before left
-                        const float mine = m;
-                        if (tile != t0) {
-                            if (!warp_wait(smem_at(&ct.agree[warp]), (tiles_of - 1) & 1, &ct.dead)) return;
-                            m = left[row];
-                        }
-                        const float before = m;
-                        if (top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack))) m = __fsub_rn(top, (float)Shape::kShift);
-                        left[row] = m;
-                        __syncwarp();
-                        if (tid % 32 == 0) bar_arrive(smem_at(&ct.agree[warp]));
                         const float base = base_of(m);
-                        if (__any_sync(~0u, mine != m)) l = __fmul_rn(l, mine == m ? 1.0f : fade<true>(__fsub_rn(mine, base)));
-                        if (tile != t0 && __any_sync(~0u, before != m)) {
-                            const float fall = before == m ? 1.0f : fade<true>(__fsub_rn(before, base));
-                            if (!settle()) return;
-#pragma unroll 1
-                            for (int cb = 0; cb < blocks; ++cb) {
-                                float y[32];
-                                tm_load(y, o + cb * 32);
-                                tm_loaded();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], fall);
-                                tm_store32(o + cb * 32, y);
-                            }
-                        }
                         const float2 by = make_float2(scale, scale), less = make_float2(-base, -base);
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-                        for (int i = 0; i < kTok; i += 32) {
-                            float x[32];
-                            scores(x, i);
+#pragma unroll
+                        for (int i = 0; i < kOwn; i += 32) {
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
-                                const float2 e = fma2(make_float2(x[k], x[k + 1]), by, less);
+                                const float2 e = fma2(make_float2(x[i + k], x[i + k + 1]), by, less);
                                 const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
                                 sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
                                 split2(y.x, y.y, hi[k / 2], lo[k / 2], T());
@@ -909,7 +899,7 @@ struct TreeMma {
                         l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
                         tm_stored();
                     }
-                    if (row == 0 && tile == t0) *(volatile int *)&ct.keep_o = 0;
+                    if (tid == 0 && tile == t0) *(volatile int *)&ct.keep_o = 0;
                     // The values have come, and are not given up before the weights below are told.
                     const int fill = 2 * g + 1, slot = fill % kSlots;
                     if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
@@ -917,12 +907,13 @@ struct TreeMma {
                     if (tile + 1 == end) bad = ((volatile int *)ct.bad)[count & 15] == count;
                     if (!whole) {
                         unsigned char *values = smem + slot * Shape::kSlot;
-                        const uint32_t word = __ballot_sync(~0u, row < kTok && row_is_odd(values, row, p.head_dim / 8));
-                        volatile uint32_t *odd = ct.odd[half][meetings & 1];
-                        if (tid % 32 == 0) odd[warp] = word;
+                        const uint32_t word = __ballot_sync(~0u, tid < kTok && row_is_odd(values, tid, p.head_dim / 8));
+                        volatile uint32_t *odd = ct.odd[meetings & 1];
+                        if (tid % 32 == 0 && half == 0) odd[warp] = word;
                         if (!meet(ct, meetings)) return;
                         if (odd[0] | odd[1] | odd[2] | odd[3]) {
-                            if (!settle() || !odd_values(ct, odd, meetings, values, here, o, p.head_dim, tile == t0, works)) return;
+                            if (!settle() || !odd_values(ct, odd, meetings, values, tmem + (g & 1) * kTok, o, p.head_dim, tile == t0, works))
+                                return;
                         }
                     }
                     mma_before();
@@ -932,17 +923,14 @@ struct TreeMma {
                 if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return;
                 mma_after();
                 if (works) {
-                    // the last maximum, and the other half's sum
-                    if (!warp_wait(smem_at(&ct.agree[warp]), (tiles_of - 1) & 1, &ct.dead)) return;
-                    const float last_m = left[row];
-                    if (last_m != m) l = __fmul_rn(l, fade<true>(__fsub_rn(m, base_of(last_m))));
-                    m = last_m;
-                    ct.sums[half][row] = bad ? quiet_nan() : l;
-                    __syncwarp();
-                    if (tid % 32 == 0) bar_arrive(smem_at(&ct.both[warp]));
-                    if (!warp_wait(smem_at(&ct.both[warp]), ends++ & 1, &ct.dead)) return;
-                    l = __fadd_rn(((volatile float *)ct.sums[0])[row], ((volatile float *)ct.sums[1])[row]);
+                    const float mine = l;
+                    if (!hand(ct, handed, l)) return;
+                    l = __fadd_rn(l, mine);
                     const bool last = t1 == end, before = t0 != u.tile;
+                    if (last && bad) {
+                        l = quiet_nan();
+                        if (tid == 0) flag_bad_index(p.status);
+                    }
                     float top = m, fa = 0.0f, fb = 1.0f, sum = l;
                     if (before) {
                         fold_factors<true>(fm, m, top, fa, fb);
@@ -969,18 +957,13 @@ struct TreeMma {
                         }
                         __syncwarp();
                     }
-                    if (!last) {
+                    if (!last)
                         tm_stored();
-                    } else {
+                    else
                         finish(top, sum);
-                        if (bad && row == 0) flag_bad_index(p.status);
-                    }
                     fm = top, fl = sum;
                 }
-                mma_before();
-                bar_arrive(smem_at(&ct.o_free));
             }
-            if (!works) tiles_of -= end - u.tile;
         }
     }
 };
