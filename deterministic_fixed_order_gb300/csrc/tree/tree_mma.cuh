@@ -9,7 +9,7 @@
 // chunks. O is multiplied by the change of the maximum only where that grew by more than kSlack (a power of
 // two's exponent; weights stay below 2^(kShift + kSlack)). Warp 8 issues the products: scores up to a tile ahead of weighted
 // values. Warps 9 to 12 copy: pages may be one token long and end inside a tile, so a thread copies 16
-// bytes of a row at a time to where the swizzled operand has them, and writes by the generic proxy are fenced before the
+// bytes of a row at a time to where the swizzled operand has them; these writes by the generic proxy are fenced before the
 // products read them. Warp 13 works out what the CTA does next. One CTA an SM goes from unit to unit; copies and
 // products run ahead over their ends.
 //
@@ -212,50 +212,48 @@ struct Unit {
     int slot;                      // where its triple goes, or -1: the outputs
 };
 
-// A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By a whole warp.
+// A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By a whole warp, a lane a
+// sequence. (At most 2^30 rows in all, or kFill pairs a sequence: the counts fit.)
 struct Units {
-    int64_t next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
-    int b0, n, c;
+    int next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
+    int b0, pairs, units, each, per, first, end, n, c, tiles, blocks;  // this lane's sequence
 
     __device__ __forceinline__ void load(const TreeWork &w)
     {
         const int lane = threadIdx.x % 32, b = b0 + lane;
-        upto = 0, n = 0, c = 0;
-        if (b < w.p.batch) {
-            n = w.p.lens[b], c = w.p.counts ? w.p.counts[b] : w.p.nodes;
-            const TreeSeq s = tree_seq(w, n, c);
-            upto = (int64_t)s.units * s.pairs;
-        }
+        TreeSeq s = {};
+        if (b < w.p.batch) s = tree_seq_of(w, b);
+        pairs = s.pairs, units = s.units, each = s.each * s.per, per = s.per, first = s.first, end = s.end, n = s.n, c = s.c;
+        tiles = s.tiles, blocks = s.blocks;
+        upto = units * pairs;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
-            const int64_t y = __shfl_up_sync(~0u, (long long)upto, k);
+            const int y = __shfl_up_sync(~0u, upto, k);
             if (lane >= k) upto += y;
         }
     }
     __device__ __forceinline__ bool take(const TreeWork &w, Unit &u)
     {
-        int64_t all;
-        while (b0 < 0 || (all = __shfl_sync(~0u, (long long)upto, 31)) <= next - base) {
+        int all;
+        while (b0 < 0 || (all = __shfl_sync(~0u, upto, 31)) <= next - base) {
             if (b0 >= 0) base += all;
             b0 = b0 < 0 ? 0 : b0 + 32;
             if (b0 >= w.p.batch) return false;
             load(w);
         }
-        const int64_t at = next - base;
-        const int lane = __ffs(__ballot_sync(~0u, upto > at)) - 1;
+        const int lane = __ffs(__ballot_sync(~0u, upto > next - base)) - 1;
+        const auto of = [&](int x) { return __shfl_sync(~0u, x, lane); };
+        const int count = of(pairs), many = of(units), local = next - base - (of(upto) - many * count);
+        const int index = over(local, count), pair = local - index * count, rows = of(blocks);
         u.b = b0 + lane;
-        const TreeSeq s = tree_seq(w, __shfl_sync(~0u, n, lane), __shfl_sync(~0u, c, lane));
-        const int local = (int)(at - (__shfl_sync(~0u, (long long)upto, lane) - (int64_t)s.units * s.pairs));
-        const int index = over(local, s.pairs), pair = local - index * s.pairs;
-        u.n = s.n, u.c = s.c, u.first = s.first, u.stop = s.end;
-        u.kv = over(pair, s.blocks);
-        u.first_row = (pair - u.kv * s.blocks) * w.rule.rows;
-        u.rows = min(w.rule.rows, s.c * w.p.group - u.first_row);
-        u.tile = index * s.each * s.per;
-        u.end = min(s.tiles, u.tile + s.each * s.per);
-        u.per = s.per;
+        u.n = of(n), u.c = of(c), u.first = of(first), u.stop = of(end), u.per = of(per);
+        u.kv = rows == 1 ? pair : over(pair, rows);
+        u.first_row = (pair - u.kv * rows) * w.rule.rows;
+        u.rows = min(w.rule.rows, u.c * w.p.group - u.first_row);
+        u.tile = index * of(each);
+        u.end = min(of(tiles), u.tile + of(each));
         // lengths that change under the call: nothing past the workspace
-        u.slot = s.units == 1 ? -1 : local < w.slots ? local : -2;
+        u.slot = many == 1 ? -1 : local < w.slots ? local : -2;
         next += gridDim.x;
         return true;
     }
@@ -370,38 +368,11 @@ struct TreeMma {
 
     // ---------------------------------------------------------- copies
 
-    // Copies that were started, in order, and whose barriers are still to be told.
-    struct Told {
-        uint32_t first = 0, second = 0;
-        __device__ __forceinline__ void tell()
-        {
-            fence_async();
-            bar_arrive(first);
-            first = second, second = 0;
-        }
-        // The oldest, once it has come.
-        __device__ __forceinline__ void one()
-        {
-            if (second)
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            tell();
-        }
-        __device__ __forceinline__ void add(uint32_t bar)
-        {
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (!first) {
-                first = bar;
-            } else if (!second) {
-                second = bar;
-            } else {
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
-                tell();
-                second = bar;
-            }
-        }
-    };
+    // Arrives on a barrier when the copies that this thread has started are there. The products' warp fences them for its proxy.
+    static __device__ __forceinline__ void tell(uint32_t bar)
+    {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    }
 
     static __device__ __forceinline__ void copy16(uint32_t dst, const T *src, bool some)
     {
@@ -426,19 +397,9 @@ struct TreeMma {
         // the row that this lane looks up
         const int held = lane / kOwn * kTogether + warp * kOwn + lane % kOwn;
         const bool mine = piece < pieces;
-        Told told;
         Way way;
         int slot = 0, slot_round = 0, count = 0;
-        // Waits for a barrier, telling what has come meanwhile: nobody waits for a copy that is only told after this.
-        const auto wait = [&](uint64_t &b, int parity) {
-            const uint32_t bar = smem_at(&b);
-            bool ok = bar_test(bar, parity);
-            while (!ok && told.first) {
-                told.one();
-                ok = bar_test(bar, parity);
-            }
-            return __all_sync(~0u, ok || bar_wait(bar, parity, &ct.dead));
-        };
+        const auto wait = [&](uint64_t &bar, int parity) { return warp_wait(smem_at(&bar), parity, &ct.dead); };
         bool alive = true;
         for (; (alive = wait(ct.unit_full[way.i], way.round & 1)) && *(volatile int *)&ct.units[way.i].b >= 0; way.past(ct)) {
             const Unit &u = ct.units[way.i];
@@ -463,32 +424,36 @@ struct TreeMma {
                 return at;
             };
             int64_t next = look(u.tile);
-            // queries: rows behind the last are zeros
+            // queries: rows behind the last are zeros; a lane works out where a row begins
             const int qi = (seq - 1) % kQs, q_round = (seq - 1) / kQs;
+            const int asked = lane / kOwn * kTogether + warp * kOwn + lane % kOwn;
+            int64_t query = -1;
+            if (asked < rows) {
+                const int node = (int)quotient(first_row + asked, w.by_heads), head = kv * p.group + first_row + asked - node * p.group;
+                query = u.b * p.q_bs + node * p.q_ns + head * p.q_hs;
+            }
             if (!(alive = wait(ct.q_empty[qi], (q_round & 1) ^ 1))) break;
-            if (piece < padded) {
-                const T *queries = (const T *)p.q + u.b * p.q_bs + piece * 8;
-#pragma unroll 1
-                for (int r = row0; r < Shape::kRows; r += kTogether) {
-                    const uint32_t dst = q + qi * Shape::kQ + slab * (Shape::kRows * 128) + r * 128 + ((chunk ^ (r & 7)) << 4);
-                    const T *src = (const T *)p.q;
-                    const bool some = r < rows && mine;
-                    if (some) {
-                        const int node = (int)quotient(first_row + r, w.by_heads), head = kv * p.group + first_row + r - node * p.group;
-                        src = queries + node * p.q_ns + head * p.q_hs;
-                    }
-                    if (w.q_vec || !some) {
-                        copy16(dst, src, some);
-                    } else {
-                        Pack<T, 8> x;
+            const uint32_t q_to = q + qi * Shape::kQ + slab * (Shape::kRows * 128) - slab * Shape::kSlab;
+#pragma unroll 4
+            for (int i = 0; i < Shape::kRows / kTogether; ++i) {
+                const int64_t from = __shfl_sync(~0u, (long long)query, i * kOwn + lane / kLanes);
+                const uint32_t dst = q_to + (i & 1 ? odd : even) + i * (kTogether * 128);
+                const T *src = (const T *)p.q + (from >= 0 && mine ? from + piece * 8 : 0);
+                if (piece >= padded) continue;
+                if (w.q_vec) {
+                    copy16(dst, src, from >= 0 && mine);
+                } else {
+                    Pack<T, 8> x;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x.v[i] = src[i];
-                        const uint4 y = *reinterpret_cast<const uint4 *>(&x);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
-                    }
+                    for (int k = 0; k < 8; ++k) x.v[k] = from >= 0 && mine ? src[k] : from_f32<T>(0.0f);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(&x);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
                 }
             }
-            told.add(smem_at(&ct.q_full[qi]));
+            if (w.q_vec)
+                tell(smem_at(&ct.q_full[qi]));
+            else
+                bar_arrive(smem_at(&ct.q_full[qi]));
             for (int tile = u.tile; alive && tile < end; ++tile) {
                 const int64_t places = next;
                 const bool every = __all_sync(~0u, next >= 0 || held >= kTok);
@@ -514,13 +479,12 @@ struct TreeMma {
                                 copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), some ? src + at : src, some);
                         }
                     }
-                    told.add(smem_at(&ct.full[slot]));
+                    tell(smem_at(&ct.full[slot]));
                     if (++slot == kSlots) slot = 0, ++slot_round;
                 }
             }
             if (!alive) break;
         }
-        while (told.first) told.one();
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 
@@ -568,6 +532,7 @@ struct TreeMma {
             if (know_a == 1 && ga < gv + 2 && (!fresh || ready(ct.q_full[qi], q_round)) && ready(ct.full[slot_a], round_a) &&
                 (ga < 2 || ready(ct.o_done[ga & 1], (ga - 2) / 2))) {
                 did = true;
+                fence_async();
                 mma_after();
                 const uint64_t left = shared_by_all(operand(q + qi * Shape::kQ, 16));
                 const uint64_t right = shared_by_all(operand(ring + slot_a * Shape::kSlot, 16));
@@ -596,6 +561,7 @@ struct TreeMma {
             }
             if (gv < ga && ready(ct.p_ready[gv & 1], gv / 2) && ready(ct.full[slot_v], round_v)) {
                 did = true;
+                fence_async();
                 mma_after();
                 const bool first = tile_v == chunk_v && !*(volatile int *)&ct.keep_o;
                 const uint64_t right = shared_by_all(operand(ring + slot_v * Shape::kSlot, Shape::kSlab));
