@@ -25,8 +25,8 @@ struct TreeRule {
     int rows;   // rows a pair's block, at most: a power of two
     int wide;   // rows of the widest block of this type: a call whose trees have fewer may take narrower ones,
                 // which are then one block a key-value head either way
-    int least;  // tiles a chunk, at least, for up to half of the widest block's rows; twice as many for more
-    int group;  // tiles a group, at least; 0: a group is a chunk
+    int least;  // tiles a chunk, at least, for up to half of the widest block's rows; twice as many for more: a power of two
+    int group;  // tiles a group, at least: a power of two, or 1 where a group is a chunk
 };
 
 // CTAs that a sequence's chunks are to fill when it is alone.
@@ -35,7 +35,10 @@ constexpr int kFill = kSms;
 struct TreeWork {
     TreeParams p;
     TreeRule rule;
-    int by_group;     // units are groups, else chunks
+    int by_group;     // units are groups, else chunks; -1: as the sequences' lengths say (*grouped)
+    int log_tok, log_rows, log_least;
+    int most;         // chunks that sequences of one block a key-value head are cut into, at most
+    int *grouped;     // the choice, where the main kernel makes it
     int slots;        // workspace slots a sequence, 0: no pair has more than one unit
     int slot_rows;    // rows of a slot
     Divide page;      // by the page size
@@ -63,7 +66,7 @@ inline int slot_rows_of(const TreeRule &r, int group, int nodes)
 inline int64_t tree_need(const TreeRule &r, int batch, int kv_heads, int group, int nodes, int head_dim, int64_t max_len)
 {
     const int64_t rows = (int64_t)batch * slots_of(r, kv_heads, group, nodes, max_len) * slot_rows_of(r, group, nodes);
-    return rows == 0 ? 0 : (rows * 8 + 15) / 16 * 16 + rows * head_dim * 4;
+    return rows == 0 ? 0 : 16 + (rows * 8 + 15) / 16 * 16 + rows * head_dim * 4;
 }
 inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *workspace)
 {
@@ -73,8 +76,12 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
     w.slot_rows = slot_rows_of(r, p.group, p.nodes);
     w.page = divide_by(p.page_size), w.by_heads = divide_by(p.group);
     const int64_t rows = (int64_t)p.batch * w.slots * w.slot_rows;
-    w.ml = (float2 *)workspace;
-    w.acc = (float *)((char *)workspace + (rows * 8 + 15) / 16 * 16);
+    w.grouped = (int *)workspace;
+    w.ml = (float2 *)((char *)workspace + 16);
+    w.acc = (float *)((char *)workspace + 16 + (rows * 8 + 15) / 16 * 16);
+    const auto log2_of = [](int x) { return 31 - __builtin_clz((unsigned)x); };
+    w.log_tok = log2_of(r.tok), w.log_rows = log2_of(r.rows), w.log_least = log2_of(r.least);
+    w.most = p.kv_heads < kFill ? kFill / p.kv_heads : 1;
     const int per = 16 / es;
     w.q_vec = (uintptr_t)p.q % 16 == 0 && p.q_bs % per == 0 && p.q_ns % per == 0 && p.q_hs % per == 0;
     w.out_vec = (uintptr_t)p.out % 16 == 0 && p.out_bs % per == 0 && p.out_ns % per == 0 && p.out_hs % per == 0;
@@ -82,7 +89,7 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
 }
 // The float32 kernel's: a block of as many rows as four warps take.
 constexpr int kSimtTok = 32;
-inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 0}; }
+inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 1}; }
 
 cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream);
 
@@ -112,72 +119,78 @@ __device__ __forceinline__ int over(int x, int y)
 }
 __device__ __forceinline__ int over_up(int x, int y) { return over(x + y - 1, y); }
 
-// `n`, `c` as read. A sequence that cannot be attended to has one unit a pair and no tokens.
-__device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
+// `n`, `c` as read. A sequence that cannot be attended to has one unit a pair and no tokens. Few instructions where chunks
+// are of the least length: what comes before the first copy is a kernel's start.
+__device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c, bool by_group)
 {
     TreeSeq s;
     const TreeParams &p = w.p;
-    const bool bad_count = c < 0 || c > p.nodes;
+    const bool bad_count = (unsigned)c > (unsigned)p.nodes;
     s.c = bad_count ? p.nodes : c;
     s.bad = bad_count || n < 0 || n > p.max_len - s.c;
     s.n = s.bad ? 0 : n;
     s.first = p.window && s.n + 1 > p.window ? s.n + 1 - p.window : 0;
     s.end = s.bad ? 0 : s.n + s.c;
     const int rows = s.c * p.group;
-    s.blocks = (rows + w.rule.rows - 1) >> (31 - __clz(w.rule.rows));  // powers of two, and tiles
+    s.blocks = (rows + w.rule.rows - 1) >> w.log_rows;
     s.pairs = s.blocks * p.kv_heads;
-    s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) >> (31 - __clz(w.rule.tok));
-    const int least = 2 * rows > w.rule.wide ? 2 * w.rule.least : w.rule.least;
-    const int most = s.pairs < kFill ? over(kFill, max(s.pairs, 1)) : 1;
-    s.per = s.tiles <= least * most ? least : max(least, over_up(s.tiles, most));
-    s.chunks = s.c == 0 ? 0 : max(1, over_up(s.tiles, s.per));
+    s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) >> w.log_tok;
+    const int log_least = w.log_least + (2 * rows > w.rule.wide), least = 1 << log_least;
+    const int most = s.blocks <= 1 ? w.most : s.pairs < kFill ? over(kFill, s.pairs) : 1;
+    if (s.tiles <= (int64_t)most << log_least) {
+        s.per = least;
+        s.chunks = s.c == 0 ? 0 : max(1, (s.tiles + least - 1) >> log_least);
+        s.fold = max(1, w.rule.group >> log_least);  // a power of two
+        s.each = by_group ? s.fold : 1;
+        s.units = by_group ? (s.chunks + s.fold - 1) >> (31 - __clz(s.fold)) : s.chunks;
+        return s;
+    }
+    s.per = over_up(s.tiles, most);
+    s.chunks = over_up(s.tiles, s.per);
     s.fold = max(1, over_up(w.rule.group, s.per));
-    s.each = w.by_group ? s.fold : 1;
+    s.each = by_group ? s.fold : 1;
     s.units = over_up(s.chunks, s.each);
     return s;
 }
-__device__ __forceinline__ TreeSeq tree_seq_of(const TreeWork &w, int b)
+__device__ __forceinline__ TreeSeq tree_seq_of(const TreeWork &w, int b, bool by_group)
 {
-    return tree_seq(w, w.p.lens[b], w.p.counts ? w.p.counts[b] : w.p.nodes);
+    return tree_seq(w, w.p.lens[b], w.p.counts ? w.p.counts[b] : w.p.nodes, by_group);
 }
 
-// What a row's node sees: its mask without the bits behind the last node, and the first committed token.
+// A node's mask as it lies in memory, without the bits behind the last node.
 struct RowMask {
-    uint64_t bits[kMaxWords];
-    int from;
+    const int64_t *at;
+    int words, n, c, from;  // committed tokens, nodes, first committed token seen
+
+    __device__ __forceinline__ uint64_t word(int i) const
+    {
+        const int have = c - 64 * i;
+        return i >= words || have <= 0 ? 0 : (uint64_t)at[i] & (have >= 64 ? ~0ull : (1ull << have) - 1);
+    }
+    // Bits for the 64 tokens from t on: the node sees them.
+    __device__ __forceinline__ uint64_t seen_from(int t) const
+    {
+        const int off = t - n;  // bit `off` of the mask comes first
+        if (off >= 0) {
+            const int i = off >> 6, sh = off & 63;
+            return word(i) >> sh | (sh ? word(i + 1) << (64 - sh) : 0);
+        }
+        // committed ones: from `from` on, before n
+        uint64_t x = off <= -64 ? ~0ull : (1ull << -off) - 1;
+        const int skip = from - t;
+        if (skip > 0) x = skip >= 64 ? 0 : x >> skip << skip;
+        return off <= -64 ? x : x | word(0) << -off;
+    }
 };
-__device__ __forceinline__ RowMask row_mask(const TreeParams &p, int b, int node, const TreeSeq &s)
+__device__ __forceinline__ RowMask row_mask(const TreeParams &p, int b, int node, int n, int c)
 {
-    RowMask m;
-    const int64_t *at = p.mask + ((int64_t)b * p.nodes + node) * p.words;
-    int count = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxWords; ++i) {
-        const int have = s.c - 64 * i;
-        m.bits[i] = i < p.words && have > 0 ? (uint64_t)at[i] & (have >= 64 ? ~0ull : (1ull << have) - 1) : 0;
-        count += __popcll(m.bits[i]);
+    RowMask m = {p.mask + ((int64_t)b * p.nodes + node) * p.words, p.words, n, c, 0};
+    if (p.window) {
+        int count = 0;
+        for (int i = 0; i < p.words; ++i) count += __popcll(m.word(i));
+        m.from = max(0, n + max(count, 1) - p.window);
     }
-    m.from = p.window ? max(0, s.n + max(count, 1) - p.window) : 0;
     return m;
-}
-// Bits for the 64 tokens from t on: the node sees them.
-__device__ __forceinline__ uint64_t seen_from(const RowMask &m, int n, int t)
-{
-    const int off = t - n;  // bit `off` of the mask comes first
-    uint64_t x = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxWords; ++i) {
-        const int sh = 64 * i - off;  // word i's first bit, from t on
-        if (sh >= 0 && sh < 64) x |= m.bits[i] << sh;
-        if (sh < 0 && sh > -64) x |= m.bits[i] >> -sh;
-    }
-    if (off < 0) {  // committed ones: from `from` on, before n
-        uint64_t before = off <= -64 ? ~0ull : (1ull << -off) - 1;
-        const int skip = m.from - t;
-        if (skip > 0) before = skip >= 64 ? 0 : before >> skip << skip;
-        x |= before;
-    }
-    return x;
 }
 
 // The factors of a fold of two triples whose maxima are in units of log 2, or of the natural logarithm.

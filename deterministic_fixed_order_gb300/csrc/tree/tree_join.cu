@@ -8,25 +8,29 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAhead = 8;  // units whose accumulators a warp has in flight
+constexpr int kRowsEach = 2;  // rows a warp takes of its sequence
 
+// A CTA has rows of one sequence, so that what follows from the sequence is worked out once.
 template <typename T, int PER, bool LOG2>
-__global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_constant__ TreeWork w)
+__global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_constant__ TreeWork w, int across)
 {
     const TreeParams &p = w.p;
     const int lane = threadIdx.x % 32;
     enter_grid();
-    const int64_t rows = (int64_t)p.batch * p.nodes * p.q_heads;
-    for (int64_t row = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; row < rows; row += (int64_t)gridDim.x * kWarps) {
-        const int b = (int)(row / (p.nodes * p.q_heads)), in = (int)(row - (int64_t)b * p.nodes * p.q_heads);
+    const int b = blockIdx.x / across, of = p.nodes * p.q_heads;
+    const bool by_group = w.by_group < 0 ? *w.grouped != 0 : w.by_group != 0;
+    const TreeSeq s = tree_seq_of(w, b, by_group);
+    if (s.units <= 1) return;
+    const int64_t step = (int64_t)s.pairs * w.slot_rows;
+    // lengths that change under the call: no unit past the workspace
+    const int units = min(s.units, over(w.slots, max(s.pairs, 1))), group = by_group ? 1 : s.fold;
+    for (int in = ((blockIdx.x - b * across) * kWarps + threadIdx.x / 32) * kRowsEach, k = 0; k < kRowsEach; ++k, ++in) {
+        if (in >= of) return;
         const int node = in / p.q_heads, head = in - node * p.q_heads;
-        const TreeSeq s = tree_seq_of(w, b);
-        if (node >= s.c || s.units <= 1) continue;
-        const int kv = head / p.group, r = node * p.group + head - kv * p.group, block = r / w.rule.rows;
+        if (node >= s.c) return;
+        const int kv = (int)quotient(head, w.by_heads), r = node * p.group + head - kv * p.group, block = r >> w.log_rows;
         const int pair = kv * s.blocks + block;
         const int64_t first = ((int64_t)b * w.slots + pair) * w.slot_rows + (r - block * w.rule.rows);
-        const int64_t step = (int64_t)s.pairs * w.slot_rows;
-        // lengths that change under the call: no unit past the workspace
-        const int units = min(s.units, w.slots / max(s.pairs, 1)), group = w.by_group ? 1 : s.fold;
         float m = neg_inf(), l = 0.0f, a[PER], gm = neg_inf(), gl = 0.0f, ga[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) a[i] = ga[i] = 0.0f;
@@ -39,9 +43,10 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
                 if (u0 + k >= units) continue;
                 const int64_t at = first + (u0 + k) * step;
                 ml[k] = w.ml[at];
+                const float *acc = w.acc + at * p.head_dim;
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    if (lane + 32 * i < p.head_dim) x[k][i] = w.acc[at * p.head_dim + lane + 32 * i];
+                    if (lane + 32 * i < p.head_dim) x[k][i] = acc[lane + 32 * i];
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
@@ -76,19 +81,19 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (lane + 32 * i < p.head_dim) out[lane + 32 * i] = quotient_of<T>(a[i], l, inverse);
-        if (lane == 0 && p.lse) p.lse[row] = log_sum<LOG2>(m, l);
+        if (lane == 0 && p.lse) p.lse[(int64_t)b * of + in] = log_sum<LOG2>(m, l);
     }
 }
 
 template <typename T, bool LOG2>
 cudaError_t launch_type(const TreeWork &w, cudaStream_t stream)
 {
-    const int64_t need = ((int64_t)w.p.batch * w.p.nodes * w.p.q_heads + kWarps - 1) / kWarps, most = kSms * 8;
-    const dim3 grid((unsigned)(need < most ? need : most));
+    const int across = (w.p.nodes * w.p.q_heads + kWarps * kRowsEach - 1) / (kWarps * kRowsEach);
+    const dim3 grid((unsigned)((int64_t)w.p.batch * across));
     const auto kernel = w.p.head_dim <= 64    ? tree_join_kernel<T, 2, LOG2>
                         : w.p.head_dim <= 128 ? tree_join_kernel<T, 4, LOG2>
                                               : tree_join_kernel<T, 8, LOG2>;
-    return launch_early(kernel, grid, kWarps * 32, 0, stream, w);
+    return launch_early(kernel, grid, kWarps * 32, 0, stream, w, across);
 }
 
 }  // namespace

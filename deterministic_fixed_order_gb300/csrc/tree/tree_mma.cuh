@@ -42,13 +42,15 @@ struct MmaShape {
     static constexpr int kShift = std::is_same_v<T, __half> ? 8 : 0, kSlack = std::is_same_v<T, __half> ? 7 : 8;
     static constexpr int kControl = 3072, kBytes = kSlots * kSlot + kQs * kQ + kControl;
     // chunks of 256 tokens at least, groups of 1024
-    static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kFolds ? 1024 / kTok : 0}; }
+    static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kFolds ? 1024 / kTok : 1}; }
 };
 
 #ifdef __CUDACC__
 
-// More units of a chunk each, as the longest sequence allows, than this many an SM: units are groups.
-constexpr int kByGroup = 4;
+// More units of a chunk each than this many a CTA: units are groups.
+constexpr int kByGroup = 12;
+// Sequences whose chunks are counted for that; of more the sizes decide.
+constexpr int kCounted = 256;
 constexpr int kSoftmax = 256, kCopy = 128, kMmaThreads = kSoftmax + 32 + kCopy + 32;
 
 // ------------------------------------------------------------------ instructions
@@ -217,12 +219,13 @@ struct Unit {
 struct Units {
     int next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
     int b0, pairs, units, each, per, first, end, n, c, tiles, blocks;  // this lane's sequence
+    bool grouped;  // units are groups
 
     __device__ __forceinline__ void load(const TreeWork &w)
     {
         const int lane = threadIdx.x % 32, b = b0 + lane;
         TreeSeq s = {};
-        if (b < w.p.batch) s = tree_seq_of(w, b);
+        if (b < w.p.batch) s = tree_seq_of(w, b, grouped);
         pairs = s.pairs, units = s.units, each = s.each * s.per, per = s.per, first = s.first, end = s.end, n = s.n, c = s.c;
         tiles = s.tiles, blocks = s.blocks;
         upto = units * pairs;
@@ -331,7 +334,18 @@ struct TreeMma {
     static __device__ __forceinline__ void schedule(const TreeWork &w, Control &ct)
     {
         Units units;
-        units.next = blockIdx.x, units.base = 0, units.b0 = -1;
+        units.next = blockIdx.x, units.base = 0, units.b0 = -1, units.grouped = w.by_group > 0;
+        if (w.by_group < 0) {
+            // groups where chunks are more than kByGroup a CTA
+            int all = 0;
+            for (units.b0 = 0; units.b0 < w.p.batch; units.b0 += 32) {
+                units.load(w);
+                all += __shfl_sync(~0u, units.upto, 31);
+            }
+            units.b0 = -1;
+            units.grouped = all > kByGroup * (int)gridDim.x;
+            if (blockIdx.x == 0 && threadIdx.x % 32 == 0) *w.grouped = units.grouped;
+        }
         bool more = true;
         for (int i = 0, round = 0; more; ) {
             Unit u;
@@ -396,6 +410,19 @@ struct TreeMma {
         static_assert(kTogether % 4 == 0, "two places");
         // the row that this lane looks up
         const int held = lane / kOwn * kTogether + warp * kOwn + lane % kOwn;
+        const bool takes = piece < padded;
+        // Rows whose places the lanes hold, -1 for zeros, to `to`.
+        const auto copy_rows = [&](uint32_t to, const T *src, int64_t places, auto passes) {
+            constexpr int kTimes = decltype(passes)::value;
+            // bit i kOwn: this thread's row of pass i is there
+            const uint32_t there = (__ballot_sync(~0u, places >= 0) & (piece < pieces ? ~0u : 0u)) >> (lane / kLanes);
+            const int64_t at = places < 0 ? 0 : places;
+#pragma unroll
+            for (int i = 0; i < kTimes; ++i) {
+                const T *from = src + __shfl_sync(~0u, (long long)at, i * kOwn + lane / kLanes);
+                if (takes) copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), from, (there >> (i * kOwn)) & 1);
+            }
+        };
         const bool mine = piece < pieces;
         Way way;
         int slot = 0, slot_round = 0, count = 0;
@@ -433,21 +460,22 @@ struct TreeMma {
                 query = u.b * p.q_bs + node * p.q_ns + head * p.q_hs;
             }
             if (!(alive = wait(ct.q_empty[qi], (q_round & 1) ^ 1))) break;
-            const uint32_t q_to = q + qi * Shape::kQ + slab * (Shape::kRows * 128) - slab * Shape::kSlab;
-#pragma unroll 4
-            for (int i = 0; i < Shape::kRows / kTogether; ++i) {
-                const int64_t from = __shfl_sync(~0u, (long long)query, i * kOwn + lane / kLanes);
-                const uint32_t dst = q_to + (i & 1 ? odd : even) + i * (kTogether * 128);
-                const T *src = (const T *)p.q + (from >= 0 && mine ? from + piece * 8 : 0);
-                if (piece >= padded) continue;
-                if (w.q_vec) {
-                    copy16(dst, src, from >= 0 && mine);
-                } else {
+            const uint32_t q_to = q + qi * Shape::kQ + slab * (Shape::kRows * 128 - Shape::kSlab);
+            if (w.q_vec) {
+                copy_rows(q_to, (const T *)p.q + (mine ? piece * 8 : 0), query, std::integral_constant<int, Shape::kRows / kTogether>());
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < Shape::kRows / kTogether; ++i) {
+                    const int64_t from = __shfl_sync(~0u, (long long)query, i * kOwn + lane / kLanes);
+                    const T *src = (const T *)p.q + (from >= 0 && mine ? from + piece * 8 : 0);
+                    if (!takes) continue;
                     Pack<T, 8> x;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) x.v[k] = from >= 0 && mine ? src[k] : from_f32<T>(0.0f);
                     const uint4 y = *reinterpret_cast<const uint4 *>(&x);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_to + (i & 1 ? odd : even) + i * (kTogether * 128)), "r"(y.x),
+                                 "r"(y.y), "r"(y.z), "r"(y.w)
+                                 : "memory");
                 }
             }
             if (w.q_vec)
@@ -456,29 +484,12 @@ struct TreeMma {
                 bar_arrive(smem_at(&ct.q_full[qi]));
             for (int tile = u.tile; alive && tile < end; ++tile) {
                 const int64_t places = next;
-                const bool every = __all_sync(~0u, next >= 0 || held >= kTok);
                 next = look(tile + 1);
 #pragma unroll 1
                 for (int value = 0; value < 2; ++value) {
                     if (!(alive = wait(ct.empty[slot], (slot_round & 1) ^ 1))) break;
-                    const T *src = (const T *)(value ? p.v : p.k) + (mine ? piece * 8 : 0);
-                    const uint32_t to = ring + slot * Shape::kSlot;
-                    if (every) {
-#pragma unroll
-                        for (int i = 0; i < kPasses; ++i) {
-                            const int64_t at = __shfl_sync(~0u, (long long)places, i * kOwn + lane / kLanes);
-                            if (mine) copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), src + at, true);
-                        }
-                    }
-                    if (!every || pieces != padded) {
-#pragma unroll 1
-                        for (int i = 0; i < kPasses; ++i) {
-                            const int64_t at = __shfl_sync(~0u, (long long)places, i * kOwn + lane / kLanes);
-                            const bool some = at >= 0 && mine;
-                            if (piece < padded && !(every && mine))
-                                copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), some ? src + at : src, some);
-                        }
-                    }
+                    copy_rows(ring + slot * Shape::kSlot, (const T *)(value ? p.v : p.k) + (mine ? piece * 8 : 0), places,
+                              std::integral_constant<int, kPasses>());
                     tell(smem_at(&ct.full[slot]));
                     if (++slot == kSlots) slot = 0, ++slot_round;
                 }
@@ -706,26 +717,61 @@ struct TreeMma {
         return true;
     }
 
-    // A row's result, or its triple, 32 places of the head at a time.
-    static __device__ __forceinline__ void put(const TreeWork &w, const float (&x)[32], int d0, T *out, float *acc, float inverse)
+    // Four lanes' four pieces of 16 bytes, turned: lane i of them gets the others' pieces i. So stores go along a row by 64
+    // bytes, a quarter of the lines that a lane a row would touch.
+    static __device__ __forceinline__ void turn(uint4 (&x)[4])
     {
+        const int lane = threadIdx.x % 4;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (d0 + 8 * k >= w.p.head_dim) continue;
-            if (out) {
-                Pack<T, 8> y;
+        for (int step = 1; step <= 2; step *= 2) {
+            const bool upper = lane & step;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y.v[i] = quotient_of<T>(x[8 * k + i], 0.0f, inverse);
-                if (w.out_vec) {
-                    *reinterpret_cast<Pack<T, 8> *>(out + d0 + 8 * k) = y;
-                } else {
+            for (int i = 0; i < 4; ++i) {
+                if (i & step) continue;
+                uint4 &a = x[i], &b = x[i + step];
+                uint32_t *p = reinterpret_cast<uint32_t *>(&a), *q = reinterpret_cast<uint32_t *>(&b);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) out[d0 + 8 * k + i] = y.v[i];
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t gives = upper ? p[k] : q[k], got = __shfl_xor_sync(~0u, gives, step);
+                    p[k] = upper ? got : p[k], q[k] = upper ? q[k] : got;
                 }
-            } else {
-                float4 *to = reinterpret_cast<float4 *>(acc + d0 + 8 * k);
-                to[0] = make_float4(x[8 * k], x[8 * k + 1], x[8 * k + 2], x[8 * k + 3]);
-                to[1] = make_float4(x[8 * k + 4], x[8 * k + 5], x[8 * k + 6], x[8 * k + 7]);
+            }
+        }
+    }
+    // Results, or accumulators, 32 places of the head at a time, of a warp's rows. `to`: where the four rows of this lane's four
+    // begin; bit i of `rows`: row i is written.
+    static __device__ __forceinline__ void put(const TreeWork &w, const float (&x)[32], int d0, T *const (&to)[4], T *own, float *acc,
+                                               uint32_t rows, bool puts, float inverse)
+    {
+        const int lane = threadIdx.x % 4;
+        if (!acc) {
+            uint4 y[4];
+            T *z = reinterpret_cast<T *>(y);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = quotient_of<T>(x[i], 0.0f, inverse);
+            if (w.out_vec) {
+                turn(y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((rows >> i & 1) && d0 + 8 * lane < w.p.head_dim) *reinterpret_cast<uint4 *>(to[i] + d0 + 8 * lane) = y[i];
+            } else if (puts) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (d0 + i < w.p.head_dim) own[d0 + i] = z[i];
+            }
+        } else {
+#pragma unroll
+            for (int part = 0; part < 32; part += 16) {
+                uint4 y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = make_uint4(__float_as_uint(x[part + 4 * i]), __float_as_uint(x[part + 4 * i + 1]),
+                                      __float_as_uint(x[part + 4 * i + 2]), __float_as_uint(x[part + 4 * i + 3]));
+                turn(y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((rows >> i & 1) && d0 + part + 4 * lane < w.p.head_dim)
+                        *reinterpret_cast<uint4 *>(acc + i * w.p.head_dim + d0 + part + 4 * lane) = y[i];
             }
         }
     }
@@ -746,19 +792,18 @@ struct TreeMma {
             const bool live = row < rows, works = warp * 32 < rows;
             const int node = live ? (int)quotient(first_row + row, w.by_heads) : 0;
             const int head = live ? u.kv * p.group + first_row + row - node * p.group : 0;
-            T *out = nullptr;
-            float *acc = nullptr;
-            int64_t slot_row = -1;
-            if (u.slot == -1) {
-                out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
-            } else if (u.slot >= 0) {
-                slot_row = ((int64_t)b * w.slots + u.slot) * w.slot_rows + row;
-                acc = w.acc + slot_row * p.head_dim;
-            }
-            const bool puts = live && (out || acc);
+            // where this row goes, the four rows of this lane and its neighbours, and which of these are written
+            const bool direct = u.slot == -1, puts = live && u.slot >= -1;
+            const int64_t slot_row = ((int64_t)b * w.slots + u.slot) * w.slot_rows + row;
+            T *const own = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
+            T *to[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = (T *)__shfl_sync(~0u, (unsigned long long)own, (tid & 28) + i);
+            float *const acc = direct ? nullptr : w.acc + (slot_row - row % 4) * p.head_dim;
+            const uint32_t written = __ballot_sync(~0u, puts) >> (tid & 28);
             const auto finish = [&](float m, float l) {
                 if (!puts || half) return;
-                if (!out)
+                if (!direct)
                     w.ml[slot_row] = make_float2(m, l);
                 else if (p.lse)
                     p.lse[((int64_t)b * p.nodes + node) * p.q_heads + head] = log_sum<true>(m, l);
@@ -768,18 +813,13 @@ struct TreeMma {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = quiet_nan();
 #pragma unroll 1
-                for (int cb = half; puts && cb < blocks; cb += 2) put(w, x, cb * 32, out, acc, 1.0f);
+                for (int cb = half; cb < blocks; cb += 2) put(w, x, cb * 32, to, own, acc, written, puts, 1.0f);
                 finish(0.0f, quiet_nan());
                 if (tid == 0) flag_bad_index(p.status);
                 continue;
             }
             const int n = u.n, first = u.first;
-            RowMask mask;
-            {
-                TreeSeq s;
-                s.n = n, s.c = c;
-                mask = row_mask(p, b, node, s);
-            }
+            const RowMask mask = row_mask(p, b, node, n, c);
             ++count;
             bool bad = false;
             float fm = neg_inf(), fl = 0.0f;  // of the chunks before
@@ -790,6 +830,8 @@ struct TreeMma {
                     const int at = first + tile * kTok;
                     const bool whole = at + kTok <= n && (!p.window || at >= n + c - p.window);
                     const uint32_t here = tmem + (g & 1) * kTok + half * kOwn;
+                    uint64_t seen = ~0ull;
+                    if (!whole && works) seen = mask.seen_from(at + half * kOwn);
                     if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
                     mma_after();
                     bool waited = tile == t0;  // for the tile before, whose product O may still change
@@ -810,7 +852,6 @@ struct TreeMma {
                             for (int i = 0; i < kOwn; ++i) x[i] = __fmul_rn(x[i], factor);
                         }
                         if (!whole) {
-                            const uint64_t seen = seen_from(mask, n, at + half * kOwn);
 #pragma unroll
                             for (int i = 0; i < kOwn; ++i)
                                 if (!((seen >> i) & 1)) x[i] = neg_inf();
@@ -918,8 +959,8 @@ struct TreeMma {
                         }
                         if (!last) {
                             if (Shape::kFolds) tm_store32(f + cb * 32, x);
-                        } else if (puts) {
-                            put(w, x, cb * 32, out, acc, inverse);
+                        } else {
+                            put(w, x, cb * 32, to, own, acc, written, puts, inverse);
                         }
                         __syncwarp();
                     }
@@ -955,7 +996,8 @@ cudaError_t launch_mma(TreeWork w, cudaStream_t stream)
     const TreeParams &p = w.p;
     const int64_t pairs = p.kv_heads * (((int64_t)p.nodes * p.group + w.rule.rows - 1) / w.rule.rows);
     const int64_t units = p.batch * (w.slots > pairs ? w.slots : pairs);
-    w.by_group = Shape::kFolds && units > kByGroup * kSms;
+    // what the sizes rule out, or, of many sequences, allow, is not worked out from the lengths
+    w.by_group = !Shape::kFolds || units <= kByGroup * kSms ? 0 : p.batch > kCounted ? 1 : -1;
     const dim3 grid((unsigned)(units < kSms ? units : kSms));
     if (cudaError_t e = launch_early(kernel, grid, kMmaThreads, Shape::kBytes, stream, w)) return e;
     const int dtype = std::is_same_v<typename Shape::T, __nv_bfloat16> ? DETFOLD_BF16 : DETFOLD_F16;

@@ -32,7 +32,8 @@ struct Simt {
     struct Shared {
         float q[kRows][DP];
         float weights[kWarps][RW][kTok];
-        RowMask masks[kRows];
+        uint64_t bits[kRows][kMaxWords];  // what each row's node sees of the drafted tokens
+        int from[kRows];                  // and from which committed one on
         alignas(16) unsigned char k[2][kTok * kPitch], v[2][kTok * kPitch];
     };
 
@@ -44,7 +45,7 @@ struct Simt {
         const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
         enter_grid();
         for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-            const TreeSeq s = tree_seq_of(w, b);
+            const TreeSeq s = tree_seq_of(w, b, false);
             for (int64_t u = blockIdx.x; u < (int64_t)s.units * s.pairs; u += gridDim.x) {
                 const int chunk = (int)(u / s.pairs), pair = (int)(u - (int64_t)chunk * s.pairs);
                 const int kv = pair / s.blocks, row0 = (pair - kv * s.blocks) * w.rule.rows;
@@ -69,7 +70,11 @@ struct Simt {
             }
             sh.q[r][d] = x;
         }
-        if (tid < rows) sh.masks[tid] = row_mask(p, b, (row0 + tid) / p.group, s);
+        if (tid < rows) {
+            const RowMask m = row_mask(p, b, (row0 + tid) / p.group, s.n, s.c);
+            for (int i = 0; i < kMaxWords; ++i) sh.bits[tid][i] = m.word(i);
+            sh.from[tid] = m.from;
+        }
         bool bad = s.bad;
         const int pieces = p.head_dim / kPer, tiles = (t_hi - t_lo + kTok - 1) / kTok;
         const auto fetch = [&](int tile) {
@@ -132,9 +137,8 @@ struct Simt {
                 if (!whole) {
                     bool here = false;
                     if (row < rows && t < t_hi) {
-                        const RowMask &mk = sh.masks[row];
                         const int j = t - s.n;
-                        here = j < 0 ? t >= mk.from : (mk.bits[j >> 6] >> (j & 63)) & 1;
+                        here = j < 0 ? t >= sh.from[row] : (sh.bits[row][j >> 6] >> (j & 63)) & 1;
                     }
                     if (!here) x[r] = neg_inf();
                     seen[r] = __ballot_sync(~0u, here);
