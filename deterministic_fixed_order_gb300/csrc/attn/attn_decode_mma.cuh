@@ -56,15 +56,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(T x, T y)
-{
-    uint16_t a, b;
-    memcpy(&a, &x, 2);
-    memcpy(&b, &y, 2);
-    return (uint32_t)b << 16 | a;
-}
-
 template <typename T_, int DP, int TOK, int NT>
 struct MmaTile {
     using T = T_;

@@ -7,6 +7,15 @@
 
 namespace detfold_attn {
 
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(T x, T y)
+{
+    uint16_t a, b;
+    memcpy(&a, &x, 2);
+    memcpy(&b, &y, 2);
+    return (uint32_t)b << 16 | a;
+}
+
 // Two weights as 16-bit pairs, hi + lo: hi truncated, so that lo, what hi leaves, is not negative, and neither part 0
 // where the weight is not. So both products with an infinite value are that infinity, as the weight's own
 // is. (Rounded to nearest, a weight of 1 leaves lo = 0, others a negative lo: NaN.) A weight of bfloat16 is off by 2^-16 of

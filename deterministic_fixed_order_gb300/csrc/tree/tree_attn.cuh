@@ -108,7 +108,7 @@ struct TreeSeq {
 };
 
 // x / y for x >= 0, y >= 1. Below 2^23 by the reciprocal, whose product with x is off by less than one.
-__device__ __forceinline__ int over(int x, int y)
+static __device__ __noinline__ int over(int x, int y)
 {
     if (x >> 23) return x / y;
     int q = (int)__fmul_rn((float)x, __frcp_rn((float)y));
@@ -170,16 +170,16 @@ struct RowMask {
     // Bits for the 64 tokens from t on: the node sees them.
     __device__ __forceinline__ uint64_t seen_from(int t) const
     {
-        const int off = t - n;  // bit `off` of the mask comes first
+        const int off = t - n, i = max(off, 0) >> 6;  // bit `off` of the mask comes first
+        uint64_t x = word(i);
         if (off >= 0) {
-            const int i = off >> 6, sh = off & 63;
-            return word(i) >> sh | (sh ? word(i + 1) << (64 - sh) : 0);
+            const int sh = off & 63;
+            return sh ? x >> sh | word(i + 1) << (64 - sh) : x;
         }
         // committed ones: from `from` on, before n
-        uint64_t x = off <= -64 ? ~0ull : (1ull << -off) - 1;
-        const int skip = from - t;
-        if (skip > 0) x = skip >= 64 ? 0 : x >> skip << skip;
-        return off <= -64 ? x : x | word(0) << -off;
+        const int skip = max(from - t, 0), back = min(-off, 64);
+        x = back < 64 ? x << back : 0;
+        return x | (skip < back ? ~0ull >> (64 - back) >> skip << skip : 0);
     }
 };
 __device__ __forceinline__ RowMask row_mask(const TreeParams &p, int b, int node, int n, int c)

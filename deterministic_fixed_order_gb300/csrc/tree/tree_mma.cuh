@@ -113,8 +113,10 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// A value that a warp's lanes share, said so that the compiler knows it: the products' operands have to be in uniform registers.
+// A value that a warp's lanes share, said so that the compiler knows it: the products' operands have to be in uniform registers,
+// and where a branch may part a warp every shuffle and vote behind it is made with a branch of its own.
 __device__ __forceinline__ uint32_t shared_by_all(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+__device__ __forceinline__ int shared_by_all(int x) { return __shfl_sync(~0u, x, 0); }
 __device__ __forceinline__ uint64_t shared_by_all(uint64_t x)
 {
     return (uint64_t)shared_by_all((uint32_t)(x >> 32)) << 32 | shared_by_all((uint32_t)x);
@@ -289,7 +291,7 @@ struct TreeMma {
         const uint32_t ring = smem_at(smem), q = ring + kSlots * Shape::kSlot;
         Control &ct = *reinterpret_cast<Control *>(smem + kSlots * Shape::kSlot + kQs * Shape::kQ);
         static_assert(sizeof(Control) <= Shape::kControl, "as kBytes has it");
-        const int tid = threadIdx.x, warp = tid / 32;
+        const int tid = threadIdx.x, warp = shared_by_all(tid / 32);
         if (tid == 0) {
             const auto set = [](uint64_t *bars, int n, int count) {
                 for (int i = 0; i < n; ++i) bar_init(smem_at(bars + i), count);
@@ -376,7 +378,7 @@ struct TreeMma {
         }
         __device__ __forceinline__ bool here(Control &ct)
         {
-            return warp_wait(smem_at(&ct.unit_full[i]), round & 1, &ct.dead) && *(volatile int *)&ct.units[i].b >= 0;
+            return warp_wait(smem_at(&ct.unit_full[i]), round & 1, &ct.dead) && shared_by_all(*(volatile int *)&ct.units[i].b) >= 0;
         }
     };
 
@@ -388,9 +390,13 @@ struct TreeMma {
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
     }
 
-    static __device__ __forceinline__ void copy16(uint32_t dst, const T *src, bool some)
+    // 16 bytes, or zeros; nothing where `not takes`. Without branches: each would cost more than the copy.
+    static __device__ __forceinline__ void copy16(uint32_t dst, const T *src, bool some, bool takes)
     {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+        asm volatile("{\n .reg .pred p, q;\n setp.eq.u32 p, %2, 0;\n setp.ne.u32 q, %3, 0;\n"
+                     " @q cp.async.cg.shared.global [%0], [%1], 16, p;\n}" ::"r"(dst),
+                     "l"(src), "r"((uint32_t)some), "r"((uint32_t)takes)
+                     : "memory");
     }
 
     static __device__ __forceinline__ void copies(const TreeWork &w, Control &ct, uint32_t ring, uint32_t q)
@@ -400,7 +406,7 @@ struct TreeMma {
         constexpr int kOwn = 32 / kLanes, kWarpRows = kPasses * kOwn;          // of them a warp's; a warp's rows of a tile
         static_assert(kWarpRows <= 32 && kTogether * kPasses == kTok, "a lane looks up a row at most");
         const TreeParams &p = w.p;
-        const int tid = threadIdx.x - kSoftmax - 32, warp = tid / 32, lane = tid % 32;
+        const int tid = threadIdx.x - kSoftmax - 32, warp = shared_by_all(tid / 32), lane = tid % 32;
         const int piece = tid % kLanes, pieces = p.head_dim / 8, padded = (pieces + 1) / 2 * 2;
         const int row0 = tid / kLanes, slab = piece / 8, chunk = piece % 8;
         // Where this thread's piece of row row0 + i kTogether lies: a place a row's last three bits, and 128 bytes a row. The
@@ -420,7 +426,7 @@ struct TreeMma {
 #pragma unroll
             for (int i = 0; i < kTimes; ++i) {
                 const T *from = src + __shfl_sync(~0u, (long long)at, i * kOwn + lane / kLanes);
-                if (takes) copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), from, (there >> (i * kOwn)) & 1);
+                copy16(to + (i & 1 ? odd : even) + i * (kTogether * 128), from, (there >> (i * kOwn)) & 1, takes);
             }
         };
         const bool mine = piece < pieces;
@@ -428,13 +434,13 @@ struct TreeMma {
         int slot = 0, slot_round = 0, count = 0;
         const auto wait = [&](uint64_t &bar, int parity) { return warp_wait(smem_at(&bar), parity, &ct.dead); };
         bool alive = true;
-        for (; (alive = wait(ct.unit_full[way.i], way.round & 1)) && *(volatile int *)&ct.units[way.i].b >= 0; way.past(ct)) {
+        for (; (alive = way.here(ct)); way.past(ct)) {
             const Unit &u = ct.units[way.i];
-            const int end = u.end, stop = u.stop, first = u.first, kv = u.kv;
-            if (u.tile >= end) continue;
+            const int begin = shared_by_all(u.tile), end = shared_by_all(u.end), stop = u.stop, first = u.first, kv = u.kv, b = u.b;
+            if (begin >= end) continue;
             const int first_row = u.first_row, rows = u.rows;
             const int seq = ++count;
-            const int32_t *table = p.table + u.b * p.table_stride;
+            const int32_t *table = p.table + b * p.table_stride;
             const int64_t in_row = kv * p.head_stride;
             // a row's place, or -1: looked up a tile ahead
             const auto look = [&](int tile) {
@@ -450,14 +456,14 @@ struct TreeMma {
                 }
                 return at;
             };
-            int64_t next = look(u.tile);
+            int64_t next = look(begin);
             // queries: rows behind the last are zeros; a lane works out where a row begins
             const int qi = (seq - 1) % kQs, q_round = (seq - 1) / kQs;
             const int asked = lane / kOwn * kTogether + warp * kOwn + lane % kOwn;
             int64_t query = -1;
             if (asked < rows) {
                 const int node = (int)quotient(first_row + asked, w.by_heads), head = kv * p.group + first_row + asked - node * p.group;
-                query = u.b * p.q_bs + node * p.q_ns + head * p.q_hs;
+                query = b * p.q_bs + node * p.q_ns + head * p.q_hs;
             }
             if (!(alive = wait(ct.q_empty[qi], (q_round & 1) ^ 1))) break;
             const uint32_t q_to = q + qi * Shape::kQ + slab * (Shape::kRows * 128 - Shape::kSlab);
@@ -482,7 +488,7 @@ struct TreeMma {
                 tell(smem_at(&ct.q_full[qi]));
             else
                 bar_arrive(smem_at(&ct.q_full[qi]));
-            for (int tile = u.tile; alive && tile < end; ++tile) {
+            for (int tile = begin; alive && tile < end; ++tile) {
                 const int64_t places = next;
                 next = look(tile + 1);
 #pragma unroll 1
@@ -512,8 +518,8 @@ struct TreeMma {
         const auto look = [&](Way &way, bool frees, int &know, int &tile, int &end, int &per) {
             while (know == 0 && ready(ct.unit_full[way.i], way.round)) {
                 const volatile Unit &u = ct.units[way.i];
-                tile = u.tile, end = u.end, per = u.per;
-                if (u.b < 0)
+                tile = shared_by_all(u.tile), end = shared_by_all(u.end), per = shared_by_all(u.per);
+                if (shared_by_all(u.b) < 0)
                     know = 2;
                 else if (tile < end)  // units without tokens have no products
                     know = 1;
@@ -550,11 +556,13 @@ struct TreeMma {
                 const uint32_t to = shared_by_all(tmem + (ga & 1) * kTok);
                 const bool ends = tile_a + 1 == end_a;
                 if (one_lane()) {
-#pragma unroll
-                    for (int k = 0; k < kNS * 4; ++k)  // 32 bytes on, in the next slab after four
-                        if (k < steps)
-                            mma_ss(to, left + ((k >> 2) * (Shape::kRows * 8) + (k & 3) * 2),
-                                   right + ((k >> 2) * (Shape::kSlab / 16) + (k & 3) * 2), scores, k > 0);
+                    uint64_t a = left, b = right;
+#pragma unroll 1
+                    for (int k = 0; k < steps; ++k) {  // 32 bytes on, in the next slab after four
+                        mma_ss(to, a, b, scores, k > 0);
+                        const bool slab = (k & 3) == 3;
+                        a += slab ? Shape::kRows * 8 - 6 : 2, b += slab ? Shape::kSlab / 16 - 6 : 2;
+                    }
                     mma_commit(smem_at(&ct.s_full[ga & 1]));
                     mma_commit(smem_at(&ct.empty[slot_a]));
                     if (ends) mma_commit(smem_at(&ct.q_empty[qi]));
@@ -574,17 +582,24 @@ struct TreeMma {
                 did = true;
                 fence_async();
                 mma_after();
-                const bool first = tile_v == chunk_v && !*(volatile int *)&ct.keep_o;
+                const bool first = tile_v == chunk_v && !shared_by_all(*(volatile int *)&ct.keep_o);
                 const uint64_t right = shared_by_all(operand(ring + slot_v * Shape::kSlot, Shape::kSlab));
                 const uint32_t weights = shared_by_all(tmem + (gv & 1) * kTok), to = shared_by_all(tmem + Shape::kColO);
                 if (one_lane()) {
                     // weights of 32 tokens: 16 columns of upper parts, 16 of lower ones; 2048 bytes of values
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(to, weights + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, k > 0 || !first);
-#pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(to, weights + 16 + (k >> 1) * 32 + (k & 1) * 8, right + k * 128, values, true);
+                    bool add = !first;
+#pragma unroll 1
+                    for (int part = 0; part < 32; part += 16) {
+                        uint32_t a = weights + part;
+                        uint64_t b = right;
+#pragma unroll 1
+                        for (int k = 0; k < kTok / 16; k += 2) {
+                            mma_ts(to, a, b, values, add);
+                            mma_ts(to, a + 8, b + 128, values, true);
+                            a += 32, b += 256;
+                            add = true;
+                        }
+                    }
                     mma_commit(smem_at(&ct.o_done[gv & 1]));
                     mma_commit(smem_at(&ct.empty[slot_v]));
                 }
@@ -738,41 +753,45 @@ struct TreeMma {
             }
         }
     }
-    // Results, or accumulators, 32 places of the head at a time, of a warp's rows. `to`: where the four rows of this lane's four
-    // begin; bit i of `rows`: row i is written.
-    static __device__ __forceinline__ void put(const TreeWork &w, const float (&x)[32], int d0, T *const (&to)[4], T *own, float *acc,
-                                               uint32_t rows, bool puts, float inverse)
+    // 16 bytes to where elements only are aligned.
+    static __device__ __noinline__ void put_apart(char *to, uint4 y)
     {
-        const int lane = threadIdx.x % 4;
-        if (!acc) {
+        uint16_t *at = reinterpret_cast<uint16_t *>(to);
+        const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at[2 * k] = (uint16_t)x[k], at[2 * k + 1] = (uint16_t)(x[k] >> 16);
+    }
+    // 32 places of the head of a warp's rows: results, or accumulators. `to`: where the four rows of this lane's four begin; bit
+    // i of `rows`: row i is written.
+    static __device__ __forceinline__ void put(const TreeWork &w, float (&x)[32], int d0, char *const (&to)[4], bool direct, uint32_t rows,
+                                               float inverse)
+    {
+        const int lane = threadIdx.x % 4, row_bytes = w.p.head_dim * (direct ? 2 : 4);
+        int at = d0 * (direct ? 2 : 4) + 16 * lane;
+#pragma unroll 1
+        for (int part = direct ? 1 : 0; part < 2; ++part, at += 64) {
             uint4 y[4];
-            T *z = reinterpret_cast<T *>(y);
+            uint32_t *z = reinterpret_cast<uint32_t *>(y);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = quotient_of<T>(x[i], 0.0f, inverse);
-            if (w.out_vec) {
-                turn(y);
+            for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(x[i]);
+            if (direct) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if ((rows >> i & 1) && d0 + 8 * lane < w.p.head_dim) *reinterpret_cast<uint4 *>(to[i] + d0 + 8 * lane) = y[i];
-            } else if (puts) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (d0 + i < w.p.head_dim) own[d0 + i] = z[i];
+                for (int i = 0; i < 16; ++i) {
+                    const T u = quotient_of<T>(x[2 * i], 0.0f, inverse), v = quotient_of<T>(x[2 * i + 1], 0.0f, inverse);
+                    z[i] = pack2(u, v);
+                }
             }
-        } else {
+            turn(y);
 #pragma unroll
-            for (int part = 0; part < 32; part += 16) {
-                uint4 y[4];
+            for (int i = 0; i < 4; ++i)
+                if ((rows >> i & 1) && at < row_bytes) {
+                    if (!direct || w.out_vec)
+                        *reinterpret_cast<uint4 *>(to[i] + at) = y[i];
+                    else
+                        put_apart(to[i] + at, y[i]);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[i] = make_uint4(__float_as_uint(x[part + 4 * i]), __float_as_uint(x[part + 4 * i + 1]),
-                                      __float_as_uint(x[part + 4 * i + 2]), __float_as_uint(x[part + 4 * i + 3]));
-                turn(y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if ((rows >> i & 1) && d0 + part + 4 * lane < w.p.head_dim)
-                        *reinterpret_cast<uint4 *>(acc + i * w.p.head_dim + d0 + part + 4 * lane) = y[i];
-            }
+            for (int i = 0; i < 16; ++i) x[i] = x[i + 16];
         }
     }
 
@@ -781,25 +800,26 @@ struct TreeMma {
     {
         constexpr int kOwn = kTok / 2;
         const TreeParams &p = w.p;
-        const int tid = threadIdx.x, row = tid % 128, half = tid / 128, warp = row / 32, blocks = (p.head_dim + 31) / 32;
+        const int tid = threadIdx.x, row = tid % 128, half = shared_by_all(tid / 128), warp = shared_by_all(row / 32), blocks = (p.head_dim + 31) / 32;
         // a positive scale goes into the exponent's product; another one is multiplied in first
         const float factor = __fmul_rn(p.scale, kLog2e), scale = factor > 0.0f ? factor : 1.0f;
         const uint32_t o = tmem + Shape::kColO, f = tmem + Shape::kColF;
         int g = 0, count = 0, meetings = 0, handed = 0;
         for (Way way; way.here(ct); way.past(ct)) {
             const Unit &u = ct.units[way.i];
-            const int rows = u.rows, first_row = u.first_row, b = u.b, end = u.end, per = u.per, c = u.c;
+            const int rows = shared_by_all(u.rows), first_row = u.first_row, b = u.b, begin = shared_by_all(u.tile), end = shared_by_all(u.end);
+            const int per = shared_by_all(u.per), c = shared_by_all(u.c), n = shared_by_all(u.n), first = shared_by_all(u.first), slot = shared_by_all(u.slot);
             const bool live = row < rows, works = warp * 32 < rows;
             const int node = live ? (int)quotient(first_row + row, w.by_heads) : 0;
             const int head = live ? u.kv * p.group + first_row + row - node * p.group : 0;
             // where this row goes, the four rows of this lane and its neighbours, and which of these are written
-            const bool direct = u.slot == -1, puts = live && u.slot >= -1;
-            const int64_t slot_row = ((int64_t)b * w.slots + u.slot) * w.slot_rows + row;
-            T *const own = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
-            T *to[4];
+            const bool direct = slot == -1, puts = live && slot >= -1;
+            const int64_t slot_row = ((int64_t)b * w.slots + slot) * w.slot_rows + row;
+            const char *const own =
+                direct ? (const char *)((const T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs) : (const char *)(w.acc + slot_row * p.head_dim);
+            char *to[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) to[i] = (T *)__shfl_sync(~0u, (unsigned long long)own, (tid & 28) + i);
-            float *const acc = direct ? nullptr : w.acc + (slot_row - row % 4) * p.head_dim;
+            for (int i = 0; i < 4; ++i) to[i] = (char *)__shfl_sync(~0u, (unsigned long long)own, (tid & 28) + i);
             const uint32_t written = __ballot_sync(~0u, puts) >> (tid & 28);
             const auto finish = [&](float m, float l) {
                 if (!puts || half) return;
@@ -808,22 +828,12 @@ struct TreeMma {
                 else if (p.lse)
                     p.lse[((int64_t)b * p.nodes + node) * p.q_heads + head] = log_sum<true>(m, l);
             };
-            if (u.tile >= end) {  // a sequence that cannot be attended to
-                float x[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = quiet_nan();
-#pragma unroll 1
-                for (int cb = half; cb < blocks; cb += 2) put(w, x, cb * 32, to, own, acc, written, puts, 1.0f);
-                finish(0.0f, quiet_nan());
-                if (tid == 0) flag_bad_index(p.status);
-                continue;
-            }
-            const int n = u.n, first = u.first;
             const RowMask mask = row_mask(p, b, node, n, c);
-            ++count;
-            bool bad = false;
+            const bool none = begin >= end;  // a sequence that cannot be attended to
+            count += !none;
+            bool bad = none;
             float fm = neg_inf(), fl = 0.0f;  // of the chunks before
-            for (int t0 = u.tile; t0 < end; t0 += per) {
+            for (int t0 = begin; t0 < end || none; t0 += per) {
                 const int t1 = min(end, t0 + per);
                 float m = neg_inf(), l = 0.0f;  // l: of this thread's tokens
                 for (int tile = t0; tile < t1; ++tile, ++g) {
@@ -890,18 +900,21 @@ struct TreeMma {
                         const float base = base_of(m);
                         const float2 by = make_float2(scale, scale), less = make_float2(-base, -base);
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < kOwn; i += 32) {
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
-                                const float2 e = fma2(make_float2(x[i + k], x[i + k + 1]), by, less);
+                                const float2 e = fma2(make_float2(x[k], x[k + 1]), by, less);
                                 const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
                                 sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
                                 split2(y.x, y.y, hi[k / 2], lo[k / 2], T());
                             }
                             tm_store16(here + i, hi);
                             tm_store16(here + i + 16, lo);
+                            // the other 32 in the same registers: half the code
+#pragma unroll
+                            for (int k = 0; k + 32 < kOwn; ++k) x[k] = x[k + 32];
                         }
                         l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
                         tm_stored();
@@ -911,14 +924,14 @@ struct TreeMma {
                     const int fill = 2 * g + 1, slot = fill % kSlots;
                     if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
                     // every copy of this unit has been told: what it found is known
-                    if (tile + 1 == end) bad = ((volatile int *)ct.bad)[count & 15] == count;
+                    if (tile + 1 == end) bad = shared_by_all(((volatile int *)ct.bad)[count & 15]) == count;
                     if (!whole) {
                         unsigned char *values = smem + slot * Shape::kSlot;
                         const uint32_t word = __ballot_sync(~0u, tid < kTok && row_is_odd(values, tid, p.head_dim / 8));
                         volatile uint32_t *odd = ct.odd[meetings & 1];
                         if (tid % 32 == 0 && half == 0) odd[warp] = word;
                         if (!meet(ct, meetings)) return;
-                        if (odd[0] | odd[1] | odd[2] | odd[3]) {
+                        if (shared_by_all(odd[0] | odd[1] | odd[2] | odd[3])) {
                             if (!settle() || !odd_values(ct, odd, meetings, values, tmem + (g & 1) * kTok, o, p.head_dim, tile == t0, works))
                                 return;
                         }
@@ -927,13 +940,13 @@ struct TreeMma {
                     bar_arrive(smem_at(&ct.p_ready[g & 1]));
                 }
                 // the chunk's end: O is whole
-                if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return;
+                if (!none && !warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return;
                 mma_after();
                 if (works) {
                     const float mine = l;
                     if (!hand(ct, handed, l)) return;
                     l = __fadd_rn(l, mine);
-                    const bool last = t1 == end, before = t0 != u.tile;
+                    const bool last = none || t1 == end, before = t0 != begin;
                     if (last && bad) {
                         l = quiet_nan();
                         if (tid == 0) flag_bad_index(p.status);
@@ -960,7 +973,7 @@ struct TreeMma {
                         if (!last) {
                             if (Shape::kFolds) tm_store32(f + cb * 32, x);
                         } else {
-                            put(w, x, cb * 32, to, own, acc, written, puts, inverse);
+                            put(w, x, cb * 32, to, direct, written, inverse);
                         }
                         __syncwarp();
                     }
@@ -970,6 +983,7 @@ struct TreeMma {
                         finish(top, sum);
                     fm = top, fl = sum;
                 }
+                if (none) break;
             }
         }
     }

@@ -12,9 +12,12 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kTok = kSimtTok;
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
+// 16 bytes, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("{\n .reg .pred p;\n setp.eq.u32 p, %2, 0;\n cp.async.cg.shared.global [%0], [%1], 16, p;\n}" ::"r"(dst), "l"(src),
+                 "r"((uint32_t)some)
+                 : "memory");
 }
 
 template <typename T>
@@ -94,10 +97,10 @@ struct Simt {
                     const int r = i / (DP / kPer), d = i - r * (DP / kPer);
                     const int64_t from = __shfl_sync(~0u, at, r);
                     if (d >= pieces) continue;
-                    const int bytes = from < 0 ? 0 : 16;
+                    const bool some = from >= 0;
                     const int64_t el = from < 0 ? 0 : from + d * kPer;
-                    copy16((uint32_t)__cvta_generic_to_shared(k + r * kPitch + d * 16), (const T *)p.k + el, bytes);
-                    copy16((uint32_t)__cvta_generic_to_shared(v + r * kPitch + d * 16), (const T *)p.v + el, bytes);
+                    copy16((uint32_t)__cvta_generic_to_shared(k + r * kPitch + d * 16), (const T *)p.k + el, some);
+                    copy16((uint32_t)__cvta_generic_to_shared(v + r * kPitch + d * 16), (const T *)p.v + el, some);
                 }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
