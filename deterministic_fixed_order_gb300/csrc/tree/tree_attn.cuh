@@ -8,11 +8,9 @@
 //
 // Fixed order. The rows of one key-value head go by blocks ("pairs" of a sequence and such a
 // block); the tokens of a sequence, the committed ones that a root sees and then the drafted ones, by
-// chunks of tiles, and chunks by groups. All of it follows from the sequence's own length, tree and the head
-// counts. A group's triple is the fold of its chunks' in ascending order, the pair's the fold of its groups'.
-// The unit of work that a CTA takes is a chunk, or a whole group that it folds by itself where there is
-// work enough: the call's choice, which the bits do not depend on. Units of pairs that are
-// more than one leave their triples in the workspace for the join kernel.
+// chunks of tiles. Both follow from the sequence's own length, tree and the head counts. A chunk of a pair is
+// a unit of work; which CTA takes it is free. Where a pair has one, that is its result; else the units leave
+// their triples in the workspace, and the join kernel folds them in ascending order.
 #pragma once
 
 #include "tree_common.cuh"
@@ -26,7 +24,6 @@ struct TreeRule {
     int wide;   // rows of the widest block of this type: a call whose trees have fewer may take narrower ones,
                 // which are then one block a key-value head either way
     int least;  // tiles a chunk, at least, for up to half of the widest block's rows; twice as many for more: a power of two
-    int group;  // tiles a group, at least: a power of two, or 1 where a group is a chunk
 };
 
 // CTAs that a sequence's chunks are to fill when it is alone.
@@ -35,10 +32,8 @@ constexpr int kFill = kSms;
 struct TreeWork {
     TreeParams p;
     TreeRule rule;
-    int by_group;     // units are groups, else chunks; -1: as the sequences' lengths say (*grouped)
     int log_tok, log_rows, log_least;
     int most;         // chunks that sequences of one block a key-value head are cut into, at most
-    int *grouped;     // the choice, where the main kernel makes it
     int slots;        // workspace slots a sequence, 0: no pair has more than one unit
     int slot_rows;    // rows of a slot
     Divide page;      // by the page size
@@ -66,7 +61,7 @@ inline int slot_rows_of(const TreeRule &r, int group, int nodes)
 inline int64_t tree_need(const TreeRule &r, int batch, int kv_heads, int group, int nodes, int head_dim, int64_t max_len)
 {
     const int64_t rows = (int64_t)batch * slots_of(r, kv_heads, group, nodes, max_len) * slot_rows_of(r, group, nodes);
-    return rows == 0 ? 0 : 16 + (rows * 8 + 15) / 16 * 16 + rows * head_dim * 4;
+    return rows == 0 ? 0 : (rows * 8 + 15) / 16 * 16 + rows * head_dim * 4;
 }
 inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *workspace)
 {
@@ -76,9 +71,8 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
     w.slot_rows = slot_rows_of(r, p.group, p.nodes);
     w.page = divide_by(p.page_size), w.by_heads = divide_by(p.group);
     const int64_t rows = (int64_t)p.batch * w.slots * w.slot_rows;
-    w.grouped = (int *)workspace;
-    w.ml = (float2 *)((char *)workspace + 16);
-    w.acc = (float *)((char *)workspace + 16 + (rows * 8 + 15) / 16 * 16);
+    w.ml = (float2 *)workspace;
+    w.acc = (float *)((char *)workspace + (rows * 8 + 15) / 16 * 16);
     const auto log2_of = [](int x) { return 31 - __builtin_clz((unsigned)x); };
     w.log_tok = log2_of(r.tok), w.log_rows = log2_of(r.rows), w.log_least = log2_of(r.least);
     w.most = p.kv_heads < kFill ? kFill / p.kv_heads : 1;
@@ -89,7 +83,7 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
 }
 // The float32 kernel's: a block of as many rows as four warps take.
 constexpr int kSimtTok = 32;
-inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 1}; }
+inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4}; }
 
 cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream);
 
@@ -101,8 +95,7 @@ struct TreeSeq {
     int first;      // first token that a root sees
     int end;        // n + c
     int tiles, per; // tiles, and tiles a chunk
-    int chunks, each, units;  // chunks; chunks a unit; units a pair
-    int fold;       // chunks a group
+    int units;      // chunks
     int blocks, pairs;
     bool bad;
 };
@@ -121,7 +114,7 @@ __device__ __forceinline__ int over_up(int x, int y) { return over(x + y - 1, y)
 
 // `n`, `c` as read. A sequence that cannot be attended to has one unit a pair and no tokens. Few instructions where chunks
 // are of the least length: what comes before the first copy is a kernel's start.
-__device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c, bool by_group)
+__device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
 {
     TreeSeq s;
     const TreeParams &p = w.p;
@@ -137,24 +130,17 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c, boo
     s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) >> w.log_tok;
     const int log_least = w.log_least + (2 * rows > w.rule.wide), least = 1 << log_least;
     const int most = s.blocks <= 1 ? w.most : s.pairs < kFill ? over(kFill, s.pairs) : 1;
-    if (s.tiles <= (int64_t)most << log_least) {
-        s.per = least;
-        s.chunks = s.c == 0 ? 0 : max(1, (s.tiles + least - 1) >> log_least);
-        s.fold = max(1, w.rule.group >> log_least);  // a power of two
-        s.each = by_group ? s.fold : 1;
-        s.units = by_group ? (s.chunks + s.fold - 1) >> (31 - __clz(s.fold)) : s.chunks;
-        return s;
+    s.per = least;
+    s.units = s.c == 0 ? 0 : max(1, (s.tiles + least - 1) >> log_least);
+    if (s.units > most) {
+        s.per = over_up(s.tiles, most);
+        s.units = over_up(s.tiles, s.per);
     }
-    s.per = over_up(s.tiles, most);
-    s.chunks = over_up(s.tiles, s.per);
-    s.fold = max(1, over_up(w.rule.group, s.per));
-    s.each = by_group ? s.fold : 1;
-    s.units = over_up(s.chunks, s.each);
     return s;
 }
-__device__ __forceinline__ TreeSeq tree_seq_of(const TreeWork &w, int b, bool by_group)
+__device__ __forceinline__ TreeSeq tree_seq_of(const TreeWork &w, int b)
 {
-    return tree_seq(w, w.p.lens[b], w.p.counts ? w.p.counts[b] : w.p.nodes, by_group);
+    return tree_seq(w, w.p.lens[b], w.p.counts ? w.p.counts[b] : w.p.nodes);
 }
 
 // A node's mask as it lies in memory, without the bits behind the last node.

@@ -1,6 +1,5 @@
 // Joins the partial results of rows whose tokens lie in several units of work: a warp a row. The units'
-// triples are folded as the fixed order has it, chunks to groups and groups to the row, each in
-// ascending order. Bound by memory and latency: each accumulator is read once, several in flight.
+// triples are folded in ascending order. Bound by memory and latency: each accumulator is read once, several in flight.
 #include "tree_attn.cuh"
 
 namespace detfold_tree {
@@ -18,12 +17,11 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
     const int lane = threadIdx.x % 32;
     enter_grid();
     const int b = blockIdx.x / across, of = p.nodes * p.q_heads;
-    const bool by_group = w.by_group < 0 ? *w.grouped != 0 : w.by_group != 0;
-    const TreeSeq s = tree_seq_of(w, b, by_group);
+    const TreeSeq s = tree_seq_of(w, b);
     if (s.units <= 1) return;
     const int64_t step = (int64_t)s.pairs * w.slot_rows;
     // lengths that change under the call: no unit past the workspace
-    const int units = min(s.units, over(w.slots, max(s.pairs, 1))), group = by_group ? 1 : s.fold;
+    const int units = min(s.units, over(w.slots, max(s.pairs, 1)));
     for (int in = ((blockIdx.x - b * across) * kWarps + threadIdx.x / 32) * kRowsEach, k = 0; k < kRowsEach; ++k, ++in) {
         if (in >= of) return;
         const int node = in / p.q_heads, head = in - node * p.q_heads;
@@ -31,10 +29,9 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
         const int kv = (int)quotient(head, w.by_heads), r = node * p.group + head - kv * p.group, block = r >> w.log_rows;
         const int pair = kv * s.blocks + block;
         const int64_t first = ((int64_t)b * w.slots + pair) * w.slot_rows + (r - block * w.rule.rows);
-        float m = neg_inf(), l = 0.0f, a[PER], gm = neg_inf(), gl = 0.0f, ga[PER];
+        float m = neg_inf(), l = 0.0f, a[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) a[i] = ga[i] = 0.0f;
-        int left = group;
+        for (int i = 0; i < PER; ++i) a[i] = 0.0f;
         for (int u0 = 0; u0 < units; u0 += kAhead) {
             float2 ml[kAhead];
             float x[kAhead][PER];
@@ -52,28 +49,10 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
             for (int k = 0; k < kAhead; ++k) {
                 if (u0 + k >= units) continue;
                 float top, fa, fb;
-                if (left == group) {  // a group's first
-                    gm = ml[k].x, gl = ml[k].y;
+                fold_factors<LOG2>(m, ml[k].x, top, fa, fb);
+                m = top, l = fold_in(l, ml[k].y, fa, fb);
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) ga[i] = x[k][i];
-                } else {
-                    fold_factors<LOG2>(gm, ml[k].x, top, fa, fb);
-                    gm = top, gl = fold_in(gl, ml[k].y, fa, fb);
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) ga[i] = fold_in(ga[i], x[k][i], fa, fb);
-                }
-                if (--left && u0 + k + 1 < units) continue;
-                if (u0 + k < group) {  // the first group
-                    m = gm, l = gl;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) a[i] = ga[i];
-                } else {
-                    fold_factors<LOG2>(m, gm, top, fa, fb);
-                    m = top, l = fold_in(l, gl, fa, fb);
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) a[i] = fold_in(a[i], ga[i], fa, fb);
-                }
-                left = group;
+                for (int i = 0; i < PER; ++i) a[i] = fold_in(a[i], x[k][i], fa, fb);
             }
         }
         T *out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;

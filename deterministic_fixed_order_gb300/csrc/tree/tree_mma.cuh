@@ -37,21 +37,16 @@ struct MmaShape {
     static constexpr int kQ = NS * kRows * 128;
     static constexpr int kSlots = NS == 1 ? 8 : 5;  // tiles of keys or values in shared memory
     static constexpr int kQs = NS == 4 ? 1 : 2;
-    static constexpr bool kFolds = NS <= 3;         // tensor memory has room for a second accumulator
-    static constexpr int kColO = 2 * kTok, kColF = kColO + NS * 64;
+    static constexpr int kOs = NS == 4 ? 1 : 2;     // accumulators: one is written out while the next one's tiles are multiplied
+    static constexpr int kColO = 2 * kTok, kColsO = NS * 64;
     static constexpr int kShift = std::is_same_v<T, __half> ? 8 : 0, kSlack = std::is_same_v<T, __half> ? 7 : 8;
-    static constexpr int kControl = 3072, kBytes = kSlots * kSlot + kQs * kQ + kControl;
-    // chunks of 256 tokens at least, groups of 1024
-    static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kFolds ? 1024 / kTok : 1}; }
+    static constexpr int kControl = NS % 2 ? 4096 : 3072, kBytes = kSlots * kSlot + kQs * kQ + kControl;
+    static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok}; }  // chunks of 256 tokens at least
 };
 
 #ifdef __CUDACC__
 
-// More units of a chunk each than this many a CTA: units are groups.
-constexpr int kByGroup = 12;
-// Sequences whose chunks are counted for that; of more the sizes decide.
-constexpr int kCounted = 256;
-constexpr int kSoftmax = 256, kCopy = 128, kMmaThreads = kSoftmax + 32 + kCopy + 32;
+constexpr int kSoftmax = 256, kCopy = 128, kWrite = 128, kMmaThreads = kSoftmax + kCopy + kWrite + 64;
 
 // ------------------------------------------------------------------ instructions
 
@@ -210,9 +205,9 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 
 // A unit as the warps of a CTA are told it: tiles [tile, end) of a block of rows.
 struct Unit {
-    int b, n, c, first, stop;      // the sequence: committed tokens, nodes, first token seen, end of its tokens
+    int b, n, c, first;            // the sequence: committed tokens, nodes, first token seen
     int kv, first_row, rows;       // key-value head; rows of it
-    int tile, end, per;            // tiles; tiles a chunk
+    int tile, end;                 // tiles
     int slot;                      // where its triple goes, or -1: the outputs
 };
 
@@ -220,16 +215,14 @@ struct Unit {
 // sequence. (At most 2^30 rows in all, or kFill pairs a sequence: the counts fit.)
 struct Units {
     int next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
-    int b0, pairs, units, each, per, first, end, n, c, tiles, blocks;  // this lane's sequence
-    bool grouped;  // units are groups
+    int b0, pairs, units, per, first, n, c, tiles, blocks;  // this lane's sequence
 
     __device__ __forceinline__ void load(const TreeWork &w)
     {
         const int lane = threadIdx.x % 32, b = b0 + lane;
         TreeSeq s = {};
-        if (b < w.p.batch) s = tree_seq_of(w, b, grouped);
-        pairs = s.pairs, units = s.units, each = s.each * s.per, per = s.per, first = s.first, end = s.end, n = s.n, c = s.c;
-        tiles = s.tiles, blocks = s.blocks;
+        if (b < w.p.batch) s = tree_seq_of(w, b);
+        pairs = s.pairs, units = s.units, per = s.per, first = s.first, n = s.n, c = s.c, tiles = s.tiles, blocks = s.blocks;
         upto = units * pairs;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -251,12 +244,12 @@ struct Units {
         const int count = of(pairs), many = of(units), local = next - base - (of(upto) - many * count);
         const int index = over(local, count), pair = local - index * count, rows = of(blocks);
         u.b = b0 + lane;
-        u.n = of(n), u.c = of(c), u.first = of(first), u.stop = of(end), u.per = of(per);
+        u.n = of(n), u.c = of(c), u.first = of(first);
         u.kv = rows == 1 ? pair : over(pair, rows);
         u.first_row = (pair - u.kv * rows) * w.rule.rows;
         u.rows = min(w.rule.rows, u.c * w.p.group - u.first_row);
-        u.tile = index * of(each);
-        u.end = min(of(tiles), u.tile + of(each));
+        u.tile = index * of(per);
+        u.end = min(of(tiles), u.tile + of(per));
         // lengths that change under the call: nothing past the workspace
         u.slot = many == 1 ? -1 : local < w.slots ? local : -2;
         next += gridDim.x;
@@ -266,23 +259,25 @@ struct Units {
 
 // ------------------------------------------------------------------ the kernel
 
-constexpr int kUnits = 4;  // units that the warps are told ahead
+constexpr int kUnits = 3;  // units that the warps are told ahead
 
 template <typename Shape>
 struct TreeMma {
     using T = typename Shape::T;
+    static constexpr int kOs = Shape::kOs;
     static constexpr int kTok = Shape::kTok, kSlots = Shape::kSlots, kQs = Shape::kQs, kNS = Shape::kSlot / Shape::kSlab;
-    static constexpr int kSoftmaxWarps = kSoftmax / 32, kCopyWarps = kCopy / 32;
+    static constexpr int kSoftmaxWarps = kSoftmax / 32, kCopyWarps = kCopy / 32, kWriteWarps = kWrite / 32;
 
     struct Control {
-        uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2];
-        uint64_t met, agree[4], unit_full[kUnits], unit_empty[kUnits], end;
+        uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2], o_full[kOs], o_free[kOs];
+        uint64_t met, agree[4], sums_full, sums_free, unit_full[kUnits], unit_empty[kUnits], end;
         Unit units[kUnits];  // b = -1: no more
         uint32_t tmem;
         int dead, keep_o;
-        int bad[16];             // the unit (counted from 1) that has a page outside the cache, by its last bits
-        uint32_t odd[2][4];      // tokens of a tile with values that are not finite, by turns
-        float given[2][2][128];  // what the two warps of a row hand each other, by turns
+        int bad[8];               // the unit (counted from 1) that has a page outside the cache, by its last bits
+        uint32_t odd[2][4];       // tokens of a tile with values that are not finite, by turns
+        uint16_t given[2][2][128];  // what the two warps of a row hand each other, by turns
+        float top[128], sums[2][128];  // a unit's maxima, and sums of weights of either half
     };
 
     static __device__ __forceinline__ void run(const TreeWork &w)
@@ -297,16 +292,19 @@ struct TreeMma {
                 for (int i = 0; i < n; ++i) bar_init(smem_at(bars + i), count);
             };
             set(ct.full, kSlots, kCopy), set(ct.empty, kSlots, 1), set(ct.q_full, kQs, kCopy), set(ct.q_empty, kQs, 1);
-            set(ct.s_full, 2, 1), set(ct.p_ready, 2, kSoftmax), set(ct.o_done, 2, 1);
+            set(ct.s_full, 2, 1), set(ct.p_ready, 2, kSoftmax), set(ct.o_done, 2, 1), set(ct.o_full, kOs, 1);
+            set(ct.o_free, kOs, kWrite), set(&ct.sums_full, 1, kSoftmax), set(&ct.sums_free, 1, kWrite);
             set(&ct.met, 1, kSoftmaxWarps), set(ct.agree, 4, 2), set(&ct.end, 1, 1);
-            set(ct.unit_full, kUnits, 1), set(ct.unit_empty, kUnits, kSoftmaxWarps + kCopyWarps + 1);
+            set(ct.unit_full, kUnits, 1), set(ct.unit_empty, kUnits, kSoftmaxWarps + kCopyWarps + kWriteWarps + 1);
             ct.dead = 0, ct.keep_o = 0;
-            for (int i = 0; i < 16; ++i) ct.bad[i] = 0;
+            for (int i = 0; i < 8; ++i) ct.bad[i] = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         // tensor memory is taken after the wait: a kernel that is waited for may need it
         enter_grid();
-        constexpr int kProducts = kSoftmaxWarps, kScheduler = kProducts + 1 + kCopyWarps;
+        // a warp reaches the tensor memory's lanes by its number's last bits
+        constexpr int kCopies = kSoftmaxWarps, kWrites = kCopies + kCopyWarps, kProducts = kWrites + kWriteWarps;
+        static_assert(kWrites % 4 == 0, "whole groups of four warps");
         if (warp == kProducts) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(&ct.tmem)) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -315,12 +313,14 @@ struct TreeMma {
         __syncthreads();
         mma_after();
         const uint32_t tmem = *(volatile uint32_t *)&ct.tmem;
-        if (warp < kProducts)
+        if (warp < kCopies)
             softmax(w, ct, smem, tmem + ((uint32_t)(warp % 4 * 32) << 16));
+        else if (warp < kWrites)
+            copies(w, ct, ring, q);
+        else if (warp < kProducts)
+            writes(w, ct, tmem + ((uint32_t)(warp % 4 * 32) << 16));
         else if (warp == kProducts)
             products(w, ct, ring, q, tmem);
-        else if (warp < kScheduler)
-            copies(w, ct, ring, q);
         else
             schedule(w, ct);
         __syncwarp();
@@ -336,18 +336,7 @@ struct TreeMma {
     static __device__ __forceinline__ void schedule(const TreeWork &w, Control &ct)
     {
         Units units;
-        units.next = blockIdx.x, units.base = 0, units.b0 = -1, units.grouped = w.by_group > 0;
-        if (w.by_group < 0) {
-            // groups where chunks are more than kByGroup a CTA
-            int all = 0;
-            for (units.b0 = 0; units.b0 < w.p.batch; units.b0 += 32) {
-                units.load(w);
-                all += __shfl_sync(~0u, units.upto, 31);
-            }
-            units.b0 = -1;
-            units.grouped = all > kByGroup * (int)gridDim.x;
-            if (blockIdx.x == 0 && threadIdx.x % 32 == 0) *w.grouped = units.grouped;
-        }
+        units.next = blockIdx.x, units.base = 0, units.b0 = -1;
         bool more = true;
         for (int i = 0, round = 0; more; ) {
             Unit u;
@@ -406,7 +395,7 @@ struct TreeMma {
         constexpr int kOwn = 32 / kLanes, kWarpRows = kPasses * kOwn;          // of them a warp's; a warp's rows of a tile
         static_assert(kWarpRows <= 32 && kTogether * kPasses == kTok, "a lane looks up a row at most");
         const TreeParams &p = w.p;
-        const int tid = threadIdx.x - kSoftmax - 32, warp = shared_by_all(tid / 32), lane = tid % 32;
+        const int tid = threadIdx.x - kSoftmax, warp = shared_by_all(tid / 32), lane = tid % 32;
         const int piece = tid % kLanes, pieces = p.head_dim / 8, padded = (pieces + 1) / 2 * 2;
         const int row0 = tid / kLanes, slab = piece / 8, chunk = piece % 8;
         // Where this thread's piece of row row0 + i kTogether lies: a place a row's last three bits, and 128 bytes a row. The
@@ -436,7 +425,7 @@ struct TreeMma {
         bool alive = true;
         for (; (alive = way.here(ct)); way.past(ct)) {
             const Unit &u = ct.units[way.i];
-            const int begin = shared_by_all(u.tile), end = shared_by_all(u.end), stop = u.stop, first = u.first, kv = u.kv, b = u.b;
+            const int begin = shared_by_all(u.tile), end = shared_by_all(u.end), first = u.first, stop = u.n + u.c, kv = u.kv, b = u.b;
             if (begin >= end) continue;
             const int first_row = u.first_row, rows = u.rows;
             const int seq = ++count;
@@ -452,7 +441,7 @@ struct TreeMma {
                     if (page >= 0 && page < p.num_pages)
                         at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + in_row;
                     else
-                        ((volatile int *)ct.bad)[seq & 15] = seq;
+                        ((volatile int *)ct.bad)[seq & 7] = seq;
                 }
                 return at;
             };
@@ -514,11 +503,11 @@ struct TreeMma {
         const auto ready = [&](uint64_t &bar, int parity) { return __all_sync(~0u, bar_test(smem_at(&bar), parity & 1)); };
         // The unit whose scores are next, and the one whose weighted values are: 0 not known, 1 known, 2 no more.
         Way way_a, way_v;
-        int know_a = 0, know_v = 0, tile_a = 0, end_a = 0, tile_v = 0, end_v = 0, chunk_v = 0, per_v = 0;
-        const auto look = [&](Way &way, bool frees, int &know, int &tile, int &end, int &per) {
+        int know_a = 0, know_v = 0, tile_a = 0, end_a = 0, tile_v = 0, end_v = 0, first_v = 0;
+        const auto look = [&](Way &way, bool frees, int &know, int &tile, int &end) {
             while (know == 0 && ready(ct.unit_full[way.i], way.round)) {
                 const volatile Unit &u = ct.units[way.i];
-                tile = shared_by_all(u.tile), end = shared_by_all(u.end), per = shared_by_all(u.per);
+                tile = shared_by_all(u.tile), end = shared_by_all(u.end);
                 if (shared_by_all(u.b) < 0)
                     know = 2;
                 else if (tile < end)  // units without tokens have no products
@@ -530,20 +519,21 @@ struct TreeMma {
             }
         };
         bool fresh = true;  // the first tile of scores of a unit
-        int ga = 0, gv = 0, qi = 0, q_round = 0, idle = 0, per = 0;
+        int ga = 0, gv = 0, qi = 0, q_round = 0, idle = 0, oi = 0, o_round = 0;
         int slot_a = 0, round_a = 0, slot_v = 1, round_v = 0;  // slots go keys, values, keys, ...
         const auto past = [&](int &slot, int &round) {
             if ((slot += 2) >= kSlots) slot -= kSlots, ++round;
         };
         long long t0 = 0;
         // Whichever product can be made: a tile's scores once the weights that lay in their place have been multiplied, at
-        // most a tile ahead; a tile's weighted values once the weights are there.
+        // most a tile ahead; a tile's weighted values once the weights are
+        // there, a unit's first once the accumulator has been written out.
         while (true) {
             bool did = false;
-            look(way_a, false, know_a, tile_a, end_a, per);
+            look(way_a, false, know_a, tile_a, end_a);
             if (know_v == 0) {
-                look(way_v, true, know_v, tile_v, end_v, per_v);
-                chunk_v = tile_v;
+                look(way_v, true, know_v, tile_v, end_v);
+                first_v = tile_v;
             }
             if (know_v == 2) break;
             if (know_a == 1 && ga < gv + 2 && (!fresh || ready(ct.q_full[qi], q_round)) && ready(ct.full[slot_a], round_a) &&
@@ -578,13 +568,14 @@ struct TreeMma {
                     if (++qi == kQs) qi = 0, ++q_round;
                 }
             }
-            if (gv < ga && ready(ct.p_ready[gv & 1], gv / 2) && ready(ct.full[slot_v], round_v)) {
+            if (gv < ga && ready(ct.p_ready[gv & 1], gv / 2) && ready(ct.full[slot_v], round_v) &&
+                (tile_v != first_v || ready(ct.o_free[oi], o_round ^ 1))) {
                 did = true;
                 fence_async();
                 mma_after();
-                const bool first = tile_v == chunk_v && !shared_by_all(*(volatile int *)&ct.keep_o);
+                const bool ends = tile_v + 1 == end_v, first = tile_v == first_v && !shared_by_all(*(volatile int *)&ct.keep_o);
                 const uint64_t right = shared_by_all(operand(ring + slot_v * Shape::kSlot, Shape::kSlab));
-                const uint32_t weights = shared_by_all(tmem + (gv & 1) * kTok), to = shared_by_all(tmem + Shape::kColO);
+                const uint32_t weights = shared_by_all(tmem + (gv & 1) * kTok), to = shared_by_all(tmem + Shape::kColO + oi * Shape::kColsO);
                 if (one_lane()) {
                     // weights of 32 tokens: 16 columns of upper parts, 16 of lower ones; 2048 bytes of values
                     bool add = !first;
@@ -601,22 +592,23 @@ struct TreeMma {
                         }
                     }
                     mma_commit(smem_at(&ct.o_done[gv & 1]));
+                    if (ends) mma_commit(smem_at(&ct.o_full[oi]));
                     mma_commit(smem_at(&ct.empty[slot_v]));
                 }
                 __syncwarp();
                 ++gv;
                 past(slot_v, round_v);
-                if (++tile_v == end_v) {
+                ++tile_v;
+                if (ends) {
                     know_v = 0;
                     way_v.past(ct);
-                } else if (tile_v == chunk_v + per_v) {
-                    chunk_v = tile_v;
+                    if (++oi == kOs) oi = 0, o_round ^= 1;
                 }
             }
             // bounded, as every wait
             if (did) {
                 idle = 0;
-            } else if ((++idle & 1023) == 0) {
+            } else if (__nanosleep(20), (++idle & 1023) == 0) {
                 long long t;
                 asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
                 if (idle == 1024) t0 = t;
@@ -644,16 +636,17 @@ struct TreeMma {
         mma_after();
         return ok;
     }
-    // The two warps of the same rows hand each other a number a row.
-    static __device__ __forceinline__ bool hand(Control &ct, int &handed, float &x)
+    // The two warps of the same rows agree on the greater of their numbers a row, rounded up to 16 bits.
+    static __device__ __forceinline__ bool agree(Control &ct, int &agreed, float &x)
     {
         const int row = threadIdx.x % 128, half = threadIdx.x / 128, bar = row / 32;
-        volatile float(*at)[128] = ct.given[handed & 1];
-        at[half][row] = x;
+        volatile uint16_t(*at)[128] = ct.given[agreed & 1];
+        const uint32_t u = __float_as_uint(x), up = u + (u >> 31 ? 0 : 0xffff);  // towards +inf; an infinity stays
+        at[half][row] = (uint16_t)(up >> 16);
         __syncwarp();
         if (row % 32 == 0) bar_arrive(smem_at(&ct.agree[bar]));
-        const bool ok = warp_wait(smem_at(&ct.agree[bar]), handed++ & 1, &ct.dead);
-        x = at[half ^ 1][row];
+        const bool ok = warp_wait(smem_at(&ct.agree[bar]), agreed++ & 1, &ct.dead);
+        x = fmaxf(__uint_as_float(up & 0xffff0000u), __uint_as_float((uint32_t)at[half ^ 1][row] << 16));
         return ok;
     }
     // Where 16 bytes of a tile's row lie.
@@ -732,68 +725,83 @@ struct TreeMma {
         return true;
     }
 
-    // Four lanes' four pieces of 16 bytes, turned: lane i of them gets the others' pieces i. So stores go along a row by 64
-    // bytes, a quarter of the lines that a lane a row would touch.
-    static __device__ __forceinline__ void turn(uint4 (&x)[4])
+    // ---------------------------------------------------------- results
+
+    // Writes a unit's results, or its triples, a thread a row, while the other warps go on with the next unit.
+    static __device__ __forceinline__ void writes(const TreeWork &w, Control &ct, uint32_t tmem)
     {
-        const int lane = threadIdx.x % 4;
-#pragma unroll
-        for (int step = 1; step <= 2; step *= 2) {
-            const bool upper = lane & step;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i & step) continue;
-                uint4 &a = x[i], &b = x[i + step];
-                uint32_t *p = reinterpret_cast<uint32_t *>(&a), *q = reinterpret_cast<uint32_t *>(&b);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t gives = upper ? p[k] : q[k], got = __shfl_xor_sync(~0u, gives, step);
-                    p[k] = upper ? got : p[k], q[k] = upper ? q[k] : got;
-                }
+        const TreeParams &p = w.p;
+        const int row = threadIdx.x % 128, warp = shared_by_all(row / 32), blocks = (p.head_dim + 31) / 32;
+        int oi = 0, o_round = 0, count = 0;
+        for (Way way; way.here(ct); ) {
+            const Unit &u = ct.units[way.i];
+            const int rows = shared_by_all(u.rows), slot = shared_by_all(u.slot), b = u.b;
+            const bool none = shared_by_all(u.tile >= u.end);  // a sequence that cannot be attended to
+            const bool live = row < rows, works = warp * 32 < rows, direct = slot == -1, puts = live && slot >= -1;
+            const int at_row = u.first_row + row, node = live ? (int)quotient(at_row, w.by_heads) : 0;
+            const int head = live ? u.kv * p.group + at_row - node * p.group : 0;
+            way.past(ct);
+            T *const out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
+            const int64_t slot_row = ((int64_t)b * w.slots + slot) * w.slot_rows + row;
+            float *const acc = w.acc + slot_row * p.head_dim;
+            float top = 0.0f, sum = quiet_nan();
+            if (!none) {
+                if (!warp_wait(smem_at(&ct.sums_full), count++ & 1, &ct.dead)) return;
+                top = ct.top[row], sum = __fadd_rn(ct.sums[0][row], ct.sums[1][row]);
+                bar_arrive(smem_at(&ct.sums_free));
+                if (!warp_wait(smem_at(&ct.o_full[oi]), o_round, &ct.dead)) return;
+                mma_after();
             }
-        }
-    }
-    // 16 bytes to where elements only are aligned.
-    static __device__ __noinline__ void put_apart(char *to, uint4 y)
-    {
-        uint16_t *at = reinterpret_cast<uint16_t *>(to);
-        const uint32_t x[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) at[2 * k] = (uint16_t)x[k], at[2 * k + 1] = (uint16_t)(x[k] >> 16);
-    }
-    // 32 places of the head of a warp's rows: results, or accumulators. `to`: where the four rows of this lane's four begin; bit
-    // i of `rows`: row i is written.
-    static __device__ __forceinline__ void put(const TreeWork &w, float (&x)[32], int d0, char *const (&to)[4], bool direct, uint32_t rows,
-                                               float inverse)
-    {
-        const int lane = threadIdx.x % 4, row_bytes = w.p.head_dim * (direct ? 2 : 4);
-        int at = d0 * (direct ? 2 : 4) + 16 * lane;
+            if (none && row == 0) flag_bad_index(p.status);
+            const float inverse = inverse_of(sum);
 #pragma unroll 1
-        for (int part = direct ? 1 : 0; part < 2; ++part, at += 64) {
-            uint4 y[4];
-            uint32_t *z = reinterpret_cast<uint32_t *>(y);
+            for (int cb = 0; works && cb < blocks; ++cb) {
+                float x[32];
+                if (none) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(x[i]);
-            if (direct) {
+                    for (int i = 0; i < 32; ++i) x[i] = quiet_nan();
+                } else {
+                    tm_load(x, tmem + Shape::kColO + oi * Shape::kColsO + cb * 32);
+                    tm_loaded();
+                }
+                if (!puts) continue;
+                if (direct) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const T u = quotient_of<T>(x[2 * i], 0.0f, inverse), v = quotient_of<T>(x[2 * i + 1], 0.0f, inverse);
-                    z[i] = pack2(u, v);
+                    for (int k = 0; k < 4; ++k) {
+                        const int d = cb * 32 + 8 * k;
+                        if (d >= p.head_dim) continue;
+                        Pack<T, 8> y;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y.v[i] = quotient_of<T>(x[8 * k + i], 0.0f, inverse);
+                        if (w.out_vec) {
+                            *reinterpret_cast<Pack<T, 8> *>(out + d) = y;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) out[d + i] = y.v[i];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (cb * 32 + 4 * k < p.head_dim)
+                            reinterpret_cast<float4 *>(acc + cb * 32)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                 }
             }
-            turn(y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if ((rows >> i & 1) && at < row_bytes) {
-                    if (!direct || w.out_vec)
-                        *reinterpret_cast<uint4 *>(to[i] + at) = y[i];
-                    else
-                        put_apart(to[i] + at, y[i]);
-                }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = x[i + 16];
+            __syncwarp();
+            if (!none) {
+                mma_before();
+                bar_arrive(smem_at(&ct.o_free[oi]));
+                if (++oi == kOs) oi = 0, o_round ^= 1;
+            }
+            if (!puts) continue;
+            if (!direct)
+                w.ml[slot_row] = make_float2(top, sum);
+            else if (p.lse)
+                p.lse[((int64_t)b * p.nodes + node) * p.q_heads + head] = log_sum<true>(top, sum);
         }
     }
+
+    // ---------------------------------------------------------- weights
 
     // Two threads a row, each with half of a tile's tokens and, of the accumulator, every other 32 places of the head.
     static __device__ __forceinline__ void softmax(const TreeWork &w, Control &ct, unsigned char *smem, uint32_t tmem)
@@ -803,40 +811,20 @@ struct TreeMma {
         const int tid = threadIdx.x, row = tid % 128, half = shared_by_all(tid / 128), warp = shared_by_all(row / 32), blocks = (p.head_dim + 31) / 32;
         // a positive scale goes into the exponent's product; another one is multiplied in first
         const float factor = __fmul_rn(p.scale, kLog2e), scale = factor > 0.0f ? factor : 1.0f;
-        const uint32_t o = tmem + Shape::kColO, f = tmem + Shape::kColF;
-        int g = 0, count = 0, meetings = 0, handed = 0;
+        int g = 0, count = 0, meetings = 0, agreed = 0;
         for (Way way; way.here(ct); way.past(ct)) {
             const Unit &u = ct.units[way.i];
-            const int rows = shared_by_all(u.rows), first_row = u.first_row, b = u.b, begin = shared_by_all(u.tile), end = shared_by_all(u.end);
-            const int per = shared_by_all(u.per), c = shared_by_all(u.c), n = shared_by_all(u.n), first = shared_by_all(u.first), slot = shared_by_all(u.slot);
-            const bool live = row < rows, works = warp * 32 < rows;
-            const int node = live ? (int)quotient(first_row + row, w.by_heads) : 0;
-            const int head = live ? u.kv * p.group + first_row + row - node * p.group : 0;
-            // where this row goes, the four rows of this lane and its neighbours, and which of these are written
-            const bool direct = slot == -1, puts = live && slot >= -1;
-            const int64_t slot_row = ((int64_t)b * w.slots + slot) * w.slot_rows + row;
-            const char *const own =
-                direct ? (const char *)((const T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs) : (const char *)(w.acc + slot_row * p.head_dim);
-            char *to[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) to[i] = (char *)__shfl_sync(~0u, (unsigned long long)own, (tid & 28) + i);
-            const uint32_t written = __ballot_sync(~0u, puts) >> (tid & 28);
-            const auto finish = [&](float m, float l) {
-                if (!puts || half) return;
-                if (!direct)
-                    w.ml[slot_row] = make_float2(m, l);
-                else if (p.lse)
-                    p.lse[((int64_t)b * p.nodes + node) * p.q_heads + head] = log_sum<true>(m, l);
-            };
-            const RowMask mask = row_mask(p, b, node, n, c);
-            const bool none = begin >= end;  // a sequence that cannot be attended to
-            count += !none;
-            bool bad = none;
-            float fm = neg_inf(), fl = 0.0f;  // of the chunks before
-            for (int t0 = begin; t0 < end || none; t0 += per) {
-                const int t1 = min(end, t0 + per);
-                float m = neg_inf(), l = 0.0f;  // l: of this thread's tokens
-                for (int tile = t0; tile < t1; ++tile, ++g) {
+            const int begin = shared_by_all(u.tile), end = shared_by_all(u.end);
+            if (begin >= end) continue;
+            const int rows = shared_by_all(u.rows), n = shared_by_all(u.n), c = shared_by_all(u.c), first = shared_by_all(u.first);
+            const bool works = warp * 32 < rows;
+            const RowMask mask = row_mask(p, u.b, row < rows ? (int)quotient(u.first_row + row, w.by_heads) : 0, n, c);
+            const uint32_t o = tmem + Shape::kColO + count % kOs * Shape::kColsO;
+            ++count;
+            bool bad = false;
+            float m = neg_inf(), l = 0.0f;  // l: of this thread's tokens
+            {
+                for (int tile = begin; tile < end; ++tile, ++g) {
                     const int at = first + tile * kTok;
                     const bool whole = at + kTok <= n && (!p.window || at >= n + c - p.window);
                     const uint32_t here = tmem + (g & 1) * kTok + half * kOwn;
@@ -844,7 +832,7 @@ struct TreeMma {
                     if (!whole && works) seen = mask.seen_from(at + half * kOwn);
                     if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
                     mma_after();
-                    bool waited = tile == t0;  // for the tile before, whose product O may still change
+                    bool waited = tile == begin;  // for the tile before, whose product O may still change
                     const auto settle = [&]() {
                         if (waited) return true;
                         waited = true;
@@ -853,38 +841,46 @@ struct TreeMma {
                         return true;
                     };
                     if (works) {
-                        float x[kOwn];
+                        // 32 of this thread's tokens, -inf where they are not seen. Read twice: the registers of one CTA of 18 warps
+                        // do not hold all 64 between the maximum and the weights.
+                        const auto scores = [&](float (&x)[32], int i) {
+                            tm_load(x, here + i);
+                            tm_loaded();
+                            if (!(factor > 0.0f)) {
 #pragma unroll
-                        for (int i = 0; i < kOwn; i += 32) tm_load(x + i, here + i);
-                        tm_loaded();
-                        if (!(factor > 0.0f)) {
+                                for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], factor);
+                            }
+                            if (!whole) {
+                                const uint32_t bits = (uint32_t)(seen >> i);
 #pragma unroll
-                            for (int i = 0; i < kOwn; ++i) x[i] = __fmul_rn(x[i], factor);
+                                for (int k = 0; k < 32; ++k)
+                                    if (!((bits >> k) & 1)) x[k] = neg_inf();
+                            }
+                        };
+                        float top = neg_inf();
+#pragma unroll 1
+                        for (int i = 0; i < kOwn; i += 32) {
+                            float x[32];
+                            scores(x, i);
+                            float t4[4] = {fmaxf(top, x[0]), x[1], x[2], x[3]};
+#pragma unroll
+                            for (int k = 4; k < 28; k += 8) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) t4[j] = max3(t4[j], x[k + j], x[k + 4 + j]);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) t4[j] = fmaxf(t4[j], x[28 + j]);
+                            top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
                         }
-                        if (!whole) {
-#pragma unroll
-                            for (int i = 0; i < kOwn; ++i)
-                                if (!((seen >> i) & 1)) x[i] = neg_inf();
-                        }
-                        float t4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                        for (int i = 4; i < kOwn - 4; i += 8) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) t4[k] = max3(t4[k], x[i + k], x[i + 4 + k]);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], x[kOwn - 4 + k]);
-                        const float mine = __fmul_rn(fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]), scale);
-                        float top = mine;
-                        if (!hand(ct, handed, top)) return;
-                        top = fmaxf(top, mine);
+                        top = __fmul_rn(top, scale);
+                        if (!agree(ct, agreed, top)) return;
                         const bool moves = top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack));
                         if (__any_sync(~0u, moves)) {
                             const float next = moves ? __fsub_rn(top, (float)Shape::kShift) : m;
                             const float fall = moves ? fade<true>(__fsub_rn(m, base_of(next))) : 1.0f;
                             m = next;
                             l = __fmul_rn(l, fall);
-                            if (tile != t0) {
+                            if (tile != begin) {
                                 if (!settle()) return;
 #pragma unroll 1
                                 for (int cb = half; cb < blocks; cb += 2) {
@@ -902,6 +898,8 @@ struct TreeMma {
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
                         for (int i = 0; i < kOwn; i += 32) {
+                            float x[32];
+                            scores(x, i);
                             uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
@@ -912,19 +910,16 @@ struct TreeMma {
                             }
                             tm_store16(here + i, hi);
                             tm_store16(here + i + 16, lo);
-                            // the other 32 in the same registers: half the code
-#pragma unroll
-                            for (int k = 0; k + 32 < kOwn; ++k) x[k] = x[k + 32];
                         }
                         l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
                         tm_stored();
                     }
-                    if (tid == 0 && tile == t0) *(volatile int *)&ct.keep_o = 0;
+                    if (tid == 0 && tile == begin) *(volatile int *)&ct.keep_o = 0;
                     // The values have come, and are not given up before the weights below are told.
                     const int fill = 2 * g + 1, slot = fill % kSlots;
                     if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
                     // every copy of this unit has been told: what it found is known
-                    if (tile + 1 == end) bad = shared_by_all(((volatile int *)ct.bad)[count & 15]) == count;
+                    if (tile + 1 == end) bad = shared_by_all(((volatile int *)ct.bad)[count & 7]) == count;
                     if (!whole) {
                         unsigned char *values = smem + slot * Shape::kSlot;
                         const uint32_t word = __ballot_sync(~0u, tid < kTok && row_is_odd(values, tid, p.head_dim / 8));
@@ -932,59 +927,20 @@ struct TreeMma {
                         if (tid % 32 == 0 && half == 0) odd[warp] = word;
                         if (!meet(ct, meetings)) return;
                         if (shared_by_all(odd[0] | odd[1] | odd[2] | odd[3])) {
-                            if (!settle() || !odd_values(ct, odd, meetings, values, tmem + (g & 1) * kTok, o, p.head_dim, tile == t0, works))
+                            if (!settle() || !odd_values(ct, odd, meetings, values, tmem + (g & 1) * kTok, o, p.head_dim, tile == begin, works))
                                 return;
                         }
                     }
                     mma_before();
                     bar_arrive(smem_at(&ct.p_ready[g & 1]));
                 }
-                // the chunk's end: O is whole
-                if (!none && !warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return;
-                mma_after();
-                if (works) {
-                    const float mine = l;
-                    if (!hand(ct, handed, l)) return;
-                    l = __fadd_rn(l, mine);
-                    const bool last = none || t1 == end, before = t0 != begin;
-                    if (last && bad) {
-                        l = quiet_nan();
-                        if (tid == 0) flag_bad_index(p.status);
-                    }
-                    float top = m, fa = 0.0f, fb = 1.0f, sum = l;
-                    if (before) {
-                        fold_factors<true>(fm, m, top, fa, fb);
-                        sum = fold_in(fl, l, fa, fb);
-                    }
-                    const float inverse = inverse_of(sum);
-#pragma unroll 1
-                    for (int cb = half; cb < blocks; cb += 2) {
-                        float x[32];
-                        tm_load(x, o + cb * 32);
-                        if (Shape::kFolds && before) {
-                            float y[32];
-                            tm_load(y, f + cb * 32);
-                            tm_loaded();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = fold_in(y[i], x[i], fa, fb);
-                        } else {
-                            tm_loaded();
-                        }
-                        if (!last) {
-                            if (Shape::kFolds) tm_store32(f + cb * 32, x);
-                        } else {
-                            put(w, x, cb * 32, to, direct, written, inverse);
-                        }
-                        __syncwarp();
-                    }
-                    if (!last)
-                        tm_stored();
-                    else
-                        finish(top, sum);
-                    fm = top, fl = sum;
-                }
-                if (none) break;
             }
+            // the unit's end: what the results are made of
+            if (count > 1 && !warp_wait(smem_at(&ct.sums_free), count & 1, &ct.dead)) return;
+            if (!half) ct.top[row] = m;
+            ct.sums[half][row] = bad ? quiet_nan() : l;
+            if (bad && tid == 0) flag_bad_index(p.status);
+            bar_arrive(smem_at(&ct.sums_full));
         }
     }
 };
@@ -996,7 +952,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_mma_kernel(const __grid_c
 }
 
 template <typename Shape>
-cudaError_t launch_mma(TreeWork w, cudaStream_t stream)
+cudaError_t launch_mma(const TreeWork &w, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     const auto kernel = tree_mma_kernel<Shape>;
@@ -1010,8 +966,6 @@ cudaError_t launch_mma(TreeWork w, cudaStream_t stream)
     const TreeParams &p = w.p;
     const int64_t pairs = p.kv_heads * (((int64_t)p.nodes * p.group + w.rule.rows - 1) / w.rule.rows);
     const int64_t units = p.batch * (w.slots > pairs ? w.slots : pairs);
-    // what the sizes rule out, or, of many sequences, allow, is not worked out from the lengths
-    w.by_group = !Shape::kFolds || units <= kByGroup * kSms ? 0 : p.batch > kCounted ? 1 : -1;
     const dim3 grid((unsigned)(units < kSms ? units : kSms));
     if (cudaError_t e = launch_early(kernel, grid, kMmaThreads, Shape::kBytes, stream, w)) return e;
     const int dtype = std::is_same_v<typename Shape::T, __nv_bfloat16> ? DETFOLD_BF16 : DETFOLD_F16;

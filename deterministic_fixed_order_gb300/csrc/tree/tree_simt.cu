@@ -48,7 +48,7 @@ struct Simt {
         const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
         enter_grid();
         for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-            const TreeSeq s = tree_seq_of(w, b, false);
+            const TreeSeq s = tree_seq_of(w, b);
             for (int64_t u = blockIdx.x; u < (int64_t)s.units * s.pairs; u += gridDim.x) {
                 const int chunk = (int)(u / s.pairs), pair = (int)(u - (int64_t)chunk * s.pairs);
                 const int kv = pair / s.blocks, row0 = (pair - kv * s.blocks) * w.rule.rows;
