@@ -7,9 +7,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAhead = 8;  // units whose accumulators a warp has in flight
-constexpr int kRowsEach = 2;  // rows a warp takes of its sequence
+constexpr int kRowsEach = 4;  // rows a warp takes of its sequence
 
 // A CTA has rows of one sequence, so that what follows from the sequence is worked out once.
+// PER: groups of four places of the head that a lane has.
 template <typename T, int PER, bool LOG2>
 __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_constant__ TreeWork w, int across)
 {
@@ -29,21 +30,23 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
         const int kv = (int)quotient(head, w.by_heads), r = node * p.group + head - kv * p.group, block = r >> w.log_rows;
         const int pair = kv * s.blocks + block;
         const int64_t first = ((int64_t)b * w.slots + pair) * w.slot_rows + (r - block * w.rule.rows);
-        float m = neg_inf(), l = 0.0f, a[PER];
+        float m = neg_inf(), l = 0.0f;
+        float4 a[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) a[i] = 0.0f;
+        for (int i = 0; i < PER; ++i) a[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int fours = p.head_dim / 4;
         for (int u0 = 0; u0 < units; u0 += kAhead) {
             float2 ml[kAhead];
-            float x[kAhead][PER];
+            float4 x[kAhead][PER];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (u0 + k >= units) continue;
                 const int64_t at = first + (u0 + k) * step;
                 ml[k] = w.ml[at];
-                const float *acc = w.acc + at * p.head_dim;
+                const float4 *acc = reinterpret_cast<const float4 *>(w.acc + at * p.head_dim);
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    if (lane + 32 * i < p.head_dim) x[k][i] = acc[lane + 32 * i];
+                    if (lane + 32 * i < fours) x[k][i] = acc[lane + 32 * i];
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
@@ -52,14 +55,28 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const __grid_con
                 fold_factors<LOG2>(m, ml[k].x, top, fa, fb);
                 m = top, l = fold_in(l, ml[k].y, fa, fb);
 #pragma unroll
-                for (int i = 0; i < PER; ++i) a[i] = fold_in(a[i], x[k][i], fa, fb);
+                for (int i = 0; i < PER; ++i) {
+                    a[i].x = fold_in(a[i].x, x[k][i].x, fa, fb), a[i].y = fold_in(a[i].y, x[k][i].y, fa, fb);
+                    a[i].z = fold_in(a[i].z, x[k][i].z, fa, fb), a[i].w = fold_in(a[i].w, x[k][i].w, fa, fb);
+                }
             }
         }
         T *out = (T *)p.out + b * p.out_bs + node * p.out_ns + head * p.out_hs;
         const float inverse = inverse_of(l);
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 32 * i < p.head_dim) out[lane + 32 * i] = quotient_of<T>(a[i], l, inverse);
+        for (int i = 0; i < PER; ++i) {
+            if (lane + 32 * i >= fours) continue;
+            Pack<T, 4> y;
+            y.v[0] = quotient_of<T>(a[i].x, l, inverse), y.v[1] = quotient_of<T>(a[i].y, l, inverse);
+            y.v[2] = quotient_of<T>(a[i].z, l, inverse), y.v[3] = quotient_of<T>(a[i].w, l, inverse);
+            T *to = out + (lane + 32 * i) * 4;
+            if (w.out_vec) {
+                *reinterpret_cast<Pack<T, 4> *>(to) = y;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) to[k] = y.v[k];
+            }
+        }
         if (lane == 0 && p.lse) p.lse[(int64_t)b * of + in] = log_sum<LOG2>(m, l);
     }
 }
@@ -69,9 +86,7 @@ cudaError_t launch_type(const TreeWork &w, cudaStream_t stream)
 {
     const int across = (w.p.nodes * w.p.q_heads + kWarps * kRowsEach - 1) / (kWarps * kRowsEach);
     const dim3 grid((unsigned)((int64_t)w.p.batch * across));
-    const auto kernel = w.p.head_dim <= 64    ? tree_join_kernel<T, 2, LOG2>
-                        : w.p.head_dim <= 128 ? tree_join_kernel<T, 4, LOG2>
-                                              : tree_join_kernel<T, 8, LOG2>;
+    const auto kernel = w.p.head_dim <= 128 ? tree_join_kernel<T, 1, LOG2> : tree_join_kernel<T, 2, LOG2>;
     return launch_early(kernel, grid, kWarps * 32, 0, stream, w, across);
 }
 

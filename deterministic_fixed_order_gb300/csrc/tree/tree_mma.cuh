@@ -3,7 +3,8 @@
 // S = Q K^T and O += P V are products of 128 rows by a tile's tokens: with a tree's nodes and a group's query heads
 // side by side a tile of keys and values is read once for all of them. The accumulators, S (two, in turn) and O,
 // lie in tensor memory, and P goes back there in the place of its S, so that the second product takes it
-// from there. P is split in two 16-bit parts (split2), both multiplied.
+// from there. P is split in two 16-bit parts, both multiplied: one part alone
+// would round each weight as much as the output is.
 //
 // Warps 0 to 7 have two threads a row, half of a tile's tokens each: they mask, take the maximum, make the weights, and finish
 // chunks. O is multiplied by the change of the maximum only where that grew by more than kSlack (a power of
@@ -19,9 +20,9 @@
 #pragma once
 
 #include <atomic>
+#include <cstring>
 #include <type_traits>
 
-#include "attn/attn_split.cuh"
 #include "tree_attn.cuh"
 
 namespace detfold_tree {
@@ -192,6 +193,30 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+
+// Two weights as two 16-bit parts each, the upper one truncated (to the bits of bfloat16, or of float16's mantissa: there a weight
+// under 2^-14 of the units that it is held in is rounded to their last place), the lower one what that leaves, off by 2^-16 or 2^-22
+// of the weight. `least`: 1 in both halves makes no lower part 0, so that an infinite value that every row sees gives the infinity,
+// not NaN; where values that are not finite are taken out it is 0.
+__device__ __forceinline__ void parts(float2 x, uint32_t least, uint32_t &hi, uint32_t &lo, __nv_bfloat16)
+{
+    const uint32_t u = __float_as_uint(x.x), v = __float_as_uint(x.y);
+    hi = __byte_perm(u, v, 0x7632);
+    const float2 rest = add2(x, make_float2(-__uint_as_float(u & 0xffff0000u), -__uint_as_float(v & 0xffff0000u)));
+    const __nv_bfloat162 y = __floats2bfloat162_rn(rest.x, rest.y);
+    memcpy(&lo, &y, 4);
+    lo |= least;
+}
+__device__ __forceinline__ void parts(float2 x, uint32_t least, uint32_t &hi, uint32_t &lo, __half)
+{
+    const float2 upper = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u), __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
+    __half2 y = __floats2half2_rn(upper.x, upper.y);
+    memcpy(&hi, &y, 4);
+    const float2 rest = add2(x, make_float2(-upper.x, -upper.y));
+    y = __floats2half2_rn(rest.x, rest.y);
+    memcpy(&lo, &y, 4);
+    lo |= least;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -895,6 +920,7 @@ struct TreeMma {
                         }
                         const float base = base_of(m);
                         const float2 by = make_float2(scale, scale), less = make_float2(-base, -base);
+                        const uint32_t least = whole ? 0x00010001u : 0;
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
                         for (int i = 0; i < kOwn; i += 32) {
@@ -906,7 +932,7 @@ struct TreeMma {
                                 const float2 e = fma2(make_float2(x[k], x[k + 1]), by, less);
                                 const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
                                 sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
-                                split2(y.x, y.y, hi[k / 2], lo[k / 2], T());
+                                parts(y, least, hi[k / 2], lo[k / 2], T());
                             }
                             tm_store16(here + i, hi);
                             tm_store16(here + i + 16, lo);
