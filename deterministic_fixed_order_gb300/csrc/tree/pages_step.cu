@@ -5,36 +5,44 @@
 // order, found by counting the free pages of each part of the pool and the needs of each row.
 //
 // Phases, with the whole cluster meeting between them:
-//   1. the counts are copied (unless they are changed in place);
+//   1. every CTA reads and checks the rows; the counts are copied (unless they are changed in place);
 //   2. old rows' pages are released, kept pages counted, and kept pages written to the new table. A
 //      row that goes on in its own place only releases what it does not keep;
-//   3. each CTA works out every row's need and its sum over the rows before (the same in each), and counts
-//      the free pages of its part of the pool;
+//   3. each CTA works out every row's need and its sum over the rows before (the same in each), and finds
+//      the free pages of its part of the pool, four a thread and tile as bits;
 //   4. each CTA hands out its part's free pages, and rows leave the pages that they copy.
-// Bound by latency: a few loads and atomics a phase, each phase a barrier of the cluster. The
-// counts are read past the L1, since other SMs change them.
+// Bound by latency: two or three loads or atomics one after the other a phase, each phase a barrier of the
+// cluster. The counts are read past the L1, since other SMs change them.
+#include <atomic>
+
 #include "tree_common.cuh"
 
 namespace detfold_tree {
 namespace {
 
-constexpr int kCluster = 8;
 constexpr int kThreads = 1024;
 constexpr int kRows = DETFOLD_PAGES_MAX_ROWS;
 constexpr int kEach = kRows / kThreads;
+constexpr int kMostCtas = 16;
+constexpr int kTile = kThreads * 4, kTiles = 8;  // pages a tile, and tiles whose bits a CTA holds
 
-__device__ __forceinline__ void meet()
-{
-    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// A new row: where it comes from and what it keeps. A row that does not make sense is empty.
-struct Row {
-    int origin, keep, want, kept, pages;  // `kept` columns kept, `pages` in the end
-    bool bad;
+struct Shared {
+    int origin[kRows], keep[kRows], want[kRows];
+    int end[kRows];    // pages that rows up to this one need, this one's among them
+    int first[kRows];  // first column that a fresh page goes to
+    unsigned long long warp[32];
+    int free;
 };
 
-__device__ __forceinline__ int up(int tokens, int page) { return (int)(((int64_t)tokens + page - 1) / page); }
+__device__ __forceinline__ void arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void meet()
+{
+    arrive();
+    wait();
+}
+
+__device__ __forceinline__ int up(int tokens, int page) { return (int)(((unsigned)tokens + page - 1) / (unsigned)page); }
 
 // Tokens of an old row, or -1.
 __device__ __forceinline__ int old_len(const PagesParams &p, int f)
@@ -42,20 +50,6 @@ __device__ __forceinline__ int old_len(const PagesParams &p, int f)
     const int n = p.lens[f];
     return n >= 0 && n <= (int64_t)p.cols * p.page_size ? n : -1;
 }
-
-__device__ __forceinline__ Row row_of(const PagesParams &p, int b)
-{
-    Row r = {p.origin[b], p.keep[b], p.want[b], 0, 0, false};
-    int most = 0;
-    if (r.origin >= 0 && r.origin < p.rows_in) most = max(old_len(p, r.origin), 0);
-    r.bad = r.origin < -1 || r.origin >= p.rows_in || r.keep < 0 || r.keep > most || r.want < r.keep ||
-            r.want > (int64_t)p.cols * p.page_size;
-    if (r.bad) r.origin = -1, r.keep = 0, r.want = 0;
-    r.kept = up(r.keep, p.page_size);
-    r.pages = up(r.want, p.page_size);
-    return r;
-}
-
 // A held page, or -1 where the table's entry is none.
 __device__ __forceinline__ int page_at(const PagesParams &p, int f, int col)
 {
@@ -63,48 +57,84 @@ __device__ __forceinline__ int page_at(const PagesParams &p, int f, int col)
     return page >= 0 && page < p.num_pages ? page : -1;
 }
 
-__device__ __forceinline__ int block_sum(int x, int *s_warp, int &before)
+// Sum of x over the threads before this one; returns that of all. Two counts in the halves of a word go together.
+__device__ __forceinline__ unsigned long long block_sum(unsigned long long x, unsigned long long *s_warp, unsigned long long &before)
 {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int sum = x;
+    unsigned long long sum = x;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-        const int y = __shfl_up_sync(~0u, sum, k);
+        const unsigned long long y = __shfl_up_sync(~0u, sum, k);
         if (lane >= k) sum += y;
     }
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    if (warp == 0) {
-        int t = s_warp[lane];
+    // each warp sums up the warps itself: one barrier
+    unsigned long long t = s_warp[lane];
 #pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-            const int y = __shfl_up_sync(~0u, t, k);
-            if (lane >= k) t += y;
-        }
-        s_warp[lane] = t;
+    for (int k = 1; k < 32; k <<= 1) {
+        const unsigned long long y = __shfl_up_sync(~0u, t, k);
+        if (lane >= k) t += y;
     }
+    const unsigned long long all = __shfl_sync(~0u, t, 31), ahead = __shfl_sync(~0u, t, warp ? warp - 1 : 0);
+    before = sum - x + (warp ? ahead : 0);
     __syncthreads();
-    before = sum - x + (warp ? s_warp[warp - 1] : 0);
-    const int total = s_warp[kThreads / 32 - 1];
-    __syncthreads();
-    return total;
+    return all;
 }
 
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
-    pages_kernel(const __grid_constant__ PagesParams p)
+// Bits of the free pages among four from `at` on, below `hi`.
+__device__ __forceinline__ uint32_t free_bits(const int *refs, int64_t at, int hi)
 {
-    __shared__ int s_end[kRows];    // pages that rows up to this one need, this one's among them
-    __shared__ int s_first[kRows];  // first column that a fresh page goes to
-    __shared__ int s_warp[32];
-    __shared__ int s_free;
-    const int tid = threadIdx.x, rank = blockIdx.x;
+    if (at + 4 <= hi && ((uintptr_t)(refs + at) & 15) == 0) {
+        const int4 x = __ldcg(reinterpret_cast<const int4 *>(refs + at));
+        return (uint32_t)((x.x == 0) | (x.y == 0) << 1 | (x.z == 0) << 2 | (x.w == 0) << 3);
+    }
+    uint32_t bits = 0;
+    for (int k = 0; k < 4 && at + k < hi; ++k) bits |= (uint32_t)(__ldcg(refs + at + k) == 0) << k;
+    return bits;
+}
+
+__global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__ PagesParams p)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(raw);
+    const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
     enter_grid();
-    const int at = rank * kThreads + tid, all = kCluster * kThreads;
+    const int at = rank * kThreads + tid, all = ctas * kThreads;
     int *refs = p.refs_out;
     if (p.refs != p.refs_out) {
-        for (int i = at; i < p.num_pages; i += all) __stcg(refs + i, p.refs[i]);
-        meet();
+        if ((((uintptr_t)p.refs | (uintptr_t)refs) & 15) == 0) {
+            const int fours = p.num_pages / 4;
+#pragma unroll 4
+            for (int i = at; i < fours; i += all) __stcg(reinterpret_cast<int4 *>(refs) + i, reinterpret_cast<const int4 *>(p.refs)[i]);
+            if (at < p.num_pages % 4) __stcg(refs + 4 * fours + at, p.refs[4 * fours + at]);
+        } else {
+#pragma unroll 4
+            for (int i = at; i < p.num_pages; i += all) __stcg(refs + i, p.refs[i]);
+        }
     }
+    // New rows: where they come from and what they keep. One that does not make sense is empty.
+    int last[kEach];  // the page that a row keeps and goes on writing into, or -1
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int b = tid * kEach + k;
+        last[k] = -1;
+        if (b >= p.rows_out) continue;
+        int origin = p.origin[b], keep = p.keep[b], want = p.want[b], most = 0;
+        if (origin >= 0 && origin < p.rows_in) most = max(old_len(p, origin), 0);
+        if (origin < -1 || origin >= p.rows_in || keep < 0 || keep > most || want < keep || want > (int64_t)p.cols * p.page_size) {
+            origin = -1, keep = 0, want = 0;
+            if (rank == 0) flag_bad_index(p.status);
+        }
+        sh.origin[b] = origin, sh.keep[b] = keep, sh.want[b] = want;
+        if (keep % p.page_size != 0 && want > keep) last[k] = page_at(p, origin, keep / p.page_size);
+        if (rank == 0) {
+            p.lens_out[b] = want;
+            p.copy_src[b] = -1, p.copy_dst[b] = -1, p.copy_rows[b] = 0;
+        }
+    }
+    __syncthreads();
+    meet();
     // Old rows. A row that the new row of the same number goes on from: that one's kept pages stay counted.
     const int warp = at / 32, warps = all / 32, lane = tid % 32;
     for (int f = warp; f < p.rows_in; f += warps) {
@@ -113,12 +143,9 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
             if (lane == 0) flag_bad_index(p.status);
             continue;
         }
-        int from = 0;
-        if (f < p.rows_out) {
-            const Row r = row_of(p, f);
-            if (r.origin == f) from = r.kept;
-        }
-        for (int j = from + lane; j < up(n, p.page_size); j += 32) {
+        const int from = f < p.rows_out && sh.origin[f] == f ? up(sh.keep[f], p.page_size) : 0, to = up(n, p.page_size);
+#pragma unroll 4
+        for (int j = from + lane; j < to; j += 32) {
             const int page = page_at(p, f, j);
             if (page >= 0)
                 atomicSub(refs + page, 1);
@@ -127,118 +154,132 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
         }
     }
     for (int b = warp; b < p.rows_out; b += warps) {
-        const Row r = row_of(p, b);
+        const int origin = sh.origin[b], kept = up(sh.keep[b], p.page_size);
         int32_t *to = p.table_out + b * p.table_out_stride;
-        for (int j = lane; j < p.cols; j += 32) {
-            int page = -1;
-            if (j < r.kept) {
-                page = page_at(p, r.origin, j);
-                if (page < 0)
-                    flag_bad_index(p.status);
-                else if (r.origin != b)
-                    atomicAdd(refs + page, 1);
-            }
+#pragma unroll 4
+        for (int j = lane; j < kept; j += 32) {
+            const int page = page_at(p, origin, j);
+            if (page < 0)
+                flag_bad_index(p.status);
+            else if (origin != b)
+                atomicAdd(refs + page, 1);
             to[j] = page;
         }
-        if (lane == 0) {
-            if (r.bad) flag_bad_index(p.status);
-            p.lens_out[b] = r.want;
-            p.copy_src[b] = -1, p.copy_dst[b] = -1, p.copy_rows[b] = 0;
-        }
+        // the rest is empty: by fours from the first multiple of 16 bytes on
+        int j = kept;
+        const int lead = min((int)((16 - ((uintptr_t)(to + j) & 15)) / 4 & 3), p.cols - j);
+        if (lane < lead) to[j + lane] = -1;
+        j += lead;
+        for (int i = lane; i < (p.cols - j) / 4; i += 32) *reinterpret_cast<int4 *>(to + j + 4 * i) = make_int4(-1, -1, -1, -1);
+        j += (p.cols - j) / 4 * 4;
+        if (j + lane < p.cols) to[j + lane] = -1;
     }
+    __syncthreads();
     meet();
-    // Needs: thread t has rows kEach t and on.
-    int need[kEach], sum = 0;
-    int leaves[kEach];  // the page that a row copies, or -1
+    // Needs: thread t has rows kEach t and on. Free pages of this CTA's part.
+    int need[kEach], sum = 0, leaves[kEach];
+    const int part = (int)(((int64_t)p.num_pages + ctas - 1) / ctas + 3) / 4 * 4;
+    const int lo = (int)min((int64_t)rank * part, (int64_t)p.num_pages), hi = min(lo + part, p.num_pages);
+    const bool once = part <= kTile * kTiles;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+        if (lo + (int64_t)i * kTile < hi) bits |= free_bits(refs, lo + (int64_t)i * kTile + tid * 4, hi) << (4 * i);
+    int mine = __popc(bits);
+    for (int64_t i = (int64_t)lo + kTile * kTiles; i < hi; i += kTile) mine += __popc(free_bits(refs, i + tid * 4, hi));
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int b = tid * kEach + k;
         need[k] = 0, leaves[k] = -1;
         if (b < p.rows_out) {
-            const Row r = row_of(p, b);
-            if (r.keep % p.page_size != 0 && r.want > r.keep) {
-                const int page = page_at(p, r.origin, r.kept - 1);
-                if (page >= 0 && __ldcg(refs + page) > 1) leaves[k] = page;
-            }
-            need[k] = r.pages - r.kept + (leaves[k] >= 0);
-            s_first[b] = r.kept - (leaves[k] >= 0);
+            if (last[k] >= 0 && __ldcg(refs + last[k]) > 1) leaves[k] = last[k];
+            const int kept = up(sh.keep[b], p.page_size);
+            need[k] = up(sh.want[b], p.page_size) - kept + (leaves[k] >= 0);
+            sh.first[b] = kept - (leaves[k] >= 0);
         }
         sum += need[k];
     }
-    int before;
-    const int wanted = block_sum(sum, s_warp, before);
+    unsigned long long before;
+    const unsigned long long total = block_sum((unsigned long long)(unsigned)sum << 32 | (unsigned)mine, sh.warp, before);
+    const int wanted = (int)(total >> 32);
+    int end = (int)(before >> 32);
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-        before += need[k];
-        if (tid * kEach + k < p.rows_out) s_end[tid * kEach + k] = before;
+        end += need[k];
+        if (tid * kEach + k < p.rows_out) sh.end[tid * kEach + k] = end;
     }
-    // Free pages of this CTA's part.
-    const int part = (p.num_pages + kCluster - 1) / kCluster, lo = min(rank * part, p.num_pages);
-    const int hi = min(lo + part, p.num_pages);
-    int mine = 0;
-    for (int i = lo + tid; i < hi; i += kThreads) mine += __ldcg(refs + i) == 0;
-    int dummy;
-    mine = block_sum(mine, s_warp, dummy);
-    if (tid == 0) s_free = mine;
+    if (tid == 0) sh.free = (int)(unsigned)total;
+    __syncthreads();
     meet();
     int nth = 0, have = 0;
-    for (int r = 0; r < kCluster; ++r) {
+    for (int r = 0; r < ctas; ++r) {
         uint32_t there;
         int x;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"((uint32_t)__cvta_generic_to_shared(&s_free)), "r"(r));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"((uint32_t)__cvta_generic_to_shared(&sh.free)), "r"(r));
         asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(there) : "memory");
         if (r < rank) nth += x;
         have += x;
     }
-    // The rows that are served, and what they leave.
+    arrive();  // no CTA ends before its number has been read
+    const auto give = [&](int page, int k) {
+        // the first row whose end is past k
+        int a = 0, z = p.rows_out - 1;
+        while (a < z) {
+            const int m = (a + z) / 2;
+            if (sh.end[m] > k)
+                z = m;
+            else
+                a = m + 1;
+        }
+        if (sh.end[a] > have) return;
+        const int col = sh.first[a] + (k - (a ? sh.end[a - 1] : 0));
+        p.table_out[a * p.table_out_stride + col] = page;
+        __stcg(refs + page, 1);
+        if (col < up(sh.keep[a], p.page_size)) p.copy_dst[a] = page;
+    };
+    const auto hand_out = [&](uint32_t free, int64_t page0, int k) {
+        for (; free && k < wanted; free &= free - 1, ++k) give((int)page0 + __ffs(free) - 1, k);
+    };
+    if (once) {
+        // a tile's counts are 4096 at most: four tiles a word
+#pragma unroll 1
+        for (int i0 = 0; i0 < kTiles && nth < wanted && lo + (int64_t)i0 * kTile < hi; i0 += 4) {
+            unsigned long long x = 0, ahead;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x |= (unsigned long long)__popc(bits >> (4 * (i0 + i)) & 15) << (16 * i);
+            const unsigned long long found = block_sum(x, sh.warp, ahead);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hand_out(bits >> (4 * (i0 + i)) & 15, lo + (int64_t)(i0 + i) * kTile + tid * 4, nth + (int)(ahead >> (16 * i) & 0xffff));
+                nth += (int)(found >> (16 * i) & 0xffff);
+            }
+        }
+    } else {
+        for (int64_t i = lo; i < hi && nth < wanted; i += kTile) {
+            const uint32_t x = free_bits(refs, i + tid * 4, hi);
+            unsigned long long ahead;
+            const int found = (int)block_sum(__popc(x), sh.warp, ahead);
+            hand_out(x, i + tid * 4, nth + (int)ahead);
+            nth += found;
+        }
+    }
+    wait();
+    // A page that is left had a count above 1, so it was none of the free ones; where parts are looked through again, that is over.
+    if (!once) meet();
     if (rank == 0) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int b = tid * kEach + k;
             if (need[k] == 0) continue;
-            if (s_end[b] > have) {
-                p.lens_out[b] = p.keep[b];
+            if (sh.end[b] > have) {
+                p.lens_out[b] = sh.keep[b];
                 flag(p.status, DETFOLD_ERR_SCRATCH_LIMIT);
             } else if (leaves[k] >= 0) {
                 p.copy_src[b] = leaves[k];
-                p.copy_rows[b] = p.keep[b] % p.page_size;
+                p.copy_rows[b] = sh.keep[b] % p.page_size;
+                atomicSub(refs + leaves[k], 1);
             }
         }
-    }
-    // Free pages in ascending order to what is needed in ascending order.
-    for (int i0 = lo; i0 < hi && nth < min(wanted, have); i0 += kThreads) {
-        const int i = i0 + tid;
-        const bool free = i < hi && __ldcg(refs + i) == 0;
-        int k;
-        const int found = block_sum(free, s_warp, k);
-        k += nth;
-        nth += found;
-        if (free && k < wanted) {
-            // the first row whose end is past k
-            int a = 0, z = p.rows_out - 1;
-            while (a < z) {
-                const int m = (a + z) / 2;
-                if (s_end[m] > k)
-                    z = m;
-                else
-                    a = m + 1;
-            }
-            if (s_end[a] <= have) {
-                const int start = a ? s_end[a - 1] : 0, col = s_first[a] + (k - start);
-                p.table_out[a * p.table_out_stride + col] = i;
-                __stcg(refs + i, 1);
-                const Row r = row_of(p, a);
-                if (col < r.kept) p.copy_dst[a] = i;
-            }
-        }
-    }
-    // Others' counts of free pages have been read by now, and a page that is left had a count above 1:
-    // it is none of them.
-    meet();
-    if (rank == 0) {
-#pragma unroll
-        for (int k = 0; k < kEach; ++k)
-            if (leaves[k] >= 0 && s_end[tid * kEach + k] <= have) atomicSub(refs + leaves[k], 1);
     }
 }
 
@@ -246,7 +287,29 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
 
 cudaError_t launch_pages(const PagesParams &p, cudaStream_t stream)
 {
-    return launch_early(pages_kernel, dim3(kCluster), kThreads, 0, stream, p);
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (!(dev < 64 && (done.load(std::memory_order_acquire) & (1ull << dev)))) {
+        if (cudaError_t e = cudaFuncSetAttribute((const void *)pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared))) return e;
+        if (cudaError_t e = cudaFuncSetAttribute((const void *)pages_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
+        done.fetch_or(1ull << (dev & 63), std::memory_order_release);
+    }
+    const int64_t work = p.num_pages + (int64_t)p.rows_out * p.cols;
+    const int ctas = work <= (1 << 14) ? 1 : work <= (1 << 18) ? 8 : kMostCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, pages_kernel, p);
 }
 
 }  // namespace detfold_tree
