@@ -95,32 +95,51 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
     }
 }
 
-// Page src to page dst. A CTA takes a part of one pair's keys or values; threads go
-// along the rows that lie side by side in memory.
-template <int B>
-__global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyParams p, const Units u, int parts,
-                                                        bool by_head)
+// How a page's rows lie: all one after the other, the rows of a head one after the other, or apart.
+enum Lie { kPage, kHeads, kApart };
+
+// Page src to page dst. A CTA takes a part of one pair's keys or values; threads go along the rows that lie side by
+// side in memory. The next pair's numbers are read ahead of this one's rows.
+template <int B, int LIE>
+__global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyParams p, const Units u, int parts)
 {
     using T = typename Bytes<B>::type;
     enter_grid();
     const int64_t units = p.count * 2 * parts;
+    struct Pair {
+        int src, dst, rows;
+    };
+    const auto look = [&](int64_t w) {
+        Pair x = {-1, -1, 0};
+        if (w < units) {
+            const int64_t i = w / (2 * parts);
+            x = {p.src[i], p.dst[i], p.rows ? p.rows[i] : p.cache.page_size};
+        }
+        return x;
+    };
+    Pair next = look(blockIdx.x);
     for (int64_t w = blockIdx.x; w < units; w += gridDim.x) {
         const int64_t i = w / (2 * parts);
         const int rest = (int)(w - i * 2 * parts), part = rest >> 1;
-        const int src = p.src[i], dst = p.dst[i], rows = p.rows ? p.rows[i] : p.cache.page_size;
-        if (src < 0 || dst < 0 || src == dst) continue;
-        if (src >= p.cache.num_pages || dst >= p.cache.num_pages || rows < 0 || rows > p.cache.page_size) {
+        const Pair now = next;
+        next = look(w + gridDim.x);
+        if (now.src < 0 || now.dst < 0 || now.src == now.dst) continue;
+        if (now.src >= p.cache.num_pages || now.dst >= p.cache.num_pages || now.rows < 0 || now.rows > p.cache.page_size) {
             if (threadIdx.x == 0 && rest == 0) flag_bad_index(p.status);
             continue;
         }
-        const char *from = (rest & 1 ? u.v : u.k) + src * u.page;
-        char *to = (rest & 1 ? u.v : u.k) + dst * u.page;
-        const unsigned total = (unsigned)rows * (unsigned)u.a_row;  // units of this pair
-        const auto place = [&](unsigned x) {
-            const unsigned t = x / (unsigned)u.a_head, piece = x - t * (unsigned)u.a_head;
-            const unsigned lines = by_head ? (unsigned)rows : (unsigned)p.cache.kv_heads;
-            const unsigned outer = t / lines, inner = t - outer * lines;
-            return (by_head ? outer * u.head + inner * u.token : outer * u.token + inner * u.head) + (int64_t)piece * B;
+        const char *from = (rest & 1 ? u.v : u.k) + now.src * u.page;
+        char *to = (rest & 1 ? u.v : u.k) + now.dst * u.page;
+        const unsigned rows = (unsigned)now.rows, total = rows * (unsigned)u.a_row;  // units of this pair
+        const auto place = [&](unsigned x) -> int64_t {
+            if (LIE == kPage) return (int64_t)x * B;
+            const unsigned a = (unsigned)u.a_head;
+            if (LIE == kHeads) {
+                const unsigned line = rows * a, h = x / line;
+                return h * u.head + (int64_t)(x - h * line) * B;
+            }
+            const unsigned t = x / a, row = t / (unsigned)p.cache.kv_heads;
+            return row * u.token + (t - row * (unsigned)p.cache.kv_heads) * u.head + (int64_t)(x - t * a) * B;
         };
         const unsigned step = parts * kThreads;
         for (unsigned x0 = part * kThreads + threadIdx.x; x0 < total; x0 += step * kFlight) {
@@ -148,11 +167,17 @@ template <int B>
 cudaError_t copy(const CopyParams &p, int es, cudaStream_t stream)
 {
     const Units u = units_of(p.cache, es, B);
-    const bool by_head = p.cache.token_stride < p.cache.head_stride;
-    const int64_t page = (int64_t)p.cache.page_size * u.a_row;
-    int parts = (int)((page + kThreads * kFlight - 1) / (kThreads * kFlight));
-    const int64_t need = p.count * 2 * parts, most = kSms * 8;
-    return launch_early(copy_kernel<B>, dim3((unsigned)(need < most ? need : most)), kThreads, 0, stream, p, u, parts, by_head);
+    const detfold_kv_cache &c = p.cache;
+    const bool heads = c.kv_heads == 1 || c.head_stride == c.head_dim;  // a row's heads side by side
+    const bool tokens = c.page_size == 1 || c.token_stride == c.head_dim;  // a head's rows side by side
+    const bool page = heads && (c.page_size == 1 || c.token_stride == (int64_t)c.kv_heads * c.head_dim);
+    const int64_t units = (int64_t)c.page_size * u.a_row;
+    const int parts = (int)((units + kThreads * kFlight - 1) / (kThreads * kFlight));
+    // 2047 pages of 32 KB and 32 KB: 41.6 us (95% of the measured copy rate); 42.7 with half the CTAs, 46.3 with a quarter
+    const int64_t need = p.count * 2 * parts, most = kSms * 16;
+    const dim3 grid((unsigned)(need < most ? need : most));
+    const auto kernel = page ? copy_kernel<B, kPage> : tokens ? copy_kernel<B, kHeads> : copy_kernel<B, kApart>;
+    return launch_early(kernel, grid, kThreads, 0, stream, p, u, parts);
 }
 
 }  // namespace

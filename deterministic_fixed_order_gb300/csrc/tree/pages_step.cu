@@ -42,13 +42,18 @@ __device__ __forceinline__ void meet()
     wait();
 }
 
-__device__ __forceinline__ int up(int tokens, int page) { return (int)(((unsigned)tokens + page - 1) / (unsigned)page); }
+// Pages of so many tokens, 2^30 at most.
+__device__ __forceinline__ int up(const PagesParams &p, int tokens) { return tokens ? (int)quotient((unsigned)tokens - 1, p.page) + 1 : 0; }
+__device__ __forceinline__ int most_tokens(const PagesParams &p)
+{
+    return (int)min((int64_t)p.cols * p.page_size, (int64_t)DETFOLD_ATTN_MAX_LEN);
+}
 
 // Tokens of an old row, or -1.
 __device__ __forceinline__ int old_len(const PagesParams &p, int f)
 {
     const int n = p.lens[f];
-    return n >= 0 && n <= (int64_t)p.cols * p.page_size ? n : -1;
+    return n >= 0 && n <= most_tokens(p) ? n : -1;
 }
 // A held page, or -1 where the table's entry is none.
 __device__ __forceinline__ int page_at(const PagesParams &p, int f, int col)
@@ -114,20 +119,23 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
         }
     }
     // New rows: where they come from and what they keep. One that does not make sense is empty.
+    const int each = (p.rows_out + kThreads - 1) / kThreads;  // rows a thread, side by side
     int last[kEach];  // the page that a row keeps and goes on writing into, or -1
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-        const int b = tid * kEach + k;
+        const int b = tid * each + k;
         last[k] = -1;
+        if (k >= each) break;
         if (b >= p.rows_out) continue;
         int origin = p.origin[b], keep = p.keep[b], want = p.want[b], most = 0;
         if (origin >= 0 && origin < p.rows_in) most = max(old_len(p, origin), 0);
-        if (origin < -1 || origin >= p.rows_in || keep < 0 || keep > most || want < keep || want > (int64_t)p.cols * p.page_size) {
+        if (origin < -1 || origin >= p.rows_in || keep < 0 || keep > most || want < keep || want > most_tokens(p)) {
             origin = -1, keep = 0, want = 0;
             if (rank == 0) flag_bad_index(p.status);
         }
         sh.origin[b] = origin, sh.keep[b] = keep, sh.want[b] = want;
-        if (keep % p.page_size != 0 && want > keep) last[k] = page_at(p, origin, keep / p.page_size);
+        const int full = (int)quotient(keep, p.page);
+        if (full * p.page_size != keep && want > keep) last[k] = page_at(p, origin, full);
         if (rank == 0) {
             p.lens_out[b] = want;
             p.copy_src[b] = -1, p.copy_dst[b] = -1, p.copy_rows[b] = 0;
@@ -136,14 +144,16 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
     __syncthreads();
     meet();
     // Old rows. A row that the new row of the same number goes on from: that one's kept pages stay counted.
-    const int warp = at / 32, warps = all / 32, lane = tid % 32;
-    for (int f = warp; f < p.rows_in; f += warps) {
+    // Half of the warps have old rows, half new ones.
+    const int warp = at / 64, warps = all / 64, lane = tid % 32;
+    const bool old = tid / 32 % 2 == 0;
+    for (int f = warp; old && f < p.rows_in; f += warps) {
         const int n = old_len(p, f);
         if (n < 0) {
             if (lane == 0) flag_bad_index(p.status);
             continue;
         }
-        const int from = f < p.rows_out && sh.origin[f] == f ? up(sh.keep[f], p.page_size) : 0, to = up(n, p.page_size);
+        const int from = f < p.rows_out && sh.origin[f] == f ? up(p, sh.keep[f]) : 0, to = up(p, n);
 #pragma unroll 4
         for (int j = from + lane; j < to; j += 32) {
             const int page = page_at(p, f, j);
@@ -153,8 +163,8 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
                 flag_bad_index(p.status);
         }
     }
-    for (int b = warp; b < p.rows_out; b += warps) {
-        const int origin = sh.origin[b], kept = up(sh.keep[b], p.page_size);
+    for (int b = warp; !old && b < p.rows_out; b += warps) {
+        const int origin = sh.origin[b], kept = up(p, sh.keep[b]);
         int32_t *to = p.table_out + b * p.table_out_stride;
 #pragma unroll 4
         for (int j = lane; j < kept; j += 32) {
@@ -189,12 +199,13 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
     for (int64_t i = (int64_t)lo + kTile * kTiles; i < hi; i += kTile) mine += __popc(free_bits(refs, i + tid * 4, hi));
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-        const int b = tid * kEach + k;
+        const int b = tid * each + k;
         need[k] = 0, leaves[k] = -1;
+        if (k >= each) continue;
         if (b < p.rows_out) {
             if (last[k] >= 0 && __ldcg(refs + last[k]) > 1) leaves[k] = last[k];
-            const int kept = up(sh.keep[b], p.page_size);
-            need[k] = up(sh.want[b], p.page_size) - kept + (leaves[k] >= 0);
+            const int kept = up(p, sh.keep[b]);
+            need[k] = up(p, sh.want[b]) - kept + (leaves[k] >= 0);
             sh.first[b] = kept - (leaves[k] >= 0);
         }
         sum += need[k];
@@ -206,22 +217,25 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         end += need[k];
-        if (tid * kEach + k < p.rows_out) sh.end[tid * kEach + k] = end;
+        if (k < each && tid * each + k < p.rows_out) sh.end[tid * each + k] = end;
     }
     if (tid == 0) sh.free = (int)(unsigned)total;
     __syncthreads();
     meet();
+    // a lane reads a CTA's number
     int nth = 0, have = 0;
-    for (int r = 0; r < ctas; ++r) {
+    {
         uint32_t there;
-        int x;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"((uint32_t)__cvta_generic_to_shared(&sh.free)), "r"(r));
+        int x = 0;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"((uint32_t)__cvta_generic_to_shared(&sh.free)), "r"(min(lane, ctas - 1)));
         asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(there) : "memory");
-        if (r < rank) nth += x;
-        have += x;
+        have = __reduce_add_sync(~0u, lane < ctas ? x : 0);
+        nth = __reduce_add_sync(~0u, lane < rank ? x : 0);
     }
     arrive();  // no CTA ends before its number has been read
-    const auto give = [&](int page, int k) {
+    // Pages of these bits to what is needed from the k-th on.
+    const auto hand_out = [&](uint32_t free, int64_t page0, int k) {
+        if (!free || k >= wanted) return;
         // the first row whose end is past k
         int a = 0, z = p.rows_out - 1;
         while (a < z) {
@@ -231,14 +245,14 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
             else
                 a = m + 1;
         }
-        if (sh.end[a] > have) return;
-        const int col = sh.first[a] + (k - (a ? sh.end[a - 1] : 0));
-        p.table_out[a * p.table_out_stride + col] = page;
-        __stcg(refs + page, 1);
-        if (col < up(sh.keep[a], p.page_size)) p.copy_dst[a] = page;
-    };
-    const auto hand_out = [&](uint32_t free, int64_t page0, int k) {
-        for (; free && k < wanted; free &= free - 1, ++k) give((int)page0 + __ffs(free) - 1, k);
+        for (; free && k < wanted; free &= free - 1, ++k) {
+            while (sh.end[a] <= k) ++a;
+            if (sh.end[a] > have) return;
+            const int page = (int)page0 + __ffs(free) - 1, col = sh.first[a] + (k - (a ? sh.end[a - 1] : 0));
+            p.table_out[a * p.table_out_stride + col] = page;
+            __stcg(refs + page, 1);
+            if (col < up(p, sh.keep[a])) p.copy_dst[a] = page;
+        }
     };
     if (once) {
         // a tile's counts are 4096 at most: four tiles a word
@@ -248,8 +262,8 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 4; ++i) x |= (unsigned long long)__popc(bits >> (4 * (i0 + i)) & 15) << (16 * i);
             const unsigned long long found = block_sum(x, sh.warp, ahead);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+#pragma unroll 1
+            for (int i = 0; i < 4 && nth < wanted; ++i) {
                 hand_out(bits >> (4 * (i0 + i)) & 15, lo + (int64_t)(i0 + i) * kTile + tid * 4, nth + (int)(ahead >> (16 * i) & 0xffff));
                 nth += (int)(found >> (16 * i) & 0xffff);
             }
@@ -269,14 +283,14 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
     if (rank == 0) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int b = tid * kEach + k;
+            const int b = tid * each + k;
             if (need[k] == 0) continue;
             if (sh.end[b] > have) {
                 p.lens_out[b] = sh.keep[b];
                 flag(p.status, DETFOLD_ERR_SCRATCH_LIMIT);
             } else if (leaves[k] >= 0) {
                 p.copy_src[b] = leaves[k];
-                p.copy_rows[b] = sh.keep[b] % p.page_size;
+                p.copy_rows[b] = sh.keep[b] - (int)quotient(sh.keep[b], p.page) * p.page_size;
                 atomicSub(refs + leaves[k], 1);
             }
         }

@@ -234,7 +234,7 @@ int detfold_pages_step(int32_t *refs_out, int32_t *table_out, int64_t table_out_
     if (conflicts(written, read)) return DETFOLD_ERR_OVERLAP;
     const PagesParams p = {refs_out, table_out, lens_out, copy_src, copy_dst, copy_rows, refs, table, lens, origin,
                            keep, want, table_out_stride, table_stride, (int)num_pages, (int)table_cols, page_size,
-                           rows_in, rows_out, d_status};
+                           rows_in, rows_out, d_status, divide_by(page_size)};
     return cuda_status(launch_pages(p, (cudaStream_t)stream));
 }
 

@@ -24,10 +24,8 @@ struct TreeRule {
     int wide;   // rows of the widest block of this type: a call whose trees have fewer may take narrower ones,
                 // which are then one block a key-value head either way
     int least;  // tiles a chunk, at least, for up to half of the widest block's rows; twice as many for more: a power of two
+    int fill;   // units that a sequence's chunks are to make where it is alone: CTAs that the GPU holds
 };
-
-// CTAs that a sequence's chunks are to fill when it is alone.
-constexpr int kFill = kSms;
 
 struct TreeWork {
     TreeParams p;
@@ -44,13 +42,13 @@ struct TreeWork {
 };
 
 // Slots of one sequence: pairs x units never pass these, and they only grow with max_len. (There are at most
-// kFill / pairs chunks, or one.)
+// fill / pairs chunks, or one.)
 inline int64_t slots_of(const TreeRule &r, int kv_heads, int group, int nodes, int64_t max_len)
 {
     const int64_t blocks = ((int64_t)nodes * group + r.rows - 1) / r.rows, pairs = kv_heads * blocks;
     const int64_t tiles = (max_len + r.tok - 1) / r.tok, chunks = (tiles + r.least - 1) / r.least;
     if (chunks <= 1) return 0;
-    const int64_t full = pairs > kFill ? pairs : kFill;
+    const int64_t full = pairs > r.fill ? pairs : r.fill;
     return full < pairs * chunks ? full : pairs * chunks;
 }
 inline int slot_rows_of(const TreeRule &r, int group, int nodes)
@@ -75,7 +73,7 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
     w.acc = (float *)((char *)workspace + (rows * 8 + 15) / 16 * 16);
     const auto log2_of = [](int x) { return 31 - __builtin_clz((unsigned)x); };
     w.log_tok = log2_of(r.tok), w.log_rows = log2_of(r.rows), w.log_least = log2_of(r.least);
-    w.most = p.kv_heads < kFill ? kFill / p.kv_heads : 1;
+    w.most = p.kv_heads < r.fill ? r.fill / p.kv_heads : 1;
     const int per = 16 / es;
     w.q_vec = (uintptr_t)p.q % 16 == 0 && p.q_bs % per == 0 && p.q_ns % per == 0 && p.q_hs % per == 0;
     w.out_vec = (uintptr_t)p.out % 16 == 0 && p.out_bs % per == 0 && p.out_ns % per == 0 && p.out_hs % per == 0;
@@ -83,7 +81,7 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
 }
 // The float32 kernel's: a block of as many rows as four warps take.
 constexpr int kSimtTok = 32;
-inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4}; }
+inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 4 * kSms}; }
 
 cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream);
 
@@ -129,7 +127,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
     s.pairs = s.blocks * p.kv_heads;
     s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) >> w.log_tok;
     const int log_least = w.log_least + (2 * rows > w.rule.wide), least = 1 << log_least;
-    const int most = s.blocks <= 1 ? w.most : s.pairs < kFill ? over(kFill, s.pairs) : 1;
+    const int most = s.blocks <= 1 ? w.most : s.pairs < w.rule.fill ? over(w.rule.fill, s.pairs) : 1;
     s.per = least;
     s.units = s.c == 0 ? 0 : max(1, (s.tiles + least - 1) >> log_least);
     if (s.units > most) {

@@ -57,6 +57,7 @@ struct PagesParams {
     int64_t table_out_stride, table_stride;
     int num_pages, cols, page_size, rows_in, rows_out;
     int *status;
+    Divide page;  // by the page size
 };
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream);

@@ -42,7 +42,7 @@ struct MmaShape {
     static constexpr int kColO = 2 * kTok, kColsO = NS * 64;
     static constexpr int kShift = std::is_same_v<T, __half> ? 8 : 0, kSlack = std::is_same_v<T, __half> ? 7 : 8;
     static constexpr int kControl = NS % 2 ? 4096 : 3072, kBytes = kSlots * kSlot + kQs * kQ + kControl;
-    static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok}; }  // chunks of 256 tokens at least
+    static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kSms}; }  // chunks of 256 tokens at least
 };
 
 #ifdef __CUDACC__
@@ -237,7 +237,7 @@ struct Unit {
 };
 
 // A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By a whole warp, a lane a
-// sequence. (At most 2^30 rows in all, or kFill pairs a sequence: the counts fit.)
+// sequence. (At most 2^30 rows in all, or `fill` pairs a sequence: the counts fit.)
 struct Units {
     int next, base, upto;  // the next unit; units before the 32 sequences at hand; units up to this lane's sequence
     int b0, pairs, units, per, first, n, c, tiles, blocks;  // this lane's sequence

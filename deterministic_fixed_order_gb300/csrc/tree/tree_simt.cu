@@ -33,8 +33,8 @@ template <typename T, int DP, int RW>
 struct Simt {
     static constexpr int kRows = kWarps * RW, kPer = 16 / sizeof(T), kPitch = DP * sizeof(T) + 16, kPlaces = DP / 32;
     struct Shared {
-        float q[kRows][DP];
-        float weights[kWarps][RW][kTok];
+        alignas(16) float q[kRows][DP];
+        alignas(16) float weights[kWarps][RW][kTok];
         uint64_t bits[kRows][kMaxWords];  // what each row's node sees of the drafted tokens
         int from[kRows];                  // and from which committed one on
         alignas(16) unsigned char k[2][kTok * kPitch], v[2][kTok * kPitch];
@@ -58,53 +58,61 @@ struct Simt {
         }
     }
 
+    // Copies a tile's keys and values; every warp looks the rows' pages up, a lane a row.
+    static __device__ __forceinline__ void fetch(const TreeWork &w, Shared &sh, int b, int kv, int t_lo, int t_hi, int tile, int tiles, int pieces,
+                                                 bool &bad)
+    {
+        const TreeParams &p = w.p;
+        const int tid = threadIdx.x, lane = tid % 32, t = t_lo + tile * kTok + lane;
+        int64_t at = -1;
+        if (tile < tiles && t < t_hi) {
+            const unsigned col = quotient(t, w.page);
+            const int page = p.table[b * p.table_stride + col];
+            if (page >= 0 && page < p.num_pages)
+                at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + kv * p.head_stride;
+            else
+                bad = true;
+        }
+        unsigned char *k = sh.k[tile & 1], *v = sh.v[tile & 1];
+        if (tile < tiles)
+#pragma unroll 4
+            for (int i = tid; i < kTok * (DP / kPer); i += kThreads) {
+                const int r = i / (DP / kPer), d = i - r * (DP / kPer);
+                const int64_t from = __shfl_sync(~0u, at, r);
+                if (d >= pieces) continue;
+                const bool some = from >= 0;
+                const int64_t el = from < 0 ? 0 : from + d * kPer;
+                copy16((uint32_t)__cvta_generic_to_shared(k + r * kPitch + d * 16), (const T *)p.k + el, some);
+                copy16((uint32_t)__cvta_generic_to_shared(v + r * kPitch + d * 16), (const T *)p.v + el, some);
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
     static __device__ __forceinline__ void unit(const TreeWork &w, Shared &sh, int b, const TreeSeq &s, int chunk, int pair,
                                                 int kv, int row0, int warp, int lane)
     {
         const TreeParams &p = w.p;
         const int tid = threadIdx.x, rows = min(w.rule.rows, s.c * p.group - row0);
         const int t_lo = s.first + chunk * s.per * kTok, t_hi = min(s.end, t_lo + s.per * kTok);
-        for (int i = tid; i < kRows * DP; i += kThreads) {
-            const int r = i / DP, d = i - r * DP;
-            float x = 0.0f;
-            if (r < rows && d < p.head_dim) {
-                const int node = (row0 + r) / p.group, head = kv * p.group + (row0 + r) - node * p.group;
-                x = to_f32(((const T *)p.q)[b * p.q_bs + node * p.q_ns + head * p.q_hs + d]);
+        bool bad = s.bad;
+        const int pieces = p.head_dim / kPer, tiles = (t_hi - t_lo + kTok - 1) / kTok;
+        fetch(w, sh, b, kv, t_lo, t_hi, 0, tiles, pieces, bad);
+        // a warp's own rows
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const int row = warp * RW + r, node = (int)quotient(row0 + row, w.by_heads), head = kv * p.group + row0 + row - node * p.group;
+            const T *from = (const T *)p.q + b * p.q_bs + node * p.q_ns + head * p.q_hs;
+#pragma unroll
+            for (int i = 0; i < kPlaces; ++i) {
+                const int d = lane + 32 * i;
+                sh.q[row][d] = row < rows && d < p.head_dim ? to_f32(from[d]) : 0.0f;
             }
-            sh.q[r][d] = x;
         }
         if (tid < rows) {
-            const RowMask m = row_mask(p, b, (row0 + tid) / p.group, s.n, s.c);
+            const RowMask m = row_mask(p, b, (int)quotient(row0 + tid, w.by_heads), s.n, s.c);
             for (int i = 0; i < kMaxWords; ++i) sh.bits[tid][i] = m.word(i);
             sh.from[tid] = m.from;
         }
-        bool bad = s.bad;
-        const int pieces = p.head_dim / kPer, tiles = (t_hi - t_lo + kTok - 1) / kTok;
-        const auto fetch = [&](int tile) {
-            const int t = t_lo + tile * kTok + lane;
-            int64_t at = -1;
-            if (tile < tiles && t < t_hi) {
-                const unsigned col = quotient(t, w.page);
-                const int page = p.table[b * p.table_stride + col];
-                if (page >= 0 && page < p.num_pages)
-                    at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + kv * p.head_stride;
-                else
-                    bad = true;
-            }
-            unsigned char *k = sh.k[tile & 1], *v = sh.v[tile & 1];
-            if (tile < tiles)
-                for (int i = tid; i < kTok * (DP / kPer); i += kThreads) {
-                    const int r = i / (DP / kPer), d = i - r * (DP / kPer);
-                    const int64_t from = __shfl_sync(~0u, at, r);
-                    if (d >= pieces) continue;
-                    const bool some = from >= 0;
-                    const int64_t el = from < 0 ? 0 : from + d * kPer;
-                    copy16((uint32_t)__cvta_generic_to_shared(k + r * kPitch + d * 16), (const T *)p.k + el, some);
-                    copy16((uint32_t)__cvta_generic_to_shared(v + r * kPitch + d * 16), (const T *)p.v + el, some);
-                }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        fetch(0);
         float m[RW], l[RW], o[RW][kPlaces];
 #pragma unroll
         for (int r = 0; r < RW; ++r) {
@@ -113,7 +121,7 @@ struct Simt {
             for (int i = 0; i < kPlaces; ++i) o[r][i] = 0.0f;
         }
         for (int tile = 0; tile < tiles; ++tile) {
-            fetch(tile + 1);
+            fetch(w, sh, b, kv, t_lo, t_hi, tile + 1, tiles, pieces, bad);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
             const unsigned char *k = sh.k[tile & 1], *v = sh.v[tile & 1];
@@ -123,14 +131,25 @@ struct Simt {
             float x[RW];
 #pragma unroll
             for (int r = 0; r < RW; ++r) x[r] = 0.0f;
+            // two sums a score, of even and of odd dimensions
+            float2 s2[RW];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) s2[r] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
             for (int d = 0; d < p.head_dim; d += kPer) {
                 float kk[kPer];
                 widen16<T>(k + lane * kPitch + d * sizeof(T), kk);
 #pragma unroll
                 for (int r = 0; r < RW; ++r)
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) x[r] = __fmaf_rn(sh.q[warp * RW + r][d + i], kk[i], x[r]);
+                    for (int i = 0; i < kPer; i += 4) {
+                        const float4 q = *reinterpret_cast<const float4 *>(&sh.q[warp * RW + r][d + i]);
+                        s2[r] = fma2(make_float2(q.x, q.y), make_float2(kk[i], kk[i + 1]), s2[r]);
+                        s2[r] = fma2(make_float2(q.z, q.w), make_float2(kk[i + 2], kk[i + 3]), s2[r]);
+                    }
             }
+#pragma unroll
+            for (int r = 0; r < RW; ++r) x[r] = __fadd_rn(s2[r].x, s2[r].y);
             uint32_t seen[RW];
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
@@ -160,17 +179,23 @@ struct Simt {
                 sh.weights[warp][r][lane] = y;
             }
             __syncwarp();
-            for (int j = 0; j < kTok; ++j) {
-                float vv[kPlaces];
+#pragma unroll 2
+            for (int j = 0; j < kTok; j += 4) {
+                float vv[4][kPlaces];
 #pragma unroll
-                for (int i = 0; i < kPlaces; ++i) vv[i] = to_f32(*reinterpret_cast<const T *>(v + j * kPitch + (lane + 32 * i) * sizeof(T)));
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < kPlaces; ++i)
+                        vv[k][i] = to_f32(*reinterpret_cast<const T *>(v + (j + k) * kPitch + (lane + 32 * i) * sizeof(T)));
 #pragma unroll
                 for (int r = 0; r < RW; ++r) {
-                    const float y = sh.weights[warp][r][j];
-                    if (whole || ((seen[r] >> j) & 1)) {
+                    const float4 y4 = *reinterpret_cast<const float4 *>(&sh.weights[warp][r][j]);
+                    const float y[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
-                        for (int i = 0; i < kPlaces; ++i) o[r][i] = __fmaf_rn(y, vv[i], o[r][i]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < kPlaces; ++i)  // what is not seen has no part, whatever it holds
+                            o[r][i] = __fmaf_rn(y[k], (seen[r] >> (j + k)) & 1 ? vv[k][i] : 0.0f, o[r][i]);
                 }
             }
             __syncthreads();

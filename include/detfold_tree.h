@@ -196,9 +196,9 @@ DETFOLD_API int detfold_kv_copy_pages(const detfold_kv_cache *cache, const int32
  *               held once by a row.
  *   lens        device int32 [rows_in].
  *   origin, keep, want  device int32 [rows_out].
- * An old row whose length is out of range counts as empty (d_status). So does a new row whose origin is
- * out of range, or whose keep is over that row's length, or want under keep or over the
- * table's columns; its lens_out is 0. A held table entry outside the pool is passed over, and
+ * Lengths go up to the columns' tokens, and to DETFOLD_ATTN_MAX_LEN. An old row whose length is out of
+ * range counts as empty (d_status). So does a new row whose origin is out of range, or whose keep is over that
+ * row's length, or want under keep or too long; its lens_out is 0. A held table entry outside the pool is passed over, and
  * kept as -1 (d_status). rows_in and rows_out are 0 .. DETFOLD_PAGES_MAX_ROWS; with rows_out == 0 every
  * row is released.
  */
