@@ -41,7 +41,7 @@ struct MmaShape {
     static constexpr int kOs = NS == 4 ? 1 : 2;     // accumulators: one is written out while the next one's tiles are multiplied
     static constexpr int kColO = 2 * kTok, kColsO = NS * 64;
     static constexpr int kShift = std::is_same_v<T, __half> ? 8 : 0, kSlack = std::is_same_v<T, __half> ? 7 : 8;
-    static constexpr int kControl = NS % 2 ? 4096 : 3072, kBytes = kSlots * kSlot + kQs * kQ + kControl;
+    static constexpr int kControl = NS % 2 ? 4096 : 3 * 1024, kBytes = kSlots * kSlot + kQs * kQ + kControl;
     static TreeRule rule() { return {kTok, kRows, kRows, 256 / kTok, kSms}; }  // chunks of 256 tokens at least
 };
 
@@ -231,9 +231,11 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 // A unit as the warps of a CTA are told it: tiles [tile, end) of a block of rows.
 struct Unit {
     int b, n, c, first;            // the sequence: committed tokens, nodes, first token seen
-    int kv, first_row, rows;       // key-value head; rows of it
+    int kv, first_row;             // key-value head; the first of its rows
     int tile, end;                 // tiles
     int slot;                      // where its triple goes, or -1: the outputs
+
+    __device__ __forceinline__ int rows(const TreeWork &w) const { return min(w.rule.rows, c * w.p.group - first_row); }
 };
 
 // A CTA's units, every gridDim.x-th of all: those of a sequence in turn, its pairs side by side. By a whole warp, a lane a
@@ -272,7 +274,6 @@ struct Units {
         u.n = of(n), u.c = of(c), u.first = of(first);
         u.kv = rows == 1 ? pair : over(pair, rows);
         u.first_row = (pair - u.kv * rows) * w.rule.rows;
-        u.rows = min(w.rule.rows, u.c * w.p.group - u.first_row);
         u.tile = index * of(per);
         u.end = min(of(tiles), u.tile + of(per));
         // lengths that change under the call: nothing past the workspace
@@ -295,13 +296,14 @@ struct TreeMma {
 
     struct Control {
         uint64_t full[kSlots], empty[kSlots], q_full[kQs], q_empty[kQs], s_full[2], p_ready[2], o_done[2], o_full[kOs], o_free[kOs];
-        uint64_t met, agree[4], sums_full, sums_free, unit_full[kUnits], unit_empty[kUnits], end;
+        uint64_t met, given_there[4], given_read[4], sums_full, sums_free, unit_full[kUnits], unit_empty[kUnits], end;
         Unit units[kUnits];  // b = -1: no more
         uint32_t tmem;
-        int dead, keep_o;
-        int bad[8];               // the unit (counted from 1) that has a page outside the cache, by its last bits
+        int dead;
+        uint8_t keep_o[2];        // of a unit's first tile, by turns: its product adds to what O holds
+        int bad[4];               // the unit (counted from 1) that has a page outside the cache, by its last bits
         uint32_t odd[2][4];       // tokens of a tile with values that are not finite, by turns
-        uint16_t given[2][2][128];  // what the two warps of a row hand each other, by turns
+        float given[2][128];      // what the two warps of a row hand each other
         float top[128], sums[2][128];  // a unit's maxima, and sums of weights of either half
     };
 
@@ -319,10 +321,10 @@ struct TreeMma {
             set(ct.full, kSlots, kCopy), set(ct.empty, kSlots, 1), set(ct.q_full, kQs, kCopy), set(ct.q_empty, kQs, 1);
             set(ct.s_full, 2, 1), set(ct.p_ready, 2, kSoftmax), set(ct.o_done, 2, 1), set(ct.o_full, kOs, 1);
             set(ct.o_free, kOs, kWrite), set(&ct.sums_full, 1, kSoftmax), set(&ct.sums_free, 1, kWrite);
-            set(&ct.met, 1, kSoftmaxWarps), set(ct.agree, 4, 2), set(&ct.end, 1, 1);
+            set(&ct.met, 1, kSoftmaxWarps), set(ct.given_there, 4, 2), set(ct.given_read, 4, 2), set(&ct.end, 1, 1);
             set(ct.unit_full, kUnits, 1), set(ct.unit_empty, kUnits, kSoftmaxWarps + kCopyWarps + kWriteWarps + 1);
-            ct.dead = 0, ct.keep_o = 0;
-            for (int i = 0; i < 8; ++i) ct.bad[i] = 0;
+            ct.dead = 0;
+            for (int i = 0; i < 4; ++i) ct.bad[i] = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         // tensor memory is taken after the wait: a kernel that is waited for may need it
@@ -452,7 +454,7 @@ struct TreeMma {
             const Unit &u = ct.units[way.i];
             const int begin = shared_by_all(u.tile), end = shared_by_all(u.end), first = u.first, stop = u.n + u.c, kv = u.kv, b = u.b;
             if (begin >= end) continue;
-            const int first_row = u.first_row, rows = u.rows;
+            const int first_row = u.first_row, rows = u.rows(w);
             const int seq = ++count;
             const int32_t *table = p.table + b * p.table_stride;
             const int64_t in_row = kv * p.head_stride;
@@ -466,7 +468,7 @@ struct TreeMma {
                     if (page >= 0 && page < p.num_pages)
                         at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + in_row;
                     else
-                        ((volatile int *)ct.bad)[seq & 7] = seq;
+                        ((volatile int *)ct.bad)[seq & 3] = seq;
                 }
                 return at;
             };
@@ -572,7 +574,7 @@ struct TreeMma {
                 const bool ends = tile_a + 1 == end_a;
                 if (one_lane()) {
                     uint64_t a = left, b = right;
-#pragma unroll 1
+#pragma unroll 4
                     for (int k = 0; k < steps; ++k) {  // 32 bytes on, in the next slab after four
                         mma_ss(to, a, b, scores, k > 0);
                         const bool slab = (k & 3) == 3;
@@ -598,7 +600,7 @@ struct TreeMma {
                 did = true;
                 fence_async();
                 mma_after();
-                const bool ends = tile_v + 1 == end_v, first = tile_v == first_v && !shared_by_all(*(volatile int *)&ct.keep_o);
+                const bool ends = tile_v + 1 == end_v, first = tile_v == first_v && !shared_by_all((int)((volatile uint8_t *)ct.keep_o)[gv & 1]);
                 const uint64_t right = shared_by_all(operand(ring + slot_v * Shape::kSlot, Shape::kSlab));
                 const uint32_t weights = shared_by_all(tmem + (gv & 1) * kTok), to = shared_by_all(tmem + Shape::kColO + oi * Shape::kColsO);
                 if (one_lane()) {
@@ -608,7 +610,7 @@ struct TreeMma {
                     for (int part = 0; part < 32; part += 16) {
                         uint32_t a = weights + part;
                         uint64_t b = right;
-#pragma unroll 1
+#pragma unroll
                         for (int k = 0; k < kTok / 16; k += 2) {
                             mma_ts(to, a, b, values, add);
                             mma_ts(to, a + 8, b + 128, values, true);
@@ -633,7 +635,10 @@ struct TreeMma {
             // bounded, as every wait
             if (did) {
                 idle = 0;
-            } else if (__nanosleep(20), (++idle & 1023) == 0) {
+                continue;
+            }
+            __nanosleep(20);
+            if ((++idle & 1023) == 0) {
                 long long t;
                 asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
                 if (idle == 1024) t0 = t;
@@ -661,18 +666,21 @@ struct TreeMma {
         mma_after();
         return ok;
     }
-    // The two warps of the same rows agree on the greater of their numbers a row, rounded up to 16 bits.
+    // The two warps of the same rows agree on the greater of their numbers a row. Neither writes its next one before the other
+    // has read this one.
     static __device__ __forceinline__ bool agree(Control &ct, int &agreed, float &x)
     {
         const int row = threadIdx.x % 128, half = threadIdx.x / 128, bar = row / 32;
-        volatile uint16_t(*at)[128] = ct.given[agreed & 1];
-        const uint32_t u = __float_as_uint(x), up = u + (u >> 31 ? 0 : 0xffff);  // towards +inf; an infinity stays
-        at[half][row] = (uint16_t)(up >> 16);
+        volatile float(*at)[128] = ct.given;
+        if (agreed && !warp_wait(smem_at(&ct.given_read[bar]), (agreed - 1) & 1, &ct.dead)) return false;
+        at[half][row] = x;
         __syncwarp();
-        if (row % 32 == 0) bar_arrive(smem_at(&ct.agree[bar]));
-        const bool ok = warp_wait(smem_at(&ct.agree[bar]), agreed++ & 1, &ct.dead);
-        x = fmaxf(__uint_as_float(up & 0xffff0000u), __uint_as_float((uint32_t)at[half ^ 1][row] << 16));
-        return ok;
+        if (row % 32 == 0) bar_arrive(smem_at(&ct.given_there[bar]));
+        if (!warp_wait(smem_at(&ct.given_there[bar]), agreed++ & 1, &ct.dead)) return false;
+        x = fmaxf(x, at[half ^ 1][row]);
+        __syncwarp();
+        if (row % 32 == 0) bar_arrive(smem_at(&ct.given_read[bar]));
+        return true;
     }
     // Where 16 bytes of a tile's row lie.
     static __device__ __forceinline__ uint4 *piece_of(unsigned char *slot, int row, int piece)
@@ -695,7 +703,7 @@ struct TreeMma {
     }
 
     // Values that are not finite, in a tile that not every row sees: added by the rows that see them, then zeros.
-    static __device__ __noinline__ bool odd_values(Control &ct, const volatile uint32_t *odd, int &meetings, unsigned char *slot,
+    static __device__ __noinline__ bool odd_values(Control &ct, const volatile uint32_t *odd, int &meetings, int turn, unsigned char *slot,
                                                    uint32_t weights, uint32_t o, int d, bool first, bool works)
     {
         const int tid = threadIdx.x, half = tid / 128, blocks = (d + 31) / 32, pieces = d / 8;
@@ -746,7 +754,7 @@ struct TreeMma {
                 *piece_of(slot, tid, i) = *reinterpret_cast<const uint4 *>(&y);
             }
         fence_async();
-        if (tid == 0 && first) *(volatile int *)&ct.keep_o = 1;
+        if (tid == 0 && first) ((volatile uint8_t *)ct.keep_o)[turn] = 1;
         return true;
     }
 
@@ -760,7 +768,7 @@ struct TreeMma {
         int oi = 0, o_round = 0, count = 0;
         for (Way way; way.here(ct); ) {
             const Unit &u = ct.units[way.i];
-            const int rows = shared_by_all(u.rows), slot = shared_by_all(u.slot), b = u.b;
+            const int rows = shared_by_all(u.rows(w)), slot = shared_by_all(u.slot), b = u.b;
             const bool none = shared_by_all(u.tile >= u.end);  // a sequence that cannot be attended to
             const bool live = row < rows, works = warp * 32 < rows, direct = slot == -1, puts = live && slot >= -1;
             const int at_row = u.first_row + row, node = live ? (int)quotient(at_row, w.by_heads) : 0;
@@ -836,130 +844,133 @@ struct TreeMma {
         const int tid = threadIdx.x, row = tid % 128, half = shared_by_all(tid / 128), warp = shared_by_all(row / 32), blocks = (p.head_dim + 31) / 32;
         // a positive scale goes into the exponent's product; another one is multiplied in first
         const float factor = __fmul_rn(p.scale, kLog2e), scale = factor > 0.0f ? factor : 1.0f;
-        int g = 0, count = 0, meetings = 0, agreed = 0;
+        int g = 0, count = 0, meetings = 0, looks = 0, agreed = 0;
         for (Way way; way.here(ct); way.past(ct)) {
             const Unit &u = ct.units[way.i];
             const int begin = shared_by_all(u.tile), end = shared_by_all(u.end);
             if (begin >= end) continue;
-            const int rows = shared_by_all(u.rows), n = shared_by_all(u.n), c = shared_by_all(u.c), first = shared_by_all(u.first);
+            const int rows = shared_by_all(u.rows(w)), n = shared_by_all(u.n), c = shared_by_all(u.c), first = shared_by_all(u.first);
             const bool works = warp * 32 < rows;
             const RowMask mask = row_mask(p, u.b, row < rows ? (int)quotient(u.first_row + row, w.by_heads) : 0, n, c);
             const uint32_t o = tmem + Shape::kColO + count % kOs * Shape::kColsO;
             ++count;
             bool bad = false;
             float m = neg_inf(), l = 0.0f;  // l: of this thread's tokens
-            {
-                for (int tile = begin; tile < end; ++tile, ++g) {
-                    const int at = first + tile * kTok;
-                    const bool whole = at + kTok <= n && (!p.window || at >= n + c - p.window);
-                    const uint32_t here = tmem + (g & 1) * kTok + half * kOwn;
-                    uint64_t seen = ~0ull;
-                    if (!whole && works) seen = mask.seen_from(at + half * kOwn);
-                    if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
+            for (int tile = begin; tile < end; ++tile, ++g) {
+                const int at = first + tile * kTok;
+                const bool whole = at + kTok <= n && (!p.window || at >= n + c - p.window);
+                const uint32_t here = tmem + (g & 1) * kTok + half * kOwn;
+                uint64_t seen = ~0ull;
+                if (!whole && works) seen = mask.seen_from(at + half * kOwn);
+                if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
+                mma_after();
+                bool waited = tile == begin;  // for the tile before, whose product O may still change
+                const auto settle = [&]() {
+                    if (waited) return true;
+                    waited = true;
+                    if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return false;
                     mma_after();
-                    bool waited = tile == begin;  // for the tile before, whose product O may still change
-                    const auto settle = [&]() {
-                        if (waited) return true;
-                        waited = true;
-                        if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return false;
-                        mma_after();
-                        return true;
+                    return true;
+                };
+                if (works) {
+                    // 32 of this thread's tokens, -inf where they are not seen. Read twice: the registers of one CTA of 18 warps
+                    // do not hold all 64 between the maximum and the weights.
+                    const auto scores = [&](float (&x)[32], int i) {
+                        tm_load(x, here + i);
+                        tm_loaded();
+                        if (!(factor > 0.0f)) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], factor);
+                        }
+                        if (!whole) {
+                            const uint32_t bits = (uint32_t)(seen >> i);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((bits >> k) & 1)) x[k] = neg_inf();
+                        }
                     };
-                    if (works) {
-                        // 32 of this thread's tokens, -inf where they are not seen. Read twice: the registers of one CTA of 18 warps
-                        // do not hold all 64 between the maximum and the weights.
-                        const auto scores = [&](float (&x)[32], int i) {
-                            tm_load(x, here + i);
-                            tm_loaded();
-                            if (!(factor > 0.0f)) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], factor);
-                            }
-                            if (!whole) {
-                                const uint32_t bits = (uint32_t)(seen >> i);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!((bits >> k) & 1)) x[k] = neg_inf();
-                            }
-                        };
-                        float top = neg_inf();
+                    float top = neg_inf();
 #pragma unroll 1
-                        for (int i = 0; i < kOwn; i += 32) {
-                            float x[32];
-                            scores(x, i);
-                            float t4[4] = {fmaxf(top, x[0]), x[1], x[2], x[3]};
+                    for (int i = 0; i < kOwn; i += 32) {
+                        float x[32];
+                        scores(x, i);
+                        float t4[4] = {fmaxf(top, x[0]), x[1], x[2], x[3]};
 #pragma unroll
-                            for (int k = 4; k < 28; k += 8) {
+                        for (int k = 4; k < 28; k += 8) {
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) t4[j] = max3(t4[j], x[k + j], x[k + 4 + j]);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) t4[j] = fmaxf(t4[j], x[28 + j]);
-                            top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+                            for (int j = 0; j < 4; ++j) t4[j] = max3(t4[j], x[k + j], x[k + 4 + j]);
                         }
-                        top = __fmul_rn(top, scale);
-                        if (!agree(ct, agreed, top)) return;
-                        const bool moves = top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack));
-                        if (__any_sync(~0u, moves)) {
-                            const float next = moves ? __fsub_rn(top, (float)Shape::kShift) : m;
-                            const float fall = moves ? fade<true>(__fsub_rn(m, base_of(next))) : 1.0f;
-                            m = next;
-                            l = __fmul_rn(l, fall);
-                            if (tile != begin) {
-                                if (!settle()) return;
-#pragma unroll 1
-                                for (int cb = half; cb < blocks; cb += 2) {
-                                    float y[32];
-                                    tm_load(y, o + cb * 32);
-                                    tm_loaded();
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], fall);
-                                    tm_store32(o + cb * 32, y);
-                                }
-                            }
-                        }
-                        const float base = base_of(m);
-                        const float2 by = make_float2(scale, scale), less = make_float2(-base, -base);
-                        const uint32_t least = whole ? 0x00010001u : 0;
-                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-                        for (int i = 0; i < kOwn; i += 32) {
-                            float x[32];
-                            scores(x, i);
-                            uint32_t hi[16], lo[16];
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float2 e = fma2(make_float2(x[k], x[k + 1]), by, less);
-                                const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
-                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
-                                parts(y, least, hi[k / 2], lo[k / 2], T());
-                            }
-                            tm_store16(here + i, hi);
-                            tm_store16(here + i + 16, lo);
-                        }
-                        l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
-                        tm_stored();
+                        for (int j = 0; j < 4; ++j) t4[j] = fmaxf(t4[j], x[28 + j]);
+                        top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
                     }
-                    if (tid == 0 && tile == begin) *(volatile int *)&ct.keep_o = 0;
-                    // The values have come, and are not given up before the weights below are told.
-                    const int fill = 2 * g + 1, slot = fill % kSlots;
-                    if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
-                    // every copy of this unit has been told: what it found is known
-                    if (tile + 1 == end) bad = shared_by_all(((volatile int *)ct.bad)[count & 7]) == count;
-                    if (!whole) {
-                        unsigned char *values = smem + slot * Shape::kSlot;
-                        const uint32_t word = __ballot_sync(~0u, tid < kTok && row_is_odd(values, tid, p.head_dim / 8));
-                        volatile uint32_t *odd = ct.odd[meetings & 1];
-                        if (tid % 32 == 0 && half == 0) odd[warp] = word;
-                        if (!meet(ct, meetings)) return;
-                        if (shared_by_all(odd[0] | odd[1] | odd[2] | odd[3])) {
-                            if (!settle() || !odd_values(ct, odd, meetings, values, tmem + (g & 1) * kTok, o, p.head_dim, tile == begin, works))
-                                return;
+                    top = __fmul_rn(top, scale);
+                    if (!agree(ct, agreed, top)) return;
+                    const bool moves = top > __fadd_rn(m, (float)(Shape::kShift + Shape::kSlack));
+                    if (__any_sync(~0u, moves)) {
+                        const float next = moves ? __fsub_rn(top, (float)Shape::kShift) : m;
+                        const float fall = moves ? fade<true>(__fsub_rn(m, base_of(next))) : 1.0f;
+                        m = next;
+                        l = __fmul_rn(l, fall);
+                        if (tile != begin) {
+                            if (!settle()) return;
+#pragma unroll 1
+                            for (int cb = half; cb < blocks; cb += 2) {
+                                float y[32];
+                                tm_load(y, o + cb * 32);
+                                tm_loaded();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], fall);
+                                tm_store32(o + cb * 32, y);
+                            }
                         }
                     }
-                    mma_before();
-                    bar_arrive(smem_at(&ct.p_ready[g & 1]));
+                    const float base = base_of(m);
+                    const float2 by = make_float2(scale, scale), less = make_float2(-base, -base);
+                    const uint32_t least = whole ? 0x00010001u : 0;
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+                    for (int i = 0; i < kOwn; i += 32) {
+                        float x[32];
+                        scores(x, i);
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 e = fma2(make_float2(x[k], x[k + 1]), by, less);
+                            const float2 y = make_float2(fade<true>(e.x), fade<true>(e.y));
+                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], y);
+                            parts(y, least, hi[k / 2], lo[k / 2], T());
+                        }
+                        tm_store16(here + i, hi);
+                        tm_store16(here + i + 16, lo);
+                    }
+                    l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
+                    tm_stored();
                 }
+                if (tid == 0 && tile == begin) ((volatile uint8_t *)ct.keep_o)[g & 1] = 0;
+                // The values have come, and are not given up before the weights below are told.
+                const int fill = 2 * g + 1, slot = fill % kSlots;
+                if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
+                // every copy of this unit has been told: what it found is known
+                if (tile + 1 == end) bad = shared_by_all(((volatile int *)ct.bad)[count & 3]) == count;
+                if (!whole) {
+                    unsigned char *values = smem + slot * Shape::kSlot;
+                    const uint32_t word = __ballot_sync(~0u, tid < kTok && row_is_odd(values, tid, p.head_dim / 8));
+                    volatile uint32_t *odd = ct.odd[looks++ & 1];
+                    if (tid % 32 == 0 && half == 0) odd[warp] = word;
+                    if (!meet(ct, meetings)) return;
+                    if (shared_by_all(odd[0] | odd[1] | odd[2] | odd[3])) {
+                        // O is this unit's: the tile before has been added, or the unit that had it before is written out
+                        const int k = count - 1;
+                        if (tile == begin && !warp_wait(smem_at(&ct.o_free[k % kOs]), k / kOs & 1 ^ 1, &ct.dead)) return;
+                        mma_after();
+                        if (!settle() || !odd_values(ct, odd, meetings, g & 1, values, tmem + (g & 1) * kTok, o, p.head_dim, tile == begin, works))
+                            return;
+                        mma_after();
+                    }
+                }
+                mma_before();
+                bar_arrive(smem_at(&ct.p_ready[g & 1]));
             }
             // the unit's end: what the results are made of
             if (count > 1 && !warp_wait(smem_at(&ct.sums_free), count & 1, &ct.dead)) return;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import tree_ref as ref
-from attn_ref import assert_near
+from attn_ref import U, assert_near, final_round
 
 pytestmark = pytest.mark.gpu
 
@@ -226,6 +226,48 @@ def test_scores_of_all_sizes(df, dtype):
     for sign in (1, -1):
         c.k[at] = ((q.float() * sign * 0.02)[None, None] * (up[:, None, None] / 12.0)).to(dtype).expand(-1, 2, -1)
         c.check(df)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("size", [1, -1])
+def test_scores_that_are_large_and_close(df, dtype, size):
+    """Scores of 2^14 and a few units: what a maximum loses by rounding would be the whole weight. The products are
+    exact, so that a score's only error is its size's last places, four of them at most."""
+    c = Case(dtype, [700, 3], 20, 4, 2, 64, 16, scale=1.0)
+    c.q.zero_()[..., 0], c.q[..., 1] = 128, 1
+    finite = ~torch.isnan(c.k[..., :1].float())
+    steps = torch.arange(c.k.shape[0] * c.k.shape[1], device=DEV).reshape(c.k.shape[:2]) % 7
+    c.k[..., 2:] = torch.where(finite, 0.0, math.nan).to(dtype)
+    c.k[..., 0] = torch.where(finite[..., 0], 128.0 * size, math.nan).to(dtype)
+    c.k[..., 1] = torch.where(finite[..., 0], steps[..., None].float(), math.nan).to(dtype)
+    out, lse = c.run(df)
+    o, s, _, _, _ = c.want()
+    score = 4 * U * (2 ** 14 + 7)
+    v = float(c.v[finite.expand_as(c.v)].double().abs().max())
+    tol = 2 * v * (score + 8 * U + (720 + 64) * 2 * U + 2.0 ** -16)
+    assert_near(out, o, tol + final_round(o, dtype), "out")
+    assert_near(lse, s, torch.full_like(s, 2 * (score + 8 * U + (720 + 64) * 2 * U) + 8 * U * 2 ** 14), "lse")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_values_that_are_not_finite_in_many_sequences(df, dtype, d):
+    """More sequences than run at once, each a few tokens long and with an infinite value that some of its nodes attend to:
+    what one leaves behind must not reach the next."""
+    nodes, batch = 6, 500
+    mask = ref.words(ref.ancestors(ref.parents_of(3, nodes, "roots")), nodes)
+    c = Case(dtype, [b % 9 for b in range(batch)], nodes, 2, 1, d, 16, masks=[mask] * batch)
+    for b in range(batch):
+        c.v[int(c.table[b, 0]), b % 9 + b % nodes, 0, b % d] = math.inf if b & 1 else -math.inf
+    out, lse = c.run(df)
+    o, s, tol, ltol, _ = c.want()
+    odd = ~torch.isfinite(o)
+    rest = torch.ones(batch, nodes, dtype=torch.bool)
+    rest[torch.arange(batch), torch.arange(batch) % nodes] = False
+    assert_near(out[rest.to(DEV)], o[rest], tol[rest], "nodes that do not attend to it")
+    got = out.double().cpu()
+    assert bool((torch.isinf(got) == odd).all()) and bool((got[odd] == o[odd]).all())
+    assert_near(lse, s, ltol, "lse")
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])

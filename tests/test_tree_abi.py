@@ -160,7 +160,7 @@ def test_copy_refusals(df, change, kw, status):
     ({3: E + 256}, -5), ({7: B + 4}, -5), ({0: E}, -5),
 ])
 def test_pages_refusals(df, change, status):
-    a = [B, C, 4, E + 1024, E + 2048, E + 3072, E + 4096, B, D, 4, E, E + 64, E + 128, E + 256, 100, 4, 16, 3, 5, 0, 0]
+    a = [B, C, 4, E + 1024, E + 2048, E + 3 * 1024, E + 4096, B, D, 4, E, E + 64, E + 128, E + 256, 100, 4, 16, 3, 5, 0, 0]
     for i, x in change.items():
         a[i] = x
     assert df.tree.lib.detfold_pages_step(*a) == status
