@@ -126,7 +126,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
     s.blocks = (rows + w.rule.rows - 1) >> w.log_rows;
     s.pairs = s.blocks * p.kv_heads;
     s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) >> w.log_tok;
-    const int log_least = w.log_least + (2 * rows > w.rule.wide), least = 1 << log_least;
+    const int log_least = w.log_least + (rows > w.rule.wide / 2), least = 1 << log_least;
     const int most = s.blocks <= 1 ? w.most : s.pairs < w.rule.fill ? over(w.rule.fill, s.pairs) : 1;
     s.per = least;
     s.units = s.c == 0 ? 0 : max(1, (s.tiles + least - 1) >> log_least);

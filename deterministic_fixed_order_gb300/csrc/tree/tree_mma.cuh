@@ -1,18 +1,19 @@
 // Attention of trees in 16-bit types on the matrix units (tcgen05): 128 rows a CTA.
 //
 // S = Q K^T and O += P V are products of 128 rows by a tile's tokens: with a tree's nodes and a group's query heads
-// side by side a tile of keys and values is read once for all of them. The accumulators, S (two, in turn) and O,
-// lie in tensor memory, and P goes back there in the place of its S, so that the second product takes it
-// from there. P is split in two 16-bit parts, both multiplied: one part alone
-// would round each weight as much as the output is.
+// side by side a tile of keys and values is read once for all of them. The accumulators lie in tensor memory, S twice and
+// O twice, and P goes back there in the place of its S, so that the second product takes it from there. P is split in
+// two 16-bit parts, both multiplied: one part alone would round each weight as much as the output is.
 //
-// Warps 0 to 7 have two threads a row, half of a tile's tokens each: they mask, take the maximum, make the weights, and finish
-// chunks. O is multiplied by the change of the maximum only where that grew by more than kSlack (a power of
-// two's exponent; weights stay below 2^(kShift + kSlack)). Warp 8 issues the products: scores up to a tile ahead of weighted
-// values. Warps 9 to 12 copy: pages may be one token long and end inside a tile, so a thread copies 16
-// bytes of a row at a time to where the swizzled operand has them; these writes by the generic proxy are fenced before the
-// products read them. Warp 13 works out what the CTA does next. One CTA an SM goes from unit to unit; copies and
-// products run ahead over their ends.
+// One CTA an SM, whose warps have parts of their own and go from unit to unit without meeting:
+//   0 to 7    the weights: two threads a row, half of a tile's tokens each. They mask, agree on the maximum and make P. O is
+//             multiplied by the change of the maximum only where that grew by more than kSlack (a power of two's exponent;
+//             weights stay below 2^(kShift + kSlack));
+//   8 to 11   copy: pages may be one token long and end inside a tile, so a thread copies 16 bytes of a row at a time to
+//             where the swizzled operand has them. The copies arrive on the barrier by themselves; the products' warp fences them;
+//   12 to 15  write the results of a unit out of the one O while the next unit goes on in the other;
+//   16        issues the products, whichever can be made: scores up to a tile ahead of weighted values;
+//   17        works out the CTA's units.
 //
 // Tiles whose tokens are not seen by every row (the drafted ones, a window's edge) are masked by bits. There a value
 // that is not finite must not meet a weight of 0: such values are looked for, taken out of the tile, and added
@@ -78,28 +79,37 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, int parity)
                  : "memory");
     return ok != 0;
 }
-// Bounded: two seconds, or until another wait of this CTA has run out. Out of line: there are a dozen waits, and the
-// warps' different loops share one instruction cache.
-static __device__ __noinline__ bool bar_wait_on(uint32_t bar, int parity, volatile int *dead)
+// What a CTA's waits look at: whether one of them has run out, and how many tiles have been multiplied.
+struct Pulse {
+    int dead;
+    unsigned beat;
+};
+// Bounded: two seconds in which no tile has been multiplied, or until another wait of this CTA has run out. (A unit of a very
+// long sequence takes longer than that, and the warps that write results wait for all of it.) Out of line: there are a dozen
+// waits, and the warps' different loops share one instruction cache.
+static __device__ __noinline__ bool bar_wait_on(uint32_t bar, int parity, volatile Pulse *pulse)
 {
     long long t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    for (int i = 0; i < (1 << 24); ++i) {
-        if (bar_try(bar, parity)) return true;
+    unsigned beat = pulse->beat;
+    while (!bar_try(bar, parity)) {
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-        if (*dead || t - t0 > 2000000000LL) break;
+        if (pulse->beat != beat) beat = pulse->beat, t0 = t;
+        if (pulse->dead || t - t0 > 2000000000LL) {
+            pulse->dead = 1;
+            return false;
+        }
     }
-    *dead = 1;
-    return false;
+    return true;
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, int parity, volatile int *dead)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, int parity, volatile Pulse *pulse)
 {
-    return bar_try(bar, parity) || bar_wait_on(bar, parity, dead);
+    return bar_try(bar, parity) || bar_wait_on(bar, parity, pulse);
 }
 // By a whole warp, with one verdict.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, int parity, volatile int *dead)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, int parity, volatile Pulse *pulse)
 {
-    return __all_sync(~0u, bar_wait(bar, parity, dead));
+    return __all_sync(~0u, bar_wait(bar, parity, pulse));
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void mma_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -299,7 +309,7 @@ struct TreeMma {
         uint64_t met, given_there[4], given_read[4], sums_full, sums_free, unit_full[kUnits], unit_empty[kUnits], end;
         Unit units[kUnits];  // b = -1: no more
         uint32_t tmem;
-        int dead;
+        Pulse pulse;
         uint8_t keep_o[2];        // of a unit's first tile, by turns: its product adds to what O holds
         int bad[4];               // the unit (counted from 1) that has a page outside the cache, by its last bits
         uint32_t odd[2][4];       // tokens of a tile with values that are not finite, by turns
@@ -323,7 +333,7 @@ struct TreeMma {
             set(ct.o_free, kOs, kWrite), set(&ct.sums_full, 1, kSoftmax), set(&ct.sums_free, 1, kWrite);
             set(&ct.met, 1, kSoftmaxWarps), set(ct.given_there, 4, 2), set(ct.given_read, 4, 2), set(&ct.end, 1, 1);
             set(ct.unit_full, kUnits, 1), set(ct.unit_empty, kUnits, kSoftmaxWarps + kCopyWarps + kWriteWarps + 1);
-            ct.dead = 0;
+            ct.pulse.dead = 0, ct.pulse.beat = 0;
             for (int i = 0; i < 4; ++i) ct.bad[i] = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -355,7 +365,7 @@ struct TreeMma {
         __syncthreads();
         mma_after();
         if (warp == kProducts) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-        if (tid == 0 && ct.dead) flag(w.p.status, DETFOLD_ERR_CUDA);
+        if (tid == 0 && ct.pulse.dead) flag(w.p.status, DETFOLD_ERR_CUDA);
     }
 
     // ---------------------------------------------------------- units
@@ -368,7 +378,7 @@ struct TreeMma {
         for (int i = 0, round = 0; more; ) {
             Unit u;
             more = units.take(w, u);
-            if (!warp_wait(smem_at(&ct.unit_empty[i]), (round & 1) ^ 1, &ct.dead)) break;
+            if (!warp_wait(smem_at(&ct.unit_empty[i]), (round & 1) ^ 1, &ct.pulse)) break;
             if (threadIdx.x % 32 == 0) {
                 if (!more) u.b = -1;
                 ct.units[i] = u;
@@ -394,7 +404,7 @@ struct TreeMma {
         }
         __device__ __forceinline__ bool here(Control &ct)
         {
-            return warp_wait(smem_at(&ct.unit_full[i]), round & 1, &ct.dead) && shared_by_all(*(volatile int *)&ct.units[i].b) >= 0;
+            return warp_wait(smem_at(&ct.unit_full[i]), round & 1, &ct.pulse) && shared_by_all(*(volatile int *)&ct.units[i].b) >= 0;
         }
     };
 
@@ -448,7 +458,7 @@ struct TreeMma {
         const bool mine = piece < pieces;
         Way way;
         int slot = 0, slot_round = 0, count = 0;
-        const auto wait = [&](uint64_t &bar, int parity) { return warp_wait(smem_at(&bar), parity, &ct.dead); };
+        const auto wait = [&](uint64_t &bar, int parity) { return warp_wait(smem_at(&bar), parity, &ct.pulse); };
         bool alive = true;
         for (; (alive = way.here(ct)); way.past(ct)) {
             const Unit &u = ct.units[way.i];
@@ -468,7 +478,7 @@ struct TreeMma {
                     if (page >= 0 && page < p.num_pages)
                         at = page * p.page_stride + (int64_t)(t - col * (unsigned)p.page_size) * p.token_stride + in_row;
                     else
-                        ((volatile int *)ct.bad)[seq & 3] = seq;
+                        ((volatile int *)ct.bad)[seq & 3] = seq, __threadfence_block();  // before this tile is told
                 }
                 return at;
             };
@@ -624,6 +634,7 @@ struct TreeMma {
                 }
                 __syncwarp();
                 ++gv;
+                ((volatile Pulse &)ct.pulse).beat = gv;
                 past(slot_v, round_v);
                 ++tile_v;
                 if (ends) {
@@ -642,16 +653,18 @@ struct TreeMma {
                 long long t;
                 asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
                 if (idle == 1024) t0 = t;
-                if (__any_sync(~0u, *(volatile int *)&ct.dead || t - t0 > 2000000000LL || idle > (1 << 28))) {
-                    *(volatile int *)&ct.dead = 1;
+                volatile Pulse &pulse = ct.pulse;
+                if (__any_sync(~0u, pulse.dead || t - t0 > 2000000000LL)) {
+                    pulse.dead = 1;
                     break;
                 }
             }
         }
-        // whatever was issued is done before the tensor memory goes back
+        // Whatever was issued is done before the tensor memory goes back, also after a wait has run out.
         if (one_lane()) mma_commit(smem_at(&ct.end));
         __syncwarp();
-        warp_wait(smem_at(&ct.end), 0, &ct.dead);
+        Pulse own = {0, 0};
+        if (!warp_wait(smem_at(&ct.end), 0, &own)) ((volatile Pulse &)ct.pulse).dead = 1;
     }
 
     // ---------------------------------------------------------- softmax
@@ -662,7 +675,7 @@ struct TreeMma {
         mma_before();
         __syncwarp();
         if (threadIdx.x % 32 == 0) bar_arrive(smem_at(&ct.met));
-        const bool ok = warp_wait(smem_at(&ct.met), meetings++ & 1, &ct.dead);
+        const bool ok = warp_wait(smem_at(&ct.met), meetings++ & 1, &ct.pulse);
         mma_after();
         return ok;
     }
@@ -672,11 +685,11 @@ struct TreeMma {
     {
         const int row = threadIdx.x % 128, half = threadIdx.x / 128, bar = row / 32;
         volatile float(*at)[128] = ct.given;
-        if (agreed && !warp_wait(smem_at(&ct.given_read[bar]), (agreed - 1) & 1, &ct.dead)) return false;
+        if (agreed && !warp_wait(smem_at(&ct.given_read[bar]), (agreed - 1) & 1, &ct.pulse)) return false;
         at[half][row] = x;
         __syncwarp();
         if (row % 32 == 0) bar_arrive(smem_at(&ct.given_there[bar]));
-        if (!warp_wait(smem_at(&ct.given_there[bar]), agreed++ & 1, &ct.dead)) return false;
+        if (!warp_wait(smem_at(&ct.given_there[bar]), agreed++ & 1, &ct.pulse)) return false;
         x = fmaxf(x, at[half ^ 1][row]);
         __syncwarp();
         if (row % 32 == 0) bar_arrive(smem_at(&ct.given_read[bar]));
@@ -779,10 +792,10 @@ struct TreeMma {
             float *const acc = w.acc + slot_row * p.head_dim;
             float top = 0.0f, sum = quiet_nan();
             if (!none) {
-                if (!warp_wait(smem_at(&ct.sums_full), count++ & 1, &ct.dead)) return;
+                if (!warp_wait(smem_at(&ct.sums_full), count++ & 1, &ct.pulse)) return;
                 top = ct.top[row], sum = __fadd_rn(ct.sums[0][row], ct.sums[1][row]);
                 bar_arrive(smem_at(&ct.sums_free));
-                if (!warp_wait(smem_at(&ct.o_full[oi]), o_round, &ct.dead)) return;
+                if (!warp_wait(smem_at(&ct.o_full[oi]), o_round, &ct.pulse)) return;
                 mma_after();
             }
             if (none && row == 0) flag_bad_index(p.status);
@@ -862,13 +875,13 @@ struct TreeMma {
                 const uint32_t here = tmem + (g & 1) * kTok + half * kOwn;
                 uint64_t seen = ~0ull;
                 if (!whole && works) seen = mask.seen_from(at + half * kOwn);
-                if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.dead)) return;
+                if (!warp_wait(smem_at(&ct.s_full[g & 1]), g / 2 & 1, &ct.pulse)) return;
                 mma_after();
                 bool waited = tile == begin;  // for the tile before, whose product O may still change
                 const auto settle = [&]() {
                     if (waited) return true;
                     waited = true;
-                    if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.dead)) return false;
+                    if (!warp_wait(smem_at(&ct.o_done[(g - 1) & 1]), (g - 1) / 2 & 1, &ct.pulse)) return false;
                     mma_after();
                     return true;
                 };
@@ -950,7 +963,7 @@ struct TreeMma {
                 if (tid == 0 && tile == begin) ((volatile uint8_t *)ct.keep_o)[g & 1] = 0;
                 // The values have come, and are not given up before the weights below are told.
                 const int fill = 2 * g + 1, slot = fill % kSlots;
-                if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.dead)) return;
+                if ((!whole || tile + 1 == end) && !warp_wait(smem_at(&ct.full[slot]), fill / kSlots & 1, &ct.pulse)) return;
                 // every copy of this unit has been told: what it found is known
                 if (tile + 1 == end) bad = shared_by_all(((volatile int *)ct.bad)[count & 3]) == count;
                 if (!whole) {
@@ -962,7 +975,7 @@ struct TreeMma {
                     if (shared_by_all(odd[0] | odd[1] | odd[2] | odd[3])) {
                         // O is this unit's: the tile before has been added, or the unit that had it before is written out
                         const int k = count - 1;
-                        if (tile == begin && !warp_wait(smem_at(&ct.o_free[k % kOs]), k / kOs & 1 ^ 1, &ct.dead)) return;
+                        if (tile == begin && !warp_wait(smem_at(&ct.o_free[k % kOs]), k / kOs & 1 ^ 1, &ct.pulse)) return;
                         mma_after();
                         if (!settle() || !odd_values(ct, odd, meetings, g & 1, values, tmem + (g & 1) * kTok, o, p.head_dim, tile == begin, works))
                             return;
@@ -973,7 +986,7 @@ struct TreeMma {
                 bar_arrive(smem_at(&ct.p_ready[g & 1]));
             }
             // the unit's end: what the results are made of
-            if (count > 1 && !warp_wait(smem_at(&ct.sums_free), count & 1, &ct.dead)) return;
+            if (count > 1 && !warp_wait(smem_at(&ct.sums_free), count & 1, &ct.pulse)) return;
             if (!half) ct.top[row] = m;
             ct.sums[half][row] = bad ? quiet_nan() : l;
             if (bad && tid == 0) flag_bad_index(p.status);

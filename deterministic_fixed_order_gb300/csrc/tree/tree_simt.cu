@@ -245,7 +245,7 @@ cudaError_t launch_rows(const TreeWork &w, cudaStream_t stream)
     using K = Simt<T, DP, RW>;
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
-    if (!(dev < 64 && (done.load() & (1ull << dev)))) {
+    if (!(dev < 64 && (done.load(std::memory_order_acquire) & (1ull << dev)))) {
         if (cudaError_t e = cudaFuncSetAttribute((const void *)tree_simt_kernel<T, DP, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)sizeof(typename K::Shared)))
             return e;
