@@ -20,10 +20,10 @@ namespace detfold_tree {
 // How sequences are cut, for one element type and head dimension.
 struct TreeRule {
     int tok;    // tokens a tile: a power of two
-    int rows;   // rows a pair's block, at most: a power of two
-    int wide;   // rows of the widest block of this type: a call whose trees have fewer may take narrower ones,
-                // which are then one block a key-value head either way
-    int least;  // tiles a chunk, at least, for up to half of the widest block's rows; twice as many for more: a power of two
+    int rows;   // rows a pair's block, at most: a power of two. A call whose trees have fewer may take narrower blocks, which are
+                // then one a key-value head either way
+    int least;  // tiles a chunk, at least: a power of two
+    int twice;  // rows a key-value head above which it is twice as many
     int fill;   // units that a sequence's chunks are to make where it is alone: CTAs that the GPU holds
 };
 
@@ -79,9 +79,12 @@ inline TreeWork tree_work(const TreeParams &p, const TreeRule &r, int es, void *
     w.out_vec = (uintptr_t)p.out % 16 == 0 && p.out_bs % per == 0 && p.out_ns % per == 0 && p.out_hs % per == 0;
     return w;
 }
-// The float32 kernel's: a block of as many rows as four warps take.
+// The float32 kernel's: a block of as many rows as four warps take. 7 nodes of 8 heads of 64 over 6000 tokens: 19.7 us in blocks
+// of 8 rows, 24.8 and 35.7 of 16 and 32; 16 sequences of 26 nodes over 2000: 157, 122 and 114. Chunks of 128 tokens at least: 64
+// nodes over 6000 take 51 us, 69 with 256, and 7 nodes 19.7, 21.0 with 64. Units for four CTAs an SM: 8 nodes of two query heads
+// a key-value head over 6000 tokens 24.9 us, 35.9 for one an SM, 27.1 for two, 24.8 for eight.
 constexpr int kSimtTok = 32;
-inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 32, 4, 4 * kSms}; }
+inline TreeRule simt_rule(int rows) { return {kSimtTok, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 4, INT32_MAX, 4 * kSms}; }
 
 cudaError_t launch_tree_join(const TreeWork &w, int dtype, cudaStream_t stream);
 
@@ -126,7 +129,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeWork &w, int n, int c)
     s.blocks = (rows + w.rule.rows - 1) >> w.log_rows;
     s.pairs = s.blocks * p.kv_heads;
     s.tiles = s.bad ? 0 : (s.end - s.first + w.rule.tok - 1) >> w.log_tok;
-    const int log_least = w.log_least + (rows > w.rule.wide / 2), least = 1 << log_least;
+    const int log_least = w.log_least + (rows > w.rule.twice), least = 1 << log_least;
     const int most = s.blocks <= 1 ? w.most : s.pairs < w.rule.fill ? over(w.rule.fill, s.pairs) : 1;
     s.per = least;
     s.units = s.c == 0 ? 0 : max(1, (s.tiles + least - 1) >> log_least);

@@ -1,5 +1,7 @@
 // Joins the partial results of rows whose tokens lie in several units of work: a warp a row. The units'
-// triples are folded in ascending order. Bound by memory and latency: each accumulator is read once, several in flight.
+// triples are folded in ascending order. Bound by memory and latency: each accumulator is read once, several in flight. In a batch of
+// 32 sequences of 128 rows a key-value head it takes 10 of 56 us; with two or four rows a warp, one after the other, the batch
+// took 2 and 5 us more.
 #include "tree_attn.cuh"
 
 namespace detfold_tree {
