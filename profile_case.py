@@ -4,7 +4,8 @@
     python profile_case.py operator --case NAME [--launches K]
 
 `operator` runs one of the listed cases of perf/operators.py (the decode-step
-operators) with the library's kernels. ROW is one of: stacked, ptrs, allreduce,
+operators) or perf/more_operators.py (those of a step with drafted tokens) with
+the libraries' kernels. ROW is one of: stacked, ptrs, allreduce,
 staged, scale, small, or torch_add
 (torch's own elementwise add of two operands, W = 2, as a reference for a
 launch of the same size that this library does not run). Inputs are
@@ -31,11 +32,17 @@ def operator_case(name: str, launches: int) -> int:
 
     import torch
 
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(_ROOT, "perf", "operators.py"))
-    ops = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ops)
+    for file in ("operators", "more_operators"):
+        spec = importlib.util.spec_from_file_location(file, os.path.join(_ROOT, "perf", file + ".py"))
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        case = next((c for c in ops.listed() if c["name"] == name), None)
+        if case is not None:
+            break
+    else:
+        raise SystemExit(f"profile_case operator: no case {name}")
     ops.own = True
-    state = ops.prepare(next(c for c in ops.listed() if c["name"] == name), 1)
+    state = ops.prepare(case, 1)
     for _ in range(launches):
         ops.run(state)
     torch.cuda.synchronize()
