@@ -9,11 +9,11 @@
 //   2. old rows' pages are released, kept pages counted, and kept pages written to the new table. A
 //      row that goes on in its own place only releases what it does not keep;
 //   3. each CTA works out every row's need and its sum over the rows before (the same in each), and finds
-//      the free pages of its part of the pool, four a thread and tile as bits;
+//      the free pages of its part of the pool, as bits, up to 32 a thread;
 //   4. each CTA hands out its part's free pages, and rows leave the pages that they copy.
 // Bound by latency: two or three loads or atomics one after the other a phase, each phase a barrier of the
-// cluster: 9.9 us for 64 rows of up to 512 pages, 17.2 us for 512 rows of up to 1024 of 262144 pages (4 MB of tables and counts,
-// 0.6 us at the memory's rate). The counts are read past the L1, since other SMs change them.
+// cluster: 8.9 us for 64 rows of up to 512 pages, 17 us for 512 rows of up to 1024 of 262144 pages (4 MB of tables and counts,
+// 0.6 us at the memory's rate; there what 16 SMs can store and count a cycle). The counts are read past the L1, since other SMs change them.
 #include <atomic>
 
 #include "tree_common.cuh"
@@ -25,7 +25,8 @@ constexpr int kThreads = 1024;
 constexpr int kRows = DETFOLD_PAGES_MAX_ROWS;
 constexpr int kEach = kRows / kThreads;
 constexpr int kMostCtas = 16;
-constexpr int kTile = kThreads * 4, kTiles = 8;  // pages a tile, and tiles whose bits a CTA holds
+constexpr int kAcross = 8;  // columns a lane asks for before it uses the first: with them 11.0 us for 64 rows and 65536 pages, 12.0 without
+constexpr int kTile = kThreads * 4, kTiles = 8;  // pages a tile, and tiles whose bits the threads hold
 
 struct Shared {
     int origin[kRows], keep[kRows], want[kRows];
@@ -100,7 +101,7 @@ __device__ __forceinline__ uint32_t free_bits(const int *refs, int64_t at, int h
     return bits;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__ PagesParams p)
+__global__ void __launch_bounds__(kThreads, 1) pages_kernel(const __grid_constant__ PagesParams p)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
@@ -145,36 +146,47 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
     __syncthreads();
     meet();
     // Old rows. A row that the new row of the same number goes on from: that one's kept pages stay counted.
-    // Half of the warps have old rows, half new ones.
-    const int warp = at / 64, warps = all / 64, lane = tid % 32;
-    const bool old = tid / 32 % 2 == 0;
-    for (int f = warp; old && f < p.rows_in; f += warps) {
+    // A row a warp, the old ones from the last warp on; kAcross columns a lane are asked for before the first is used.
+    const int warp = at / 32, warps = all / 32, lane = tid % 32;
+    const auto look = [&](int (&page)[kAcross], int f, int j0, int to) {
+#pragma unroll
+        for (int k = 0; k < kAcross; ++k) page[k] = j0 + 32 * k + lane < to ? page_at(p, f, j0 + 32 * k + lane) : 0;
+    };
+    for (int f = warps - 1 - warp; f < p.rows_in; f += warps) {
         const int n = old_len(p, f);
         if (n < 0) {
             if (lane == 0) flag_bad_index(p.status);
             continue;
         }
         const int from = f < p.rows_out && sh.origin[f] == f ? up(p, sh.keep[f]) : 0, to = up(p, n);
-#pragma unroll 4
-        for (int j = from + lane; j < to; j += 32) {
-            const int page = page_at(p, f, j);
-            if (page >= 0)
-                atomicSub(refs + page, 1);
-            else
-                flag_bad_index(p.status);
+        for (int j0 = from; j0 < to; j0 += 32 * kAcross) {
+            int page[kAcross];
+            look(page, f, j0, to);
+#pragma unroll
+            for (int k = 0; k < kAcross; ++k) {
+                if (page[k] < 0)
+                    flag_bad_index(p.status);
+                else if (j0 + 32 * k + lane < to)
+                    atomicSub(refs + page[k], 1);
+            }
         }
     }
-    for (int b = warp; !old && b < p.rows_out; b += warps) {
+    for (int b = warp; b < p.rows_out; b += warps) {
         const int origin = sh.origin[b], kept = up(p, sh.keep[b]);
         int32_t *to = p.table_out + b * p.table_out_stride;
-#pragma unroll 4
-        for (int j = lane; j < kept; j += 32) {
-            const int page = page_at(p, origin, j);
-            if (page < 0)
-                flag_bad_index(p.status);
-            else if (origin != b)
-                atomicAdd(refs + page, 1);
-            to[j] = page;
+        for (int j0 = 0; j0 < kept; j0 += 32 * kAcross) {
+            int page[kAcross];
+            look(page, origin, j0, kept);
+#pragma unroll
+            for (int k = 0; k < kAcross; ++k) {
+                const int j = j0 + 32 * k + lane;
+                if (j >= kept) continue;
+                if (page[k] < 0)
+                    flag_bad_index(p.status);
+                else if (origin != b)
+                    atomicAdd(refs + page[k], 1);
+                to[j] = page[k];
+            }
         }
         // the rest is empty: by fours from the first multiple of 16 bytes on
         int j = kept;
@@ -191,13 +203,17 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
     int need[kEach], sum = 0, leaves[kEach];
     const int part = (int)(((int64_t)p.num_pages + ctas - 1) / ctas + 3) / 4 * 4;
     const int lo = (int)min((int64_t)rank * part, (int64_t)p.num_pages), hi = min(lo + part, p.num_pages);
+    // A thread has up to 32 pages side by side, so that the sum below gives it the number of those before; in larger parts
+    // tiles of all threads are looked through twice.
     const bool once = part <= kTile * kTiles;
+    const int tiles = once ? (part + kTile - 1) / kTile : 0;
+    const int64_t page0 = (int64_t)lo + tid * 4 * tiles;
     uint32_t bits = 0;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
-        if (lo + (int64_t)i * kTile < hi) bits |= free_bits(refs, lo + (int64_t)i * kTile + tid * 4, hi) << (4 * i);
+        if (i < tiles) bits |= free_bits(refs, page0 + 4 * i, hi) << (4 * i);
     int mine = __popc(bits);
-    for (int64_t i = (int64_t)lo + kTile * kTiles; i < hi; i += kTile) mine += __popc(free_bits(refs, i + tid * 4, hi));
+    for (int64_t i = lo; !once && i < hi; i += kTile) mine += __popc(free_bits(refs, i + tid * 4, hi));
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int b = tid * each + k;
@@ -235,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
     }
     arrive();  // no CTA ends before its number has been read
     // Pages of these bits to what is needed from the k-th on.
-    const auto hand_out = [&](uint32_t free, int64_t page0, int k) {
+    const auto hand_out = [&](uint32_t free, int64_t at, int k) {
         if (!free || k >= wanted) return;
         // the first row whose end is past k
         int a = 0, z = p.rows_out - 1;
@@ -249,26 +265,14 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
         for (; free && k < wanted; free &= free - 1, ++k) {
             while (sh.end[a] <= k) ++a;
             if (sh.end[a] > have) return;
-            const int page = (int)page0 + __ffs(free) - 1, col = sh.first[a] + (k - (a ? sh.end[a - 1] : 0));
+            const int page = (int)at + __ffs(free) - 1, col = sh.first[a] + (k - (a ? sh.end[a - 1] : 0));
             p.table_out[a * p.table_out_stride + col] = page;
             __stcg(refs + page, 1);
             if (col < up(p, sh.keep[a])) p.copy_dst[a] = page;
         }
     };
     if (once) {
-        // a tile's counts are 4096 at most: four tiles a word
-#pragma unroll 1
-        for (int i0 = 0; i0 < kTiles && nth < wanted && lo + (int64_t)i0 * kTile < hi; i0 += 4) {
-            unsigned long long x = 0, ahead;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x |= (unsigned long long)__popc(bits >> (4 * (i0 + i)) & 15) << (16 * i);
-            const unsigned long long found = block_sum(x, sh.warp, ahead);
-#pragma unroll 1
-            for (int i = 0; i < 4 && nth < wanted; ++i) {
-                hand_out(bits >> (4 * (i0 + i)) & 15, lo + (int64_t)(i0 + i) * kTile + tid * 4, nth + (int)(ahead >> (16 * i) & 0xffff));
-                nth += (int)(found >> (16 * i) & 0xffff);
-            }
-        }
+        hand_out(bits, page0, nth + (int)(unsigned)before);
     } else {
         for (int64_t i = lo; i < hi && nth < wanted; i += kTile) {
             const uint32_t x = free_bits(refs, i + tid * 4, hi);
@@ -311,9 +315,9 @@ cudaError_t launch_pages(const PagesParams &p, cudaStream_t stream)
         done.fetch_or(1ull << (dev & 63), std::memory_order_release);
     }
     const int64_t work = p.num_pages + (int64_t)p.rows_out * p.cols;
-    // More CTAs share the pool and the tables; more of them take longer to meet. 64 rows of 512 pages, us with 1, 4, 8, 16: of 16384
-    // pages 14.1, 9.8, 9.9, 10.8, of 65536 23.7, 13.3, 12.3, 12.5; 512 rows of 512 pages of 131072 59.8, 22.1, 16.0, 14.1. Eight rows
-    // of 64 pages of 2048 7.9, 7.9, 8.2, 9.0.
+    // More CTAs share the pool and the tables; more of them take longer to meet. 64 rows of 512 pages, us with 2, 4, 8, 16: of 16384
+    // pages 10.9, 8.9, 9.0, 9.8, of 65536 20.6, 13.2, 11.0, 10.6; 512 rows of 512 pages of 131072 34.2, 26.0, 15.9, 13.4. Eight rows
+    // of 64 pages of 2048 7.3, 7.2, 7.4, 8.3.
     const int ctas = work <= (1 << 16) ? 4 : work <= (1 << 18) ? 8 : kMostCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
