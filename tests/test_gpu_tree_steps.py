@@ -7,6 +7,7 @@ import torch
 
 import tree_ref as ref
 from test_gpu_tree import BF16, DEV, F16, F32, Case, df  # noqa: F401  (df: the fixture)
+from test_gpu_tree_rows import check_step
 
 pytestmark = pytest.mark.gpu
 
@@ -224,3 +225,38 @@ def test_no_status_word_and_no_lse(df):
     df.detfold_kv_compact(cache, c.table[1:], torch.tensor([0], **I32), torch.tensor([[1]], **I32), torch.tensor([1], **I32))
     df.detfold_kv_copy_pages(cache, torch.tensor([1 << 30], **I32), torch.tensor([0], **I32))
     assert torch.equal(c.k.nan_to_num(), before.nan_to_num())
+
+
+@pytest.mark.parametrize("pool", [524288, 524289, 700001])
+def test_pages_of_very_large_pools(df, pool):
+    """Pools that are looked through in tiles, nearly full, with enough free pages and with too few."""
+    r = random.Random(pool)
+    page, cols, rows = 16, 9, 300
+    refs = [1] * pool
+    for e in r.sample(range(pool), 2500):
+        refs[e] = 0
+    free = [e for e, x in enumerate(refs) if x == 0]
+    r.shuffle(free)
+    table, lens = [], []
+    for _ in range(rows):
+        n = r.randint(0, 3 * page)
+        mine = [free.pop() for _ in range(-(-n // page))]
+        for e in mine:
+            refs[e] = 1
+        table.append(mine + [-1] * (cols - len(mine)))
+        lens.append(n)
+    for more in (20, 100):
+        origin = [r.choice([b, r.randrange(rows)]) for b in range(rows)]
+        keep = [lens[o] for o in origin]
+        check_step(df, refs, table, lens, origin, keep, [min(cols * page, k + r.randint(0, more)) for k in keep], page, cols)
+
+
+def test_forks_of_one_sequence(df):
+    """One prompt, as many rows as there may be, each of which goes on writing behind a page that they share."""
+    page, cols, pool = 16, 40, 6000
+    refs = [0] * pool
+    mine = random.Random(2).sample(range(pool), 38)
+    for e in mine:
+        refs[e] = 1
+    for length in (37 * 16 + 5, 38 * 16):
+        check_step(df, refs, [mine + [-1, -1]], [length], [0] * 4096, [length] * 4096, [length + 1] * 4096, page, cols)
