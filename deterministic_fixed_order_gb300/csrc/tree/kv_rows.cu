@@ -46,26 +46,26 @@ int widest(const detfold_kv_cache &c, int es)
 // Row n + path[i] goes to row n + i, i ascending. A thread takes one place of the rows and all
 // of the path there. Within a group of kFlight all are read before one is written; an earlier group wrote
 // rows under n + i, and path[j] >= j >= i for the later ones, so every row is read as it was. Bound by latency: lengths, path, table
-// and rows, one load after the other; 192 paths of 8 rows, 8 heads of 128 in 16 bits, take 3.6 us, one of 4 rows 3.1.
+// and rows, the path with the lengths; 192 paths of 8 rows, 8 heads of 128 in 16 bits, take 3.1 us, one of 4 rows 2.2.
 template <int B>
-__global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactParams p, const Units u)
+__global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant__ CompactParams p, const Units u, const Divide by_page)
 {
     using T = typename Bytes<B>::type;
     __shared__ int64_t s_from[DETFOLD_TREE_MAX_NODES], s_to[DETFOLD_TREE_MAX_NODES];
     enter_grid();
     const int b = blockIdx.x, tid = threadIdx.x;
-    const int n = p.lens[b], count = p.path_lens[b];
+    // asked for together; a path's numbers behind its length are not looked at
+    const int32_t *path = p.path + b * p.path_stride;
+    const int n = p.lens[b], count = p.path_lens[b], j = tid < p.max_path ? path[tid] : 0, before = tid && tid < p.max_path ? path[tid - 1] : -1;
     bool bad = n < 0 || n > DETFOLD_ATTN_MAX_LEN - DETFOLD_TREE_MAX_NODES || count < 0 || count > p.max_path;
     if (!bad && tid < count) {
-        const int32_t *path = p.path + b * p.path_stride;
-        const int j = path[tid], before = tid ? path[tid - 1] : -1;
         bad = j <= before || j >= DETFOLD_TREE_MAX_NODES;
         int64_t at[2] = {0, 0};
         if (!bad && j != tid) {
             const unsigned t[2] = {(unsigned)(n + j), (unsigned)(n + tid)};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const unsigned col = t[k] / (unsigned)p.cache.page_size;
+                const unsigned col = quotient(t[k], by_page);
                 const int page = col < p.table_cols ? p.table[b * p.table_stride + col] : -1;
                 if (page < 0 || page >= p.cache.num_pages) bad = true;
                 at[k] = page * u.page + (int64_t)(t[k] - col * (unsigned)p.cache.page_size) * u.token;
@@ -161,7 +161,7 @@ cudaError_t compact(const CompactParams &p, int es, cudaStream_t stream)
     const Units u = units_of(p.cache, es, B);
     const int64_t across = (2 * u.a_row + kThreads - 1) / kThreads;
     const dim3 grid((unsigned)p.batch, (unsigned)(across < 65535 ? across : 65535));
-    return launch_early(compact_kernel<B>, grid, kThreads, 0, stream, p, u);
+    return launch_early(compact_kernel<B>, grid, kThreads, 0, stream, p, u, divide_by(p.cache.page_size));
 }
 
 template <int B>
