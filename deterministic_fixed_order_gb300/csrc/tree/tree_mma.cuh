@@ -211,8 +211,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 
 // Two weights as two 16-bit parts each, the upper one truncated (to the bits of bfloat16, or of float16's mantissa: there a weight
 // under 2^-14 of the units that it is held in is rounded to their last place), the lower one what that leaves, off by 2^-16 or 2^-22
-// of the weight. `least`: 1 in both halves makes no lower part 0, so that an infinite value that every row sees gives the infinity,
-// not NaN; where values that are not finite are taken out it is 0.
+// of the weight. `least`: 1 in both halves makes no part 0 (in bfloat16 an upper part is 0 only where binary32's weight is), so that
+// an infinite value that every row sees gives the infinity, not NaN; where values that are not finite are taken out it is 0.
 __device__ __forceinline__ void parts(float2 x, uint32_t least, uint32_t &hi, uint32_t &lo, __nv_bfloat16)
 {
     const uint32_t u = __float_as_uint(x.x), v = __float_as_uint(x.y);
@@ -227,6 +227,7 @@ __device__ __forceinline__ void parts(float2 x, uint32_t least, uint32_t &hi, ui
     const float2 upper = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u), __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
     __half2 y = __floats2half2_rn(upper.x, upper.y);
     memcpy(&hi, &y, 4);
+    hi = __vmaxu2(hi, least);
     const float2 rest = add2(x, make_float2(-upper.x, -upper.y));
     y = __floats2half2_rn(rest.x, rest.y);
     memcpy(&lo, &y, 4);

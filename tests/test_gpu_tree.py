@@ -213,6 +213,23 @@ def test_values_that_are_not_finite_in_committed_tokens(df, dtype, window):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("gap", [0, 16, 24, 40, 60])
+def test_infinite_values_of_small_weights(df, dtype, gap):
+    """A token that every node attends to, whose score is up to 60 under the others': e^-60 of infinity is infinity."""
+    c = Case(dtype, [700], 9, 4, 2, 64, 16, scale=1.0)
+    c.q.zero_()[..., 0] = 1
+    finite = ~torch.isnan(c.k[..., :1].float()).expand_as(c.k)
+    c.k.copy_(torch.where(finite, 0.0, math.nan))
+    for t, sign in ((3, 1), (300, -1), (530, 1)):
+        at = int(c.table[0, t // 16]), t % 16
+        c.k[at][:, 0] = -gap
+        c.v[at][:, t % 64] = sign * math.inf
+    got, want = c.run(df)[0][0].double().cpu(), c.want()[0][0]
+    assert bool(torch.isinf(want).any()) and not bool(torch.isnan(got).any())
+    assert bool((torch.where(torch.isinf(want), want, 0.0) == torch.where(torch.isinf(got), got, 0.0)).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_scores_of_all_sizes(df, dtype):
     """Maxima that jump from tile to tile, by little and by much, upwards and downwards."""
     c = Case(dtype, [1200], 16, 8, 2, 128, 16)
