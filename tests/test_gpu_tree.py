@@ -230,6 +230,27 @@ def test_infinite_values_of_small_weights(df, dtype, gap):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("gap", [0, 8, 16])
+@pytest.mark.parametrize("n", [0, 70, 500])
+def test_infinite_values_of_small_weights_among_drafted_tokens(df, dtype, gap, n):
+    """The same of drafted tokens, which some nodes attend to: the infinity for these, nothing for the others. Weights are held
+    down to e^-22 of the largest there in float16."""
+    nodes = 12
+    sets = [{i} | ({3} if i % 3 == 0 else set()) | ({7} if i > 6 else set()) for i in range(nodes)]
+    c = Case(dtype, [n], nodes, 4, 2, 64, 16, scale=1.0, masks=[ref.words(sets, nodes)])
+    c.q.zero_()[..., 0] = 1
+    finite = ~torch.isnan(c.k[..., :1].float()).expand_as(c.k)
+    c.k.copy_(torch.where(finite, 0.0, math.nan))
+    for j, sign in ((3, 1), (7, -1)):
+        at = int(c.table[0, (n + j) // 16]), (n + j) % 16
+        c.k[at][:, 0] = -gap
+        c.v[at][:, 5 + j] = sign * math.inf
+    got, want = c.run(df)[0][0].double().cpu(), c.want()[0][0]
+    assert bool(torch.isinf(want).any()) and not bool(torch.isnan(got).any())
+    assert bool((torch.where(torch.isinf(want), want, 0.0) == torch.where(torch.isinf(got), got, 0.0)).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_scores_of_all_sizes(df, dtype):
     """Maxima that jump from tile to tile, by little and by much, upwards and downwards."""
     c = Case(dtype, [1200], 16, 8, 2, 128, 16)
